@@ -361,6 +361,150 @@ nvfp4_status nvfp4_modulate_gemm_ring(const uint16_t* x, int64_t M, int64_t K, i
                                       uint16_t* out, int64_t ldo, void* gemm_workspace, size_t gemm_workspace_bytes,
                                       void* stream);
 
+/* ---- Rotary positions, the 8-bit key/value cache and attention over it ----
+ * What lies between the QKV projection and the quantizer of the attention
+ * output's projection: rotate the queries (nvfp4_rope), write keys and values
+ * into a paged cache of 8-bit codes (nvfp4_kv_write, rotating the keys on the
+ * way where asked), and attend over the cache (nvfp4_kv_attention).  All of
+ * them enqueue kernels only, keep no state between calls, and replay correctly
+ * under graph capture. */
+
+/* Heads [rows, heads, dim] in device memory, bf16, unit stride along dim: head
+ * h of row m starts at data + m * row_stride + h * head_stride (elements, both
+ * multiples of 8 and not negative; data 16-byte aligned).  A third of a QKV
+ * product and [heads, rows, dim] are both of this form.  As an output no two
+ * heads may overlap: row_stride >= (heads - 1) * head_stride + dim with
+ * head_stride >= dim, or head_stride >= (rows - 1) * row_stride + dim with
+ * row_stride >= dim. */
+typedef struct {
+    uint16_t* data;
+    int64_t row_stride;
+    int64_t head_stride;
+} nvfp4_heads;
+
+/* Rotary positions with 1 to 4 axes (a token's place, or time, height and
+ * width).  A head's first 2 * sum(pairs) dims are rotated; the pairs are shared
+ * out over the axes in order, axis a taking pairs[a] of them.  Pair i is dims
+ * (2i, 2i + 1), or with split != 0 dims (i, i + sum(pairs)).  Pair i of axis a
+ * (its first being i0) turns by the angle whose (cos, sin) is
+ * table[a][positions[m][a]][i - i0], binary32:
+ *   y1 = bf16(RN(RN(x1 cos) - RN(x2 sin))),  y2 = bf16(RN(RN(x2 cos) + RN(x1 sin))).
+ * pairs[a] >= 1, sum(pairs) a multiple of 8 and at most dim / 2.  table[a] is a
+ * DEVICE array [rows[a]][pairs[a]][2] (8-byte aligned, rows[a] >= 1), positions
+ * a DEVICE int32 array [M][axes] with row stride ld_positions >= axes.  A
+ * position outside [0, rows[a]) gives NaN; nothing is read for it. */
+#define NVFP4_ROPE_MAX_AXES 4
+typedef struct {
+    int32_t axes;
+    int32_t split;
+    int32_t pairs[NVFP4_ROPE_MAX_AXES];
+    int64_t rows[NVFP4_ROPE_MAX_AXES];
+    const float* table[NVFP4_ROPE_MAX_AXES];
+    const int32_t* positions;
+    int64_t ld_positions;
+} nvfp4_rope_params;
+
+/* The usual table of one axis: (cos, sin) of p * theta^(-j / pairs) for
+ * positions p < rows and j < pairs, formed in binary64 and rounded to binary32.
+ * rows >= 1, pairs >= 1, rows * pairs < 2^31, theta > 0 and finite. */
+nvfp4_status nvfp4_rope_table(float* table, int64_t rows, int32_t pairs, double theta, void* stream);
+
+/* Rotates x [M, heads, dim] into out; dims past the rotated ones are copied.
+ * out may be x itself (same data and strides); otherwise they must not overlap.
+ * dim a multiple of 16, at most 512; 1 <= M <= 2^23; a bad rope table returns
+ * NVFP4_ERR_SHAPE. */
+nvfp4_status nvfp4_rope(const nvfp4_heads* x, int64_t M, int32_t heads, int32_t dim, const nvfp4_rope_params* rope,
+                        const nvfp4_heads* out, void* stream);
+
+/* A pool of cache blocks.  A block holds 64 positions of every key/value head:
+ * for each head one E4M3 code per value and, apart for keys and values, one
+ * power of two, held as the byte b that stands for 2^(b - 127).  The power is
+ * the smallest with amax <= 448 * 2^(b - 127) over the block's finite values
+ * (b >= 1); a code is the nearest E4M3 (ties to even) of value / 2^(b - 127),
+ * or a NaN code where the value is not finite; with b = 247, the largest that
+ * occurs, codes stop at 240, so that code * power is finite.  A power of two leaves E4M3's
+ * relative precision as it is and makes code * power exact in bf16.
+ *   k [blocks][heads][dim / 16][64][16]: dims 16c..16c+15 of position t at [c][t]
+ *   v [blocks][heads][4][dim][16]: position t = 32u + 16e + 8m + 4h + j (e, m, h
+ *     in {0, 1}, j < 4) of dim d at [2u + h][d][8e + 4m + j]
+ *   k_power, v_power [blocks][heads]
+ * dim 64 or 128; k and v 16-byte aligned.  A block needs no initial value. */
+#define NVFP4_KV_BLOCK 64
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* k_power;
+    uint8_t* v_power;
+    int64_t blocks;
+    int32_t heads;
+    int32_t dim;
+} nvfp4_kv_cache;
+
+/* `count` sequences, all arrays DEVICE int32.  Sequence b has new rows
+ * [row_start[b], row_start[b + 1]) of the M rows of a call (count + 1 entries,
+ * nondecreasing; a sequence may have none, and rows outside all sequences are
+ * neither read nor written), which are its last positions: with lens[b]
+ * positions in all, the new ones among them, row row_start[b] + i is position
+ * lens[b] - n + i.  Position p lies in cache block table[b][p / 64]
+ * (table row stride ld_table >= table_blocks, entries of unused blocks are not
+ * read).  1 <= count <= 2^20.  The arrays' contents are not checked by the host:
+ * whatever they hold, no access leaves the arrays, M rows and pool given. */
+typedef struct {
+    int64_t count;
+    const int32_t* row_start;
+    const int32_t* lens;
+    const int32_t* table;
+    int64_t ld_table;
+    int64_t table_blocks;
+} nvfp4_kv_sequences;
+
+/* Quantises the M rows of k and v [M, heads, dim] and writes them to their
+ * positions; with a rope the keys are rotated first, as nvfp4_rope does.  A
+ * block that already holds positions of the sequence before the new ones keeps
+ * them: its power becomes the larger of the old and what the new values need,
+ * and where it grew the held codes are re-encoded, E4M3(code * 2^(old - new)).
+ * Bytes of positions after the last are left as they were.  Rows whose block
+ * does not exist (an entry outside the pool, a length that the table cannot
+ * hold, a position before 0) are skipped.  Two sequences must not write to the
+ * same block in one call.  1 <= M <= 2^23. */
+nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences* seqs, int64_t M,
+                            const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_rope_params* rope, void* stream);
+
+/* Reads the positions of the M rows back: k and v [M, heads, dim] = code *
+ * power, exact in bf16.  A row before position 0 is 0; one whose block does not
+ * exist, NaN. */
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences* seqs, int64_t M,
+                           const nvfp4_heads* k, const nvfp4_heads* v, void* stream);
+
+/* Attention of the queries q [M, q_heads, dim] over their sequences' cached
+ * keys and values; query head g reads key/value head g / (q_heads / heads).
+ *   out[m][g] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q.k_j - max)
+ * over positions j below the row's limit: lens[b] with causal_block = 0; with
+ * causal_block = c >= 1 the end of the row's own run of c positions, at most
+ * lens[b] (c = 1: a row sees itself and what is before it).  A row that sees
+ * nothing gives 0.  Whatever a hidden position holds has no effect; a NaN that
+ * is seen, a query that is not finite, a block outside the pool or a length
+ * that the table cannot hold gives NaN.
+ * Products and sums are binary32.  The keys' codes are multiplied as they are;
+ * a query is split into two E4M3 numbers that together hold each bf16 element
+ * to its last bit, or to 2^-21 of the row's largest element where that is
+ * more.  Probabilities are rounded to bf16 for the product with the values, and
+ * the output once to bf16.  The order of the sums depends on the sizes and
+ * max_len only: the same call gives the same bytes.
+ * max_len is the host's bound on the lengths, used to decide how far the keys
+ * of few rows are shared out over workgroups (results for longer sequences are
+ * right all the same).  The workspace needs
+ * nvfp4_kv_attention_workspace_bytes(...) bytes for the same sizes (16-byte
+ * aligned; may be NULL when that is 0); calls that can overlap must not share
+ * it.  scale > 0 and finite; causal_block, max_len >= 0; q_heads a multiple of
+ * cache->heads, M * q_heads < 2^31, M * (q_heads / heads) <= 2^28; out may be q
+ * itself. */
+size_t nvfp4_kv_attention_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
+                                          int64_t max_len);
+nvfp4_status nvfp4_kv_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads, const nvfp4_kv_cache* cache,
+                                const nvfp4_kv_sequences* seqs, float scale, int32_t causal_block, int64_t max_len,
+                                const nvfp4_heads* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- Single-step entry points ------------------------------------------
  * Elementwise versions of single producer steps, running the very device
  * functions the producer kernels use, so that each step can be checked over

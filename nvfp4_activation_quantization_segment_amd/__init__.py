@@ -8,7 +8,9 @@ without the built library raises.
 Functions named like the C entry points (``nvfp4_modulate_absmax`` ...) take
 torch tensors and the same arguments as the C ABI (``include/nvfp4.h``);
 ``modulate_quantize``, ``swiglu_quantize`` and ``gemm`` are conveniences that
-allocate their outputs with torch.
+allocate their outputs with torch, and so are ``rope_table``, ``rope``,
+``KvCache``, ``kv_write``, ``kv_read`` and ``kv_attention`` for what lies between
+the QKV projection and the attention output's quantizer.
 """
 from __future__ import annotations
 
@@ -45,6 +47,31 @@ class RowGates(ctypes.Structure):
                 ("gate", ctypes.c_void_p), ("ld", ctypes.c_int64)]
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+ROPE_MAX_AXES = 4
+KV_BLOCK = 64
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("split", ctypes.c_int32), ("pairs", ctypes.c_int32 * ROPE_MAX_AXES),
+                ("rows", ctypes.c_int64 * ROPE_MAX_AXES), ("table", ctypes.c_void_p * ROPE_MAX_AXES),
+                ("positions", ctypes.c_void_p), ("ld_positions", ctypes.c_int64)]
+
+
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_power", ctypes.c_void_p),
+                ("v_power", ctypes.c_void_p), ("blocks", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32)]
+
+
+class KvSequences(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("row_start", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("table_blocks", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run nvfp4_activation_quantization_segment_amd/build.py")
@@ -52,6 +79,8 @@ def _load():
     P, I64, I32, V = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
     SEG = ctypes.POINTER(Segments)
     GATES = ctypes.POINTER(RowGates)
+    HEADS, ROPE = ctypes.POINTER(Heads), ctypes.POINTER(RopeParams)
+    CACHE, SEQS = ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvSequences)
     sigs = {
         "nvfp4_padded_rows": (I64, [I64]),
         "nvfp4_absmax_workspace_bytes": (ctypes.c_size_t, []),
@@ -74,6 +103,13 @@ def _load():
         "nvfp4_ring_gemm_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I64]),
         "nvfp4_modulate_gemm_ring": (I32, [P, I64, I64, I64, SEG, P, P, P, P, I32, I64, P, P, P, I64, P, I64, P,
                                            ctypes.c_size_t, V]),
+        "nvfp4_rope_table": (I32, [P, I64, I32, ctypes.c_double, V]),
+        "nvfp4_rope": (I32, [HEADS, I64, I32, I32, ROPE, HEADS, V]),
+        "nvfp4_kv_write": (I32, [CACHE, SEQS, I64, HEADS, HEADS, ROPE, V]),
+        "nvfp4_kv_read": (I32, [CACHE, SEQS, I64, HEADS, HEADS, V]),
+        "nvfp4_kv_attention_workspace_bytes": (ctypes.c_size_t, [I64, I64, I32, I32, I32, I64]),
+        "nvfp4_kv_attention": (I32, [HEADS, I64, I32, CACHE, SEQS, ctypes.c_float, I32, I64, HEADS, P,
+                                     ctypes.c_size_t, V]),
         "nvfp4_step_modulate": (I32, [P, P, P, P, I64, V]),
         "nvfp4_step_swiglu": (I32, [P, P, P, I64, V]),
         "nvfp4_step_block_scale": (I32, [P, P, P, I64, V]),
@@ -493,3 +529,216 @@ def modulate_gemm_ring(x: torch.Tensor, row_start, shift: torch.Tensor, scale: t
                              sfw, w_scale, N, out, out.stride(0), gws, need, st)
     del keep
     return out, ts, amax, ring
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, the 8-bit key/value cache and attention over it
+# ---------------------------------------------------------------------------
+def _same_device(dev: torch.device, **tensors):
+    if dev.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {dev}")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _heads(name: str, x: torch.Tensor, shape=None) -> Heads:
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected bf16, got {x.dtype}")
+    if x.dim() != 3 or (shape is not None and tuple(x.shape) != tuple(shape)):
+        raise ValueError(f"{name}: expected {'[rows, heads, dim]' if shape is None else list(shape)}, got {list(x.shape)}")
+    if x.stride(2) != 1 and x.shape[2] > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    # the stride of a dimension of one element says nothing
+    return Heads(x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0)
+
+
+def _int32(name: str, t: torch.Tensor, dims: int) -> torch.Tensor:
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name}: expected int32, got {t.dtype}")
+    if t.dim() != dims or (t.stride(dims - 1) != 1 and t.shape[dims - 1] > 1):
+        raise ValueError(f"{name} must have {dims} dimension(s) and unit stride along the last")
+    return t
+
+
+def _rope_params(tables, positions: torch.Tensor, rows: int, split: bool) -> RopeParams:
+    if not 1 <= len(tables) <= ROPE_MAX_AXES:
+        raise ValueError(f"expected 1 to {ROPE_MAX_AXES} tables, got {len(tables)}")
+    _int32("positions", positions, 2)
+    if tuple(positions.shape) != (rows, len(tables)):
+        raise ValueError(f"positions: expected [{rows}, {len(tables)}], got {list(positions.shape)}")
+    p = RopeParams()
+    p.axes, p.split = len(tables), int(bool(split))
+    for a, t in enumerate(tables):
+        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[2] != 2 or not t.is_contiguous():
+            raise ValueError("a rope table is a contiguous fp32 [positions, pairs, 2]")
+        if t.device != positions.device:
+            raise ValueError(f"table {a} is on {t.device}, positions on {positions.device}")
+        p.pairs[a], p.rows[a], p.table[a] = t.shape[1], t.shape[0], t.data_ptr()
+    p.positions, p.ld_positions = positions.data_ptr(), positions.stride(0) if rows > 1 else len(tables)
+    return p
+
+
+def _call(fn: str, dev: torch.device, stream, *args):
+    """One launch on the tensors' device: on `stream`, or that device's current stream."""
+    st = _torch_stream(stream, dev)
+    if st.device != dev:
+        raise ValueError(f"the stream is on {st.device}, the tensors on {dev}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(fn, getattr(lib, fn)(*args, st.cuda_stream))
+    else:
+        _check(fn, getattr(lib, fn)(*args, st.cuda_stream))
+
+
+def rope_table(positions: int, pairs: int, theta: float = 10000.0, device=None, stream=None) -> torch.Tensor:
+    """(cos, sin) of p * theta^(-j / pairs) for positions p and pairs j, fp32 [positions, pairs, 2]
+    (formed in binary64): the table of one axis for `rope` and `kv_write`."""
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    _same_device(dev)
+    with torch.cuda.stream(_torch_stream(stream, dev)):
+        table = torch.empty((positions, pairs, 2), dtype=torch.float32, device=dev)
+    _call("nvfp4_rope_table", dev, stream, table.data_ptr(), positions, pairs, float(theta))
+    return table
+
+
+def rope(x: torch.Tensor, tables, positions: torch.Tensor, split: bool = False, out: torch.Tensor | None = None,
+         stream=None) -> torch.Tensor:
+    """Rotates the heads x [rows, heads, dim] (bf16, any row and head strides) by their positions.
+
+    tables: one [positions, pairs, 2] table for each axis (rope_table); positions: int32 [rows, axes].
+    Pairs are neighbouring dims, or with split dims half of the rotated part apart.  out may be x."""
+    dev = x.device
+    _same_device(dev, positions=positions, out=out)
+    hx = _heads("x", x)
+    rows, heads, dim = x.shape
+    r = _rope_params(tables, positions, rows, split)
+    if out is None:
+        with torch.cuda.stream(_torch_stream(stream, dev)):
+            out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev)
+    ho = _heads("out", out, x.shape)
+    if rows:
+        _call("nvfp4_rope", dev, stream, hx, rows, heads, dim, r, ho)
+    return out
+
+
+class KvCache:
+    """A pool of 8-bit key/value cache blocks of 64 positions, as four uint8 tensors:
+
+    k [blocks, heads, dim / 16, 64, 16] and v [blocks, heads, 4, dim, 16], E4M3 codes in the order that the
+    attention kernels read them; k_power and v_power [blocks, heads], byte b standing for 2^(b - 127)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_power: torch.Tensor, v_power: torch.Tensor):
+        if k.dim() != 5:
+            raise ValueError("k must be [blocks, heads, dim / 16, 64, 16]")
+        blocks, heads, dim = k.shape[0], k.shape[1], 16 * k.shape[2]
+        for name, t, shape in (("k", k, (blocks, heads, dim // 16, KV_BLOCK, 16)), ("v", v, (blocks, heads, 4, dim, 16)),
+                               ("k_power", k_power, (blocks, heads)), ("v_power", v_power, (blocks, heads))):
+            if t.dtype != torch.uint8:
+                raise TypeError(f"{name}: expected uint8, got {t.dtype}")
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name}: expected contiguous {list(shape)}, got {list(t.shape)}")
+        _same_device(k.device, v=v, k_power=k_power, v_power=v_power)
+        self.k, self.v, self.k_power, self.v_power = k, v, k_power, v_power
+        self.blocks, self.heads, self.dim, self.device = blocks, heads, dim, k.device
+        self._struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_power.data_ptr(), v_power.data_ptr(), blocks, heads,
+                                     dim)
+
+    @classmethod
+    def empty(cls, blocks: int, heads: int, dim: int, device=None) -> "KvCache":
+        """A pool of zero blocks on `device` (default: the current GPU); dim 64 or 128."""
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        make = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=dev)  # noqa: E731
+        return cls(make(blocks, heads, dim // 16, KV_BLOCK, 16), make(blocks, heads, 4, dim, 16), make(blocks, heads),
+                   make(blocks, heads))
+
+
+def _sequences(row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, dev: torch.device) -> KvSequences:
+    _same_device(dev, row_start=row_start, lens=lens, table=table)
+    _int32("row_start", row_start, 1)
+    _int32("lens", lens, 1)
+    _int32("table", table, 2)
+    n = lens.shape[0]
+    if row_start.shape[0] != n + 1 or table.shape[0] != n:
+        raise ValueError(f"{n} lengths need {n + 1} row starts and {n} table rows, got {row_start.shape[0]} and "
+                         f"{table.shape[0]}")
+    return KvSequences(n, row_start.data_ptr(), lens.data_ptr(), table.data_ptr(),
+                       table.stride(0) if n > 1 else table.shape[1], table.shape[1])
+
+
+def kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor, lens: torch.Tensor,
+             table: torch.Tensor, tables=(), positions: torch.Tensor | None = None, split: bool = False, stream=None):
+    """Quantises the new rows k and v [rows, heads, dim] (bf16) into the cache.
+
+    Sequence b's rows are row_start[b] .. row_start[b + 1], its last positions once it holds lens[b] of them;
+    table [sequences, blocks] names its cache blocks (all int32 on the GPU).  With tables and positions the keys
+    are rotated on the way, as `rope` does."""
+    dev = cache.device
+    _same_device(dev, k=k, v=v, positions=positions)
+    shape = (k.shape[0], cache.heads, cache.dim)
+    hk, hv = _heads("k", k, shape), _heads("v", v, shape)
+    q = _sequences(row_start, lens, table, dev)
+    r = None
+    if len(tables):
+        if positions is None:
+            raise ValueError("rotating the keys needs their positions")
+        r = _rope_params(tables, positions, k.shape[0], split)
+    if k.shape[0]:
+        _call("nvfp4_kv_write", dev, stream, cache._struct, q, k.shape[0], hk, hv, r)
+
+
+def kv_read(cache: KvCache, rows: int, row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+            k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """Reads the positions of `rows` rows (as kv_write addresses them) back: k and v, bf16 [rows, heads, dim]."""
+    dev = cache.device
+    _same_device(dev, k=k, v=v)
+    q = _sequences(row_start, lens, table, dev)
+    shape = (rows, cache.heads, cache.dim)
+    with torch.cuda.stream(_torch_stream(stream, dev)):
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    hk, hv = _heads("k", k, shape), _heads("v", v, shape)
+    if rows:
+        _call("nvfp4_kv_read", dev, stream, cache._struct, q, rows, hk, hv)
+    return k, v
+
+
+def nvfp4_kv_attention_workspace_bytes(M, count, q_heads, heads, dim, max_len):
+    return int(lib.nvfp4_kv_attention_workspace_bytes(M, count, q_heads, heads, dim, max_len))
+
+
+def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                 scale: float | None = None, causal_block: int = 0, max_len: int | None = None,
+                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the queries q [rows, q_heads, dim] (bf16) over their sequences' cached keys and values.
+
+    Rows and positions as in kv_write.  causal_block: 0 for no mask, 1 for causal, c for runs of c positions that
+    see one another and all before them.  scale: dim^-0.5 by default.  max_len: a bound on the lengths known to the
+    host (default: what the table holds), which decides how far the keys of few rows are shared out over
+    workgroups.  A workspace of nvfp4_kv_attention_workspace_bytes(...) is allocated with torch when none is given,
+    on the stream that the call runs on."""
+    dev = cache.device
+    _same_device(dev, q=q, out=out, workspace=workspace)
+    hq = _heads("q", q)
+    rows, q_heads, dim = q.shape
+    if dim != cache.dim:
+        raise ValueError(f"q has heads of {dim}, the cache of {cache.dim}")
+    s = _sequences(row_start, lens, table, dev)
+    if max_len is None:
+        max_len = table.shape[1] * KV_BLOCK
+    need = int(lib.nvfp4_kv_attention_workspace_bytes(rows, s.count, q_heads, cache.heads, dim, max_len)) if rows else 0
+    if out is None or (need and workspace is None):
+        with torch.cuda.stream(_torch_stream(stream, dev)):
+            if out is None:
+                out = torch.empty((rows, q_heads, dim), dtype=torch.bfloat16, device=dev)
+            if need and workspace is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ho = _heads("out", out, q.shape)
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if rows:
+        _call("nvfp4_kv_attention", dev, stream, hq, rows, q_heads, cache._struct, s,
+              dim ** -0.5 if scale is None else float(scale), causal_block, max_len, ho,
+              None if workspace is None else workspace.data_ptr(), size)
+    return out

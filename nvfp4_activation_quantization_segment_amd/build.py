@@ -8,7 +8,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
-SOURCES = ["api.hip", "producer.hip", "gemm.hip"]
+SOURCES = ["api.hip", "producer.hip", "gemm.hip", "api_attention.hip", "kv_cache.hip", "attention.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "kv_internal.h"
 
 using namespace nvfp4;
 
@@ -126,6 +127,8 @@ nvfp4_status scratch_of_current_device(void** out) {
 }
 
 }  // namespace
+
+nvfp4_status nvfp4::report_hip(hipError_t e) { return hip_status(e); }
 
 BarrierArgs nvfp4::next_barrier_args() {
     constexpr uint64_t kTagMask = ((uint64_t)1 << 44) - 1;

@@ -1,0 +1,486 @@
+// Attention over the paged 8-bit key/value cache:
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - max),  j < limit(row).
+//
+// The rows of a tile are the queries of one sequence and one key/value head,
+// (token, query head of the group) in that order, 32 to a wave.  Scores are
+// formed transposed, S^T = K Q^T, so that a lane holds one query's scores and
+// the softmax needs one exchange, between the lane's two halves of the keys.
+//
+// Keys are multiplied as they lie in the cache, 8-bit codes whose power of two
+// the matrix instruction applies.  A query is split into two E4M3 numbers,
+//   q 2^-e = hi + lo / 16,  2^e the row's power of two (amax <= 448 2^e),
+// each rounded to nearest: bf16's 8 bits are 4 + 4, so the split is exact for
+// elements of at least 2^-6 2^e and off by at most 2^-14 2^e below (the largest
+// element is above 224 2^e, so by less than 2^-21 of it).  Two 8-bit products at twice the bf16
+// rate cost what one bf16 product would, and the keys need no conversion.
+//
+// Values become bf16 (exact: code times a power of two) and are multiplied with
+// probabilities rounded to bf16 (half a step is 2^-9 of each p, and their sum
+// is taken before that rounding).  Scores, maxima, sums and outputs are held in
+// binary32.
+#include "kv_device.h"
+
+namespace nvfp4 {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kRows = 32;  // rows of a wave
+// A running maximum is kept until a score passes it by this much (in powers of
+// two): p stays below 2^8, and most blocks need no rescaling of the output.
+constexpr float kSlack = 8.0f;
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
+__device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
+
+struct Tile {
+    bool any;
+    bool bad;         // a length that the table cannot hold
+    int64_t b;
+    int64_t row0;     // first row of the sequence
+    int32_t n;        // its new tokens
+    int32_t first;    // first tile row, counted in the sequence
+    int32_t rows;     // n * group
+    int64_t len;
+};
+
+__device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int64_t unit, int64_t T) {
+    Tile t;
+    t.any = false;
+    const SeqArgs& q = a.seqs;
+    const auto base = [&](int64_t b) { return tile_base(clamp64(q.row_start[b], 0, q.M), b, a.group, T); };
+    t.b = uniform64(find_sequence(unit, q.B, base));
+    const RowRange r = row_range(q.row_start[t.b], q.row_start[t.b + 1], q.M);
+    const int64_t n = r.last - r.first, local = unit - tile_base(r.first, t.b, a.group, T);
+    if (local < 0 || local * T >= n * a.group) return t;
+    t.any = true;
+    t.row0 = r.first;
+    t.n = (int32_t)n;
+    t.first = (int32_t)(local * T);
+    t.rows = (int32_t)(n * a.group);
+    t.len = q.lens[t.b];
+    t.bad = kv_length_bad(t.len, q.table_blocks);
+    return t;
+}
+
+// What a lane knows of its row.
+struct Row {
+    bool valid;
+    int64_t token;   // row of q and out
+    int32_t head;    // query head
+    int32_t limit;   // keys it sees
+};
+
+__device__ __forceinline__ Row find_row(const AttentionArgs& a, const Tile& t, int32_t rr, int32_t kv_head) {
+    Row r;
+    r.valid = rr < t.rows;
+    const int32_t at = r.valid ? rr : t.rows - 1;
+    const int32_t i = at / a.group;
+    r.token = t.row0 + i;
+    r.head = kv_head * a.group + (at - i * a.group);
+    r.limit = t.bad ? 0 : (int32_t)kv_limit(t.len - t.n + i, t.len, a.causal);
+    return r;
+}
+
+// A row of queries as second operands: hi and lo for each 64 dims, and the
+// power bytes of the two.
+template <int D>
+struct Query {
+    i32x8 hi[D / 64], lo[D / 64];
+    int32_t power_hi, power_lo;
+    bool nan;  // an element is not finite
+};
+
+template <int D>
+__device__ __forceinline__ void load_query(Query<D>& f, const AttentionArgs& a, const Row& r) {
+    const int h = (threadIdx.x & 63) >> 5;
+    uint32_t w[D / 64][16];  // this half's 32 dims of each 64: pieces 4k + 2h and 4k + 2h + 1 of 16
+    const uint16_t* p = a.q.data + r.token * a.q.row + r.head * a.q.head;
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (r.valid) x = *reinterpret_cast<const uint4*>(p + 64 * k + 32 * h + 8 * j);
+            w[k][4 * j] = x.x, w[k][4 * j + 1] = x.y, w[k][4 * j + 2] = x.z, w[k][4 * j + 3] = x.w;
+            m = pk_max_u16(m, pk_max_u16(pk_max_u16(mag2(x.x), mag2(x.y)), pk_max_u16(mag2(x.z), mag2(x.w))));
+        }
+    m = fold_max(m);
+    const uint32_t other = (uint32_t)__shfl_xor((int)m, 32);
+    m = m > other ? m : other;
+    f.nan = m >= 0x7F80u;
+    uint32_t e = f.nan ? 127u : power_for(m);
+    e = e < 5u ? 5u : e;  // the low part's power is 2^-4 of it
+    f.power_hi = (int32_t)e;
+    f.power_lo = (int32_t)(e - 4u);
+    const float inv = power_inverse(e);
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x0 = bf16_lo(w[k][2 * j]) * inv, x1 = bf16_hi(w[k][2 * j]) * inv;
+            const float x2 = bf16_lo(w[k][2 * j + 1]) * inv, x3 = bf16_hi(w[k][2 * j + 1]) * inv;
+            const uint32_t c = fp8_pack4(x0, x1, x2, x3);
+            const auto v01 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false);
+            const auto v23 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+            const uint32_t l = fp8_pack4((x0 - v01[0]) * 16.0f, (x1 - v01[1]) * 16.0f, (x2 - v23[0]) * 16.0f,
+                                         (x3 - v23[1]) * 16.0f);
+            f.hi[k][j] = f.nan ? 0 : (int)c;
+            f.lo[k][j] = f.nan ? 0 : (int)l;
+        }
+}
+
+__device__ __forceinline__ i32x8 pieces(uint4 a, uint4 b) {
+    return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+__device__ __forceinline__ f32x16 mul_scores(i32x8 k, i32x8 q, f32x16 acc, int k_power, int q_power) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, q, acc, 0, 0, 0, k_power, 0, q_power);
+}
+
+__device__ __forceinline__ bf16x8 values_bf16(uint32_t a, uint32_t b, float scale) {
+    const uint4 w = make_uint4(fp8_to_bf16x2<false>(a, scale), fp8_to_bf16x2<true>(a, scale),
+                               fp8_to_bf16x2<false>(b, scale), fp8_to_bf16x2<true>(b, scale));
+    return __builtin_bit_cast(bf16x8, w);
+}
+
+// The running softmax of a lane's row.
+struct Softmax {
+    float m;  // reference maximum, scaled, base 2
+    float l;  // sum of this half's p
+};
+
+// One block's scores (two tiles of 32 keys) -> probabilities in bf16, the
+// second operands of the products with the values.
+template <int NO>
+__device__ __forceinline__ void softmax_block(f32x16 s[2], Softmax& st, f32x16 (&o)[NO], float scale_log2, bf16x8 p[4]) {
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[0][i]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[1][i]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    top *= scale_log2;
+    if (__any(top > st.m + kSlack)) {
+        const float m = fmaxf(st.m, top);
+        const float alpha = m == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+        st.l *= alpha;
+#pragma unroll
+        for (int d = 0; d < NO; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
+        st.m = m;
+    }
+    const float ref = st.m == neg_inf() ? 0.0f : st.m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][8 * k + 2 * i], scale_log2, -ref));
+                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][8 * k + 2 * i + 1], scale_log2, -ref));
+                sum += x;
+                sum += y;
+                w[i] = pack_bf16x2(x, y);
+            }
+            p[2 * t + k] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+    st.l += sum;
+}
+
+// Scores of keys past the row's limit become -inf.  left: the limit counted
+// from the block's first key.
+__device__ __forceinline__ void mask_scores(f32x16 s[2], int32_t left) {
+    const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (32 * t + 8 * (i / 4) + 4 * h + i % 4 >= left) s[t][i] = neg_inf();
+}
+
+// ---------------------------------------------------------------------------
+// Narrow tiles: 32 rows to a workgroup of 4 waves that share out the blocks of
+// keys, each with its own softmax, joined at the end through LDS; the keys of
+// long sequences are shared out over workgroups too (parts).  For single tokens
+// and other short row tiles.  Every lane loads its operands from the cache
+// itself, 1 KB of neighbouring bytes a wave and load; keys of the next block
+// are in flight while this one's softmax runs, values while its scores are
+// formed.
+// ---------------------------------------------------------------------------
+constexpr int kNarrowWaves = 4;
+
+template <int D>
+__global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(AttentionArgs a) {
+    constexpr int kDT = D / 32, kK = D / 64;
+    constexpr int kBytes = kKvBlock * D;
+    constexpr int kLd = D + 4;
+    __shared__ __align__(16) float so[kNarrowWaves][kRows][kLd];
+    __shared__ float sm[kNarrowWaves][kRows], sl[kNarrowWaves][kRows];
+    const Tile t = find_tile(a, blockIdx.x, kRows);
+    if (!t.any) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int c = lane & 31, h = lane >> 5;
+    const int kv_head = blockIdx.y, part = blockIdx.z;
+    const Row row = find_row(a, t, t.first + c, kv_head);
+    // blocks that the tile's last row sees, and keys that all its rows see
+    const int last = t.first + kRows < t.rows ? t.first + kRows - 1 : t.rows - 1;
+    const int seen = find_row(a, t, last, kv_head).limit;
+    const int all = find_row(a, t, t.first, kv_head).limit;
+    const BlockRange range = kv_part((seen + kKvBlock - 1) / kKvBlock, part, a.parts);
+    const int64_t at0 = range.first + wave;
+
+    Query<D> q;
+    load_query<D>(q, a, row);
+    Softmax st = {neg_inf(), 0.0f};
+    f32x16 o[kDT];
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
+
+    const int32_t* table = a.seqs.table + t.b * a.seqs.ld_table;
+    // page of a block, -1 where there is none
+    const auto page_of = [&](int64_t at) -> int64_t {
+        const int64_t p = at < range.last ? __builtin_amdgcn_readfirstlane(table[at]) : -1;
+        return p >= 0 && p < a.cache.blocks ? p : -1;
+    };
+    uint4 kf[2][2 * kK];
+    const auto load_keys = [&](int64_t page) {
+        const uint8_t* p = a.cache.k + (page * a.cache.heads + kv_head) * kBytes + (2 * h) * (kKvBlock * 16) + c * 16;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int k = 0; k < kK; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    kf[tt][2 * k + i] = *reinterpret_cast<const uint4*>(p + (4 * k + i) * (kKvBlock * 16) + tt * 32 * 16);
+    };
+    int64_t page = page_of(at0), next = page_of(at0 + kNarrowWaves);
+    if (page >= 0) load_keys(page);
+    for (int64_t at = at0; at < range.last; at += kNarrowWaves) {
+        const bool good = page >= 0;
+        uint4 vf[kDT][2];
+        uint32_t kp = 127, vp = 127;
+        if (good) {
+            const uint8_t* p = a.cache.v + (page * a.cache.heads + kv_head) * kBytes + c * 16;
+#pragma unroll
+            for (int d = 0; d < kDT; ++d)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    vf[d][u] = *reinterpret_cast<const uint4*>(p + (2 * u + h) * (D * 16) + d * 32 * 16);
+            kp = clamp_power(a.cache.k_power[page * a.cache.heads + kv_head]);
+            vp = clamp_power(a.cache.v_power[page * a.cache.heads + kv_head]);
+        } else {
+#pragma unroll
+            for (int d = 0; d < kDT; ++d)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) vf[d][u] = make_uint4(0, 0, 0, 0);
+        }
+        f32x16 s[2];
+        if (good) {
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                s[tt] = f32x16{};
+#pragma unroll
+                for (int k = 0; k < kK; ++k) {
+                    const i32x8 f = pieces(kf[tt][2 * k], kf[tt][2 * k + 1]);
+                    s[tt] = mul_scores(f, q.hi[k], s[tt], (int)kp, q.power_hi);
+                    s[tt] = mul_scores(f, q.lo[k], s[tt], (int)kp, q.power_lo);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[tt][i] = quiet_nan();  // no such block: whoever sees it gets NaN
+        }
+        page = next;
+        if (page >= 0) load_keys(page);
+        next = page_of(at + 2 * kNarrowWaves);
+
+        const int first_key = (int)at * kKvBlock;
+        const bool edge = first_key + kKvBlock > all;
+        if (edge) mask_scores(s, row.limit - first_key);
+        bf16x8 p[4];
+        softmax_block<kDT>(s, st, o, a.scale_log2, p);
+        if (edge) {
+            // A masked key has p = 0, but 0 times a NaN value is NaN: NaN codes
+            // are taken out and given back to the rows that see their key.
+            bool nan = false;
+#pragma unroll
+            for (int d = 0; d < kDT; ++d)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    nan |= fp8_any_nan(vf[d][u].x) || fp8_any_nan(vf[d][u].y) || fp8_any_nan(vf[d][u].z) ||
+                           fp8_any_nan(vf[d][u].w);
+            if (__any(nan)) {
+#pragma unroll
+                for (int d = 0; d < kDT; ++d) {
+                    int lowest = kKvBlock;  // first key of this lane's dim with a NaN
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t w[4] = {vf[d][u].x, vf[d][u].y, vf[d][u].z, vf[d][u].w};
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t code = (w[i / 4] >> (8 * (i % 4))) & 0x7Fu;
+                            if (code == 0x7Fu) {
+                                const int key = 32 * u + 16 * (i / 8) + 8 * (i / 4 % 2) + 4 * h + i % 4;
+                                lowest = key < lowest ? key : lowest;
+                                w[i / 4] &= ~(0xFFu << (8 * (i % 4)));
+                            }
+                        }
+                        vf[d][u] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    const int other = __shfl_xor(lowest, 32);
+                    lowest = lowest < other ? lowest : other;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int key = __shfl(lowest, 8 * (i / 4) + 4 * h + i % 4);
+                        if (key < row.limit - first_key && key < kKvBlock) o[d][i] = quiet_nan();
+                    }
+                }
+            }
+        }
+        const float vs = power_value(vp);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int d = 0; d < kDT; ++d) {
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_bf16(vf[d][u].x, vf[d][u].y, vs), p[2 * u], o[d],
+                                                              0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_bf16(vf[d][u].z, vf[d][u].w, vs), p[2 * u + 1],
+                                                              o[d], 0, 0, 0);
+            }
+    }
+
+    // join the waves: each row's largest maximum is the common reference
+    st.l += __shfl_xor(st.l, 32);
+    if (q.nan && row.limit > 0) st.l = quiet_nan();
+    if (h == 0) {
+        sm[wave][c] = st.m;
+        sl[wave][c] = st.l;
+    }
+#pragma unroll
+    for (int d = 0; d < kDT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(&so[wave][c][32 * d + 8 * i + 4 * h]) =
+                make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]);
+    __syncthreads();
+    constexpr int kEach = D / 8;  // dims of a thread: 8 threads a row
+    const int rr = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * kEach;
+    const Row mine = find_row(a, t, t.first + rr, kv_head);
+    if (!mine.valid) return;
+    float m = sm[0][rr];
+#pragma unroll
+    for (int w = 1; w < kNarrowWaves; ++w) m = fmaxf(m, sm[w][rr]);
+    const float ref = m == neg_inf() ? 0.0f : m;
+    float l = 0.0f, acc[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kNarrowWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(sm[w][rr] - ref);  // 0 for a wave that saw nothing
+        const float lw = sl[w][rr];
+        l += lw != lw ? lw : f * lw;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) acc[i] += f * so[w][rr][d0 + i];
+    }
+    const int64_t at = mine.token * a.q_heads + mine.head;
+    if (a.parts == 1) {
+        // no key: 0; a length that the table cannot hold: NaN
+        const float inv = t.bad ? quiet_nan() : l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* p = a.out.data + mine.token * a.out.row + mine.head * a.out.head + d0;
+#pragma unroll
+        for (int i = 0; i < kEach; i += 8)
+            *reinterpret_cast<uint4*>(p + i) =
+                make_uint4(pack_bf16x2(acc[i] * inv, acc[i + 1] * inv), pack_bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
+                           pack_bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), pack_bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));
+    } else {
+        const int64_t all_rows = a.seqs.M * a.q_heads;
+        float* po = a.partial + ((int64_t)part * all_rows + at) * D + d0;
+        float* pm = a.partial + (int64_t)a.parts * all_rows * D + ((int64_t)part * all_rows + at) * 2;
+#pragma unroll
+        for (int i = 0; i < kEach; i += 4)
+            *reinterpret_cast<float4*>(po + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        if ((threadIdx.x & 7) == 0) {
+            pm[0] = m;
+            pm[1] = t.bad ? quiet_nan() : l;
+        }
+    }
+}
+
+// Joins the parts of each row; rows that no sequence has are left alone.  A
+// wave takes a row, a lane D / 64 dims of it.
+template <int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
+    const int64_t all_rows = a.seqs.M * a.q_heads;
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (at >= all_rows) return;
+    const int lane = threadIdx.x & 63;
+    const int64_t token = at / a.q_heads;
+    const int32_t head = (int32_t)(at - token * a.q_heads);
+    if (token < a.seqs.row_start[0] || token >= a.seqs.row_start[a.seqs.B]) return;
+    const float* pm = a.partial + (int64_t)a.parts * all_rows * D;
+    float m = neg_inf();
+    for (int s = 0; s < a.parts; ++s) m = fmaxf(m, pm[(s * all_rows + at) * 2]);
+    const float ref = m == neg_inf() ? 0.0f : m;
+    constexpr int kEach = D / 64;
+    float l = 0.0f, acc[kEach] = {};
+    for (int s = 0; s < a.parts; ++s) {
+        const float ls = pm[(s * all_rows + at) * 2 + 1];
+        const float f = __builtin_amdgcn_exp2f(pm[(s * all_rows + at) * 2] - ref);
+        l += ls != ls ? ls : f * ls;
+        const float* po = a.partial + (s * all_rows + at) * D + lane * kEach;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) acc[i] += f * po[i];
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* p = a.out.data + token * a.out.row + head * a.out.head + lane * kEach;
+    if constexpr (kEach == 2)
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    else
+        *p = (uint16_t)pack_bf16x2(acc[0] * inv, 0.0f);
+}
+
+}  // namespace
+
+AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len) {
+    const int32_t group = q_heads / kv_heads;
+    AttentionPlan p;
+    // pieces until two workgroups for each of 256 CUs are in flight, at least 4
+    // blocks (one a wave) to a piece
+    int64_t tiles = (M * group + kRows - 1) / kRows;
+    tiles = tiles < B ? B : tiles;
+    const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock;
+    const int64_t want = 512 / (tiles * kv_heads), most = blocks / 4;
+    p.parts = (int32_t)clamp64(want < most ? want : most, 1, 64);
+    p.workspace_bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)(M * q_heads) * (size_t)(dim + 2) * sizeof(float);
+    return p;
+}
+
+template <int D>
+static void attention_of(const AttentionArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)tile_units(a.seqs.M, a.seqs.B, a.group, kRows), (unsigned)a.cache.heads, (unsigned)a.parts);
+    attention_narrow_kernel<D><<<grid, dim3(64 * kNarrowWaves), 0, s>>>(a);
+    if (a.parts > 1) {
+        const int64_t rows = a.seqs.M * a.q_heads;
+        attention_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s>>>(a);
+    }
+}
+
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {
+    (void)hipGetLastError();
+    if (a.cache.dim == 128)
+        attention_of<128>(a, s);
+    else
+        attention_of<64>(a, s);
+    return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,575 @@
+// Rotary positions with several axes, and the paged 8-bit key/value cache:
+// quantised as it is written, and read back.  All three stream their rows once
+// and are bound by memory bandwidth.
+#include "kv_device.h"
+
+namespace nvfp4 {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Rotation of a pair by (cos, sin): y1 = x1 c - x2 s, y2 = x2 c + x1 s, each
+// product and sum a binary32 operation, the result rounded once to bf16.
+// ---------------------------------------------------------------------------
+// (cos, sin) of pair i of the row whose positions `pos` points to.  A position
+// outside its table gives NaN, and the table is not read.
+__device__ __forceinline__ float2 rope_turn(const RopeArgs& r, const int32_t* pos, int i) {
+    const float nan = __uint_as_float(0x7FC00000u);
+    float2 t = make_float2(nan, nan);
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        if (i >= r.first[a] && i < r.first[a + 1]) {
+            const int32_t p = pos[a];
+            if (p >= 0 && p < r.rows[a])
+                t = r.table[a][(int64_t)p * (r.first[a + 1] - r.first[a]) + (i - r.first[a])];
+        }
+    }
+    return t;
+}
+
+__global__ void rope_table_kernel(float2* table, int64_t n, int32_t pairs, double theta) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n) return;
+    // in binary64: at position 10^6 the angle's error is 1e-10, far below half a
+    // step of the binary32 results
+    const double angle = (double)(i / pairs) * pow(theta, -(double)(i % pairs) / (double)pairs);
+    table[i] = make_float2((float)cos(angle), (float)sin(angle));
+}
+
+// A thread owns 16 dims of a head, either 8 rotated pairs or 16 dims that pass
+// through, looks up its 8 (cos, sin) once and goes over the row's heads with
+// them: the table is read once per row and not once per head.
+struct RopeGeo {
+    int64_t M;
+    int32_t heads, units;  // 16-dim units per head
+    int32_t slots, rows;   // heads and rows that a workgroup takes at once
+};
+
+template <bool SPLIT>
+__global__ __launch_bounds__(256) void rope_kernel(HeadsIn x, HeadsOut out, RopeArgs r, RopeGeo g) {
+    const int u = threadIdx.x % g.units;
+    const int rest = threadIdx.x / g.units;
+    const int slot = rest % g.slots, in = rest / g.slots;
+    const int64_t row = (int64_t)blockIdx.x * g.rows + in;
+    if (in >= g.rows || row >= g.M) return;
+    const bool turns = u < r.total / 8;
+    const int d0 = SPLIT && turns ? 8 * u : 16 * u;
+    const int d1 = SPLIT && turns ? r.total + 8 * u : 16 * u + 8;
+    const uint16_t* src = x.data + row * x.row;
+    uint16_t* dst = out.data + row * out.row;
+    float2 t[8];
+    if (turns) {
+        const int32_t* pos = r.positions + row * r.ld_positions;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = rope_turn(r, pos, 8 * u + j);
+    }
+    for (int h = slot; h < g.heads; h += g.slots) {
+        uint4 a = *reinterpret_cast<const uint4*>(src + h * x.head + d0);
+        uint4 b = *reinterpret_cast<const uint4*>(src + h * x.head + d1);
+        if (turns) {
+            uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            if constexpr (SPLIT) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 c0 = t[2 * j], c1 = t[2 * j + 1];
+                    const float p0 = bf16_lo(w[j]), p1 = bf16_hi(w[j]), q0 = bf16_lo(w[4 + j]), q1 = bf16_hi(w[4 + j]);
+                    w[j] = pack_bf16x2(p0 * c0.x - q0 * c0.y, p1 * c1.x - q1 * c1.y);
+                    w[4 + j] = pack_bf16x2(q0 * c0.x + p0 * c0.y, q1 * c1.x + p1 * c1.y);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float p = bf16_lo(w[j]), q = bf16_hi(w[j]);
+                    w[j] = pack_bf16x2(p * t[j].x - q * t[j].y, q * t[j].x + p * t[j].y);
+                }
+            }
+            a = make_uint4(w[0], w[1], w[2], w[3]);
+            b = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        *reinterpret_cast<uint4*>(dst + h * out.head + d0) = a;
+        *reinterpret_cast<uint4*>(dst + h * out.head + d1) = b;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The cache's writer and reader.  A workgroup takes one block of 64 positions
+// of one sequence and several heads.  A thread owns 4 neighbouring positions
+// (one dword of a value piece) of 8 dims; a wave owns one or two whole value
+// pieces, so that values change places within the wave only.
+//   D = 128: 256 threads, wave = (u, h), lane = (e, m) x 16 dim groups
+//   D =  64: 128 threads, wave = u, lane = (h, e, m) x 8 dim groups
+// ---------------------------------------------------------------------------
+template <int D>
+struct Owner {
+    static constexpr int kGroups = D / 8;     // dim groups
+    static constexpr int kThreads = 2 * D;
+    static constexpr int kWaves = kThreads / 64;
+    int g, t0;      // dims 8g.., positions t0..t0+3
+    int piece, em;  // value piece 2u + h and dword 2e + m
+    __device__ __forceinline__ Owner() {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        g = lane % kGroups;
+        const int sub = lane / kGroups;
+        const int u = D == 128 ? wave >> 1 : wave;
+        const int h = D == 128 ? wave & 1 : sub >> 2;
+        em = sub & 3;
+        piece = 2 * u + h;
+        t0 = 32 * u + 16 * (em >> 1) + 8 * (em & 1) + 4 * h;
+    }
+};
+
+// Where a work unit stands.
+struct BlockUnit {
+    bool any;       // whether there is anything to do
+    bool good;      // whether its cache block exists
+    bool bad_len;   // a length that the table cannot hold
+    int64_t row0;   // row of the sequence's first new position
+    int64_t first;  // first new position
+    int64_t len;
+    int64_t start;  // position of the block's first slot (negative: before the sequence)
+    int64_t page;
+};
+
+__device__ __forceinline__ BlockUnit block_unit(const SeqArgs& q, int64_t blocks, int64_t unit) {
+    BlockUnit u;
+    u.any = false;
+    const auto base = [&](int64_t b) { return block_base(clamp64(q.row_start[b], 0, q.M), b); };
+    const int64_t b = uniform64(find_sequence(unit, q.B, base));
+    const RowRange r = row_range(q.row_start[b], q.row_start[b + 1], q.M);
+    const int64_t n = r.last - r.first, local = unit - block_base(r.first, b);
+    if (n <= 0 || local < 0) return u;
+    u.len = q.lens[b];
+    u.first = u.len - n;
+    u.row0 = r.first;
+    const int64_t at = floor_div(u.first, kKvBlock) + local;
+    if (at * kKvBlock >= u.len) return u;
+    u.any = true;
+    u.start = at * kKvBlock;
+    u.bad_len = kv_length_bad(u.len, q.table_blocks);
+    u.good = at >= 0 && at < q.table_blocks && !u.bad_len;
+    u.page = u.good ? q.table[b * q.ld_table + at] : 0;
+    if (u.page < 0 || u.page >= blocks) u.good = false;
+    return u;
+}
+
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t m2) {
+    return ((m2 & 0x7F80u) == 0x7F80u ? 0u : m2 & 0xFFFFu) | ((m2 & 0x7F800000u) == 0x7F800000u ? 0u : m2 & 0xFFFF0000u);
+}
+
+// The largest of both halves over the workgroup, each half for itself.
+template <int WAVES>
+__device__ __forceinline__ uint32_t group_max(uint32_t m, uint32_t* slot) {
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, s));
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = slot[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) m = pk_max_u16(m, slot[w]);
+    return m;
+}
+
+// Code of one value: the nearest E4M3 of x / p, or the NaN code for what is not
+// finite.  With the largest power, 2^120, codes stop at 240: 256 * 2^120 = 2^128,
+// the nearest to values above 1.9375 * 2^127, would not be finite any more.
+__device__ __forceinline__ uint32_t encode_any(float x, uint32_t power) {
+    const float most = power >= 247u ? 240.0f : 448.0f;
+    const float y = fminf(fmaxf(x * power_inverse(power), -most), most);
+    const uint32_t bits = __float_as_uint(x) & 0x7F800000u;
+    return bits == 0x7F800000u ? 0x7Fu : (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, 0.0f, 0, false) & 0xFFu;
+}
+
+// Four stored codes moved to a larger power of two.
+__device__ __forceinline__ uint32_t shrink4(uint32_t w, float factor) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t c = (w >> (8 * i)) & 0xFFu;
+        const uint32_t n = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(e4m3_value(c) * factor, 0.0f, 0, false) & 0xFFu;
+        r |= ((c & 0x7Fu) == 0x7Fu ? c : n) << (8 * i);
+    }
+    return r;
+}
+
+enum { ROPE_NONE = 0, ROPE_PAIRS = 1, ROPE_SPLIT = 2 };
+
+__device__ __forceinline__ float half_of(const uint32_t* w, int i) { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
+
+template <int D, int MODE>
+__global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q, HeadsIn kx, HeadsIn vx, RopeArgs r,
+                                                         int32_t heads_each) {
+    using Own = Owner<D>;
+    constexpr int kBytes = kKvBlock * D;
+    constexpr int kPieceBytes = 16 * D;
+    __shared__ uint32_t red[2][Own::kWaves];
+    __shared__ uint32_t red2[2][Own::kWaves];
+    __shared__ __align__(16) uint32_t stage[kBytes / 4];
+    const BlockUnit u = block_unit(q, c.blocks, blockIdx.x);
+    if (!u.any || !u.good) return;
+    const Own o;
+    // positions of the block that are new: [lo, hi); those before lo are kept
+    const int lo = (int)(u.first > u.start ? u.first - u.start : 0);
+    const int hi = (int)(u.len - u.start < kKvBlock ? u.len - u.start : kKvBlock);
+    const bool full = lo == 0 && hi == kKvBlock;
+    const int64_t row = u.row0 + (u.start - u.first) + o.t0;  // of position t0, where that is new
+    bool fresh[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fresh[j] = o.t0 + j >= lo && o.t0 + j < hi;
+
+    // this thread's angles, kept over the heads
+    constexpr int kTurns = MODE == ROPE_SPLIT ? 8 : 4;
+    float cs[4][MODE == ROPE_NONE ? 1 : kTurns], sn[4][MODE == ROPE_NONE ? 1 : kTurns];
+    bool turns = false;
+    int partner = 0;
+    if constexpr (MODE != ROPE_NONE) {
+        const int lane = threadIdx.x & 63;
+        int pair0 = 4 * o.g;
+        turns = 8 * o.g < 2 * r.total;
+        partner = lane;
+        if constexpr (MODE == ROPE_SPLIT) {
+            const bool upper = 8 * o.g >= r.total;
+            pair0 = 8 * o.g - (upper ? r.total : 0);
+            if (turns) partner = lane + (upper ? -(r.total / 8) : r.total / 8);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int32_t* pos = r.positions + (row + j) * r.ld_positions;
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) {
+                float2 t = make_float2(1.0f, 0.0f);
+                if (turns && fresh[j]) t = rope_turn(r, pos, pair0 + i);
+                cs[j][i] = t.x;
+                // y1 = x1 c + x2 (-s): the sign goes with the sine
+                sn[j][i] = MODE == ROPE_SPLIT && 8 * o.g < r.total ? -t.y : t.y;
+            }
+        }
+    }
+
+    const int h0 = blockIdx.y * heads_each;
+    const int h1 = h0 + heads_each < c.heads ? h0 + heads_each : c.heads;
+    for (int h = h0; h < h1; ++h) {
+        const int parity = (h - h0) & 1;
+        const int64_t at = u.page * c.heads + h;
+        uint8_t* const kb = c.k + at * kBytes;
+        uint8_t* const vb = c.v + at * kBytes;
+        uint32_t kw[4][4], vw[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (fresh[j]) {
+                a = *reinterpret_cast<const uint4*>(kx.data + (row + j) * kx.row + h * kx.head + 8 * o.g);
+                b = *reinterpret_cast<const uint4*>(vx.data + (row + j) * vx.row + h * vx.head + 8 * o.g);
+            }
+            kw[j][0] = a.x, kw[j][1] = a.y, kw[j][2] = a.z, kw[j][3] = a.w;
+            vw[j][0] = b.x, vw[j][1] = b.y, vw[j][2] = b.z, vw[j][3] = b.w;
+        }
+        uint32_t had_k = 0, had_v = 0;
+        if (lo > 0) {
+            had_k = clamp_power(c.k_power[at]);
+            had_v = clamp_power(c.v_power[at]);
+        }
+        if constexpr (MODE == ROPE_PAIRS) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x1 = bf16_lo(kw[j][i]), x2 = bf16_hi(kw[j][i]);
+                    const uint32_t y = pack_bf16x2(x1 * cs[j][i] - x2 * sn[j][i], x2 * cs[j][i] + x1 * sn[j][i]);
+                    kw[j][i] = turns ? y : kw[j][i];
+                }
+        } else if constexpr (MODE == ROPE_SPLIT) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t p = (uint32_t)__shfl((int)kw[j][i], partner);
+                    const float y0 = bf16_lo(kw[j][i]) * cs[j][2 * i] + bf16_lo(p) * sn[j][2 * i];
+                    const float y1 = bf16_hi(kw[j][i]) * cs[j][2 * i + 1] + bf16_hi(p) * sn[j][2 * i + 1];
+                    kw[j][i] = turns ? pack_bf16x2(y0, y1) : kw[j][i];
+                }
+        }
+        uint32_t mk = 0, mv = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mk = pk_max_u16(mk, mag2(kw[j][i]));
+                mv = pk_max_u16(mv, mag2(vw[j][i]));
+            }
+        uint32_t top = group_max<Own::kWaves>((fold_max(mk) << 16) | fold_max(mv), red[parity]);
+        // a value is not finite, or so large that its block takes the largest power
+        const bool odd = (top & 0xFFFFu) > 0x7F60u || (top >> 16) > 0x7F60u;
+        if (odd) {
+            mk = mv = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mk = pk_max_u16(mk, drop_nonfinite(mag2(kw[j][i])));
+                    mv = pk_max_u16(mv, drop_nonfinite(mag2(vw[j][i])));
+                }
+            top = group_max<Own::kWaves>((fold_max(mk) << 16) | fold_max(mv), red2[parity]);
+        }
+        uint32_t pk = power_for(top >> 16), pv = power_for(top & 0xFFFFu);
+        pk = pk > had_k ? pk : had_k;
+        pv = pv > had_v ? pv : had_v;
+        const float ik = power_inverse(pk), iv = power_inverse(pv);
+
+        // codes: keys as 8 bytes of each position, values as one dword of 4
+        // positions for each dim
+        uint32_t kc[4][2], vc[8];
+        if (!odd) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    kc[j][i] = fp8_pack4(bf16_lo(kw[j][2 * i]) * ik, bf16_hi(kw[j][2 * i]) * ik,
+                                         bf16_lo(kw[j][2 * i + 1]) * ik, bf16_hi(kw[j][2 * i + 1]) * ik);
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                vc[d] = fp8_pack4(half_of(vw[0], d) * iv, half_of(vw[1], d) * iv, half_of(vw[2], d) * iv,
+                                  half_of(vw[3], d) * iv);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    kc[j][i] = 0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) kc[j][i] |= encode_any(half_of(kw[j], 4 * i + x), pk) << (8 * x);
+                }
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                vc[d] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) vc[d] |= encode_any(half_of(vw[j], d), pv) << (8 * j);
+            }
+        }
+
+        if (full) {
+            // keys: neighbouring dim groups swap halves, so that each stores
+            // whole 16-byte pieces of two positions
+            const bool upper = o.g & 1;
+            uint32_t got[2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    got[j][i] = (uint32_t)__shfl_xor((int)(upper ? kc[j][i] : kc[2 + j][i]), 1);
+            uint4* kp = reinterpret_cast<uint4*>(kb + (o.g >> 1) * (kKvBlock * 16) + (o.t0 + (upper ? 2 : 0)) * 16);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                kp[j] = upper ? make_uint4(got[j][0], got[j][1], kc[2 + j][0], kc[2 + j][1])
+                              : make_uint4(kc[j][0], kc[j][1], got[j][0], got[j][1]);
+            // values: through LDS, 16-byte slot s = (piece, dim) at
+            // s ^ ((s >> 3) & 7), so that the 64 lanes' dwords fall on all banks
+            const int s0 = o.piece * D + 8 * o.g;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) stage[4 * ((s0 + d) ^ (((s0 + d) >> 3) & 7)) + o.em] = vc[d];
+            wave_lds_sync();
+            const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int s = wave * 128 + i * 64 + lane;
+                reinterpret_cast<uint4*>(vb)[s] = reinterpret_cast<const uint4*>(stage)[s ^ ((s >> 3) & 7)];
+            }
+            wave_lds_sync();
+        } else {
+            // part of a block: every dword has one owner, which keeps the bytes
+            // that are not new (re-encoded where the power of two grew)
+            const float fk = had_k && pk > had_k ? power_value(127u - (pk - had_k < 126u ? pk - had_k : 126u)) : 1.0f;
+            const float fv = had_v && pv > had_v ? power_value(127u - (pv - had_v < 126u ? pv - had_v : 126u)) : 1.0f;
+            const bool grew_k = had_k && pk > had_k, grew_v = had_v && pv > had_v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint2* p = reinterpret_cast<uint2*>(kb + kv_key_offset(o.t0 + j, 8 * o.g));
+                if (fresh[j]) {
+                    *p = make_uint2(kc[j][0], kc[j][1]);
+                } else if (grew_k && o.t0 + j < lo) {
+                    const uint2 w = *p;
+                    *p = make_uint2(shrink4(w.x, fk), shrink4(w.y, fk));
+                }
+            }
+            uint32_t keep = 0, old = 0;  // bytes that stay, and those of them that are positions before lo
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (!fresh[j]) keep |= 0xFFu << (8 * j);
+                if (o.t0 + j < lo) old |= 0xFFu << (8 * j);
+            }
+            if (keep != 0xFFFFFFFFu || (grew_v && old)) {
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    uint32_t* p = reinterpret_cast<uint32_t*>(vb + o.piece * kPieceBytes + (8 * o.g + d) * 16 + 4 * o.em);
+                    uint32_t w = keep ? *p : 0u;
+                    if (grew_v) w = (shrink4(w, fv) & old) | (w & ~old);
+                    *p = (w & keep) | (vc[d] & ~keep);
+                }
+            }
+        }
+        if (threadIdx.x == 0) {
+            c.k_power[at] = (uint8_t)pk;
+            c.v_power[at] = (uint8_t)pv;
+        }
+    }
+}
+
+// The inverse of the writer: the same ownership, the same rows.
+template <int D>
+__global__ __launch_bounds__(2 * D) void kv_read_kernel(CacheArgs c, SeqArgs q, HeadsOut kx, HeadsOut vx,
+                                                        int32_t heads_each) {
+    using Own = Owner<D>;
+    constexpr int kBytes = kKvBlock * D;
+    __shared__ __align__(16) uint32_t stage[kBytes / 4];
+    const BlockUnit u = block_unit(q, c.blocks, blockIdx.x);
+    if (!u.any) return;
+    const Own o;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lo = (int)(u.first > u.start ? u.first - u.start : 0);
+    const int hi = (int)(u.len - u.start < kKvBlock ? u.len - u.start : kKvBlock);
+    const int64_t row = u.row0 + (u.start - u.first);  // of the block's first position
+    const bool wrong = !u.good && (u.bad_len || u.start >= 0);
+    const uint32_t fill = wrong ? 0x7FC07FC0u : 0u;  // no such block or length: NaN; before the sequence: 0
+    const int h0 = blockIdx.y * heads_each;
+    const int h1 = h0 + heads_each < c.heads ? h0 + heads_each : c.heads;
+    for (int h = h0; h < h1; ++h) {
+        if (!u.good) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = o.t0 + j;
+                if (t < lo || t >= hi) continue;
+                const uint4 f = make_uint4(fill, fill, fill, fill);
+                *reinterpret_cast<uint4*>(kx.data + (row + t) * kx.row + h * kx.head + 8 * o.g) = f;
+                *reinterpret_cast<uint4*>(vx.data + (row + t) * vx.row + h * vx.head + 8 * o.g) = f;
+            }
+            continue;
+        }
+        const int64_t at = u.page * c.heads + h;
+        const uint8_t* const kb = c.k + at * kBytes;
+        const uint8_t* const vb = c.v + at * kBytes;
+        const float sk = power_value(clamp_power(c.k_power[at])), sv = power_value(clamp_power(c.v_power[at]));
+        // keys: a lane takes whole 16-byte pieces, D / 16 lanes a position
+        uint4 kw[2], vw[2];
+        constexpr int kPieces = D / 16;
+        const int piece = threadIdx.x % kPieces, t1 = threadIdx.x / kPieces;  // positions t1 and t1 + 32
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            kw[i] = *reinterpret_cast<const uint4*>(kb + piece * (kKvBlock * 16) + (t1 + 32 * i) * 16);
+            vw[i] = reinterpret_cast<const uint4*>(vb)[wave * 128 + i * 64 + lane];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int s = wave * 128 + i * 64 + lane;
+            reinterpret_cast<uint4*>(stage)[s ^ ((s >> 3) & 7)] = vw[i];
+            const int t = t1 + 32 * i;
+            if (t >= lo && t < hi) {
+                uint4* p = reinterpret_cast<uint4*>(kx.data + (row + t) * kx.row + h * kx.head + 16 * piece);
+                p[0] = make_uint4(fp8_to_bf16x2<false>(kw[i].x, sk), fp8_to_bf16x2<true>(kw[i].x, sk),
+                                  fp8_to_bf16x2<false>(kw[i].y, sk), fp8_to_bf16x2<true>(kw[i].y, sk));
+                p[1] = make_uint4(fp8_to_bf16x2<false>(kw[i].z, sk), fp8_to_bf16x2<true>(kw[i].z, sk),
+                                  fp8_to_bf16x2<false>(kw[i].w, sk), fp8_to_bf16x2<true>(kw[i].w, sk));
+            }
+        }
+        wave_lds_sync();
+        // values: 4 positions of 8 dims, dword d holding dim d of all four
+        const int s0 = o.piece * D + 8 * o.g;
+        uint32_t a[8], b[8];  // positions 0, 1 and 2, 3 of each dim
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+            const uint32_t w = stage[4 * ((s0 + d) ^ (((s0 + d) >> 3) & 7)) + o.em];
+            a[d] = fp8_to_bf16x2<false>(w, sv);
+            b[d] = fp8_to_bf16x2<true>(w, sv);
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = o.t0 + j;
+            if (t < lo || t >= hi) continue;
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t x = j < 2 ? a[2 * i] : b[2 * i], y = j < 2 ? a[2 * i + 1] : b[2 * i + 1];
+                w[i] = j & 1 ? (x >> 16) | (y & 0xFFFF0000u) : (x & 0xFFFFu) | (y << 16);
+            }
+            *reinterpret_cast<uint4*>(vx.data + (row + t) * vx.row + h * vx.head + 8 * o.g) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// Heads that one workgroup takes: as many as leave about 8 workgroups for each
+// of 256 CUs, so that a long write looks its angles up once for several heads
+// and a short one still fills the chip.
+int heads_each(int64_t units, int32_t heads) {
+    const int64_t n = units * heads / 2048;
+    return (int)clamp64(n, 1, 8);
+}
+
+}  // namespace
+
+hipError_t launch_rope_table(float2* table, int64_t rows, int32_t pairs, double theta, hipStream_t s) {
+    const int64_t n = rows * pairs;
+    (void)hipGetLastError();
+    rope_table_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s>>>(table, n, pairs, theta);
+    return hipGetLastError();
+}
+
+hipError_t launch_rope(const HeadsIn& x, const HeadsOut& out, int64_t M, int32_t heads, int32_t dim, const RopeArgs& r,
+                       hipStream_t s) {
+    RopeGeo g;
+    g.M = M;
+    g.heads = heads;
+    g.units = dim / 16;
+    const int slots = 256 / g.units;  // heads' worth of threads
+    if (heads <= slots) {
+        g.slots = heads;
+        g.rows = slots / heads;
+    } else {
+        const int turns = (heads + slots - 1) / slots;
+        g.slots = (heads + turns - 1) / turns;  // the same share each turn
+        g.rows = 1;
+    }
+    const dim3 grid((unsigned)((M + g.rows - 1) / g.rows)), block((unsigned)((g.units * g.slots * g.rows + 63) / 64 * 64));
+    (void)hipGetLastError();
+    if (r.split)
+        rope_kernel<true><<<grid, block, 0, s>>>(x, out, r, g);
+    else
+        rope_kernel<false><<<grid, block, 0, s>>>(x, out, r, g);
+    return hipGetLastError();
+}
+
+template <int D>
+static void kv_write_of(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, const HeadsIn& v, const RopeArgs& r,
+                        hipStream_t s) {
+    const int64_t units = block_units(q.M, q.B);
+    const int each = heads_each(units, c.heads);
+    const dim3 grid((unsigned)units, (unsigned)((c.heads + each - 1) / each)), block(2 * D);
+    if (r.axes == 0)
+        kv_write_kernel<D, ROPE_NONE><<<grid, block, 0, s>>>(c, q, k, v, r, each);
+    else if (r.split)
+        kv_write_kernel<D, ROPE_SPLIT><<<grid, block, 0, s>>>(c, q, k, v, r, each);
+    else
+        kv_write_kernel<D, ROPE_PAIRS><<<grid, block, 0, s>>>(c, q, k, v, r, each);
+}
+
+hipError_t launch_kv_write(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, const HeadsIn& v, const RopeArgs& r,
+                           hipStream_t s) {
+    (void)hipGetLastError();
+    if (c.dim == 128)
+        kv_write_of<128>(c, q, k, v, r, s);
+    else
+        kv_write_of<64>(c, q, k, v, r, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const CacheArgs& c, const SeqArgs& q, const HeadsOut& k, const HeadsOut& v, hipStream_t s) {
+    const int64_t units = block_units(q.M, q.B);
+    const int each = heads_each(units, c.heads);
+    const dim3 grid((unsigned)units, (unsigned)((c.heads + each - 1) / each));
+    (void)hipGetLastError();
+    if (c.dim == 128)
+        kv_read_kernel<128><<<grid, dim3(256), 0, s>>>(c, q, k, v, each);
+    else
+        kv_read_kernel<64><<<grid, dim3(128), 0, s>>>(c, q, k, v, each);
+    return hipGetLastError();
+}
+
+}  // namespace nvfp4

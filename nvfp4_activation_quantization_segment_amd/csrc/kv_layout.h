@@ -1,0 +1,83 @@
+// Index arithmetic of the paged 8-bit key/value cache and of the work units
+// that its kernels run on.  Plain constexpr C++ (host and device), so that the
+// bounds it promises are checked on the CPU.
+#pragma once
+
+#include <stdint.h>
+
+namespace nvfp4 {
+
+// Positions of one cache block (one head's keys or values of 64 positions).
+constexpr int kKvBlock = 64;
+
+// ---------------------------------------------------------------------------
+// Layout inside a block: the order in which the matrix instructions of the
+// attention kernels take their operands, so that every load of theirs is 16
+// contiguous bytes per lane and whole lines per wave.
+//
+// Keys [D/16][64][16]: a 32x32x64 instruction multiplies 32 keys by 64 dims;
+// lane l holds 32 dims of key l % 32, two 16-byte pieces.
+//
+// Values [4][D][16]: the scores of a 32x32 tile leave lane l with the 16 keys
+// 8 (i / 4) + 4 (l / 32) + i % 4 of query l % 32.  They are used as they lie as
+// the second operand of the 32x32x16 products with the values, k-step s taking
+// i = 8 (s % 2) .. + 7 of tile s / 2; the first operand then needs the values of
+// these keys side by side.  Position t = 32u + 16e + 8m + 4h + j has k-step
+// 2u + e, lane half h and place 4m + j, and a 16-byte piece holds the two
+// k-steps of one u: piece 2u + h, byte 8e + 4m + j.
+// ---------------------------------------------------------------------------
+constexpr int kv_key_offset(int t, int d) { return (d / 16) * (kKvBlock * 16) + t * 16 + d % 16; }
+constexpr int kv_value_offset(int t, int d, int D) {
+    return (2 * (t / 32) + t / 4 % 2) * (D * 16) + d * 16 + 8 * (t / 16 % 2) + 4 * (t / 8 % 2) + t % 4;
+}
+
+constexpr int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
+constexpr int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); }  // b > 0
+
+// ---------------------------------------------------------------------------
+// Work units.  The number of new rows of each sequence is known on the device
+// only, so a grid is sized for every way the M rows can be shared out, and a
+// sequence's first unit is found from the rows before it.
+//
+// Tiles of T rows (each of `per` rows per token): a sequence of n tokens has
+// ceil(n per / T) of them, and tile_base(b + 1) - tile_base(b) >=
+// floor(n per / T) + 1 is never less.
+// Blocks of 64 positions: n positions starting anywhere touch at most
+// (n + 62) / 64 + 1 <= floor(n / 64) + 2 of them.
+// ---------------------------------------------------------------------------
+constexpr int64_t tile_base(int64_t row, int64_t b, int64_t per, int64_t T) { return row * per / T + b; }
+constexpr int64_t tile_units(int64_t M, int64_t B, int64_t per, int64_t T) { return M * per / T + B; }
+constexpr int64_t block_base(int64_t row, int64_t b) { return row / kKvBlock + 2 * b; }
+constexpr int64_t block_units(int64_t M, int64_t B) { return M / kKvBlock + 2 * B; }
+
+// Rows [first, last) of sequence b of row_start, whatever the array holds.
+struct RowRange {
+    int64_t first, last;
+};
+constexpr RowRange row_range(int64_t start, int64_t end, int64_t M) {
+    const int64_t a = clamp64(start, 0, M);
+    return RowRange{a, clamp64(end, a, M)};
+}
+
+// A length that a table of `blocks` blocks cannot hold.
+constexpr bool kv_length_bad(int64_t len, int64_t blocks) { return len < 0 || len > blocks * kKvBlock; }
+
+// First key that the query at position pos does not see: all len keys
+// (causal = 0), or those of its own run of `causal` positions and before.
+constexpr int64_t kv_limit(int64_t pos, int64_t len, int64_t causal) {
+    if (causal == 0) return len;
+    const int64_t end = (floor_div(pos, causal) + 1) * causal;
+    return clamp64(end, 0, len);
+}
+
+// Blocks [first, last) of part s of S of a row tile that sees n blocks.
+struct BlockRange {
+    int64_t first, last;
+};
+constexpr BlockRange kv_part(int64_t n, int64_t s, int64_t S) {
+    const int64_t per = (n + S - 1) / S;
+    const int64_t a = clamp64(s * per, 0, n);
+    return BlockRange{a, clamp64(a + per, a, n)};
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,278 @@
+"""CPU tests of the rotary, cache and attention entry points: refusals (nothing is launched), the workspace rule, and
+the index arithmetic of the cache layout and the work units, compiled from the header that the kernels use."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from tests import kv_ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "nvfp4_activation_quantization_segment_amd", "csrc")
+FAKE = 1 << 20  # never dereferenced: every call below fails validation first
+OK, INVALID, SHAPE, ALIGNMENT = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import nvfp4_activation_quantization_segment_amd as m
+
+    return m
+
+
+def heads(nv, data=FAKE, row=1024, head=128):
+    return nv.Heads(data, row, head)
+
+
+def rope(nv, axes=2, pairs=(8, 8), rows=(4, 4), table=FAKE, positions=FAKE, ld=None):
+    p = nv.RopeParams()
+    p.axes = axes
+    for a in range(min(axes, 4)) if axes > 0 else ():
+        p.pairs[a], p.rows[a], p.table[a] = pairs[a % len(pairs)], rows[a % len(rows)], table
+    p.positions, p.ld_positions = positions, axes if ld is None else ld
+    return p
+
+
+def cache(nv, k=FAKE, v=FAKE, kp=FAKE, vp=FAKE, blocks=4, heads=8, dim=128):
+    return nv.KvCacheStruct(k, v, kp, vp, blocks, heads, dim)
+
+
+def seqs(nv, count=2, row_start=FAKE, lens=FAKE, table=FAKE, ld=4, blocks=4):
+    return nv.KvSequences(count, row_start, lens, table, ld, blocks)
+
+
+HEADS_ERRORS = [(dict(data=None), INVALID), (dict(row=-8), INVALID), (dict(head=-8), INVALID), (dict(data=FAKE + 8), ALIGNMENT),
+                (dict(row=1028), ALIGNMENT), (dict(head=132), ALIGNMENT), (dict(row=1 << 40), SHAPE)]
+# as outputs: heads or rows that overlap
+OVERLAPS = [dict(row=1016), dict(head=120), dict(row=0), dict(head=0), dict(row=128, head=1272)]
+ROPE_ERRORS = [(dict(axes=0), SHAPE), (dict(axes=5), SHAPE), (dict(positions=None), INVALID), (dict(ld=1), INVALID),
+               (dict(table=None), INVALID), (dict(pairs=(0, 8)), SHAPE), (dict(pairs=(4, 8)), SHAPE), (dict(pairs=(64, 8)), SHAPE),
+               (dict(rows=(0, 4)), SHAPE), (dict(rows=(1 << 31, 4)), SHAPE), (dict(table=FAKE + 4), ALIGNMENT),
+               (dict(positions=FAKE + 2), ALIGNMENT)]
+CACHE_ERRORS = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(kp=None), INVALID), (dict(vp=None), INVALID),
+                (dict(blocks=0), INVALID), (dict(heads=0), INVALID), (dict(dim=96), SHAPE), (dict(dim=256), SHAPE),
+                (dict(heads=65536), SHAPE), (dict(blocks=1 << 31), SHAPE), (dict(k=FAKE + 8), ALIGNMENT), (dict(v=FAKE + 4), ALIGNMENT)]
+SEQ_ERRORS = [(dict(count=0), INVALID), (dict(row_start=None), INVALID), (dict(lens=None), INVALID), (dict(table=None), INVALID),
+              (dict(blocks=0), INVALID), (dict(ld=3), INVALID), (dict(count=(1 << 20) + 1), SHAPE),
+              (dict(ld=1 << 26, blocks=1 << 26), SHAPE), (dict(lens=FAKE + 2), ALIGNMENT), (dict(row_start=FAKE + 1), ALIGNMENT),
+              (dict(table=FAKE + 2), ALIGNMENT)]
+ROWS_ERRORS = [(0, INVALID), (-1, INVALID), ((1 << 23) + 1, SHAPE)]
+
+
+def test_rope_refusals(nv):
+    L = nv.lib
+    call = lambda x=None, M=10, h=8, d=128, r=None, o=None: L.nvfp4_rope(  # noqa: E731
+        x or heads(nv), M, h, d, r or rope(nv), o or heads(nv), None)
+    for bad, want in HEADS_ERRORS:
+        assert call(x=heads(nv, **bad)) == want, bad
+        assert call(o=heads(nv, **bad)) == want, bad
+    for bad in OVERLAPS:
+        assert call(o=heads(nv, **bad)) == INVALID, bad
+    for bad, want in ROPE_ERRORS:
+        assert call(r=rope(nv, **bad)) == want, bad
+    for M, want in ROWS_ERRORS:
+        assert call(M=M) == want
+    assert call(h=0) == INVALID and call(h=65536) == SHAPE
+    assert call(d=0) == INVALID and call(d=120) == SHAPE and call(d=528) == SHAPE
+    assert L.nvfp4_rope(heads(nv), 10, 8, 128, None, heads(nv), None) == INVALID
+
+
+def test_rope_table_refusals(nv):
+    f = nv.lib.nvfp4_rope_table
+    assert f(None, 4, 4, 1e4, None) == INVALID
+    assert f(FAKE, 0, 4, 1e4, None) == INVALID
+    assert f(FAKE, 4, 0, 1e4, None) == INVALID
+    for theta in (0.0, -1.0, float("inf"), float("nan")):
+        assert f(FAKE, 4, 4, theta, None) == INVALID
+    assert f(FAKE, 1 << 30, 4, 1e4, None) == SHAPE
+    assert f(FAKE + 4, 4, 4, 1e4, None) == ALIGNMENT
+
+
+def test_cache_refusals(nv):
+    for f in (lambda c, s, M, k, v: nv.lib.nvfp4_kv_write(c, s, M, k, v, None, None),
+              lambda c, s, M, k, v: nv.lib.nvfp4_kv_read(c, s, M, k, v, None)):
+        good = dict(c=cache(nv), s=seqs(nv), M=10, k=heads(nv), v=heads(nv))
+        for bad, want in CACHE_ERRORS:
+            assert f(**dict(good, c=cache(nv, **bad))) == want, bad
+        for bad, want in SEQ_ERRORS:
+            assert f(**dict(good, s=seqs(nv, **bad))) == want, bad
+        for M, want in ROWS_ERRORS:
+            assert f(**dict(good, M=M)) == want, M
+        for bad, want in HEADS_ERRORS:
+            assert f(**dict(good, k=heads(nv, **bad))) == want, bad
+            assert f(**dict(good, v=heads(nv, **bad))) == want, bad
+        assert f(**dict(good, c=None)) == INVALID and f(**dict(good, s=None)) == INVALID
+        assert f(**dict(good, k=None)) == INVALID and f(**dict(good, v=None)) == INVALID
+    for bad in OVERLAPS:
+        assert nv.lib.nvfp4_kv_read(cache(nv), seqs(nv), 10, heads(nv, **bad), heads(nv), None) == INVALID, bad
+        assert nv.lib.nvfp4_kv_read(cache(nv), seqs(nv), 10, heads(nv), heads(nv, **bad), None) == INVALID, bad
+    for bad, want in ROPE_ERRORS:
+        assert nv.lib.nvfp4_kv_write(cache(nv), seqs(nv), 10, heads(nv), heads(nv), rope(nv, **bad), None) == want, bad
+
+
+def test_attention_refusals(nv):
+    def call(q=None, M=10, q_heads=8, c=None, s=None, scale=0.1, causal=1, max_len=64, out=None, ws=FAKE, size=1 << 40):
+        return nv.lib.nvfp4_kv_attention(q or heads(nv), M, q_heads, c or cache(nv), s or seqs(nv), scale, causal, max_len,
+                                         out or heads(nv), ws, size, None)
+
+    for bad, want in CACHE_ERRORS:
+        assert call(c=cache(nv, **bad)) == want, bad
+    for bad, want in SEQ_ERRORS:
+        assert call(s=seqs(nv, **bad)) == want, bad
+    for M, want in ROWS_ERRORS:
+        assert call(M=M) == want, M
+    for bad, want in HEADS_ERRORS:
+        assert call(q=heads(nv, **bad)) == want, bad
+        assert call(out=heads(nv, **bad)) == want, bad
+    for bad in OVERLAPS:
+        assert call(out=heads(nv, **bad)) == INVALID, bad
+    for scale in (0.0, -1.0, float("inf"), float("nan")):
+        assert call(scale=scale) == INVALID
+    assert call(causal=-1) == INVALID and call(max_len=-1) == INVALID
+    assert call(q_heads=0) == INVALID
+    assert call(q_heads=12) == SHAPE                                  # not a multiple of the cache's 8
+    assert call(M=1 << 23, q_heads=256) == SHAPE                      # M * q_heads = 2^31
+    assert call(M=1 << 23, q_heads=255, c=cache(nv, heads=5)) == SHAPE   # M * 51 > 2^28
+    need = nv.lib.nvfp4_kv_attention_workspace_bytes(1, 1, 8, 8, 128, 100000)
+    one = dict(M=1, s=seqs(nv, count=1), max_len=100000)
+    assert need > 0
+    assert call(**one, ws=None) == INVALID
+    assert call(**one, size=need - 1) == INVALID
+    assert call(**one, ws=FAKE + 8, size=need) == ALIGNMENT
+
+
+def test_attention_workspace(nv):
+    f = nv.lib.nvfp4_kv_attention_workspace_bytes
+    assert f(37810, 1, 56, 56, 128, 37810) == 0        # enough rows: the keys are not shared out
+    assert f(1, 1, 8, 8, 128, 64) == 0                 # one block: nothing to share out
+    for bad in ((0, 1, 8, 8, 128, 64), (1, 0, 8, 8, 128, 64), (1, 1, 9, 8, 128, 64), (1, 1, 8, 8, 96, 64),
+                (1, 1, 8, 8, 128, -1), (1, 1, 8, 0, 128, 64), (1 << 24, 1, 8, 8, 128, 64)):
+        assert f(*bad) == 0
+    per = 8 * (128 + 2) * 4                            # one part of 8 query heads
+    assert f(1, 1, 8, 8, 128, 100000) % per == 0 and f(1, 1, 8, 8, 128, 100000) >= 2 * per
+
+
+def test_python_checks(nv):
+    import torch
+
+    x = torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        nv.rope(x, [torch.zeros(4, 8, 2)], torch.zeros(2, 1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="GPU"):
+        nv.KvCache.empty(1, 1, 64, device="cpu")
+    with pytest.raises(ValueError, match="contiguous"):
+        nv.KvCache(torch.zeros(1, 1, 4, 64, 16, dtype=torch.uint8), torch.zeros(1, 1, 4, 32, 16, dtype=torch.uint8),
+                   torch.zeros(1, 1, dtype=torch.uint8), torch.zeros(1, 1, dtype=torch.uint8))
+
+
+LAYOUT = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+#include "kv_layout.h"
+using namespace nvfp4;
+static void need(bool ok, const char* what) { if (!ok) { printf("wrong: %s\n", what); exit(1); } }
+int main() {
+    for (int D : {64, 128}) {
+        std::vector<int> k(64 * D), v(64 * D);
+        for (int t = 0; t < 64; ++t)
+            for (int d = 0; d < D; ++d) {
+                const int a = kv_key_offset(t, d), b = kv_value_offset(t, d, D);
+                need(a >= 0 && a < 64 * D && b >= 0 && b < 64 * D, "offset");
+                ++k[a], ++v[b];
+                printf("%d %d %d %d %d\n", D, t, d, a, b);
+            }
+        for (int i = 0; i < 64 * D; ++i) need(k[i] == 1 && v[i] == 1, "every byte once");
+    }
+    // every sequence's units fit between its base and the next one's, for all ways to share rows out
+    srand(1);
+    for (int round = 0; round < 20000; ++round) {
+        const int B = 1 + rand() % 6;
+        const int64_t per = 1 + rand() % 9, T = (round & 1) ? 32 : 128;
+        std::vector<int64_t> start(1, rand() % 3 ? 0 : rand() % 200);
+        for (int b = 0; b < B; ++b) start.push_back(start.back() + (rand() % 3 ? rand() % 200 : 0));
+        const int64_t M = start.back() + rand() % 3;
+        for (int b = 0; b < B; ++b) {
+            const RowRange r = row_range(start[b], start[b + 1], M);
+            const int64_t n = r.last - r.first;
+            const int64_t end = b + 1 < B ? tile_base(start[b + 1], b + 1, per, T) : tile_units(M, B, per, T);
+            need((n * per + T - 1) / T <= end - tile_base(r.first, b, per, T), "tiles");
+            const int64_t bend = b + 1 < B ? block_base(start[b + 1], b + 1) : block_units(M, B);
+            const int64_t first = rand() % 300 - 100, len = first + n;
+            const int64_t touched = n ? floor_div(len - 1, 64) - floor_div(first, 64) + 1 : 0;
+            need(touched <= bend - block_base(r.first, b), "blocks");
+        }
+    }
+    // any row starts stay inside the rows
+    const int64_t odd[] = {INT32_MIN, -5, 0, 3, 7, 100, INT32_MAX};
+    for (int64_t a : odd)
+        for (int64_t b : odd) {
+            const RowRange r = row_range(a, b, 7);
+            need(0 <= r.first && r.first <= r.last && r.last <= 7, "range");
+        }
+    need(kv_length_bad(-1, 4) && kv_length_bad(257, 4) && !kv_length_bad(256, 4) && !kv_length_bad(0, 4), "length");
+    for (int64_t c : {0, 1, 7, 64, 1000, INT32_MAX})
+        for (int64_t len = 0; len < 200; ++len)
+            for (int64_t pos = -70; pos < len; ++pos) {
+                int64_t want = 0;
+                for (int64_t j = 0; j < len; ++j)
+                    want += c == 0 || (pos >= 0 && j / c <= pos / c);
+                need(kv_limit(pos, len, c) == want, "limit");
+            }
+    // parts cover every block once, in order
+    for (int64_t n = 0; n < 70; ++n)
+        for (int64_t S = 1; S < 20; ++S) {
+            int64_t at = 0;
+            for (int64_t s = 0; s < S; ++s) {
+                const BlockRange r = kv_part(n, s, S);
+                need(r.first == at || (r.first == n && r.last == n), "part");
+                need(r.first <= r.last && r.last <= n, "part end");
+                at = r.last;
+            }
+            need(at == n, "all parts");
+        }
+    return 0;
+}
+"""
+
+
+def test_layout_and_units(tmp_path):
+    src, exe = tmp_path / "layout.cpp", tmp_path / "layout"
+    src.write_text(LAYOUT)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", CSRC, str(src), "-o",
+                    str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert got.returncode == 0, got.stdout[-200:] + got.stderr[-500:]
+    off = {D: kv_ref.offsets(D) for D in (64, 128)}
+    for line in got.stdout.split("\n")[:-1]:
+        D, t, d, a, b = map(int, line.split())
+        assert off[D][0][t, d] == a and off[D][1][t, d] == b
+
+
+def test_reference_encoder():
+    """The oracle's own encoder against torch's conversion, over every bf16 magnitude up to 448 and both signs."""
+    import numpy as np
+    import torch
+
+    x = torch.arange(0, 0x43E1, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    for v in (x, -x):
+        want = v.float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+        assert np.array_equal(kv_ref.nearest_code(v.double().numpy()), want)
+
+
+def test_structs_match_the_header(nv, tmp_path):
+    """The binding's structures have the header's sizes and offsets."""
+    names = {"nvfp4_heads": nv.Heads, "nvfp4_rope_params": nv.RopeParams, "nvfp4_kv_cache": nv.KvCacheStruct,
+             "nvfp4_kv_sequences": nv.KvSequences}
+    body = "".join(f'printf("{n} %zu", sizeof({n}));' +
+                   "".join(f'printf(" %zu", offsetof({n}, {f[0]}));' for f in t._fields_) + 'printf("\\n");'
+                   for n, t in names.items())
+    src, exe = tmp_path / "structs.c", tmp_path / "structs"
+    src.write_text(f'#include <stdio.h>\n#include "{ROOT}/include/nvfp4.h"\nint main(void) {{ {body} return 0; }}\n')
+    subprocess.run(["gcc", "-std=c11", str(src), "-o", str(exe)], check=True)
+    for line in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.strip().split("\n"):
+        name, size, *at = line.split()
+        t = names[name]
+        assert ctypes.sizeof(t) == int(size)
+        assert [getattr(t, f[0]).offset for f in t._fields_] == [int(a) for a in at]

@@ -1,0 +1,697 @@
+"""Rotary positions, the 8-bit key/value cache and attention over it, against plain references (tests/kv_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+from tests import kv_ref
+from tests.gpu_util import device
+
+pytestmark = pytest.mark.gpu
+BLOCK = 64
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import nvfp4_activation_quantization_segment_amd as m
+
+    device()
+    return m
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape, sigma=1.0):
+    return (torch.randn(*shape, generator=g) * sigma).to(torch.bfloat16)
+
+
+def bits(t):
+    return t.contiguous().cpu().view(torch.int16).numpy()
+
+
+def same(a, b):
+    """Whether two bf16 tensors hold the same bits."""
+    return bool((bits(a) == bits(b)).all())
+
+
+def i32(a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+def strided(x, layout):
+    """x [rows, heads, dim] on the GPU in another layout, same values."""
+    rows, heads, dim = x.shape
+    if layout == "qkv":  # the middle of a wider product
+        wide = torch.full((rows, 3 * heads, dim), 7.0, dtype=x.dtype, device="cuda")
+        wide[:, heads:2 * heads] = x.cuda()
+        return wide[:, heads:2 * heads]
+    if layout == "heads":  # [heads, rows, dim]
+        return x.cuda().transpose(0, 1).contiguous().transpose(0, 1)
+    return x.cuda()
+
+
+def tables_for(pairs, size, theta=100.0):
+    got = []
+    for n, p in zip(size, pairs):
+        angle = torch.arange(n, dtype=torch.float64)[:, None] * theta ** (-torch.arange(p, dtype=torch.float64) / p)
+        got.append(torch.stack([angle.cos(), angle.sin()], -1).float())
+    return got
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,heads,dim,pairs,split,layout", [
+    (1, 1, 64, [32], False, "plain"),
+    (1, 1, 16, [8], True, "plain"),
+    (5, 3, 64, [8, 8, 16], False, "qkv"),
+    (5, 3, 64, [22, 5, 5], True, "heads"),
+    (129, 56, 128, [16, 24, 24], False, "qkv"),
+    (67, 56, 128, [22, 21, 21], True, "qkv"),
+    (33, 7, 128, [32], True, "plain"),
+    (33, 33, 128, [1, 1, 1, 13], False, "heads"),
+    (19, 5, 80, [40], False, "plain"),
+    (3, 300, 64, [16], True, "plain"),
+    (2, 2, 512, [100, 100], False, "plain"),
+    (300, 1, 96, [24, 16], True, "qkv"),
+])
+def test_rope_is_the_formula_bit_for_bit(nv, rows, heads, dim, pairs, split, layout):
+    g = gen(rows * dim + heads)
+    x = normal(g, rows, heads, dim)
+    size = [11 + 3 * a for a in range(len(pairs))]
+    tables = tables_for(pairs, size)
+    positions = torch.stack([torch.randint(0, n, (rows,), generator=g) for n in size], 1).int()
+    want = kv_ref.rotate(x, tables, positions, split)
+    xs = strided(x, layout)
+    got = nv.rope(xs, [t.cuda() for t in tables], positions.cuda(), split=split)
+    assert same(got, want.to(torch.bfloat16))
+    # against the formula in 64 bits: two products and a sum in binary32, then bf16
+    exact = kv_ref.rotate(x, tables, positions, split, torch.float64)
+    # each output is a sum of two products of an element and a cosine or sine, so at most 2 amax
+    amax = float(x.abs().max())
+    assert float((got.cpu().double() - exact).abs().max()) <= 2 * amax * (2.0 ** -8 + 4 * 2.0 ** -24)
+    out = strided(torch.zeros_like(x), layout)
+    assert nv.rope(xs, [t.cuda() for t in tables], positions.cuda(), split=split, out=out) is out
+    assert same(out, got)
+    if layout == "qkv":  # what lies beside the heads is untouched, also in place
+        nv.rope(xs, [t.cuda() for t in tables], positions.cuda(), split=split, out=xs)
+        wide = xs._base if xs._base is not None else xs
+        assert same(xs, got)
+        wide = torch.as_strided(xs, (rows, 3 * heads, dim), (3 * heads * dim, dim, 1), 0)
+        assert bool((wide[:, :heads] == 7).all()) and bool((wide[:, 2 * heads:] == 7).all())
+
+
+def test_rope_leaves_the_other_dims_and_marks_bad_positions(nv):
+    x = normal(gen(1), 6, 2, 128)
+    x[..., 64:] = torch.tensor([float("nan"), float("inf"), -0.0, float("-inf")] * 16, dtype=torch.bfloat16)
+    tables = [t.cuda() for t in tables_for([16, 16], [5, 7])]
+    positions = torch.tensor([[0, 0], [4, 6], [5, 0], [0, 7], [-1, 0], [2**31 - 1, -2**31]], dtype=torch.int32)
+    for split in (False, True):
+        got = nv.rope(x.cuda(), tables, positions.cuda(), split=split).cpu()
+        assert same(got[..., 64:], x[..., 64:])
+        good = kv_ref.rotate(x[:2], [t.cpu() for t in tables], positions[:2], split).to(torch.bfloat16)
+        assert same(got[:2, :, :64], good[..., :64])
+        nan = got[..., :64].isnan()
+        by_axis = torch.zeros(64, dtype=torch.int64)
+        for i in range(32):
+            p, q = (i, i + 32) if split else (2 * i, 2 * i + 1)
+            by_axis[p] = by_axis[q] = i // 16
+        bad = torch.tensor([[False, False], [False, False], [True, False], [False, True], [True, False], [True, True]])
+        assert torch.equal(nan, bad[:, by_axis][:, None, :].expand(-1, 2, -1))
+
+
+def test_rope_table(nv):
+    t = nv.rope_table(5000, 21, theta=10000.0).cpu().double()
+    angle = torch.arange(5000, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(21, dtype=torch.float64) / 21)
+    want = torch.stack([angle.cos(), angle.sin()], -1)
+    # binary64 angles (an error of a few 2^-53 of up to 5000) rounded once to binary32, values at most 1
+    assert float((t - want).abs().max()) <= 2.0 ** -25 + 5000 * 8 * 2.0 ** -53
+    assert tuple(nv.rope_table(1, 1).shape) == (1, 1, 2)
+
+
+# ---------------------------------------------------------------------------
+# the cache
+# ---------------------------------------------------------------------------
+class Pool:
+    """A GPU cache and the same pool on the host, filled with the same bytes."""
+
+    def __init__(self, nv, seed, heads, dim, lens, spare=2, filled=True):
+        g = gen(seed)
+        self.heads, self.dim = heads, dim
+        need = [max(1, -(-n // BLOCK)) for n in lens]
+        blocks = sum(need) + spare
+        order = torch.randperm(blocks, generator=g).tolist()
+        self.table = np.full((len(lens), max(need)), -7, np.int64)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.ref = kv_ref.Cache(blocks, heads, dim)
+        if filled:
+            r = np.random.RandomState(seed)
+            for kind in range(2):
+                self.ref.codes[kind][:] = r.randint(0, 256, self.ref.codes[kind].shape)
+                c = self.ref.codes[kind]
+                c[(c & 0x7F) == 0x7F] = 0x30  # no NaN codes
+                # codes of |value| up to 448 with powers about 2^-8: values of order 1
+                self.ref.powers[kind][:] = 118 + r.randint(0, 4, self.ref.powers[kind].shape)
+        self.gpu = nv.KvCache.empty(blocks, heads, dim)
+        self.push()
+        self.lens = i32(lens)
+        self.tab = i32(self.table.tolist())
+
+    def push(self):
+        for t, a in ((self.gpu.k, self.ref.codes[0]), (self.gpu.v, self.ref.codes[1]),
+                     (self.gpu.k_power, self.ref.powers[0]), (self.gpu.v_power, self.ref.powers[1])):
+            t.copy_(torch.from_numpy(a).reshape(t.shape))
+
+    def pulled(self):
+        return [t.cpu().numpy().reshape(a.shape) for t, a in
+                ((self.gpu.k, self.ref.codes[0]), (self.gpu.v, self.ref.codes[1]),
+                 (self.gpu.k_power, self.ref.powers[0]), (self.gpu.v_power, self.ref.powers[1]))]
+
+    def same(self):
+        for got, want, name in zip(self.pulled(), self.ref.codes + self.ref.powers, ("k", "v", "k_power", "v_power")):
+            if name in "kv":  # the sign of a NaN code is free
+                got, want = (np.where((a & 0x7F) == 0x7F, 0x7F, a) for a in (got, want))
+            bad = np.argwhere(got != want)
+            assert bad.size == 0, f"{name}: {len(bad)} bytes differ, first at {bad[0]}: {got[tuple(bad[0])]} for " \
+                                  f"{want[tuple(bad[0])]}"
+
+
+def starts(news):
+    return [0] + np.cumsum(news).tolist()
+
+
+WRITES = [
+    # heads, dim, [(past, new)]
+    (1, 64, [(0, 1)]),
+    (1, 128, [(0, 64)]),
+    (3, 128, [(0, 200)]),
+    (2, 64, [(0, 129), (0, 0), (0, 63)]),
+    (2, 128, [(63, 1), (64, 1), (65, 1), (0, 1)]),
+    (2, 64, [(1, 62), (1, 63), (1, 64), (1, 200)]),
+    (9, 64, [(37, 5), (0, 0), (130, 3), (190, 70)]),
+    (17, 128, [(77, 301), (5, 3)]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(WRITES)))
+@pytest.mark.parametrize("layout", ["plain", "qkv", "heads"])
+def test_kv_write_is_the_formula_byte_for_byte(nv, case, layout):
+    heads, dim, seqs = WRITES[case]
+    news = [n for _, n in seqs]
+    pool = Pool(nv, 10 + case, heads, dim, [p + n for p, n in seqs])
+    g = gen(100 + case)
+    k, v = normal(g, sum(news), heads, dim), normal(g, sum(news), heads, dim, sigma=0.01)
+    # heads of very different sizes, so that some blocks' powers grow and others' do not
+    k *= torch.exp2(torch.randint(-9, 10, (1, heads, 1), generator=g).float()).to(torch.bfloat16)
+    rs = starts(news)
+    pool.ref.write((k.double().numpy(), v.double().numpy()), rs, pool.lens.tolist(), pool.table)
+    nv.kv_write(pool.gpu, strided(k, layout), strided(v, layout), i32(rs), pool.lens, pool.tab)
+    pool.same()
+    # written again, the cache holds the same
+    nv.kv_write(pool.gpu, strided(k, layout), strided(v, layout), i32(rs), pool.lens, pool.tab)
+    pool.same()
+
+
+def test_kv_write_of_many_heads_and_blocks(nv):
+    """More heads than one workgroup takes at once, so that the loop over heads runs (56 heads of 700 positions)."""
+    heads, dim, n = 56, 64, 4000
+    pool = Pool(nv, 5, heads, dim, [n], filled=False)
+    g = gen(6)
+    k, v = normal(g, n, heads, dim), normal(g, n, heads, dim)
+    nv.kv_write(pool.gpu, k.cuda(), v.cuda(), i32([0, n]), pool.lens, pool.tab)
+    pool.ref.write((k.double().numpy(), v.double().numpy()), [0, n], [n], pool.table)
+    pool.same()
+
+
+def test_kv_write_of_special_values(nv):
+    """Zeros, the smallest and largest magnitudes, infinities and NaN, in blocks of their own and beside others."""
+    dim, heads = 64, 6
+    pool = Pool(nv, 3, heads, dim, [130])
+    k = normal(gen(4), 130, heads, dim)
+    k[:, 0] = 0.0
+    k[:, 1] = 2.0 ** -133
+    k[5, 1, 3] = -(2.0 ** -130)
+    k[:, 2] = torch.finfo(torch.bfloat16).max
+    k[3, 3, 5], k[70, 3, 6], k[128, 3, 0] = float("inf"), float("-inf"), float("nan")
+    k[:, 4] = float("nan")
+    k[:, 5, ::2], k[:, 5, 1::2] = -0.0, 448.0
+    v = k.flip(1)
+    rows = (k.double().numpy(), v.double().numpy())
+    nv.kv_write(pool.gpu, k.cuda(), v.cuda(), i32([0, 130]), pool.lens, pool.tab)
+    pool.ref.write(rows, [0, 130], [130], pool.table)
+    pool.same()
+    # and back: code times power, NaN where the value was not finite
+    back = nv.kv_read(pool.gpu, 130, i32([0, 130]), pool.lens, pool.tab)
+    for kind in range(2):
+        for h in range(heads):
+            want = pool.ref.sequence(kind, h, pool.table[0], 130)
+            assert np.array_equal(back[kind][:, h].cpu().double().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("fraction", range(128))
+def test_power_of_every_fraction(nv, fraction):
+    """amax = (1 + f/128) 2^e for every bf16 fraction: the power steps at 1.75, and codes stay at most 448."""
+    values = torch.tensor([(1 + fraction / 128) * 2.0 ** e for e in range(-126, 128)], dtype=torch.float64)
+    heads = len(values)
+    k = torch.zeros(1, heads, 64, dtype=torch.bfloat16)
+    k[0, :, 7] = values.to(torch.bfloat16)
+    pool = Pool(nv, 1, heads, 64, [1], filled=False)
+    nv.kv_write(pool.gpu, k.cuda(), k.cuda(), i32([0, 1]), pool.lens, pool.tab)
+    pool.ref.write((k.double().numpy(),) * 2, [0, 1], [1], pool.table)
+    pool.same()
+
+
+def test_tokens_appended_one_by_one(nv):
+    """150 single appends: each step equals the formula, whatever grew on the way."""
+    heads, dim = 3, 128
+    pool = Pool(nv, 8, heads, dim, [150])
+    g = gen(9)
+    k, v = normal(g, 150, heads, dim), normal(g, 150, heads, dim)
+    size = torch.exp2(torch.randint(-6, 7, (150, heads, 1), generator=g).float()).to(torch.bfloat16)
+    k, v = k * size, v * size.flip(0)
+    for i in range(150):
+        lens = [i + 1]
+        pool.ref.write((k[i:i + 1].double().numpy(), v[i:i + 1].double().numpy()), [0, 1], lens, pool.table)
+        nv.kv_write(pool.gpu, k[i:i + 1].cuda(), v[i:i + 1].cuda(), i32([0, 1]), i32(lens), pool.tab)
+    pool.same()
+
+
+@pytest.mark.parametrize("dim,pairs,split", [(64, [32], True), (64, [8], True), (64, [3, 5], False), (128, [16, 24, 24], False),
+                                             (128, [22, 21, 21], True), (128, [8, 8], True), (128, [40], True),
+                                             (64, [1, 2, 3, 2], True)])
+def test_kv_write_rotates_the_keys_as_rope_does(nv, dim, pairs, split):
+    heads, seqs = 5, [(0, 130), (37, 1), (60, 70)]
+    news = [n for _, n in seqs]
+    rows = sum(news)
+    g = gen(20)
+    k, v = normal(g, rows, heads, dim), normal(g, rows, heads, dim)
+    size = [9 + a for a in range(len(pairs))]
+    tables = [t.cuda() for t in tables_for(pairs, size)]
+    positions = torch.stack([torch.randint(0, n, (rows,), generator=g) for n in size], 1).int().cuda()
+    one, two = (Pool(nv, 21, heads, dim, [p + n for p, n in seqs]) for _ in range(2))
+    rs = i32(starts(news))
+    nv.kv_write(one.gpu, strided(k, "qkv"), v.cuda(), rs, one.lens, one.tab, tables=tables, positions=positions, split=split)
+    turned = nv.rope(k.cuda(), tables, positions, split=split)
+    nv.kv_write(two.gpu, turned, v.cuda(), rs, two.lens, two.tab)
+    for a, b in zip(one.pulled(), two.pulled()):
+        assert np.array_equal(a, b)
+
+
+def test_kv_write_and_read_past_the_ends(nv):
+    """Rows outside the sequences, more rows than positions, blocks and lengths that do not exist."""
+    heads, dim = 2, 64
+    k = normal(gen(30), 80, heads, dim)
+    pool = Pool(nv, 31, heads, dim, [70, 20, 64, 40, 100])
+    pool.table[2, 0] = pool.ref.blocks          # outside the pool
+    pool.table[3, 0] = -1
+    lens = [70, 20, 64, 40, 4 * BLOCK]          # the last is more than the table holds
+    rs = [3, 13, 43, 53, 63, 73]                # rows 0..2 and 73..79 belong to nobody; sequence 1 has 30 rows for 20
+    tab = i32(pool.table.tolist())
+    pool.ref.write((k.double().numpy(),) * 2, rs, lens, pool.table)
+    nv.kv_write(pool.gpu, k.cuda(), k.cuda(), i32(rs), i32(lens), tab)
+    pool.same()
+    out = [torch.full((80, heads, dim), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    nv.kv_read(pool.gpu, 80, i32(rs), i32(lens), tab, k=out[0], v=out[1])
+    for kind in range(2):
+        got = out[kind].cpu().double().numpy()
+        assert (got[:3] == 5).all() and (got[73:] == 5).all()
+        for h in range(heads):
+            assert np.array_equal(got[3:13, h], pool.ref.sequence(kind, h, pool.table[0], 70)[60:])
+            assert (got[13:23, h] == 0).all()
+            assert np.array_equal(got[23:43, h], pool.ref.sequence(kind, h, pool.table[1], 20))
+        assert np.isnan(got[43:73]).all()
+
+
+@pytest.mark.parametrize("rs,lens", [([5, 2, 9], [4, 4]), ([-3, 40, 2000], [64, 64]), ([0, 0, 0], [0, 0]),
+                                     ([10, 10, 3], [2**31 - 1, -2**31]), ([2**31 - 1, -2**31, 5], [64, -1])])
+def test_arrays_that_make_no_sense_stay_in_bounds(nv, rs, lens):
+    """Row starts and lengths of any content: no access leaves the arrays (checked by what surrounds them)."""
+    heads, dim, M = 2, 64, 12
+    k = normal(gen(33), M, heads, dim).cuda()
+    pool = Pool(nv, 34, heads, dim, [64, 64])
+    tab = pool.tab
+    nv.kv_write(pool.gpu, k, k, i32(rs), i32(lens), tab)
+    big = torch.full((M + 20, heads, dim), 5.0, dtype=torch.bfloat16, device="cuda")
+    nv.kv_read(pool.gpu, M, i32(rs), i32(lens), tab, k=big[10:10 + M], v=torch.empty_like(k))
+    assert bool((big[:10] == 5).all()) and bool((big[10 + M:] == 5).all())
+    big.fill_(5.0)
+    nv.kv_attention(k, pool.gpu, i32(rs), i32(lens), tab, out=big[10:10 + M], causal_block=1)
+    assert bool((big[:10] == 5).all()) and bool((big[10 + M:] == 5).all())
+
+
+@pytest.mark.parametrize("dim,heads,seqs", [(64, 1, [(0, 1)]), (128, 3, [(10, 60), (0, 200)]), (64, 5, [(63, 2), (64, 64), (0, 0)]),
+                                            (128, 1, [(500, 77)])])
+@pytest.mark.parametrize("layout", ["plain", "qkv", "heads"])
+def test_kv_read(nv, dim, heads, seqs, layout):
+    news = [n for _, n in seqs]
+    lens = [p + n for p, n in seqs]
+    pool = Pool(nv, 40 + dim, heads, dim, lens)
+    rs, rows = starts(news), sum(news)
+    k, v = (strided(torch.zeros(rows, heads, dim, dtype=torch.bfloat16), layout) for _ in range(2))
+    got = nv.kv_read(pool.gpu, rows, i32(rs), pool.lens, pool.tab, k=k, v=v)
+    assert got[0] is k and got[1] is v
+    for b, (past, n) in enumerate(seqs):
+        for kind in range(2):
+            for h in range(heads):
+                want = pool.ref.sequence(kind, h, pool.table[b], past + n)[past:]
+                assert np.array_equal(got[kind][rs[b]:rs[b + 1], h].cpu().double().numpy(), want)
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+def check(got, want, tol):
+    got = got.cpu().double().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want)), "NaN in other places"
+    bad = ~np.isnan(want) & (np.abs(got - want) > tol)
+    assert not bad.any(), f"{bad.sum()} of {bad.size} outside, worst {np.nanmax(np.abs(got - want) / tol):.3g} of the bound"
+
+
+ATTENTION = [
+    # dim, kv heads, group, causal block, [(past, new)]
+    (64, 1, 1, 0, [(0, 1)]),
+    (128, 1, 1, 1, [(0, 1)]),
+    (128, 2, 4, 1, [(516, 1)]),
+    (64, 3, 1, 1, [(63, 1), (64, 1), (65, 1), (0, 1)]),
+    (128, 2, 5, 1, [(300, 1), (0, 1), (77, 1), (900, 1)]),
+    (64, 2, 8, 1, [(100, 3), (10, 2), (0, 3), (5, 0)]),
+    (128, 1, 1, 1, [(0, 33), (0, 70)]),
+    (128, 2, 3, 1, [(0, 65), (17, 100)]),
+    (64, 2, 2, 0, [(40, 90), (0, 129)]),
+    (128, 1, 4, 16, [(5, 60), (64, 48)]),
+    (64, 2, 1, 100, [(0, 250)]),
+    (128, 3, 1, 0, [(1, 200)]),
+    (64, 1, 40, 1, [(70, 3)]),
+    (128, 1, 1, 1, [(3000, 1)]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(ATTENTION)))
+def test_attention(nv, case):
+    dim, heads, group, c, seqs = ATTENTION[case]
+    news = [n for _, n in seqs]
+    pool = Pool(nv, 50 + case, heads, dim, [p + n for p, n in seqs])
+    q = normal(gen(60 + case), sum(news), heads * group, dim, sigma=1.0 + case % 3)
+    rs, scale = starts(news), dim ** -0.5
+    want, tol = kv_ref.attention(q.double().numpy(), pool.ref, rs, pool.lens.tolist(), pool.table, np.float64(np.float32(scale)),
+                                 c, bounds=True)
+    for layout in ("plain", "qkv", "heads"):
+        got = nv.kv_attention(strided(q, layout), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=c)
+        check(got, want, tol)
+    out = strided(torch.zeros_like(q), "heads")
+    nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=c, out=out)
+    assert same(out, got)
+    inplace = q.cuda()
+    nv.kv_attention(inplace, pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=c, out=inplace)
+    assert same(inplace, got)
+
+
+@pytest.mark.parametrize("dim,heads,group,c,seqs", [(128, 2, 4, 1, [(0, 700), (333, 500)]), (64, 3, 1, 0, [(900, 601)]),
+                                                    (128, 4, 1, 256, [(100, 1100)]), (64, 2, 7, 1, [(0, 300), (0, 301)])])
+def test_attention_of_longer_rows(nv, dim, heads, group, c, seqs):
+    news = [n for _, n in seqs]
+    pool = Pool(nv, 70, heads, dim, [p + n for p, n in seqs])
+    q = normal(gen(71), sum(news), heads * group, dim)
+    rs, scale = starts(news), np.float64(np.float32(0.1))
+    want, tol = kv_ref.attention_fast(q.double().numpy(), pool.ref, rs, pool.lens.tolist(), pool.table, scale, c)
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, scale=0.1, causal_block=c)
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("max_len", [0, 64, 1000, 5000, 200000])
+def test_attention_is_right_for_any_bound_on_the_lengths(nv, max_len):
+    """max_len decides the number of parts only; below and above the true lengths the result stays right."""
+    pool = Pool(nv, 80, 2, 128, [2000, 1, 130])
+    q = normal(gen(81), 3, 8, 128)
+    want, tol = kv_ref.attention(q.double().numpy(), pool.ref, [0, 1, 2, 3], [2000, 1, 130], pool.table,
+                                 np.float64(np.float32(128 ** -0.5)), 1, bounds=True)
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32([0, 1, 2, 3]), pool.lens, pool.tab, causal_block=1, max_len=max_len)
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("rows", [1, 40, 300])
+def test_rows_that_see_nothing(nv, rows):
+    """A sequence of no positions, and more rows than positions under a causal mask: those rows are 0, and rows of no
+    sequence are left as they were."""
+    pool = Pool(nv, 82, 1, 64, [0, 5, 70])
+    rs = [2, 2 + rows, 2 + 2 * rows, 2 + 3 * rows]
+    q = normal(gen(83), rs[-1] + 3, 2, 64)
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1, out=out)
+    want, tol = kv_ref.attention(q.double().numpy(), pool.ref, rs, [0, 5, 70], pool.table, np.float64(np.float32(0.125)), 1,
+                                 bounds=True)
+    inside = slice(rs[0], rs[-1])
+    check(out[inside], want[inside], tol[inside])
+    assert bool((out[:rs[0]] == 5).all()) and bool((out[rs[-1]:] == 5).all())
+    assert bool((out[rs[0]:rs[1]] == 0).all())
+    if rows > 5:
+        assert bool((out[rs[1]:rs[2] - 5] == 0).all())
+
+
+@pytest.mark.parametrize("dim,group,news", [(64, 1, [1, 1]), (128, 2, [40, 3]), (128, 1, [150, 130]), (64, 4, [200, 70])])
+def test_what_is_hidden_has_no_effect(nv, dim, group, news):
+    """NaN codes behind the last position and in masked places: the outputs' bytes do not change.  A NaN that a row
+    sees reaches that row, and no other."""
+    past = [70, 100]
+    lens = [p + n for p, n in zip(past, news)]
+    pool = Pool(nv, 84, 2, dim, lens)
+    q = normal(gen(85), sum(news), 2 * group, dim)
+    rs = starts(news)
+    call = lambda: nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1)  # noqa: E731
+    clean = call()
+    for b in range(2):  # the tail of the last block, keys, values
+        tail = lens[b] % BLOCK
+        page = pool.table[b, lens[b] // BLOCK] if tail else None
+        if page is not None:
+            for kind in range(2):
+                pool.ref.codes[kind][page][:, pool.ref.off[kind][tail:]] = 0x7F
+    pool.push()
+    assert same(call(), clean)
+    # one NaN in head 1 of sequence 0, at a position that only some rows see
+    at = past[0] + news[0] // 2
+    for kind in range(2):
+        pool.ref.codes[kind][pool.table[0, at // BLOCK], 1, pool.ref.off[kind][at % BLOCK, 3]] = 0xFF
+        pool.push()
+        got, nan = call().cpu(), torch.zeros(q.shape, dtype=torch.bool)
+        i = torch.arange(news[0])[past[0] + torch.arange(news[0]) >= at]
+        if kind == 0:
+            nan[i, group:] = True
+        else:
+            nan[i, group:, 3] = True
+        assert torch.equal(got.isnan(), nan)
+        assert np.array_equal(bits(got)[~nan.numpy()], bits(clean)[~nan.numpy()])
+        pool.ref.codes[kind][pool.table[0, at // BLOCK], 1, pool.ref.off[kind][at % BLOCK, 3]] = 0x30
+        pool.push()
+        clean = call()
+
+
+@pytest.mark.parametrize("rows", [1, 50, 200])
+def test_blocks_and_lengths_that_do_not_exist(nv, rows):
+    pool = Pool(nv, 86, 2, 64, [300, 300, 300, 300])
+    pool.table[1, 1] = pool.ref.blocks
+    pool.table[2, 4] = -2
+    lens = [300, 300, 300, 6 * BLOCK]
+    rs = [0, rows, 2 * rows, 3 * rows, 4 * rows]
+    q = normal(gen(87), 4 * rows, 2, 64)
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32(rs), i32(lens), i32(pool.table.tolist()), causal_block=1)
+    want, tol = kv_ref.attention(q.double().numpy(), pool.ref, rs, lens, pool.table, np.float64(np.float32(0.125)), 1, bounds=True)
+    check(got, want, tol)
+    assert np.isnan(want[3 * rows:]).all() and not np.isnan(want[:rows]).any()
+
+
+def test_queries_that_are_not_finite_and_large_and_small_ones(nv):
+    pool = Pool(nv, 88, 1, 128, [100, 100])
+    q = normal(gen(89), 40, 1, 128)
+    q[3, 0, 5], q[20, 0, 100], q[21, 0, 0] = float("nan"), float("inf"), float("-inf")
+    q[4] = 0.0
+    q[5] *= 2.0 ** -100
+    q[6] = 2.0 ** -133
+    q[7] *= 16.0
+    q[8, 0, ::2] *= 2.0 ** -14
+    rs = [0, 20, 40]
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1)
+    clean = q.double().numpy().copy()
+    bad = ~np.isfinite(clean).all(axis=2)
+    clean[bad] = 0.0
+    want, tol = kv_ref.attention(clean, pool.ref, rs, [100, 100], pool.table, np.float64(np.float32(128 ** -0.5)), 1, bounds=True)
+    want[bad] = np.nan
+    check(got, want, tol)
+
+
+def test_values_of_very_different_powers(nv):
+    """Blocks whose values differ by powers of two up to 2^60, and values near the ends of the range."""
+    for low, high in ((90, 150), (10, 30), (200, 240)):
+        pool = Pool(nv, 90, 2, 128, [640])
+        r = np.random.RandomState(91)
+        pool.ref.powers[1][:] = r.randint(low, high, pool.ref.powers[1].shape)
+        pool.push()
+        q = normal(gen(92), 50, 2, 128)
+        got = nv.kv_attention(q.cuda(), pool.gpu, i32([0, 50]), pool.lens, pool.tab, causal_block=1)
+        want, tol = kv_ref.attention_fast(q.double().numpy(), pool.ref, [0, 50], [640], pool.table,
+                                          np.float64(np.float32(128 ** -0.5)), 1)
+        check(got, want, tol)
+
+
+def test_scores_far_apart(nv):
+    """A growing row of scores (each block above the last by hundreds), a falling one, and one that stays."""
+    heads, dim, n = 3, 64, 640
+    pool = Pool(nv, 93, heads, dim, [n])
+    pool.ref.codes[0][:] = 0x38  # 1.0
+    for at in range(10):
+        page = pool.table[0, at]
+        pool.ref.powers[0][page, 0] = 127 + at - 6
+        pool.ref.powers[0][page, 1] = 127 + 3 - at
+        pool.ref.powers[0][page, 2] = 127
+    pool.push()
+    q = torch.ones(5, heads, dim, dtype=torch.bfloat16) * torch.tensor([1.0, -1.0, 0.1, 3.0, 40.0])[:, None, None].to(torch.bfloat16)
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32([0, 5]), pool.lens, pool.tab, scale=1.0)
+    want, tol = kv_ref.attention(q.double().numpy(), pool.ref, [0, 5], [n], pool.table, 1.0, 0, bounds=True)
+    check(got, want, tol)
+
+
+# ---------------------------------------------------------------------------
+# streams, graphs, and the whole run
+# ---------------------------------------------------------------------------
+def _serving_state(nv, seed, lens, heads=2, group=4, dim=128):
+    pool = Pool(nv, seed, heads, dim, [n + 8 for n in lens], filled=False)
+    g = gen(seed)
+    past = torch.randn(sum(lens), heads, dim, generator=g).to(torch.bfloat16).cuda()
+    nv.kv_write(pool.gpu, past, past.flip(0), i32(starts(lens)), i32(lens), pool.tab)
+    return pool
+
+
+def test_captured_tokens_replay(nv):
+    """Append and attend for four sequences captured once and replayed with new inputs and lengths, eager work in
+    between, two graphs alive at once: every replay equals the eager calls."""
+    lens = [70, 1, 600, 127]
+    one, two = _serving_state(nv, 95, lens), _serving_state(nv, 95, lens)
+    third = _serving_state(nv, 95, lens)
+    tables = [nv.rope_table(1024, 64)]
+    g = gen(96)
+    new = lambda: torch.randn(4, 16, 128, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    rs = i32([0, 1, 2, 3, 4])
+
+    def step(pool, x, n, pos):
+        q = nv.rope(x[:, :8], tables, pos)
+        nv.kv_write(pool.gpu, x[:, 8:10], x[:, 10:12], rs, n, pool.tab, tables=tables, positions=pos)
+        return nv.kv_attention(q, pool.gpu, rs, n, pool.tab, causal_block=1)
+
+    made = []
+    for pool in (one, two):
+        x, n, pos = new(), i32(lens), i32([[p] for p in lens])
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = step(pool, x, n, pos)
+        made.append((graph, x, n, pos, out))
+    for i in range(6):
+        x = new()
+        now = [p + i + 1 for p in lens]
+        want = step(third, x, i32(now), i32([[p - 1] for p in now])).clone()
+        for graph, gx, gn, gpos, out in made:
+            gx.copy_(x), gn.copy_(i32(now)), gpos.copy_(i32([[p - 1] for p in now]))
+            graph.replay()
+        torch.cuda.synchronize()
+        for pool, (_, _, _, _, out) in zip((one, two), made):
+            assert same(out, want), f"replay {i}"
+            for a, b in zip(pool.pulled(), third.pulled()):
+                assert np.array_equal(a, b)
+
+
+def test_other_streams(nv):
+    """Calls on side streams, two at once with workspaces of their own, equal the calls on the main one."""
+    pool = Pool(nv, 97, 2, 128, [3000])
+    q = normal(gen(98), 1, 8, 128).cuda()
+    rs = i32([0, 1])
+    want = nv.kv_attention(q, pool.gpu, rs, pool.lens, pool.tab)
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for s in side:
+            got.append(nv.kv_attention(q, pool.gpu, rs, pool.lens, pool.tab, stream=s))
+    for s in side:
+        s.synchronize()
+    for o in got:
+        assert same(o, want)
+
+
+def test_same_call_same_bytes(nv):
+    pool = Pool(nv, 99, 4, 64, [5000, 4000])
+    q = normal(gen(98), 300, 8, 64).cuda()
+    for rs in ([0, 1, 2], [0, 150, 300]):
+        rows = rs[-1]
+        runs = [bits(nv.kv_attention(q[:rows], pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1)) for _ in range(4)]
+        assert all(np.array_equal(runs[0], r) for r in runs[1:])
+
+
+def test_from_projection_to_projection(nv):
+    """The run as it is used: modulation producer, QKV product, rotation, cache, attention, plain quantizer, output
+    product, for a prompt and then single tokens; attention's inputs and outputs checked against the references."""
+    heads, dim, width = 2, 128, 512
+    g = gen(101)
+    w_qkv = nv.quantize_weight(normal(g, 3 * heads * dim, width, sigma=width ** -0.5).cuda())
+    w_out = nv.quantize_weight(normal(g, width, heads * dim, sigma=0.06).cuda())
+    shift, scale = normal(g, 1, width, sigma=0.1).cuda(), normal(g, 1, width, sigma=0.1).cuda()
+    tables = [nv.rope_table(64, p) for p in (16, 24, 24)]
+    pool = Pool(nv, 102, heads, dim, [200], filled=False)
+    length = 0
+    for rows in (150, 1, 1, 40):
+        x = normal(g, rows, width).cuda()
+        q8, sf, ts, _ = nv.modulate_quantize(x, [0, rows], shift, scale)
+        qkv = nv.gemm(q8, sf, ts, rows, *w_qkv).view(rows, 3 * heads, dim)
+        at = torch.arange(length, length + rows)
+        positions = torch.stack([at // 24, at // 6 % 4, at % 6], 1).int().cuda()
+        length += rows
+        rs, lens = i32([0, rows]), i32([length])
+        q = nv.rope(qkv[:, :heads], tables, positions)
+        nv.kv_write(pool.gpu, qkv[:, heads:2 * heads], qkv[:, 2 * heads:], rs, lens, pool.tab, tables=tables,
+                    positions=positions)
+        o = nv.kv_attention(q, pool.gpu, rs, lens, pool.tab, causal_block=1)
+        host = qkv.cpu()
+        cpu_tables = [t.cpu() for t in tables]
+        turned = [kv_ref.rotate(host[:, w:w + heads], cpu_tables, positions.cpu(), False).to(torch.bfloat16).double().numpy()
+                  for w in (0, heads)]
+        pool.ref.write((turned[1], host[:, 2 * heads:].double().numpy()), [0, rows], [length], pool.table)
+        pool.same()
+        want, tol = kv_ref.attention(turned[0], pool.ref, [0, rows], [length], pool.table,
+                                     np.float64(np.float32(dim ** -0.5)), 1, bounds=True)
+        check(o, want, tol)
+        o8, of, ot, _ = nv.quantize(o.reshape(rows, heads * dim))
+        y = nv.gemm(o8, of, ot, rows, *w_out)
+        assert tuple(y.shape) == (rows, width) and bool(y.isfinite().all())
+
+
+def test_another_devices_or_types_are_refused(nv):
+    pool = Pool(nv, 103, 1, 64, [64])
+    q = normal(gen(1), 4, 1, 64)
+    rs = i32([0, 4])
+    with pytest.raises(ValueError):
+        nv.kv_attention(q, pool.gpu, rs, pool.lens, pool.tab)
+    with pytest.raises(ValueError):
+        nv.kv_attention(q.cuda(), pool.gpu, rs.cpu(), pool.lens, pool.tab)
+    with pytest.raises(TypeError):
+        nv.kv_attention(q.cuda().float(), pool.gpu, rs, pool.lens, pool.tab)
+    with pytest.raises(TypeError):
+        nv.kv_attention(q.cuda(), pool.gpu, rs.long(), pool.lens, pool.tab)
+    with pytest.raises(nv.Nvfp4Error):
+        nv.kv_attention(q.cuda(), pool.gpu, rs, pool.lens, pool.tab, scale=0.0)
+    with pytest.raises(nv.Nvfp4Error):  # an output whose heads overlap
+        nv.kv_attention(q.cuda(), pool.gpu, rs, pool.lens, pool.tab, out=torch.empty_like(q.cuda()[:1]).expand(4, 1, 64))
+    with pytest.raises(ValueError):
+        nv.kv_write(pool.gpu, q.cuda(), q.cuda()[:3], rs, pool.lens, pool.tab)
+    with pytest.raises(ValueError):
+        nv.kv_write(pool.gpu, q.cuda(), q.cuda(), rs, pool.lens, pool.tab, tables=[nv.rope_table(4, 8)])
+    with pytest.raises(nv.Nvfp4Error):  # 4 pairs
+        nv.rope(q.cuda(), [nv.rope_table(4, 4)], torch.zeros(4, 1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(nv.Nvfp4Error):  # positions without a row of their own
+        nv.rope(q.cuda(), [nv.rope_table(4, 8)], torch.zeros(1, 1, dtype=torch.int32, device="cuda").expand(4, 1))
+    empty = nv.kv_attention(q.cuda()[:0], pool.gpu, i32([0, 0]), pool.lens, pool.tab)
+    assert tuple(empty.shape) == (0, 1, 64)
