@@ -406,7 +406,7 @@ typedef struct {
 
 /* The usual table of one axis: (cos, sin) of p * theta^(-j / pairs) for
  * positions p < rows and j < pairs, formed in binary64 and rounded to binary32.
- * rows >= 1, pairs >= 1, rows * pairs < 2^31, theta > 0 and finite. */
+ * rows >= 1, pairs >= 1, rows * pairs < 2^28, theta > 0 and finite. */
 nvfp4_status nvfp4_rope_table(float* table, int64_t rows, int32_t pairs, double theta, void* stream);
 
 /* Rotates x [M, heads, dim] into out; dims past the rotated ones are copied.

@@ -534,61 +534,82 @@ def modulate_gemm_ring(x: torch.Tensor, row_start, shift: torch.Tensor, scale: t
 # ---------------------------------------------------------------------------
 # rotary positions, the 8-bit key/value cache and attention over it
 # ---------------------------------------------------------------------------
-def _same_device(dev: torch.device, **tensors):
+# These checks run before every launch of a few microseconds, so they look at
+# each property once and build their messages only when something is wrong.
+def _same_device(dev: torch.device, *tensors):
     if dev.type != "cuda":
         raise ValueError(f"expected tensors on a GPU, got {dev}")
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+            raise ValueError(f"a tensor is on {t.device}, expected {dev}")
 
 
 def _heads(name: str, x: torch.Tensor, shape=None) -> Heads:
+    got = x.shape
     if x.dtype != torch.bfloat16:
         raise TypeError(f"{name}: expected bf16, got {x.dtype}")
-    if x.dim() != 3 or (shape is not None and tuple(x.shape) != tuple(shape)):
-        raise ValueError(f"{name}: expected {'[rows, heads, dim]' if shape is None else list(shape)}, got {list(x.shape)}")
-    if x.stride(2) != 1 and x.shape[2] > 1:
+    if len(got) != 3 or (shape is not None and got != shape):
+        raise ValueError(f"{name}: expected {'[rows, heads, dim]' if shape is None else list(shape)}, got {list(got)}")
+    row, head, unit = x.stride()
+    if unit != 1 and got[2] > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
     # the stride of a dimension of one element says nothing
-    return Heads(x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0)
+    return Heads(x.data_ptr(), row if got[0] > 1 else 0, head if got[1] > 1 else 0)
 
 
-def _int32(name: str, t: torch.Tensor, dims: int) -> torch.Tensor:
+def _int32(name: str, t: torch.Tensor, dims: int):
+    """The tensor's shape and strides, once it is found to be what the library takes."""
+    shape, stride = t.shape, t.stride()
     if t.dtype != torch.int32:
         raise TypeError(f"{name}: expected int32, got {t.dtype}")
-    if t.dim() != dims or (t.stride(dims - 1) != 1 and t.shape[dims - 1] > 1):
+    if len(shape) != dims or (stride[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must have {dims} dimension(s) and unit stride along the last")
-    return t
+    return shape, stride
 
 
-def _rope_params(tables, positions: torch.Tensor, rows: int, split: bool) -> RopeParams:
-    if not 1 <= len(tables) <= ROPE_MAX_AXES:
-        raise ValueError(f"expected 1 to {ROPE_MAX_AXES} tables, got {len(tables)}")
-    _int32("positions", positions, 2)
-    if tuple(positions.shape) != (rows, len(tables)):
-        raise ValueError(f"positions: expected [{rows}, {len(tables)}], got {list(positions.shape)}")
-    p = RopeParams()
-    p.axes, p.split = len(tables), int(bool(split))
+def _rope_params(tables, positions: torch.Tensor, rows: int, split: bool, dev: torch.device) -> RopeParams:
+    axes = len(tables)
+    if not 1 <= axes <= ROPE_MAX_AXES:
+        raise ValueError(f"expected 1 to {ROPE_MAX_AXES} tables, got {axes}")
+    shape, stride = _int32("positions", positions, 2)
+    if shape != (rows, axes):
+        raise ValueError(f"positions: expected [{rows}, {axes}], got {list(shape)}")
+    _same_device(dev, positions, *tables)
+    p = RopeParams(axes, 1 if split else 0)
     for a, t in enumerate(tables):
-        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[2] != 2 or not t.is_contiguous():
+        shape = t.shape
+        if t.dtype != torch.float32 or len(shape) != 3 or shape[2] != 2 or not t.is_contiguous():
             raise ValueError("a rope table is a contiguous fp32 [positions, pairs, 2]")
-        if t.device != positions.device:
-            raise ValueError(f"table {a} is on {t.device}, positions on {positions.device}")
-        p.pairs[a], p.rows[a], p.table[a] = t.shape[1], t.shape[0], t.data_ptr()
-    p.positions, p.ld_positions = positions.data_ptr(), positions.stride(0) if rows > 1 else len(tables)
+        p.rows[a], p.pairs[a], _ = shape
+        p.table[a] = t.data_ptr()
+    p.positions, p.ld_positions = positions.data_ptr(), stride[0] if rows > 1 else axes
     return p
 
 
-def _call(fn: str, dev: torch.device, stream, *args):
-    """One launch on the tensors' device: on `stream`, or that device's current stream."""
-    st = _torch_stream(stream, dev)
-    if st.device != dev:
-        raise ValueError(f"the stream is on {st.device}, the tensors on {dev}")
+def _empty(dev: torch.device, stream, shape, dtype=torch.bfloat16) -> torch.Tensor:
+    """A new tensor of the stream that the call runs on."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(_torch_stream(stream, dev)):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _call(name: str, fn, dev: torch.device, stream, *args):
+    """One call on the tensors' device: on `stream`, or on that device's current stream."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        st = _torch_stream(stream, dev)
+        if st.device != dev:
+            raise ValueError(f"the stream is on {st.device}, the tensors on {dev}")
+        raw = st.cuda_stream
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            _check(fn, getattr(lib, fn)(*args, st.cuda_stream))
+            status = fn(*args, raw)
     else:
-        _check(fn, getattr(lib, fn)(*args, st.cuda_stream))
+        status = fn(*args, raw)
+    if status != NVFP4_OK:
+        _check(name, status)
 
 
 def rope_table(positions: int, pairs: int, theta: float = 10000.0, device=None, stream=None) -> torch.Tensor:
@@ -598,9 +619,8 @@ def rope_table(positions: int, pairs: int, theta: float = 10000.0, device=None, 
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     _same_device(dev)
-    with torch.cuda.stream(_torch_stream(stream, dev)):
-        table = torch.empty((positions, pairs, 2), dtype=torch.float32, device=dev)
-    _call("nvfp4_rope_table", dev, stream, table.data_ptr(), positions, pairs, float(theta))
+    table = _empty(dev, stream, (positions, pairs, 2), torch.float32)
+    _call("nvfp4_rope_table", lib.nvfp4_rope_table, dev, stream, table.data_ptr(), positions, pairs, float(theta))
     return table
 
 
@@ -611,16 +631,15 @@ def rope(x: torch.Tensor, tables, positions: torch.Tensor, split: bool = False, 
     tables: one [positions, pairs, 2] table for each axis (rope_table); positions: int32 [rows, axes].
     Pairs are neighbouring dims, or with split dims half of the rotated part apart.  out may be x."""
     dev = x.device
-    _same_device(dev, positions=positions, out=out)
+    _same_device(dev, out)
     hx = _heads("x", x)
-    rows, heads, dim = x.shape
-    r = _rope_params(tables, positions, rows, split)
+    rows, heads, dim = shape = x.shape
+    r = _rope_params(tables, positions, rows, split, dev)
     if out is None:
-        with torch.cuda.stream(_torch_stream(stream, dev)):
-            out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev)
-    ho = _heads("out", out, x.shape)
+        out = _empty(dev, stream, shape)
+    ho = _heads("out", out, shape)
     if rows:
-        _call("nvfp4_rope", dev, stream, hx, rows, heads, dim, r, ho)
+        _call("nvfp4_rope", lib.nvfp4_rope, dev, stream, hx, rows, heads, dim, r, ho)
     return out
 
 
@@ -633,14 +652,15 @@ class KvCache:
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_power: torch.Tensor, v_power: torch.Tensor):
         if k.dim() != 5:
             raise ValueError("k must be [blocks, heads, dim / 16, 64, 16]")
-        blocks, heads, dim = k.shape[0], k.shape[1], 16 * k.shape[2]
-        for name, t, shape in (("k", k, (blocks, heads, dim // 16, KV_BLOCK, 16)), ("v", v, (blocks, heads, 4, dim, 16)),
-                               ("k_power", k_power, (blocks, heads)), ("v_power", v_power, (blocks, heads))):
+        blocks, heads, groups, _, _ = shape = k.shape
+        dim = 16 * groups
+        for name, t, want in (("k", k, (blocks, heads, groups, KV_BLOCK, 16)), ("v", v, (blocks, heads, 4, dim, 16)),
+                              ("k_power", k_power, shape[:2]), ("v_power", v_power, shape[:2])):
             if t.dtype != torch.uint8:
                 raise TypeError(f"{name}: expected uint8, got {t.dtype}")
-            if tuple(t.shape) != shape or not t.is_contiguous():
-                raise ValueError(f"{name}: expected contiguous {list(shape)}, got {list(t.shape)}")
-        _same_device(k.device, v=v, k_power=k_power, v_power=v_power)
+            if t.shape != want or not t.is_contiguous():
+                raise ValueError(f"{name}: expected contiguous {list(want)}, got {list(t.shape)}")
+        _same_device(k.device, v, k_power, v_power)
         self.k, self.v, self.k_power, self.v_power = k, v, k_power, v_power
         self.blocks, self.heads, self.dim, self.device = blocks, heads, dim, k.device
         self._struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_power.data_ptr(), v_power.data_ptr(), blocks, heads,
@@ -656,16 +676,13 @@ class KvCache:
 
 
 def _sequences(row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, dev: torch.device) -> KvSequences:
-    _same_device(dev, row_start=row_start, lens=lens, table=table)
-    _int32("row_start", row_start, 1)
-    _int32("lens", lens, 1)
-    _int32("table", table, 2)
-    n = lens.shape[0]
-    if row_start.shape[0] != n + 1 or table.shape[0] != n:
-        raise ValueError(f"{n} lengths need {n + 1} row starts and {n} table rows, got {row_start.shape[0]} and "
-                         f"{table.shape[0]}")
-    return KvSequences(n, row_start.data_ptr(), lens.data_ptr(), table.data_ptr(),
-                       table.stride(0) if n > 1 else table.shape[1], table.shape[1])
+    _same_device(dev, row_start, lens, table)
+    (starts,), _ = _int32("row_start", row_start, 1)
+    (n,), _ = _int32("lens", lens, 1)
+    (rows, blocks), (ld, _) = _int32("table", table, 2)
+    if starts != n + 1 or rows != n:
+        raise ValueError(f"{n} lengths need {n + 1} row starts and {n} table rows, got {starts} and {rows}")
+    return KvSequences(n, row_start.data_ptr(), lens.data_ptr(), table.data_ptr(), ld if n > 1 else blocks, blocks)
 
 
 def kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor, lens: torch.Tensor,
@@ -676,32 +693,32 @@ def kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, row_start: torch.
     table [sequences, blocks] names its cache blocks (all int32 on the GPU).  With tables and positions the keys
     are rotated on the way, as `rope` does."""
     dev = cache.device
-    _same_device(dev, k=k, v=v, positions=positions)
-    shape = (k.shape[0], cache.heads, cache.dim)
+    _same_device(dev, k, v)
+    rows = k.shape[0]
+    shape = (rows, cache.heads, cache.dim)
     hk, hv = _heads("k", k, shape), _heads("v", v, shape)
     q = _sequences(row_start, lens, table, dev)
     r = None
     if len(tables):
         if positions is None:
             raise ValueError("rotating the keys needs their positions")
-        r = _rope_params(tables, positions, k.shape[0], split)
-    if k.shape[0]:
-        _call("nvfp4_kv_write", dev, stream, cache._struct, q, k.shape[0], hk, hv, r)
+        r = _rope_params(tables, positions, rows, split, dev)
+    if rows:
+        _call("nvfp4_kv_write", lib.nvfp4_kv_write, dev, stream, cache._struct, q, rows, hk, hv, r)
 
 
 def kv_read(cache: KvCache, rows: int, row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
             k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
     """Reads the positions of `rows` rows (as kv_write addresses them) back: k and v, bf16 [rows, heads, dim]."""
     dev = cache.device
-    _same_device(dev, k=k, v=v)
+    _same_device(dev, k, v)
     q = _sequences(row_start, lens, table, dev)
     shape = (rows, cache.heads, cache.dim)
-    with torch.cuda.stream(_torch_stream(stream, dev)):
-        k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    k = _empty(dev, stream, shape) if k is None else k
+    v = _empty(dev, stream, shape) if v is None else v
     hk, hv = _heads("k", k, shape), _heads("v", v, shape)
     if rows:
-        _call("nvfp4_kv_read", dev, stream, cache._struct, q, rows, hk, hv)
+        _call("nvfp4_kv_read", lib.nvfp4_kv_read, dev, stream, cache._struct, q, rows, hk, hv)
     return k, v
 
 
@@ -720,25 +737,24 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
     workgroups.  A workspace of nvfp4_kv_attention_workspace_bytes(...) is allocated with torch when none is given,
     on the stream that the call runs on."""
     dev = cache.device
-    _same_device(dev, q=q, out=out, workspace=workspace)
+    _same_device(dev, q, out, workspace)
     hq = _heads("q", q)
-    rows, q_heads, dim = q.shape
+    rows, q_heads, dim = shape = q.shape
     if dim != cache.dim:
         raise ValueError(f"q has heads of {dim}, the cache of {cache.dim}")
     s = _sequences(row_start, lens, table, dev)
     if max_len is None:
         max_len = table.shape[1] * KV_BLOCK
-    need = int(lib.nvfp4_kv_attention_workspace_bytes(rows, s.count, q_heads, cache.heads, dim, max_len)) if rows else 0
-    if out is None or (need and workspace is None):
-        with torch.cuda.stream(_torch_stream(stream, dev)):
-            if out is None:
-                out = torch.empty((rows, q_heads, dim), dtype=torch.bfloat16, device=dev)
-            if need and workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ho = _heads("out", out, q.shape)
+    if out is None:
+        out = _empty(dev, stream, shape)
+    if workspace is None and rows:
+        need = lib.nvfp4_kv_attention_workspace_bytes(rows, s.count, q_heads, cache.heads, dim, max_len)
+        if need:
+            workspace = _empty(dev, stream, (need,), torch.uint8)
+    ho = _heads("out", out, shape)
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if rows:
-        _call("nvfp4_kv_attention", dev, stream, hq, rows, q_heads, cache._struct, s,
+        _call("nvfp4_kv_attention", lib.nvfp4_kv_attention, dev, stream, hq, rows, q_heads, cache._struct, s,
               dim ** -0.5 if scale is None else float(scale), causal_block, max_len, ho,
               None if workspace is None else workspace.data_ptr(), size)
     return out

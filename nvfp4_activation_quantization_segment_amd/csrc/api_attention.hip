@@ -42,6 +42,7 @@ nvfp4_status check_rope(const nvfp4_rope_params* p, int64_t dim, RopeArgs* r) {
     for (int a = 0; a < p->axes; ++a) {
         if (!p->table[a]) return NVFP4_ERR_INVALID_ARGUMENT;
         if (p->pairs[a] < 1 || p->pairs[a] > dim / 2 || p->rows[a] < 1 || p->rows[a] > INT32_MAX) return NVFP4_ERR_SHAPE;
+        if (p->rows[a] * p->pairs[a] >= (int64_t)1 << 28) return NVFP4_ERR_SHAPE;
         if (!aligned(p->table[a], 8)) return NVFP4_ERR_ALIGNMENT;
         r->first[a] = (int32_t)total;
         r->rows[a] = (int32_t)p->rows[a];
@@ -92,7 +93,7 @@ extern "C" {
 
 nvfp4_status nvfp4_rope_table(float* table, int64_t rows, int32_t pairs, double theta, void* stream) {
     if (!table || rows < 1 || pairs < 1 || !(theta > 0.0) || !isfinite(theta)) return NVFP4_ERR_INVALID_ARGUMENT;
-    if (rows > INT32_MAX / pairs) return NVFP4_ERR_SHAPE;
+    if (rows >= ((int64_t)1 << 28) / pairs) return NVFP4_ERR_SHAPE;
     if (!aligned(table, 8)) return NVFP4_ERR_ALIGNMENT;
     return report_hip(launch_rope_table(reinterpret_cast<float2*>(table), rows, pairs, theta, (hipStream_t)stream));
 }
@@ -164,6 +165,7 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads
     a.group = q_heads / cache->heads;
     a.scale_log2 = scale * 1.44269504088896340736f;
     a.causal = causal_block;
+    a.wide = p.wide;
     a.parts = p.parts;
     a.partial = (float*)workspace;
     return report_hip(launch_attention(a, (hipStream_t)stream));

@@ -50,9 +50,9 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int64_t unit, 
     Tile t;
     t.any = false;
     const SeqArgs& q = a.seqs;
-    const auto base = [&](int64_t b) { return tile_base(clamp64(q.row_start[b], 0, q.M), b, a.group, T); };
-    t.b = uniform64(find_sequence(unit, q.B, base));
-    const RowRange r = row_range(q.row_start[t.b], q.row_start[t.b + 1], q.M);
+    const Located at = locate(q, unit, [&](int64_t row, int64_t b) { return tile_base(row, b, a.group, T); });
+    t.b = at.b;
+    const RowRange r = row_range(at.start, at.end, q.M);
     const int64_t n = r.last - r.first, local = unit - tile_base(r.first, t.b, a.group, T);
     if (local < 0 || local * T >= n * a.group) return t;
     t.any = true;
@@ -60,7 +60,7 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int64_t unit, 
     t.n = (int32_t)n;
     t.first = (int32_t)(local * T);
     t.rows = (int32_t)(n * a.group);
-    t.len = q.lens[t.b];
+    t.len = at.len;
     t.bad = kv_length_bad(t.len, q.table_blocks);
     return t;
 }
@@ -147,6 +147,13 @@ __device__ __forceinline__ bf16x8 values_bf16(uint32_t a, uint32_t b, float scal
     return __builtin_bit_cast(bf16x8, w);
 }
 
+// The value of the lane that holds the other half of this lane's row.
+__device__ __forceinline__ float other_half(float x) {
+    const uint32_t w = __float_as_uint(x);
+    const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
 // The running softmax of a lane's row.
 struct Softmax {
     float m;  // reference maximum, scaled, base 2
@@ -162,7 +169,7 @@ __device__ __forceinline__ void softmax_block(f32x16 s[2], Softmax& st, f32x16 (
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[0][i]);
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[1][i]);
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = fmaxf(top, other_half(top));
     top *= scale_log2;
     if (__any(top > st.m + kSlack)) {
         const float m = fmaxf(st.m, top);
@@ -415,6 +422,187 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     }
 }
 
+// ---------------------------------------------------------------------------
+// Wide tiles: 128 rows to a workgroup of 4 waves, 32 rows each, that go over
+// the same blocks of keys together.  A block is staged in LDS while the one
+// before it is worked on (two buffers, one barrier a block): keys as they are,
+// values as bf16, converted once for all four waves.  Both lie in LDS in the
+// order the lanes read them, 16 neighbouring bytes each, free of conflicts.
+// ---------------------------------------------------------------------------
+constexpr int kWideWaves = 4;
+constexpr int kWideRows = kWideWaves * kRows;
+
+template <int D>
+__global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(AttentionArgs a) {
+    constexpr int kDT = D / 32, kK = D / 64;
+    constexpr int kBytes = kKvBlock * D;
+    constexpr int kPieces = kBytes / 16;                  // 16-byte pieces of a block's keys, and of its values
+    constexpr int kThreads = 64 * kWideWaves;
+    constexpr int kEach = kPieces / kThreads;             // of them a thread's
+    __shared__ __align__(16) uint4 sk[2][kPieces];
+    __shared__ __align__(16) uint4 sv[2][2 * kPieces];    // [k-step][half][dim] of 8 keys
+    __shared__ int nan_key[2][D];                         // first key whose value is a NaN code, by dim
+    __shared__ int nan_any[2];
+    const Tile t = find_tile(a, blockIdx.x, kWideRows);
+    if (!t.any) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int c = lane & 31, h = lane >> 5;
+    const int kv_head = blockIdx.y;
+    const int row0 = t.first + wave * kRows;
+    const Row row = find_row(a, t, row0 + c, kv_head);
+    // keys that the tile's last row and this wave's last row see, and keys that
+    // all rows of the tile and of the wave see
+    const auto limit_of = [&](int rr) { return find_row(a, t, rr, kv_head).limit; };
+    const int tile_seen = limit_of(t.first + kWideRows - 1), seen = row0 < t.rows ? limit_of(row0 + kRows - 1) : 0;
+    const int tile_all = limit_of(t.first), all = limit_of(row0);
+    const int blocks = (tile_seen + kKvBlock - 1) / kKvBlock;
+
+    Query<D> q;
+    load_query<D>(q, a, row);
+    Softmax st = {neg_inf(), 0.0f};
+    f32x16 o[kDT];
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) nan_key[i / D][i % D] = kKvBlock;
+    if (threadIdx.x < 2) nan_any[threadIdx.x] = 0;
+
+    const int32_t* table = a.seqs.table + t.b * a.seqs.ld_table;
+    const auto page_of = [&](int at) -> int64_t {
+        const int64_t p = at < blocks ? __builtin_amdgcn_readfirstlane(table[at]) : -1;
+        return p >= 0 && p < a.cache.blocks ? p : -1;
+    };
+    uint4 kr[kEach], vr[kEach];
+    uint32_t kp = 127, vp = 127;
+    const auto fetch = [&](int64_t page) {
+        if (page >= 0) {
+            const int64_t at = page * a.cache.heads + kv_head;
+            const uint4* pk = reinterpret_cast<const uint4*>(a.cache.k + at * kBytes);
+            const uint4* pv = reinterpret_cast<const uint4*>(a.cache.v + at * kBytes);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                kr[i] = pk[i * kThreads + threadIdx.x];
+                vr[i] = pv[i * kThreads + threadIdx.x];
+            }
+            kp = clamp_power(a.cache.k_power[at]);
+            vp = clamp_power(a.cache.v_power[at]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+        }
+    };
+    // stages the fetched block; edge: some row of the tile does not see all of it
+    const auto stage = [&](int buffer, bool edge) {
+        const float scale = power_value(vp);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = i * kThreads + threadIdx.x;
+            const int d = at % D, piece = at / D;         // piece 2u + half
+            uint4 w = vr[i];
+            if (edge && (fp8_any_nan(w.x) || fp8_any_nan(w.y) || fp8_any_nan(w.z) || fp8_any_nan(w.w))) {
+                // as in the narrow kernel: NaN codes are taken out, and given
+                // back to the rows that see their key
+                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                int lowest = kKvBlock;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (((x[j / 4] >> (8 * (j % 4))) & 0x7Fu) == 0x7Fu) {
+                        const int key = 32 * (piece / 2) + 16 * (j / 8) + 8 * (j / 4 % 2) + 4 * (piece % 2) + j % 4;
+                        lowest = key < lowest ? key : lowest;
+                        x[j / 4] &= ~(0xFFu << (8 * (j % 4)));
+                    }
+                w = make_uint4(x[0], x[1], x[2], x[3]);
+                atomicMin(&nan_key[buffer][d], lowest);
+                nan_any[buffer] = 1;
+            }
+            sk[buffer][at] = kr[i];
+            const int to = (4 * (piece / 2) + piece % 2) * D + d;   // k-step 2u; 2u + 1 is 2 D further on
+            sv[buffer][to] = __builtin_bit_cast(uint4, values_bf16(w.x, w.y, scale));
+            sv[buffer][to + 2 * D] = __builtin_bit_cast(uint4, values_bf16(w.z, w.w, scale));
+        }
+    };
+    __syncthreads();  // the NaN marks are clear
+    int64_t page = page_of(0), next = page_of(1);
+    fetch(page);
+    stage(0, kKvBlock > tile_all);
+    uint32_t kp_now = kp;
+    __syncthreads();
+    for (int at = 0; at < blocks; ++at) {
+        const int b = at & 1, first_key = at * kKvBlock;
+        const bool good = page >= 0;
+        page = next;
+        if (at + 1 < blocks) fetch(page);
+        next = page_of(at + 2);
+        if (first_key < seen) {
+            f32x16 s[2];
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                s[tt] = f32x16{};
+#pragma unroll
+                for (int k = 0; k < kK; ++k) {
+                    const i32x8 f = pieces(sk[b][(4 * k + 2 * h) * kKvBlock + tt * 32 + c],
+                                           sk[b][(4 * k + 2 * h + 1) * kKvBlock + tt * 32 + c]);
+                    s[tt] = mul_scores(f, q.hi[k], s[tt], (int)kp_now, q.power_hi);
+                    s[tt] = mul_scores(f, q.lo[k], s[tt], (int)kp_now, q.power_lo);
+                }
+            }
+            if (!good) {
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[tt][i] = quiet_nan();
+            }
+            if (first_key + kKvBlock > all) mask_scores(s, row.limit - first_key);
+            bf16x8 p[4];
+            softmax_block<kDT>(s, st, o, a.scale_log2, p);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                for (int d = 0; d < kDT; ++d)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, sv[b][(2 * ks + h) * D + 32 * d + c]), p[ks], o[d], 0, 0, 0);
+        }
+        if (first_key + kKvBlock > tile_all && nan_any[b]) {  // the same for all waves
+            if (first_key < seen) {
+#pragma unroll
+                for (int d = 0; d < kDT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int key = nan_key[b][32 * d + 8 * (i / 4) + 4 * h + i % 4];
+                        if (key < kKvBlock && key < row.limit - first_key) o[d][i] = quiet_nan();
+                    }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < D; i += kThreads) nan_key[b][i] = kKvBlock;
+            if (threadIdx.x == 0) nan_any[b] = 0;
+        }
+        if (at + 1 < blocks) stage(1 - b, first_key + 2 * kKvBlock > tile_all);
+        kp_now = kp;
+        __syncthreads();
+    }
+    if (!row.valid) return;
+
+    // no key: 0; a length that the table cannot hold, or a query that is not
+    // finite: NaN
+    float l = st.l + __shfl_xor(st.l, 32);
+    if (q.nan && row.limit > 0) l = quiet_nan();
+    const float inv = t.bad ? quiet_nan() : l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* out = a.out.data + row.token * a.out.row + row.head * a.out.head;
+#pragma unroll
+    for (int d = 0; d < kDT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            // this half has dims 8 i + 4 h .. + 3 of each i: the halves trade, and
+            // each stores 8 dims
+            uint32_t x0 = pack_bf16x2(o[d][4 * i] * inv, o[d][4 * i + 1] * inv);
+            uint32_t x1 = pack_bf16x2(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv);
+            uint32_t y0 = pack_bf16x2(o[d][4 * i + 4] * inv, o[d][4 * i + 5] * inv);
+            uint32_t y1 = pack_bf16x2(o[d][4 * i + 6] * inv, o[d][4 * i + 7] * inv);
+            const auto r0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+            const auto r1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+            *reinterpret_cast<uint4*>(out + 32 * d + 8 * i + 8 * h) = make_uint4(r0[0], r1[0], r0[1], r1[1]);
+        }
+}
+
 // Joins the parts of each row; rows that no sequence has are left alone.  A
 // wave takes a row, a lane D / 64 dims of it.
 template <int D>
@@ -459,13 +647,19 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
     tiles = tiles < B ? B : tiles;
     const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock;
     const int64_t want = 512 / (tiles * kv_heads), most = blocks / 4;
-    p.parts = (int32_t)clamp64(want < most ? want : most, 1, 64);
+    p.wide = M * group >= 96 * B;
+    p.parts = p.wide ? 1 : (int32_t)clamp64(want < most ? want : most, 1, 64);
     p.workspace_bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)(M * q_heads) * (size_t)(dim + 2) * sizeof(float);
     return p;
 }
 
 template <int D>
 static void attention_of(const AttentionArgs& a, hipStream_t s) {
+    if (a.wide) {
+        const dim3 grid((unsigned)tile_units(a.seqs.M, a.seqs.B, a.group, kWideRows), (unsigned)a.cache.heads);
+        attention_wide_kernel<D><<<grid, dim3(64 * kWideWaves), 0, s>>>(a);
+        return;
+    }
     const dim3 grid((unsigned)tile_units(a.seqs.M, a.seqs.B, a.group, kRows), (unsigned)a.cache.heads, (unsigned)a.parts);
     attention_narrow_kernel<D><<<grid, dim3(64 * kNarrowWaves), 0, s>>>(a);
     if (a.parts > 1) {

@@ -10,20 +10,48 @@ namespace {
 // Rotation of a pair by (cos, sin): y1 = x1 c - x2 s, y2 = x2 c + x1 s, each
 // product and sum a binary32 operation, the result rounded once to bf16.
 // ---------------------------------------------------------------------------
-// (cos, sin) of pair i of the row whose positions `pos` points to.  A position
-// outside its table gives NaN, and the table is not read.
-__device__ __forceinline__ float2 rope_turn(const RopeArgs& r, const int32_t* pos, int i) {
+// The axes as values of their own: held in an array, picking one by a pair's
+// index would put the array into scratch memory.
+struct Axes {
+    int32_t first1, first2, first3;      // first pairs of axes 1 to 3
+    int32_t n0, n1, n2, n3;              // pairs
+    int32_t rows0, rows1, rows2, rows3;  // positions covered
+    int64_t to1, to2, to3;               // bytes from the first table to the others
+    const char* table;
+};
+__device__ __forceinline__ Axes axes_of(const RopeArgs& r) {
+    const auto to = [&](int a) { return (int64_t)((uintptr_t)r.table[a] - (uintptr_t)r.table[0]); };
+    return Axes{r.first[1], r.first[2], r.first[3],
+                r.first[1], r.first[2] - r.first[1], r.first[3] - r.first[2], r.first[4] - r.first[3],
+                r.rows[0],  r.rows[1], r.rows[2], r.rows[3],
+                to(1), to(2), to(3), reinterpret_cast<const char*>(r.table[0])};
+}
+// A row's positions, loaded once for all its pairs.
+struct Positions {
+    int32_t p0, p1, p2, p3;
+};
+__device__ __forceinline__ Positions positions_of(const RopeArgs& r, int64_t row) {
+    const int32_t* src = r.positions + row * r.ld_positions;
+    const int last = r.axes - 1;
+    return Positions{src[0], src[last < 1 ? last : 1], src[last < 2 ? last : 2], src[last < 3 ? last : 3]};
+}
+// (cos, sin) of pair i of the rotated ones: the axis is picked with selects
+// (the first pairs of axes not in use are past every i) and one load follows,
+// so that a thread's loads are all in flight together.  A position outside its
+// table gives NaN (an entry inside is loaded in its place).
+__device__ __forceinline__ float2 rope_turn(const Axes x, const Positions pos, int i) {
+    const bool a1 = i >= x.first1, a2 = i >= x.first2, a3 = i >= x.first3;
+    const int32_t p = a3 ? pos.p3 : a2 ? pos.p2 : a1 ? pos.p1 : pos.p0;
+    const int32_t rows = a3 ? x.rows3 : a2 ? x.rows2 : a1 ? x.rows1 : x.rows0;
+    const int32_t n = a3 ? x.n3 : a2 ? x.n2 : a1 ? x.n1 : x.n0;
+    const int32_t first = a3 ? x.first3 : a2 ? x.first2 : a1 ? x.first1 : 0;
+    const int64_t to = a3 ? x.to3 : a2 ? x.to2 : a1 ? x.to1 : 0;
+    const bool ok = (uint32_t)p < (uint32_t)rows;
+    // a table is below 2^31 bytes: the offset inside it is a 32-bit one
+    const uint32_t at = (ok ? (uint32_t)(p * n + (i - first)) : 0u) * (uint32_t)sizeof(float2);
+    const float2 t = *reinterpret_cast<const float2*>(x.table + to + at);
     const float nan = __uint_as_float(0x7FC00000u);
-    float2 t = make_float2(nan, nan);
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        if (i >= r.first[a] && i < r.first[a + 1]) {
-            const int32_t p = pos[a];
-            if (p >= 0 && p < r.rows[a])
-                t = r.table[a][(int64_t)p * (r.first[a + 1] - r.first[a]) + (i - r.first[a])];
-        }
-    }
-    return t;
+    return make_float2(ok ? t.x : nan, ok ? t.y : nan);
 }
 
 __global__ void rope_table_kernel(float2* table, int64_t n, int32_t pairs, double theta) {
@@ -35,58 +63,86 @@ __global__ void rope_table_kernel(float2* table, int64_t n, int32_t pairs, doubl
     table[i] = make_float2((float)cos(angle), (float)sin(angle));
 }
 
-// A thread owns 16 dims of a head, either 8 rotated pairs or 16 dims that pass
-// through, looks up its 8 (cos, sin) once and goes over the row's heads with
-// them: the table is read once per row and not once per head.
+// A workgroup takes a few rows: it looks each row's angles up once, into LDS,
+// and then goes over the rows' units of 16 dims (8 rotated pairs, or 16 dims
+// that pass through) in the order they lie in.
 struct RopeGeo {
     int64_t M;
-    int32_t heads, units;  // 16-dim units per head
-    int32_t slots, rows;   // heads and rows that a workgroup takes at once
+    int32_t heads, units;    // 16-dim units per head
+    int32_t rows;            // rows of a workgroup
+    int32_t du, dh, dr;      // 256 units further on: so many units, heads and rows
 };
+constexpr int kRopeTurns = 1024;  // angles a workgroup holds
+
+// Rotates the 16 values of a unit: two times 8 dims.
+template <bool SPLIT>
+__device__ __forceinline__ void rope_unit(uint4& a, uint4& b, const float2 (&t)[8]) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if constexpr (SPLIT) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 c0 = t[2 * j], c1 = t[2 * j + 1];
+            const float p0 = bf16_lo(w[j]), p1 = bf16_hi(w[j]), q0 = bf16_lo(w[4 + j]), q1 = bf16_hi(w[4 + j]);
+            w[j] = pack_bf16x2(p0 * c0.x - q0 * c0.y, p1 * c1.x - q1 * c1.y);
+            w[4 + j] = pack_bf16x2(q0 * c0.x + p0 * c0.y, q1 * c1.x + p1 * c1.y);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float p = bf16_lo(w[j]), q = bf16_hi(w[j]);
+            w[j] = pack_bf16x2(p * t[j].x - q * t[j].y, q * t[j].x + p * t[j].y);
+        }
+    }
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+    b = make_uint4(w[4], w[5], w[6], w[7]);
+}
 
 template <bool SPLIT>
 __global__ __launch_bounds__(256) void rope_kernel(HeadsIn x, HeadsOut out, RopeArgs r, RopeGeo g) {
-    const int u = threadIdx.x % g.units;
-    const int rest = threadIdx.x / g.units;
-    const int slot = rest % g.slots, in = rest / g.slots;
-    const int64_t row = (int64_t)blockIdx.x * g.rows + in;
-    if (in >= g.rows || row >= g.M) return;
-    const bool turns = u < r.total / 8;
-    const int d0 = SPLIT && turns ? 8 * u : 16 * u;
-    const int d1 = SPLIT && turns ? r.total + 8 * u : 16 * u + 8;
-    const uint16_t* src = x.data + row * x.row;
-    uint16_t* dst = out.data + row * out.row;
-    float2 t[8];
-    if (turns) {
-        const int32_t* pos = r.positions + row * r.ld_positions;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = rope_turn(r, pos, 8 * u + j);
+    __shared__ __align__(16) float2 turn[kRopeTurns];
+    const int64_t row0 = (int64_t)blockIdx.x * g.rows;
+    const int rows = (int)(g.M - row0 < g.rows ? g.M - row0 : g.rows);
+    const int turning = r.total / 8;
+    int u = threadIdx.x % g.units, h = threadIdx.x / g.units % g.heads, in = threadIdx.x / g.units / g.heads;
+    // the unit's two times 8 dims, in elements from the head's first
+    const auto low = [&](int unit) { return SPLIT && unit < turning ? 8 * unit : 16 * unit; };
+    const auto high = [&](int unit) { return SPLIT && unit < turning ? r.total + 8 * unit : 16 * unit + 8; };
+    const auto load = [&](uint4& a, uint4& b) {
+        const uint16_t* p = x.data + (row0 + in) * x.row + h * x.head;
+        a = *reinterpret_cast<const uint4*>(p + low(u));
+        b = *reinterpret_cast<const uint4*>(p + high(u));
+    };
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (in < rows) load(a, b);  // on its way while the angles are looked up
+    const Axes axes = axes_of(r);
+    for (int i = threadIdx.x; i < rows * r.total; i += 256) {
+        const int j = i / r.total;
+        turn[i] = rope_turn(axes, positions_of(r, row0 + j), i - j * r.total);
     }
-    for (int h = slot; h < g.heads; h += g.slots) {
-        uint4 a = *reinterpret_cast<const uint4*>(src + h * x.head + d0);
-        uint4 b = *reinterpret_cast<const uint4*>(src + h * x.head + d1);
-        if (turns) {
-            uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            if constexpr (SPLIT) {
+    __syncthreads();
+    while (in < rows) {
+        const int u0 = u;
+        const float2* t = turn + in * r.total + 8 * u;
+        uint16_t* p = out.data + (row0 + in) * out.row + h * out.head;
+        uint4 a0 = a, b0 = b;
+        u += g.du;
+        h += g.dh;
+        in += g.dr;
+        if (u >= g.units) u -= g.units, ++h;
+        if (h >= g.heads) h -= g.heads, ++in;
+        if (in < rows) load(a, b);
+        if (u0 < turning) {
+            float2 c[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 c0 = t[2 * j], c1 = t[2 * j + 1];
-                    const float p0 = bf16_lo(w[j]), p1 = bf16_hi(w[j]), q0 = bf16_lo(w[4 + j]), q1 = bf16_hi(w[4 + j]);
-                    w[j] = pack_bf16x2(p0 * c0.x - q0 * c0.y, p1 * c1.x - q1 * c1.y);
-                    w[4 + j] = pack_bf16x2(q0 * c0.x + p0 * c0.y, q1 * c1.x + p1 * c1.y);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float p = bf16_lo(w[j]), q = bf16_hi(w[j]);
-                    w[j] = pack_bf16x2(p * t[j].x - q * t[j].y, q * t[j].x + p * t[j].y);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float4 w = reinterpret_cast<const float4*>(t)[i];
+                c[2 * i] = make_float2(w.x, w.y);
+                c[2 * i + 1] = make_float2(w.z, w.w);
             }
-            a = make_uint4(w[0], w[1], w[2], w[3]);
-            b = make_uint4(w[4], w[5], w[6], w[7]);
+            rope_unit<SPLIT>(a0, b0, c);
         }
-        *reinterpret_cast<uint4*>(dst + h * out.head + d0) = a;
-        *reinterpret_cast<uint4*>(dst + h * out.head + d1) = b;
+        *reinterpret_cast<uint4*>(p + low(u0)) = a0;
+        *reinterpret_cast<uint4*>(p + high(u0)) = b0;
     }
 }
 
@@ -132,12 +188,11 @@ struct BlockUnit {
 __device__ __forceinline__ BlockUnit block_unit(const SeqArgs& q, int64_t blocks, int64_t unit) {
     BlockUnit u;
     u.any = false;
-    const auto base = [&](int64_t b) { return block_base(clamp64(q.row_start[b], 0, q.M), b); };
-    const int64_t b = uniform64(find_sequence(unit, q.B, base));
-    const RowRange r = row_range(q.row_start[b], q.row_start[b + 1], q.M);
-    const int64_t n = r.last - r.first, local = unit - block_base(r.first, b);
+    const Located s = locate(q, unit, [](int64_t row, int64_t b) { return block_base(row, b); });
+    const RowRange r = row_range(s.start, s.end, q.M);
+    const int64_t n = r.last - r.first, local = unit - block_base(r.first, s.b);
     if (n <= 0 || local < 0) return u;
-    u.len = q.lens[b];
+    u.len = s.len;
     u.first = u.len - n;
     u.row0 = r.first;
     const int64_t at = floor_div(u.first, kKvBlock) + local;
@@ -146,8 +201,11 @@ __device__ __forceinline__ BlockUnit block_unit(const SeqArgs& q, int64_t blocks
     u.start = at * kKvBlock;
     u.bad_len = kv_length_bad(u.len, q.table_blocks);
     u.good = at >= 0 && at < q.table_blocks && !u.bad_len;
-    u.page = u.good ? q.table[b * q.ld_table + at] : 0;
-    if (u.page < 0 || u.page >= blocks) u.good = false;
+    u.page = u.good ? q.table[s.b * q.ld_table + at] : 0;
+    if (u.page < 0 || u.page >= blocks) {
+        u.good = false;
+        u.page = 0;
+    }
     return u;
 }
 
@@ -204,16 +262,24 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
     __shared__ uint32_t red2[2][Own::kWaves];
     __shared__ __align__(16) uint32_t stage[kBytes / 4];
     const BlockUnit u = block_unit(q, c.blocks, blockIdx.x);
-    if (!u.any || !u.good) return;
+    if (!u.any) return;
     const Own o;
     // positions of the block that are new: [lo, hi); those before lo are kept
     const int lo = (int)(u.first > u.start ? u.first - u.start : 0);
     const int hi = (int)(u.len - u.start < kKvBlock ? u.len - u.start : kKvBlock);
     const bool full = lo == 0 && hi == kKvBlock;
-    const int64_t row = u.row0 + (u.start - u.first) + o.t0;  // of position t0, where that is new
+    if (hi <= 0) return;  // before the sequence
+    // this thread's positions' rows; where one is not new, the sequence's first
+    // row is loaded in its place and not used
     bool fresh[4];
+    int64_t at_row[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fresh[j] = o.t0 + j >= lo && o.t0 + j < hi;
+    for (int j = 0; j < 4; ++j) {
+        fresh[j] = o.t0 + j >= lo && o.t0 + j < hi;
+        at_row[j] = fresh[j] ? u.row0 + (u.start - u.first) + o.t0 + j : u.row0;
+    }
+
+    const bool any = fresh[0] || fresh[1] || fresh[2] || fresh[3];
 
     // this thread's angles, kept over the heads
     constexpr int kTurns = MODE == ROPE_SPLIT ? 8 : 4;
@@ -222,6 +288,7 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
     int partner = 0;
     if constexpr (MODE != ROPE_NONE) {
         const int lane = threadIdx.x & 63;
+        const Axes axes = axes_of(r);
         int pair0 = 4 * o.g;
         turns = 8 * o.g < 2 * r.total;
         partner = lane;
@@ -232,11 +299,11 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int32_t* pos = r.positions + (row + j) * r.ld_positions;
+            if (!any) break;  // a short write's other threads look nothing up
+            const Positions pos = positions_of(r, at_row[j]);
 #pragma unroll
             for (int i = 0; i < kTurns; ++i) {
-                float2 t = make_float2(1.0f, 0.0f);
-                if (turns && fresh[j]) t = rope_turn(r, pos, pair0 + i);
+                const float2 t = rope_turn(axes, pos, turns ? pair0 + i : 0);
                 cs[j][i] = t.x;
                 // y1 = x1 c + x2 (-s): the sign goes with the sine
                 sn[j][i] = MODE == ROPE_SPLIT && 8 * o.g < r.total ? -t.y : t.y;
@@ -255,12 +322,21 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (fresh[j]) {
-                a = *reinterpret_cast<const uint4*>(kx.data + (row + j) * kx.row + h * kx.head + 8 * o.g);
-                b = *reinterpret_cast<const uint4*>(vx.data + (row + j) * vx.row + h * vx.head + 8 * o.g);
+            if (any) {
+                a = *reinterpret_cast<const uint4*>(kx.data + at_row[j] * kx.row + h * kx.head + 8 * o.g);
+                b = *reinterpret_cast<const uint4*>(vx.data + at_row[j] * vx.row + h * vx.head + 8 * o.g);
             }
             kw[j][0] = a.x, kw[j][1] = a.y, kw[j][2] = a.z, kw[j][3] = a.w;
             vw[j][0] = b.x, vw[j][1] = b.y, vw[j][2] = b.z, vw[j][3] = b.w;
+        }
+        // the rows are on their way while the block is looked up
+        if (!u.good) return;
+        // a part of a block: its values' dwords, of which this thread has some
+        uint32_t* const vp = reinterpret_cast<uint32_t*>(vb + o.piece * kPieceBytes + 8 * o.g * 16 + 4 * o.em);
+        uint32_t was[8] = {};
+        if (!full && o.t0 < hi) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d) was[d] = vp[4 * d];
         }
         uint32_t had_k = 0, had_v = 0;
         if (lo > 0) {
@@ -285,6 +361,15 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
                     const float y0 = bf16_lo(kw[j][i]) * cs[j][2 * i] + bf16_lo(p) * sn[j][2 * i];
                     const float y1 = bf16_hi(kw[j][i]) * cs[j][2 * i + 1] + bf16_hi(p) * sn[j][2 * i + 1];
                     kw[j][i] = turns ? pack_bf16x2(y0, y1) : kw[j][i];
+                }
+        }
+        if (!full) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    kw[j][i] = fresh[j] ? kw[j][i] : 0u;
+                    vw[j][i] = fresh[j] ? vw[j][i] : 0u;
                 }
         }
         uint32_t mk = 0, mv = 0;
@@ -398,10 +483,9 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
             if (keep != 0xFFFFFFFFu || (grew_v && old)) {
 #pragma unroll
                 for (int d = 0; d < 8; ++d) {
-                    uint32_t* p = reinterpret_cast<uint32_t*>(vb + o.piece * kPieceBytes + (8 * o.g + d) * 16 + 4 * o.em);
-                    uint32_t w = keep ? *p : 0u;
+                    uint32_t w = was[d];
                     if (grew_v) w = (shrink4(w, fv) & old) | (w & ~old);
-                    *p = (w & keep) | (vc[d] & ~keep);
+                    vp[4 * d] = (w & keep) | (vc[d] & ~keep);
                 }
             }
         }
@@ -447,27 +531,27 @@ __global__ __launch_bounds__(2 * D) void kv_read_kernel(CacheArgs c, SeqArgs q, 
         const uint8_t* const vb = c.v + at * kBytes;
         const float sk = power_value(clamp_power(c.k_power[at])), sv = power_value(clamp_power(c.v_power[at]));
         // keys: a lane takes whole 16-byte pieces, D / 16 lanes a position
-        uint4 kw[2], vw[2];
         constexpr int kPieces = D / 16;
         const int piece = threadIdx.x % kPieces, t1 = threadIdx.x / kPieces;  // positions t1 and t1 + 32
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            kw[i] = *reinterpret_cast<const uint4*>(kb + piece * (kKvBlock * 16) + (t1 + 32 * i) * 16);
-            vw[i] = reinterpret_cast<const uint4*>(vb)[wave * 128 + i * 64 + lane];
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int s = wave * 128 + i * 64 + lane;
-            reinterpret_cast<uint4*>(stage)[s ^ ((s >> 3) & 7)] = vw[i];
-            const int t = t1 + 32 * i;
-            if (t >= lo && t < hi) {
-                uint4* p = reinterpret_cast<uint4*>(kx.data + (row + t) * kx.row + h * kx.head + 16 * piece);
-                p[0] = make_uint4(fp8_to_bf16x2<false>(kw[i].x, sk), fp8_to_bf16x2<true>(kw[i].x, sk),
-                                  fp8_to_bf16x2<false>(kw[i].y, sk), fp8_to_bf16x2<true>(kw[i].y, sk));
-                p[1] = make_uint4(fp8_to_bf16x2<false>(kw[i].z, sk), fp8_to_bf16x2<true>(kw[i].z, sk),
-                                  fp8_to_bf16x2<false>(kw[i].w, sk), fp8_to_bf16x2<true>(kw[i].w, sk));
-            }
-        }
+        const uint4* const kp = reinterpret_cast<const uint4*>(kb) + piece * kKvBlock + t1;
+        const int s1 = wave * 128 + lane;
+        const uint4 v0 = reinterpret_cast<const uint4*>(vb)[s1], v1 = reinterpret_cast<const uint4*>(vb)[s1 + 64];
+        uint4 k0 = kp[0], k1 = kp[32];
+        // all loads are issued here: without this the compiler moves the keys'
+        // into the branches below, one wait for memory after the other
+        asm volatile("" : "+v"(k0.x), "+v"(k0.y), "+v"(k0.z), "+v"(k0.w), "+v"(k1.x), "+v"(k1.y), "+v"(k1.z), "+v"(k1.w));
+        reinterpret_cast<uint4*>(stage)[s1 ^ ((s1 >> 3) & 7)] = v0;
+        reinterpret_cast<uint4*>(stage)[(s1 + 64) ^ ((s1 >> 3) & 7)] = v1;
+        const auto store_key = [&](int t, uint4 w) {
+            if (t < lo || t >= hi) return;
+            uint4* p = reinterpret_cast<uint4*>(kx.data + (row + t) * kx.row + h * kx.head + 16 * piece);
+            p[0] = make_uint4(fp8_to_bf16x2<false>(w.x, sk), fp8_to_bf16x2<true>(w.x, sk),
+                              fp8_to_bf16x2<false>(w.y, sk), fp8_to_bf16x2<true>(w.y, sk));
+            p[1] = make_uint4(fp8_to_bf16x2<false>(w.z, sk), fp8_to_bf16x2<true>(w.z, sk),
+                              fp8_to_bf16x2<false>(w.w, sk), fp8_to_bf16x2<true>(w.w, sk));
+        };
+        store_key(t1, k0);
+        store_key(t1 + 32, k1);
         wave_lds_sync();
         // values: 4 positions of 8 dims, dword d holding dim d of all four
         const int s0 = o.piece * D + 8 * o.g;
@@ -518,16 +602,16 @@ hipError_t launch_rope(const HeadsIn& x, const HeadsOut& out, int64_t M, int32_t
     g.M = M;
     g.heads = heads;
     g.units = dim / 16;
-    const int slots = 256 / g.units;  // heads' worth of threads
-    if (heads <= slots) {
-        g.slots = heads;
-        g.rows = slots / heads;
-    } else {
-        const int turns = (heads + slots - 1) / slots;
-        g.slots = (heads + turns - 1) / turns;  // the same share each turn
-        g.rows = 1;
-    }
-    const dim3 grid((unsigned)((M + g.rows - 1) / g.rows)), block((unsigned)((g.units * g.slots * g.rows + 63) / 64 * 64));
+    // one unit a thread at least; 4 rows where that leaves 8 workgroups for
+    // each of 256 CUs
+    const int64_t per_row = (int64_t)heads * g.units;
+    int64_t rows = (256 + per_row - 1) / per_row;
+    if (rows < 4 && M >= 4 * 2048) rows = 4;
+    g.rows = (int32_t)clamp64(rows, 1, kRopeTurns / r.total);
+    g.du = 256 % g.units;
+    g.dh = 256 / g.units % heads;
+    g.dr = 256 / g.units / heads;
+    const dim3 grid((unsigned)((M + g.rows - 1) / g.rows)), block(256);
     (void)hipGetLastError();
     if (r.split)
         rope_kernel<true><<<grid, block, 0, s>>>(x, out, r, g);

@@ -22,28 +22,44 @@ __device__ __forceinline__ uint32_t power_for(uint32_t amax16) {
 }
 __device__ __forceinline__ uint32_t clamp_power(uint32_t b) { return b < 1u ? 1u : b > 254u ? 254u : b; }
 
-// The sequence whose units start at or before `unit`, base(b) nondecreasing.
-// All 64 lanes take part: each round they look at 64 places at once.
-template <class Base>
-__device__ __forceinline__ int64_t find_sequence(int64_t unit, int64_t B, Base base) {
-    const int lane = threadIdx.x & 63;
-    int64_t lo = 0, n = B;
-    while (n > 1) {
-        const int64_t stride = (n + 63) / 64;
-        const int64_t at = lane * stride;
-        const bool ok = at < n && (lane == 0 || base(lo + at) <= unit);
-        const uint64_t seen = __ballot(ok);
-        const int64_t skip = (63 - __builtin_clzll(seen)) * stride;
-        lo += skip;
-        n = n - skip < stride ? n - skip : stride;
-    }
-    return lo;
-}
-
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
     return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// The sequence whose units start at or before `unit`, with its rows and length.
+// base(row, b), the first unit of a sequence whose first row it is, is
+// nondecreasing.  All 64 lanes take part.  Below 64 sequences everything comes
+// from one pair of loads, so that a short kernel waits for memory once and not
+// three times; above, each round looks at 64 places at once.
+struct Located {
+    int64_t b;
+    int64_t start, end;  // row_start[b], row_start[b + 1] as they stand
+    int64_t len;
+};
+template <class Base>
+__device__ __forceinline__ Located locate(const SeqArgs& q, int64_t unit, Base base) {
+    const int lane = threadIdx.x & 63;
+    if (q.B < 64) {
+        const int32_t start = q.row_start[lane < q.B ? lane : q.B];
+        const int32_t len = q.lens[lane < q.B ? lane : 0];
+        const bool ok = lane < q.B && (lane == 0 || base(clamp64(start, 0, q.M), lane) <= unit);
+        const int b = 63 - __builtin_clzll(__ballot(ok));
+        return Located{b, __builtin_amdgcn_readlane(start, b), __builtin_amdgcn_readlane(start, b + 1),
+                       __builtin_amdgcn_readlane(len, b)};
+    }
+    int64_t lo = 0, n = q.B;
+    while (n > 1) {
+        const int64_t stride = (n + 63) / 64;
+        const int64_t at = lane * stride;
+        const bool ok = at < n && (lane == 0 || base(clamp64(q.row_start[lo + at], 0, q.M), lo + at) <= unit);
+        const int64_t skip = (63 - __builtin_clzll(__ballot(ok))) * stride;
+        lo += skip;
+        n = n - skip < stride ? n - skip : stride;
+    }
+    lo = uniform64(lo);
+    return Located{lo, q.row_start[lo], q.row_start[lo + 1], q.lens[lo]};
 }
 
 // Orders a wave's own LDS writes before its lanes' reads of one another's.

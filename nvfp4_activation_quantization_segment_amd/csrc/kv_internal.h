@@ -61,6 +61,7 @@ struct AttentionArgs {
     int32_t group;     // query heads per key/value head
     float scale_log2;  // scale * log2(e)
     int32_t causal;
+    int32_t wide;      // 128 rows to a workgroup (else 32)
     int32_t parts;     // pieces the keys of a row tile are cut into
     float* partial;    // parts x (M q_heads) x D, then parts x (M q_heads) x 2
 };
@@ -75,6 +76,7 @@ hipError_t launch_kv_read(const CacheArgs& c, const SeqArgs& q, const HeadsOut& 
 
 // How an attention call is cut: from sizes the host knows.
 struct AttentionPlan {
+    bool wide;
     int32_t parts;
     size_t workspace_bytes;
 };

@@ -48,7 +48,7 @@ HEADS_ERRORS = [(dict(data=None), INVALID), (dict(row=-8), INVALID), (dict(head=
 OVERLAPS = [dict(row=1016), dict(head=120), dict(row=0), dict(head=0), dict(row=128, head=1272)]
 ROPE_ERRORS = [(dict(axes=0), SHAPE), (dict(axes=5), SHAPE), (dict(positions=None), INVALID), (dict(ld=1), INVALID),
                (dict(table=None), INVALID), (dict(pairs=(0, 8)), SHAPE), (dict(pairs=(4, 8)), SHAPE), (dict(pairs=(64, 8)), SHAPE),
-               (dict(rows=(0, 4)), SHAPE), (dict(rows=(1 << 31, 4)), SHAPE), (dict(table=FAKE + 4), ALIGNMENT),
+               (dict(rows=(0, 4)), SHAPE), (dict(rows=(1 << 31, 4)), SHAPE), (dict(rows=(1 << 25, 4)), SHAPE), (dict(table=FAKE + 4), ALIGNMENT),
                (dict(positions=FAKE + 2), ALIGNMENT)]
 CACHE_ERRORS = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(kp=None), INVALID), (dict(vp=None), INVALID),
                 (dict(blocks=0), INVALID), (dict(heads=0), INVALID), (dict(dim=96), SHAPE), (dict(dim=256), SHAPE),
