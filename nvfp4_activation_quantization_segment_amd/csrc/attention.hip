@@ -80,7 +80,7 @@ __device__ __forceinline__ Row find_row(const AttentionArgs& a, const Tile& t, i
     const int32_t i = at / a.group;
     r.token = t.row0 + i;
     r.head = kv_head * a.group + (at - i * a.group);
-    r.limit = t.bad ? 0 : (int32_t)kv_limit(t.len - t.n + i, t.len, a.causal);
+    r.limit = t.bad ? 0 : kv_limit((int32_t)t.len - t.n + i, (int32_t)t.len, a.causal);
     return r;
 }
 
@@ -103,8 +103,8 @@ __device__ __forceinline__ void load_query(Query<D>& f, const AttentionArgs& a, 
     for (int k = 0; k < D / 64; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (r.valid) x = *reinterpret_cast<const uint4*>(p + 64 * k + 32 * h + 8 * j);
+            u32x4 x = u32x4{0, 0, 0, 0};
+            if (r.valid) x = *reinterpret_cast<const u32x4*>(p + 64 * k + 32 * h + 8 * j);
             w[k][4 * j] = x.x, w[k][4 * j + 1] = x.y, w[k][4 * j + 2] = x.z, w[k][4 * j + 3] = x.w;
             m = pk_max_u16(m, pk_max_u16(pk_max_u16(mag2(x.x), mag2(x.y)), pk_max_u16(mag2(x.z), mag2(x.w))));
         }
@@ -133,7 +133,7 @@ __device__ __forceinline__ void load_query(Query<D>& f, const AttentionArgs& a, 
         }
 }
 
-__device__ __forceinline__ i32x8 pieces(uint4 a, uint4 b) {
+__device__ __forceinline__ i32x8 pieces(u32x4 a, u32x4 b) {
     return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
@@ -142,8 +142,8 @@ __device__ __forceinline__ f32x16 mul_scores(i32x8 k, i32x8 q, f32x16 acc, int k
 }
 
 __device__ __forceinline__ bf16x8 values_bf16(uint32_t a, uint32_t b, float scale) {
-    const uint4 w = make_uint4(fp8_to_bf16x2<false>(a, scale), fp8_to_bf16x2<true>(a, scale),
-                               fp8_to_bf16x2<false>(b, scale), fp8_to_bf16x2<true>(b, scale));
+    const u32x4 w = u32x4{fp8_to_bf16x2<false>(a, scale), fp8_to_bf16x2<true>(a, scale),
+                               fp8_to_bf16x2<false>(b, scale), fp8_to_bf16x2<true>(b, scale)};
     return __builtin_bit_cast(bf16x8, w);
 }
 
@@ -160,10 +160,10 @@ struct Softmax {
     float l;  // sum of this half's p
 };
 
-// One block's scores (two tiles of 32 keys) -> probabilities in bf16, the
-// second operands of the products with the values.
+// Takes a block's scores (two tiles of 32 keys) into the running maximum,
+// rescaling the sum and the output where it passes the reference by kSlack.
 template <int NO>
-__device__ __forceinline__ void softmax_block(f32x16 s[2], Softmax& st, f32x16 (&o)[NO], float scale_log2, bf16x8 p[4]) {
+__device__ __forceinline__ void raise_maximum(const f32x16 (&s)[2], Softmax& st, f32x16 (&o)[NO], float scale_log2) {
     float top = s[0][0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[0][i]);
@@ -181,35 +181,39 @@ __device__ __forceinline__ void softmax_block(f32x16 s[2], Softmax& st, f32x16 (
             for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
         st.m = m;
     }
-    const float ref = st.m == neg_inf() ? 0.0f : st.m;
-    float sum = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][8 * k + 2 * i], scale_log2, -ref));
-                const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][8 * k + 2 * i + 1], scale_log2, -ref));
-                sum += x;
-                sum += y;
-                w[i] = pack_bf16x2(x, y);
-            }
-            p[2 * t + k] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
-        }
-    st.l += sum;
 }
+
+// The probabilities of k-step k (16 keys) in bf16, a second operand of the
+// products with the values.
+__device__ __forceinline__ bf16x8 probabilities(const f32x16 (&s)[2], int k, Softmax& st, float scale_log2, float ref) {
+    uint32_t w[4];
+    float sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k / 2][8 * (k % 2) + 2 * i], scale_log2, -ref));
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k / 2][8 * (k % 2) + 2 * i + 1], scale_log2, -ref));
+        sum[i] = x + y;
+        w[i] = pack_bf16x2(x, y);
+    }
+    st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+}
+__device__ __forceinline__ float reference_of(const Softmax& st) { return st.m == neg_inf() ? 0.0f : st.m; }
+
+// The power byte of a block's keys; the byte that stands for NaN where the block
+// does not exist, so that whoever sees it gets NaN.
+__device__ __forceinline__ int key_power(uint32_t loaded, bool good) { return good ? (int)clamp_power(loaded) : 255; }
 
 // Scores of keys past the row's limit become -inf.  left: the limit counted
 // from the block's first key.
-__device__ __forceinline__ void mask_scores(f32x16 s[2], int32_t left) {
-    const int h = (threadIdx.x & 63) >> 5;
+__device__ __forceinline__ void mask_scores(f32x16 (&s)[2], int32_t left) {
+    // against constants: 32 keys by name would be 32 registers held in the loop
+    const int mine = left - 4 * (int)((threadIdx.x & 63) >> 5);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (32 * t + 8 * (i / 4) + 4 * h + i % 4 >= left) s[t][i] = neg_inf();
+            if (32 * t + 8 * (i / 4) + i % 4 >= mine) s[t][i] = neg_inf();
 }
 
 // ---------------------------------------------------------------------------
@@ -250,71 +254,76 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
 #pragma unroll
     for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
 
+    // Table entries and powers are loaded like the keys, a block ahead, and are
+    // looked at when they are needed: a wait for one of them would be a wait for
+    // every load before it.
     const int32_t* table = a.seqs.table + t.b * a.seqs.ld_table;
-    // page of a block, -1 where there is none
-    const auto page_of = [&](int64_t at) -> int64_t {
-        const int64_t p = at < range.last ? __builtin_amdgcn_readfirstlane(table[at]) : -1;
+    const auto entry = [&](int64_t at) { return table[at < range.last ? at : range.last - 1]; };
+    const auto page_of = [&](int32_t loaded) -> int64_t {
+        const int32_t p = __builtin_amdgcn_readfirstlane(loaded);
         return p >= 0 && p < a.cache.blocks ? p : -1;
     };
-    uint4 kf[2][2 * kK];
+    u32x4 kf[2][2 * kK];
+    uint32_t kp_raw = 127, vp_raw = 127;
     const auto load_keys = [&](int64_t page) {
-        const uint8_t* p = a.cache.k + (page * a.cache.heads + kv_head) * kBytes + (2 * h) * (kKvBlock * 16) + c * 16;
+        const int64_t at = (page < 0 ? 0 : page) * a.cache.heads + kv_head;
+        const uint8_t* p = a.cache.k + at * kBytes + (2 * h) * (kKvBlock * 16) + c * 16;
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-            for (int k = 0; k < kK; ++k)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    kf[tt][2 * k + i] = *reinterpret_cast<const uint4*>(p + (4 * k + i) * (kKvBlock * 16) + tt * 32 * 16);
-    };
-    int64_t page = page_of(at0), next = page_of(at0 + kNarrowWaves);
-    if (page >= 0) load_keys(page);
-    for (int64_t at = at0; at < range.last; at += kNarrowWaves) {
-        const bool good = page >= 0;
-        uint4 vf[kDT][2];
-        uint32_t kp = 127, vp = 127;
-        if (good) {
-            const uint8_t* p = a.cache.v + (page * a.cache.heads + kv_head) * kBytes + c * 16;
-#pragma unroll
-            for (int d = 0; d < kDT; ++d)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    vf[d][u] = *reinterpret_cast<const uint4*>(p + (2 * u + h) * (D * 16) + d * 32 * 16);
-            kp = clamp_power(a.cache.k_power[page * a.cache.heads + kv_head]);
-            vp = clamp_power(a.cache.v_power[page * a.cache.heads + kv_head]);
-        } else {
-#pragma unroll
-            for (int d = 0; d < kDT; ++d)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) vf[d][u] = make_uint4(0, 0, 0, 0);
-        }
-        f32x16 s[2];
-        if (good) {
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                s[tt] = f32x16{};
-#pragma unroll
-                for (int k = 0; k < kK; ++k) {
-                    const i32x8 f = pieces(kf[tt][2 * k], kf[tt][2 * k + 1]);
-                    s[tt] = mul_scores(f, q.hi[k], s[tt], (int)kp, q.power_hi);
-                    s[tt] = mul_scores(f, q.lo[k], s[tt], (int)kp, q.power_lo);
-                }
-            }
-        } else {
+        for (int k = 0; k < kK; ++k)
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[tt][i] = quiet_nan();  // no such block: whoever sees it gets NaN
+                for (int i = 0; i < 2; ++i)
+                    kf[tt][2 * k + i] = *reinterpret_cast<const u32x4*>(p + (4 * k + i) * (kKvBlock * 16) + tt * 32 * 16);
+        kp_raw = a.cache.k_power[at];
+        vp_raw = a.cache.v_power[at];
+    };
+    int64_t page = -1;
+    int32_t next = -1;
+    if (at0 < range.last) {
+        page = page_of(entry(at0));
+        load_keys(page);
+        next = entry(at0 + kNarrowWaves);
+    }
+    for (int64_t at = at0; at < range.last; at += kNarrowWaves) {
+        const bool good = page >= 0;
+        u32x4 vf[kDT][2];
+        {
+            const uint8_t* p = a.cache.v + ((good ? page : 0) * a.cache.heads + kv_head) * kBytes + c * 16;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int d = 0; d < kDT; ++d)
+                    vf[d][u] = *reinterpret_cast<const u32x4*>(p + (2 * u + h) * (D * 16) + d * 32 * 16);
         }
-        page = next;
-        if (page >= 0) load_keys(page);
-        next = page_of(at + 2 * kNarrowWaves);
+        const int kp = key_power(kp_raw, good);
+        const float vs = power_value(clamp_power(vp_raw));
+        f32x16 s[2] = {f32x16{}, f32x16{}};
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+            const i32x8 f0 = pieces(kf[0][2 * k], kf[0][2 * k + 1]), f1 = pieces(kf[1][2 * k], kf[1][2 * k + 1]);
+            s[0] = mul_scores(f0, q.hi[k], s[0], kp, q.power_hi);
+            s[1] = mul_scores(f1, q.hi[k], s[1], kp, q.power_hi);
+            s[0] = mul_scores(f0, q.lo[k], s[0], kp, q.power_lo);
+            s[1] = mul_scores(f1, q.lo[k], s[1], kp, q.power_lo);
+        }
+        if (!good) {
+#pragma unroll
+            for (int d = 0; d < kDT; ++d)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) vf[d][u] = u32x4{0, 0, 0, 0};
+        }
+        page = page_of(next);
+        if (at + kNarrowWaves < range.last) {
+            load_keys(page);
+            next = entry(at + 2 * kNarrowWaves);
+        }
 
         const int first_key = (int)at * kKvBlock;
         const bool edge = first_key + kKvBlock > all;
         if (edge) mask_scores(s, row.limit - first_key);
-        bf16x8 p[4];
-        softmax_block<kDT>(s, st, o, a.scale_log2, p);
+        raise_maximum<kDT>(s, st, o, a.scale_log2);
+        const float ref = reference_of(st);
         if (edge) {
             // A masked key has p = 0, but 0 times a NaN value is NaN: NaN codes
             // are taken out and given back to the rows that see their key.
@@ -326,6 +335,8 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
                     nan |= fp8_any_nan(vf[d][u].x) || fp8_any_nan(vf[d][u].y) || fp8_any_nan(vf[d][u].z) ||
                            fp8_any_nan(vf[d][u].w);
             if (__any(nan)) {
+                int half = h;  // opaque: nothing of this rare path is worth registers in the loop
+                asm volatile("" : "+v"(half));
 #pragma unroll
                 for (int d = 0; d < kDT; ++d) {
                     int lowest = kKvBlock;  // first key of this lane's dim with a NaN
@@ -336,33 +347,33 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
                         for (int i = 0; i < 16; ++i) {
                             const uint32_t code = (w[i / 4] >> (8 * (i % 4))) & 0x7Fu;
                             if (code == 0x7Fu) {
-                                const int key = 32 * u + 16 * (i / 8) + 8 * (i / 4 % 2) + 4 * h + i % 4;
+                                const int key = 32 * u + 16 * (i / 8) + 8 * (i / 4 % 2) + 4 * half + i % 4;
                                 lowest = key < lowest ? key : lowest;
                                 w[i / 4] &= ~(0xFFu << (8 * (i % 4)));
                             }
                         }
-                        vf[d][u] = make_uint4(w[0], w[1], w[2], w[3]);
+                        vf[d][u] = u32x4{w[0], w[1], w[2], w[3]};
                     }
                     const int other = __shfl_xor(lowest, 32);
                     lowest = lowest < other ? lowest : other;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int key = __shfl(lowest, 8 * (i / 4) + 4 * h + i % 4);
+                        const int key = __shfl(lowest, 8 * (i / 4) + 4 * half + i % 4);
                         if (key < row.limit - first_key && key < kKvBlock) o[d][i] = quiet_nan();
                     }
                 }
             }
         }
-        const float vs = power_value(vp);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int ks = 0; ks < 4; ++ks) {
+            const bf16x8 p = probabilities(s, ks, st, a.scale_log2, ref);
 #pragma unroll
             for (int d = 0; d < kDT; ++d) {
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_bf16(vf[d][u].x, vf[d][u].y, vs), p[2 * u], o[d],
-                                                              0, 0, 0);
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_bf16(vf[d][u].z, vf[d][u].w, vs), p[2 * u + 1],
-                                                              o[d], 0, 0, 0);
+                const u32x4 w = vf[d][ks / 2];
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    ks % 2 ? values_bf16(w.z, w.w, vs) : values_bf16(w.x, w.y, vs), p, o[d], 0, 0, 0);
             }
+        }
     }
 
     // join the waves: each row's largest maximum is the common reference
@@ -405,9 +416,9 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
         uint16_t* p = a.out.data + mine.token * a.out.row + mine.head * a.out.head + d0;
 #pragma unroll
         for (int i = 0; i < kEach; i += 8)
-            *reinterpret_cast<uint4*>(p + i) =
-                make_uint4(pack_bf16x2(acc[i] * inv, acc[i + 1] * inv), pack_bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
-                           pack_bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), pack_bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));
+            *reinterpret_cast<u32x4*>(p + i) =
+                u32x4{pack_bf16x2(acc[i] * inv, acc[i + 1] * inv), pack_bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
+                           pack_bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), pack_bf16x2(acc[i + 6] * inv, acc[i + 7] * inv)};
     } else {
         const int64_t all_rows = a.seqs.M * a.q_heads;
         float* po = a.partial + ((int64_t)part * all_rows + at) * D + d0;
@@ -439,8 +450,8 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     constexpr int kPieces = kBytes / 16;                  // 16-byte pieces of a block's keys, and of its values
     constexpr int kThreads = 64 * kWideWaves;
     constexpr int kEach = kPieces / kThreads;             // of them a thread's
-    __shared__ __align__(16) uint4 sk[2][kPieces];
-    __shared__ __align__(16) uint4 sv[2][2 * kPieces];    // [k-step][half][dim] of 8 keys
+    __shared__ __align__(16) u32x4 sk[2][kPieces];
+    __shared__ __align__(16) u32x4 sv[2][2 * kPieces];    // [k-step][half][dim] of 8 keys
     __shared__ int nan_key[2][D];                         // first key whose value is a NaN code, by dim
     __shared__ int nan_any[2];
     const Tile t = find_tile(a, blockIdx.x, kWideRows);
@@ -466,38 +477,37 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) nan_key[i / D][i % D] = kKvBlock;
     if (threadIdx.x < 2) nan_any[threadIdx.x] = 0;
 
+    // table entries and powers are looked at a block after they are asked for,
+    // as in the narrow kernel
     const int32_t* table = a.seqs.table + t.b * a.seqs.ld_table;
-    const auto page_of = [&](int at) -> int64_t {
-        const int64_t p = at < blocks ? __builtin_amdgcn_readfirstlane(table[at]) : -1;
+    const auto entry = [&](int at) { return table[at < blocks ? at : blocks - 1]; };
+    const auto page_of = [&](int32_t loaded) -> int64_t {
+        const int32_t p = __builtin_amdgcn_readfirstlane(loaded);
         return p >= 0 && p < a.cache.blocks ? p : -1;
     };
-    uint4 kr[kEach], vr[kEach];
-    uint32_t kp = 127, vp = 127;
+    u32x4 kr[kEach], vr[kEach];
+    uint32_t kp_raw = 127, vp_raw = 127;
     const auto fetch = [&](int64_t page) {
-        if (page >= 0) {
-            const int64_t at = page * a.cache.heads + kv_head;
-            const uint4* pk = reinterpret_cast<const uint4*>(a.cache.k + at * kBytes);
-            const uint4* pv = reinterpret_cast<const uint4*>(a.cache.v + at * kBytes);
+        const int64_t at = (page < 0 ? 0 : page) * a.cache.heads + kv_head;
+        const u32x4* pk = reinterpret_cast<const u32x4*>(a.cache.k + at * kBytes);
+        const u32x4* pv = reinterpret_cast<const u32x4*>(a.cache.v + at * kBytes);
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                kr[i] = pk[i * kThreads + threadIdx.x];
-                vr[i] = pv[i * kThreads + threadIdx.x];
-            }
-            kp = clamp_power(a.cache.k_power[at]);
-            vp = clamp_power(a.cache.v_power[at]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kEach; ++i) {
+            kr[i] = pk[i * kThreads + threadIdx.x];
+            vr[i] = pv[i * kThreads + threadIdx.x];
         }
+        kp_raw = a.cache.k_power[at];
+        vp_raw = a.cache.v_power[at];
     };
     // stages the fetched block; edge: some row of the tile does not see all of it
-    const auto stage = [&](int buffer, bool edge) {
-        const float scale = power_value(vp);
+    const auto stage = [&](int buffer, bool good, bool edge) {
+        const float scale = power_value(clamp_power(vp_raw));
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int at = i * kThreads + threadIdx.x;
             const int d = at % D, piece = at / D;         // piece 2u + half
-            uint4 w = vr[i];
+            u32x4 w = vr[i];
+            if (!good) w = u32x4{0, 0, 0, 0};
             if (edge && (fp8_any_nan(w.x) || fp8_any_nan(w.y) || fp8_any_nan(w.z) || fp8_any_nan(w.w))) {
                 // as in the narrow kernel: NaN codes are taken out, and given
                 // back to the rows that see their key
@@ -510,64 +520,86 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
                         lowest = key < lowest ? key : lowest;
                         x[j / 4] &= ~(0xFFu << (8 * (j % 4)));
                     }
-                w = make_uint4(x[0], x[1], x[2], x[3]);
+                w = u32x4{x[0], x[1], x[2], x[3]};
                 atomicMin(&nan_key[buffer][d], lowest);
                 nan_any[buffer] = 1;
             }
             sk[buffer][at] = kr[i];
             const int to = (4 * (piece / 2) + piece % 2) * D + d;   // k-step 2u; 2u + 1 is 2 D further on
-            sv[buffer][to] = __builtin_bit_cast(uint4, values_bf16(w.x, w.y, scale));
-            sv[buffer][to + 2 * D] = __builtin_bit_cast(uint4, values_bf16(w.z, w.w, scale));
+            sv[buffer][to] = __builtin_bit_cast(u32x4, values_bf16(w.x, w.y, scale));
+            sv[buffer][to + 2 * D] = __builtin_bit_cast(u32x4, values_bf16(w.z, w.w, scale));
         }
     };
     __syncthreads();  // the NaN marks are clear
-    int64_t page = page_of(0), next = page_of(1);
-    fetch(page);
-    stage(0, kKvBlock > tile_all);
-    uint32_t kp_now = kp;
+    int32_t next = -1;
+    int kp = 127;
+    if (blocks > 0) {
+        const int64_t page = page_of(entry(0));
+        fetch(page);
+        next = entry(1);
+        const bool good = page >= 0;
+        stage(0, good, kKvBlock > tile_all);
+        kp = key_power(kp_raw, good);
+    }
     __syncthreads();
     for (int at = 0; at < blocks; ++at) {
         const int b = at & 1, first_key = at * kKvBlock;
-        const bool good = page >= 0;
-        page = next;
-        if (at + 1 < blocks) fetch(page);
-        next = page_of(at + 2);
+        const bool more = at + 1 < blocks;
+        const int64_t page = page_of(next);
+        if (more) {
+            fetch(page);
+            next = entry(at + 2);
+        }
         if (first_key < seen) {
-            f32x16 s[2];
+            u32x4 kf[2][2 * kK];
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                s[tt] = f32x16{};
-#pragma unroll
-                for (int k = 0; k < kK; ++k) {
-                    const i32x8 f = pieces(sk[b][(4 * k + 2 * h) * kKvBlock + tt * 32 + c],
-                                           sk[b][(4 * k + 2 * h + 1) * kKvBlock + tt * 32 + c]);
-                    s[tt] = mul_scores(f, q.hi[k], s[tt], (int)kp_now, q.power_hi);
-                    s[tt] = mul_scores(f, q.lo[k], s[tt], (int)kp_now, q.power_lo);
-                }
-            }
-            if (!good) {
+            for (int k = 0; k < kK; ++k)
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[tt][i] = quiet_nan();
-            }
-            if (first_key + kKvBlock > all) mask_scores(s, row.limit - first_key);
-            bf16x8 p[4];
-            softmax_block<kDT>(s, st, o, a.scale_log2, p);
+                    for (int i = 0; i < 2; ++i)
+                        kf[tt][2 * k + i] = sk[b][(4 * k + 2 * h + i) * kKvBlock + tt * 32 + c];
+            f32x16 s[2] = {f32x16{}, f32x16{}};
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
+            for (int k = 0; k < kK; ++k) {
+                const i32x8 f0 = pieces(kf[0][2 * k], kf[0][2 * k + 1]), f1 = pieces(kf[1][2 * k], kf[1][2 * k + 1]);
+                s[0] = mul_scores(f0, q.hi[k], s[0], kp, q.power_hi);
+                s[1] = mul_scores(f1, q.hi[k], s[1], kp, q.power_hi);
+                s[0] = mul_scores(f0, q.lo[k], s[0], kp, q.power_lo);
+                s[1] = mul_scores(f1, q.lo[k], s[1], kp, q.power_lo);
+            }
+            // values of the first k-step are on their way while the softmax runs,
+            // and those of the next while one is multiplied
+            u32x4 vf[2][kDT];
+#pragma unroll
+            for (int d = 0; d < kDT; ++d) vf[0][d] = sv[b][h * D + 32 * d + c];
+            __builtin_amdgcn_sched_barrier(0);
+            if (first_key + kKvBlock > all) mask_scores(s, row.limit - first_key);
+            raise_maximum<kDT>(s, st, o, a.scale_log2);
+            const float ref = reference_of(st);
+            bf16x8 p = probabilities(s, 0, st, a.scale_log2, ref);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                if (ks < 3)
+#pragma unroll
+                    for (int d = 0; d < kDT; ++d) vf[(ks + 1) & 1][d] = sv[b][(2 * (ks + 1) + h) * D + 32 * d + c];
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int d = 0; d < kDT; ++d)
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        __builtin_bit_cast(bf16x8, sv[b][(2 * ks + h) * D + 32 * d + c]), p[ks], o[d], 0, 0, 0);
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[ks & 1][d]), p, o[d], 0, 0,
+                                                                  0);
+                if (ks < 3) p = probabilities(s, ks + 1, st, a.scale_log2, ref);
+            }
         }
         if (first_key + kKvBlock > tile_all && nan_any[b]) {  // the same for all waves
             if (first_key < seen) {
+                int half = h;
+                asm volatile("" : "+v"(half));
 #pragma unroll
                 for (int d = 0; d < kDT; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int key = nan_key[b][32 * d + 8 * (i / 4) + 4 * h + i % 4];
+                        const int key = nan_key[b][32 * d + 8 * (i / 4) + 4 * half + i % 4];
                         if (key < kKvBlock && key < row.limit - first_key) o[d][i] = quiet_nan();
                     }
             }
@@ -575,8 +607,11 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
             for (int i = threadIdx.x; i < D; i += kThreads) nan_key[b][i] = kKvBlock;
             if (threadIdx.x == 0) nan_any[b] = 0;
         }
-        if (at + 1 < blocks) stage(1 - b, first_key + 2 * kKvBlock > tile_all);
-        kp_now = kp;
+        if (more) {
+            const bool good = page >= 0;
+            stage(1 - b, good, first_key + 2 * kKvBlock > tile_all);
+            kp = key_power(kp_raw, good);
+        }
         __syncthreads();
     }
     if (!row.valid) return;
@@ -599,7 +634,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
             uint32_t y1 = pack_bf16x2(o[d][4 * i + 6] * inv, o[d][4 * i + 7] * inv);
             const auto r0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
             const auto r1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-            *reinterpret_cast<uint4*>(out + 32 * d + 8 * i + 8 * h) = make_uint4(r0[0], r1[0], r0[1], r1[1]);
+            *reinterpret_cast<u32x4*>(out + 32 * d + 8 * i + 8 * h) = u32x4{r0[0], r1[0], r0[1], r1[1]};
         }
 }
 

@@ -7,6 +7,10 @@
 
 namespace nvfp4 {
 
+// 16 bytes as the compiler keeps them in registers.  (Arrays of HIP's own uint4
+// struct, copied between memories, have been left in scratch memory.)
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 // 2^(b - 127) for a power byte 1..254.
 __device__ __forceinline__ float power_value(uint32_t b) { return __uint_as_float(b << 23); }
 // Its reciprocal, exactly.

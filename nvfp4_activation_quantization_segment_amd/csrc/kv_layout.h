@@ -62,12 +62,15 @@ constexpr RowRange row_range(int64_t start, int64_t end, int64_t M) {
 // A length that a table of `blocks` blocks cannot hold.
 constexpr bool kv_length_bad(int64_t len, int64_t blocks) { return len < 0 || len > blocks * kKvBlock; }
 
-// First key that the query at position pos does not see: all len keys
+// First key that the query at position pos < len does not see: all len keys
 // (causal = 0), or those of its own run of `causal` positions and before.
-constexpr int64_t kv_limit(int64_t pos, int64_t len, int64_t causal) {
+// 32-bit throughout: a 64-bit division is a hundred instructions here.
+constexpr int32_t kv_limit(int32_t pos, int32_t len, int32_t causal) {
     if (causal == 0) return len;
-    const int64_t end = (floor_div(pos, causal) + 1) * causal;
-    return clamp64(end, 0, len);
+    if (pos < 0) return 0;
+    if (causal == 1) return pos + 1;
+    const int32_t left = causal - pos % causal;  // positions from pos to its run's end
+    return left > len - pos ? len : pos + left;
 }
 
 // Blocks [first, last) of part s of S of a row tile that sees n blocks.
