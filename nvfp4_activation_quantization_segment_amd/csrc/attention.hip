@@ -73,6 +73,16 @@ struct Row {
     int32_t limit;   // keys it sees
 };
 
+// Keys that token i of the sequence sees.
+__device__ __forceinline__ int32_t limit_of(const AttentionArgs& a, const Tile& t, int32_t i) {
+    return t.bad ? 0 : kv_limit((int32_t)t.len - t.n + i, (int32_t)t.len, a.causal);
+}
+// Keys that row rr of the sequence sees, the last row's past it.
+__device__ __forceinline__ int32_t limit_of_row(const AttentionArgs& a, const Tile& t, int32_t rr) {
+    const int32_t at = rr < t.rows ? rr : t.rows - 1;
+    return limit_of(a, t, __builtin_amdgcn_readfirstlane(at / a.group));
+}
+
 __device__ __forceinline__ Row find_row(const AttentionArgs& a, const Tile& t, int32_t rr, int32_t kv_head) {
     Row r;
     r.valid = rr < t.rows;
@@ -80,7 +90,7 @@ __device__ __forceinline__ Row find_row(const AttentionArgs& a, const Tile& t, i
     const int32_t i = at / a.group;
     r.token = t.row0 + i;
     r.head = kv_head * a.group + (at - i * a.group);
-    r.limit = t.bad ? 0 : kv_limit((int32_t)t.len - t.n + i, (int32_t)t.len, a.causal);
+    r.limit = limit_of(a, t, i);
     return r;
 }
 
@@ -241,9 +251,8 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     const int kv_head = blockIdx.y, part = blockIdx.z;
     const Row row = find_row(a, t, t.first + c, kv_head);
     // blocks that the tile's last row sees, and keys that all its rows see
-    const int last = t.first + kRows < t.rows ? t.first + kRows - 1 : t.rows - 1;
-    const int seen = find_row(a, t, last, kv_head).limit;
-    const int all = find_row(a, t, t.first, kv_head).limit;
+    const int seen = limit_of_row(a, t, t.first + kRows - 1);
+    const int all = limit_of_row(a, t, t.first);
     const BlockRange range = kv_part((seen + kKvBlock - 1) / kKvBlock, part, a.parts);
     const int64_t at0 = range.first + wave;
 
@@ -443,6 +452,29 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
 constexpr int kWideWaves = 4;
 constexpr int kWideRows = kWideWaves * kRows;
 
+// Which tile and key/value head a workgroup takes.  Workgroups go to the 8 XCDs
+// in turn; where the heads divide evenly over them, each XCD takes whole heads,
+// so that the tiles in flight at a time read the same keys from its L2.  Tiles
+// go from the last to the first: under a causal mask the later ones take
+// longer, and the short ones fill the end.
+__device__ __forceinline__ void wide_place(const AttentionArgs& a, int& unit, int& kv_head) {
+    if (gridDim.y > 1) {
+        unit = gridDim.x - 1 - blockIdx.x;
+        kv_head = blockIdx.y;
+        return;
+    }
+    const uint32_t heads = a.cache.heads, units = gridDim.x / heads;
+    if (heads % 8 == 0) {
+        const uint32_t at = blockIdx.x / 8, head = at / units;
+        kv_head = (int)((blockIdx.x % 8) * (heads / 8) + head);
+        unit = (int)(units - 1 - (at - head * units));
+    } else {
+        const uint32_t at = blockIdx.x / heads;
+        kv_head = (int)(blockIdx.x - at * heads);
+        unit = (int)(units - 1 - at);
+    }
+}
+
 template <int D>
 __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(AttentionArgs a) {
     constexpr int kDT = D / 32, kK = D / 64;
@@ -454,18 +486,19 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     __shared__ __align__(16) u32x4 sv[2][2 * kPieces];    // [k-step][half][dim] of 8 keys
     __shared__ int nan_key[2][D];                         // first key whose value is a NaN code, by dim
     __shared__ int nan_any[2];
-    const Tile t = find_tile(a, blockIdx.x, kWideRows);
+    int unit, kv_head;
+    wide_place(a, unit, kv_head);
+    const Tile t = find_tile(a, unit, kWideRows);
     if (!t.any) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int c = lane & 31, h = lane >> 5;
-    const int kv_head = blockIdx.y;
     const int row0 = t.first + wave * kRows;
     const Row row = find_row(a, t, row0 + c, kv_head);
     // keys that the tile's last row and this wave's last row see, and keys that
     // all rows of the tile and of the wave see
-    const auto limit_of = [&](int rr) { return find_row(a, t, rr, kv_head).limit; };
-    const int tile_seen = limit_of(t.first + kWideRows - 1), seen = row0 < t.rows ? limit_of(row0 + kRows - 1) : 0;
-    const int tile_all = limit_of(t.first), all = limit_of(row0);
+    const int tile_seen = limit_of_row(a, t, t.first + kWideRows - 1);
+    const int seen = row0 < t.rows ? limit_of_row(a, t, row0 + kRows - 1) : 0;
+    const int tile_all = limit_of_row(a, t, t.first), all = limit_of_row(a, t, row0);
     const int blocks = (tile_seen + kKvBlock - 1) / kKvBlock;
 
     Query<D> q;
@@ -691,7 +724,9 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
 template <int D>
 static void attention_of(const AttentionArgs& a, hipStream_t s) {
     if (a.wide) {
-        const dim3 grid((unsigned)tile_units(a.seqs.M, a.seqs.B, a.group, kWideRows), (unsigned)a.cache.heads);
+        const int64_t units = tile_units(a.seqs.M, a.seqs.B, a.group, kWideRows);
+        const bool flat = units * a.cache.heads < ((int64_t)1 << 23);  // workgroups x threads below 2^32
+        const dim3 grid((unsigned)(flat ? units * a.cache.heads : units), flat ? 1u : (unsigned)a.cache.heads);
         attention_wide_kernel<D><<<grid, dim3(64 * kWideWaves), 0, s>>>(a);
         return;
     }
