@@ -28,9 +28,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRows = 32;  // rows of a wave
-// A running maximum is kept until a score passes it by this much (in powers of
-// two): p stays below 2^8, and most blocks need no rescaling of the output.
-constexpr float kSlack = 8.0f;
+// Probabilities are taken against a reference that need not be the maximum:
+// while the sum of a lane's 16 new ones stays below this, the reference stays.
+constexpr float kMost = 256.0f;
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
@@ -166,64 +166,75 @@ __device__ __forceinline__ float other_half(float x) {
 
 // The running softmax of a lane's row.
 struct Softmax {
-    float m;  // reference maximum, scaled, base 2
+    float m;  // reference, scaled, base 2: some earlier maximum, -inf before the first
     float l;  // sum of this half's p
 };
 
-// Takes a block's scores (two tiles of 32 keys) into the running maximum,
-// rescaling the sum and the output where it passes the reference by kSlack.
+// Probabilities of a tile of 32 keys in bf16, the second operands of two
+// k-steps of the products with the values, and their sum.
+__device__ __forceinline__ float probabilities(const f32x16& s, float scale_log2, float ref, bf16x8 (&p)[2]) {
+    float sum[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t w[4];
+        float part[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * k + 2 * i], scale_log2, -ref));
+            const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * k + 2 * i + 1], scale_log2, -ref));
+            part[i] = x + y;
+            w[i] = pack_bf16x2(x, y);
+        }
+        sum[k] = (part[0] + part[1]) + (part[2] + part[3]);
+        p[k] = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+    }
+    return sum[0] + sum[1];
+}
+
+// Accepts the probabilities of a tile, or takes them again against its maximum.
+// A maximum for every tile would cost 16 comparisons and an exchange between the
+// lanes, on the way from the scores to the exponentials; instead the sum, which
+// is there anyway, tells when the reference is too low (more than kMost, or
+// infinite, or NaN for the first tile, whose reference is -inf).  p and the sums
+// are floating-point numbers: a reference below the maximum costs no precision.
 template <int NO>
-__device__ __forceinline__ void raise_maximum(const f32x16 (&s)[2], Softmax& st, f32x16 (&o)[NO], float scale_log2) {
-    float top = s[0][0];
+__device__ __forceinline__ void accept(const f32x16& s, float scale_log2, float sum, Softmax& st, f32x16 (&o)[NO],
+                                       bf16x8 (&p)[2]) {
+    const uint64_t over = __ballot(!(sum <= kMost));
+    if (over) {
+        // row by row (either half's sum decides for both): the other rows keep
+        // their references and get the same p again, so that a row's bytes do
+        // not depend on what other rows see
+        const bool raise = ((over | over >> 32) >> (threadIdx.x & 31)) & 1;
+        float top = s[0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[0][i]);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[1][i]);
-    top = fmaxf(top, other_half(top));
-    top *= scale_log2;
-    if (__any(top > st.m + kSlack)) {
-        const float m = fmaxf(st.m, top);
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+        top = fmaxf(top, other_half(top)) * scale_log2;
+        const float m = raise ? fmaxf(st.m, top) : st.m;
         const float alpha = m == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+        st.m = m;
         st.l *= alpha;
 #pragma unroll
         for (int d = 0; d < NO; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
-        st.m = m;
+        sum = probabilities(s, scale_log2, m == neg_inf() ? 0.0f : m, p);  // nothing seen yet: all 0
     }
+    st.l += sum;
 }
-
-// The probabilities of k-step k (16 keys) in bf16, a second operand of the
-// products with the values.
-__device__ __forceinline__ bf16x8 probabilities(const f32x16 (&s)[2], int k, Softmax& st, float scale_log2, float ref) {
-    uint32_t w[4];
-    float sum[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k / 2][8 * (k % 2) + 2 * i], scale_log2, -ref));
-        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k / 2][8 * (k % 2) + 2 * i + 1], scale_log2, -ref));
-        sum[i] = x + y;
-        w[i] = pack_bf16x2(x, y);
-    }
-    st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
-}
-__device__ __forceinline__ float reference_of(const Softmax& st) { return st.m == neg_inf() ? 0.0f : st.m; }
 
 // The power byte of a block's keys; the byte that stands for NaN where the block
 // does not exist, so that whoever sees it gets NaN.
 __device__ __forceinline__ int key_power(uint32_t loaded, bool good) { return good ? (int)clamp_power(loaded) : 255; }
 
 // Scores of keys past the row's limit become -inf.  left: the limit counted
-// from the block's first key.
-__device__ __forceinline__ void mask_scores(f32x16 (&s)[2], int32_t left) {
-    // against constants: 32 keys by name would be 32 registers held in the loop
+// from the tile's first key.
+__device__ __forceinline__ void mask_scores(f32x16& s, int32_t left) {
+    // against constants: 16 keys by name would be 16 registers held in the loop
     const int mine = left - 4 * (int)((threadIdx.x & 63) >> 5);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (32 * t + 8 * (i / 4) + i % 4 >= mine) s[t][i] = neg_inf();
+    for (int i = 0; i < 16; ++i)
+        if (8 * (i / 4) + i % 4 >= mine) s[i] = neg_inf();
 }
 
 // ---------------------------------------------------------------------------
@@ -330,9 +341,10 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
 
         const int first_key = (int)at * kKvBlock;
         const bool edge = first_key + kKvBlock > all;
-        if (edge) mask_scores(s, row.limit - first_key);
-        raise_maximum<kDT>(s, st, o, a.scale_log2);
-        const float ref = reference_of(st);
+        if (edge) {
+            mask_scores(s[0], row.limit - first_key);
+            mask_scores(s[1], row.limit - first_key - 32);
+        }
         if (edge) {
             // A masked key has p = 0, but 0 times a NaN value is NaN: NaN codes
             // are taken out and given back to the rows that see their key.
@@ -374,14 +386,18 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
             }
         }
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            const bf16x8 p = probabilities(s, ks, st, a.scale_log2, ref);
+        for (int tt = 0; tt < 2; ++tt) {
+            bf16x8 p[2];
+            const float sum = probabilities(s[tt], a.scale_log2, st.m, p);
+            accept<kDT>(s[tt], a.scale_log2, sum, st, o, p);
 #pragma unroll
-            for (int d = 0; d < kDT; ++d) {
-                const u32x4 w = vf[d][ks / 2];
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    ks % 2 ? values_bf16(w.z, w.w, vs) : values_bf16(w.x, w.y, vs), p, o[d], 0, 0, 0);
-            }
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int d = 0; d < kDT; ++d) {
+                    const u32x4 w = vf[d][tt];
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        k ? values_bf16(w.z, w.w, vs) : values_bf16(w.x, w.y, vs), p[k], o[d], 0, 0, 0);
+                }
         }
     }
 
@@ -475,6 +491,17 @@ __device__ __forceinline__ void wide_place(const AttentionArgs& a, int& unit, in
     }
 }
 
+// Asks the compiler to lay MATRIX matrix instructions of a stretch of code out
+// among VECTOR vector instructions.
+template <int MATRIX, int VECTOR>
+__device__ __forceinline__ void alternate() {
+#pragma unroll
+    for (int i = 0; i < MATRIX; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, VECTOR / MATRIX, 0);
+    }
+}
+
 template <int D>
 __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(AttentionArgs a) {
     constexpr int kDT = D / 32, kK = D / 64;
@@ -532,15 +559,15 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
         kp_raw = a.cache.k_power[at];
         vp_raw = a.cache.v_power[at];
     };
-    // stages the fetched block; edge: some row of the tile does not see all of it
-    const auto stage = [&](int buffer, bool good, bool edge) {
+    // stages the fetched block; edge: some row of the tile does not see all of
+    // it, or it stands in for one that does not exist
+    const auto stage = [&](int buffer, bool edge) {
         const float scale = power_value(clamp_power(vp_raw));
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int at = i * kThreads + threadIdx.x;
             const int d = at % D, piece = at / D;         // piece 2u + half
             u32x4 w = vr[i];
-            if (!good) w = u32x4{0, 0, 0, 0};
             if (edge && (fp8_any_nan(w.x) || fp8_any_nan(w.y) || fp8_any_nan(w.z) || fp8_any_nan(w.w))) {
                 // as in the narrow kernel: NaN codes are taken out, and given
                 // back to the rows that see their key
@@ -566,12 +593,14 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     __syncthreads();  // the NaN marks are clear
     int32_t next = -1;
     int kp = 127;
+    bool edge_now = false;
     if (blocks > 0) {
         const int64_t page = page_of(entry(0));
         fetch(page);
         next = entry(1);
         const bool good = page >= 0;
-        stage(0, good, kKvBlock > tile_all);
+        edge_now = !good || kKvBlock > tile_all;
+        stage(0, edge_now);
         kp = key_power(kp_raw, good);
     }
     __syncthreads();
@@ -592,39 +621,55 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         kf[tt][2 * k + i] = sk[b][(4 * k + 2 * h + i) * kKvBlock + tt * 32 + c];
+            // Two tiles of 32 keys.  The second's scores are multiplied while the
+            // first's exponentials are taken, and the first's products with the
+            // values while the second's are: matrix and vector instructions of
+            // one wave overlap where they alternate.
+            const bool edge = first_key + kKvBlock > all;
             f32x16 s[2] = {f32x16{}, f32x16{}};
+            const auto scores = [&](int tt) {
 #pragma unroll
-            for (int k = 0; k < kK; ++k) {
-                const i32x8 f0 = pieces(kf[0][2 * k], kf[0][2 * k + 1]), f1 = pieces(kf[1][2 * k], kf[1][2 * k + 1]);
-                s[0] = mul_scores(f0, q.hi[k], s[0], kp, q.power_hi);
-                s[1] = mul_scores(f1, q.hi[k], s[1], kp, q.power_hi);
-                s[0] = mul_scores(f0, q.lo[k], s[0], kp, q.power_lo);
-                s[1] = mul_scores(f1, q.lo[k], s[1], kp, q.power_lo);
-            }
-            // values of the first k-step are on their way while the softmax runs,
-            // and those of the next while one is multiplied
+                for (int k = 0; k < kK; ++k) {
+                    const i32x8 f = pieces(kf[tt][2 * k], kf[tt][2 * k + 1]);
+                    s[tt] = mul_scores(f, q.hi[k], s[tt], kp, q.power_hi);
+                    s[tt] = mul_scores(f, q.lo[k], s[tt], kp, q.power_lo);
+                }
+            };
+            // values of a k-step are on their way while the one before is multiplied
             u32x4 vf[2][kDT];
+            const auto values = [&](int ks) {
 #pragma unroll
-            for (int d = 0; d < kDT; ++d) vf[0][d] = sv[b][h * D + 32 * d + c];
-            __builtin_amdgcn_sched_barrier(0);
-            if (first_key + kKvBlock > all) mask_scores(s, row.limit - first_key);
-            raise_maximum<kDT>(s, st, o, a.scale_log2);
-            const float ref = reference_of(st);
-            bf16x8 p = probabilities(s, 0, st, a.scale_log2, ref);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                if (ks < 3)
-#pragma unroll
-                    for (int d = 0; d < kDT; ++d) vf[(ks + 1) & 1][d] = sv[b][(2 * (ks + 1) + h) * D + 32 * d + c];
-                __builtin_amdgcn_sched_barrier(0);
+                for (int d = 0; d < kDT; ++d) vf[ks & 1][d] = sv[b][(2 * ks + h) * D + 32 * d + c];
+            };
+            const auto multiply = [&](int ks, bf16x8 p) {
 #pragma unroll
                 for (int d = 0; d < kDT; ++d)
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[ks & 1][d]), p, o[d], 0, 0,
                                                                   0);
-                if (ks < 3) p = probabilities(s, ks + 1, st, a.scale_log2, ref);
-            }
+            };
+            bf16x8 p0[2], p1[2];
+            scores(0);
+            values(0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (edge) mask_scores(s[0], row.limit - first_key);
+            scores(1);
+            const float sum0 = probabilities(s[0], a.scale_log2, st.m, p0);
+            values(1);
+            alternate<2 * kK, 56>();
+            asm volatile("" : "+v"(s[1]));  // issued here, not after the branch below
+            accept<kDT>(s[0], a.scale_log2, sum0, st, o, p0);
+            if (edge) mask_scores(s[1], row.limit - first_key - 32);
+            multiply(0, p0[0]);
+            values(2);
+            multiply(1, p0[1]);
+            const float sum1 = probabilities(s[1], a.scale_log2, st.m, p1);
+            values(3);
+            alternate<2 * kDT, 56>();
+            accept<kDT>(s[1], a.scale_log2, sum1, st, o, p1);
+            multiply(2, p1[0]);
+            multiply(3, p1[1]);
         }
-        if (first_key + kKvBlock > tile_all && nan_any[b]) {  // the same for all waves
+        if (edge_now && nan_any[b]) {  // the same for all waves
             if (first_key < seen) {
                 int half = h;
                 asm volatile("" : "+v"(half));
@@ -642,7 +687,8 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
         }
         if (more) {
             const bool good = page >= 0;
-            stage(1 - b, good, first_key + 2 * kKvBlock > tile_all);
+            edge_now = !good || first_key + 2 * kKvBlock > tile_all;
+            stage(1 - b, edge_now);
             kp = key_power(kp_raw, good);
         }
         __syncthreads();
