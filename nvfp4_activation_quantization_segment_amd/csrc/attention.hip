@@ -103,21 +103,23 @@ struct Query {
     bool nan;  // an element is not finite
 };
 
+// The row's bf16 elements as loaded: this half's 32 dims of each 64.  (Rows past
+// the tile's end load its last row's.)
 template <int D>
-__device__ __forceinline__ void load_query(Query<D>& f, const AttentionArgs& a, const Row& r) {
-    const int h = (threadIdx.x & 63) >> 5;
-    uint32_t w[D / 64][16];  // this half's 32 dims of each 64: pieces 4k + 2h and 4k + 2h + 1 of 16
-    const uint16_t* p = a.q.data + r.token * a.q.row + r.head * a.q.head;
-    uint32_t m = 0;
+__device__ __forceinline__ void fetch_query(u32x4 (&w)[D / 16], const AttentionArgs& a, const Row& r) {
+    const uint16_t* p = a.q.data + r.token * a.q.row + r.head * a.q.head + 32 * ((threadIdx.x & 63) >> 5);
 #pragma unroll
     for (int k = 0; k < D / 64; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            u32x4 x = u32x4{0, 0, 0, 0};
-            if (r.valid) x = *reinterpret_cast<const u32x4*>(p + 64 * k + 32 * h + 8 * j);
-            w[k][4 * j] = x.x, w[k][4 * j + 1] = x.y, w[k][4 * j + 2] = x.z, w[k][4 * j + 3] = x.w;
-            m = pk_max_u16(m, pk_max_u16(pk_max_u16(mag2(x.x), mag2(x.y)), pk_max_u16(mag2(x.z), mag2(x.w))));
-        }
+        for (int j = 0; j < 4; ++j) w[4 * k + j] = *reinterpret_cast<const u32x4*>(p + 64 * k + 8 * j);
+}
+
+template <int D>
+__device__ __forceinline__ void split_query(Query<D>& f, const u32x4 (&w)[D / 16]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+        m = pk_max_u16(m, pk_max_u16(pk_max_u16(mag2(w[j].x), mag2(w[j].y)), pk_max_u16(mag2(w[j].z), mag2(w[j].w))));
     m = fold_max(m);
     const uint32_t other = (uint32_t)__shfl_xor((int)m, 32);
     m = m > other ? m : other;
@@ -131,8 +133,8 @@ __device__ __forceinline__ void load_query(Query<D>& f, const AttentionArgs& a, 
     for (int k = 0; k < D / 64; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float x0 = bf16_lo(w[k][2 * j]) * inv, x1 = bf16_hi(w[k][2 * j]) * inv;
-            const float x2 = bf16_lo(w[k][2 * j + 1]) * inv, x3 = bf16_hi(w[k][2 * j + 1]) * inv;
+            const uint32_t v0 = w[4 * k + j / 2][2 * (j % 2)], v1 = w[4 * k + j / 2][2 * (j % 2) + 1];
+            const float x0 = bf16_lo(v0) * inv, x1 = bf16_hi(v0) * inv, x2 = bf16_lo(v1) * inv, x3 = bf16_hi(v1) * inv;
             const uint32_t c = fp8_pack4(x0, x1, x2, x3);
             const auto v01 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false);
             const auto v23 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
@@ -266,13 +268,8 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     const int all = limit_of_row(a, t, t.first);
     const BlockRange range = kv_part((seen + kKvBlock - 1) / kKvBlock, part, a.parts);
     const int64_t at0 = range.first + wave;
-
-    Query<D> q;
-    load_query<D>(q, a, row);
-    Softmax st = {neg_inf(), 0.0f};
-    f32x16 o[kDT];
-#pragma unroll
-    for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
+    u32x4 qw[D / 16];
+    fetch_query<D>(qw, a, row);
 
     // Table entries and powers are loaded like the keys, a block ahead, and are
     // looked at when they are needed: a wait for one of them would be a wait for
@@ -305,6 +302,13 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
         load_keys(page);
         next = entry(at0 + kNarrowWaves);
     }
+    // the first keys are on their way while the queries are split
+    Query<D> q;
+    split_query<D>(q, qw);
+    Softmax st = {neg_inf(), 0.0f};
+    f32x16 o[kDT];
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
     for (int64_t at = at0; at < range.last; at += kNarrowWaves) {
         const bool good = page >= 0;
         u32x4 vf[kDT][2];
@@ -528,12 +532,8 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     const int tile_all = limit_of_row(a, t, t.first), all = limit_of_row(a, t, row0);
     const int blocks = (tile_seen + kKvBlock - 1) / kKvBlock;
 
-    Query<D> q;
-    load_query<D>(q, a, row);
-    Softmax st = {neg_inf(), 0.0f};
-    f32x16 o[kDT];
-#pragma unroll
-    for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
+    u32x4 qw[D / 16];
+    fetch_query<D>(qw, a, row);
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) nan_key[i / D][i % D] = kKvBlock;
     if (threadIdx.x < 2) nan_any[threadIdx.x] = 0;
 
@@ -593,15 +593,24 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     __syncthreads();  // the NaN marks are clear
     int32_t next = -1;
     int kp = 127;
-    bool edge_now = false;
+    bool edge_now = false, first_good = false;
     if (blocks > 0) {
         const int64_t page = page_of(entry(0));
         fetch(page);
         next = entry(1);
-        const bool good = page >= 0;
-        edge_now = !good || kKvBlock > tile_all;
+        edge_now = page < 0 || kKvBlock > tile_all;
+        first_good = page >= 0;
+    }
+    // the first block is on its way while the queries are split
+    Query<D> q;
+    split_query<D>(q, qw);
+    Softmax st = {neg_inf(), 0.0f};
+    f32x16 o[kDT];
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
+    if (blocks > 0) {
         stage(0, edge_now);
-        kp = key_power(kp_raw, good);
+        kp = key_power(kp_raw, first_good);
     }
     __syncthreads();
     for (int at = 0; at < blocks; ++at) {
