@@ -530,7 +530,9 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     const int tile_seen = limit_of_row(a, t, t.first + kWideRows - 1);
     const int seen = row0 < t.rows ? limit_of_row(a, t, row0 + kRows - 1) : 0;
     const int tile_all = limit_of_row(a, t, t.first), all = limit_of_row(a, t, row0);
-    const int blocks = (tile_seen + kKvBlock - 1) / kKvBlock;
+    const int part = blockIdx.z;
+    const BlockRange range = kv_part((tile_seen + kKvBlock - 1) / kKvBlock, part, a.parts);
+    const int at0 = (int)range.first, end = (int)range.last;
 
     u32x4 qw[D / 16];
     fetch_query<D>(qw, a, row);
@@ -540,7 +542,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     // table entries and powers are looked at a block after they are asked for,
     // as in the narrow kernel
     const int32_t* table = a.seqs.table + t.b * a.seqs.ld_table;
-    const auto entry = [&](int at) { return table[at < blocks ? at : blocks - 1]; };
+    const auto entry = [&](int at) { return table[at < end ? at : end - 1]; };
     const auto page_of = [&](int32_t loaded) -> int64_t {
         const int32_t p = __builtin_amdgcn_readfirstlane(loaded);
         return p >= 0 && p < a.cache.blocks ? p : -1;
@@ -594,11 +596,11 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     int32_t next = -1;
     int kp = 127;
     bool edge_now = false, first_good = false;
-    if (blocks > 0) {
-        const int64_t page = page_of(entry(0));
+    if (at0 < end) {
+        const int64_t page = page_of(entry(at0));
         fetch(page);
-        next = entry(1);
-        edge_now = page < 0 || kKvBlock > tile_all;
+        next = entry(at0 + 1);
+        edge_now = page < 0 || (at0 + 1) * kKvBlock > tile_all;
         first_good = page >= 0;
     }
     // the first block is on its way while the queries are split
@@ -608,14 +610,14 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     f32x16 o[kDT];
 #pragma unroll
     for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
-    if (blocks > 0) {
+    if (at0 < end) {
         stage(0, edge_now);
         kp = key_power(kp_raw, first_good);
     }
     __syncthreads();
-    for (int at = 0; at < blocks; ++at) {
-        const int b = at & 1, first_key = at * kKvBlock;
-        const bool more = at + 1 < blocks;
+    for (int at = at0; at < end; ++at) {
+        const int b = (at - at0) & 1, first_key = at * kKvBlock;
+        const bool more = at + 1 < end;
         const int64_t page = page_of(next);
         if (more) {
             fetch(page);
@@ -708,7 +710,21 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     // finite: NaN
     float l = st.l + __shfl_xor(st.l, 32);
     if (q.nan && row.limit > 0) l = quiet_nan();
-    const float inv = t.bad ? quiet_nan() : l == 0.0f ? 0.0f : 1.0f / l;
+    if (t.bad) l = quiet_nan();
+    if (a.parts > 1) {
+        const int64_t all_rows = a.seqs.M * a.q_heads, mine = (int64_t)part * all_rows + row.token * a.q_heads + row.head;
+        float* po = a.partial + mine * D + 4 * h;
+#pragma unroll
+        for (int d = 0; d < kDT; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(po + 32 * d + 8 * i) =
+                    make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]);
+        if (h == 0)
+            *reinterpret_cast<float2*>(a.partial + (int64_t)a.parts * all_rows * D + mine * 2) = make_float2(st.m, l);
+        return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t* out = a.out.data + row.token * a.out.row + row.head * a.out.head;
 #pragma unroll
     for (int d = 0; d < kDT; ++d)
@@ -726,35 +742,61 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
         }
 }
 
-// Joins the parts of each row; rows that no sequence has are left alone.  A
-// wave takes a row, a lane D / 64 dims of it.
-template <int D>
+// Joins the parts of each row; rows that no sequence has are left alone.  WAVES
+// waves take a row: each has the maximum and sum of every part in its lanes
+// (part s in lane s, at most 64), adds up its share of at most EACH parts, D / 64
+// dims a lane, with all their loads in flight at once, and the first adds up
+// the waves.  (64 parts of one wave's, eight loads at a time, took 12 us where
+// the attention before it takes 25.)
+constexpr int kMaxParts = 64;
+
+template <int D, int WAVES, int EACH>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
+    constexpr int kEach = D / 64;
+    typedef float Dims __attribute__((ext_vector_type(kEach)));
+    __shared__ Dims share[4][64];
     const int64_t all_rows = a.seqs.M * a.q_heads;
-    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (at >= all_rows) return;
-    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+    const int64_t at = (int64_t)blockIdx.x * (4 / WAVES) + wave / WAVES;
+    if (at >= all_rows) return;  // with one wave a row only: no barrier below
     const int64_t token = at / a.q_heads;
     const int32_t head = (int32_t)(at - token * a.q_heads);
-    if (token < a.seqs.row_start[0] || token >= a.seqs.row_start[a.seqs.B]) return;
-    const float* pm = a.partial + (int64_t)a.parts * all_rows * D;
-    float m = neg_inf();
-    for (int s = 0; s < a.parts; ++s) m = fmaxf(m, pm[(s * all_rows + at) * 2]);
-    const float ref = m == neg_inf() ? 0.0f : m;
-    constexpr int kEach = D / 64;
-    float l = 0.0f, acc[kEach] = {};
-    for (int s = 0; s < a.parts; ++s) {
-        const float ls = pm[(s * all_rows + at) * 2 + 1];
-        const float f = __builtin_amdgcn_exp2f(pm[(s * all_rows + at) * 2] - ref);
-        l += ls != ls ? ls : f * ls;
-        const float* po = a.partial + (s * all_rows + at) * D + lane * kEach;
+    const int32_t first = a.seqs.row_start[0], last = a.seqs.row_start[a.seqs.B];
+    const int mine = lane < a.parts ? lane : 0, own = wave % WAVES;
+    const float2 ml = *reinterpret_cast<const float2*>(a.partial + a.parts * all_rows * D + (mine * all_rows + at) * 2);
+    const float* po = a.partial + at * D + lane * kEach;
+    Dims v[EACH];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) acc[i] += f * po[i];
+    for (int i = 0; i < EACH; ++i) {
+        const int s = own + i * WAVES;
+        v[i] = *reinterpret_cast<const Dims*>(po + (s < a.parts ? s : 0) * all_rows * D);
+    }
+    if (token < first || token >= last) return;
+    float m = lane < a.parts ? ml.x : neg_inf();
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
+    const float w = lane < a.parts ? __builtin_amdgcn_exp2f(ml.x - (m == neg_inf() ? 0.0f : m)) : 0.0f;
+    float l = lane >= a.parts ? 0.0f : ml.y != ml.y ? ml.y : w * ml.y;
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s);
+    Dims acc = {};
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int s = own + i * WAVES;
+        const Dims more = __shfl(w, s & 63) * v[i];
+        acc += s < a.parts ? more : Dims{};
+    }
+    if constexpr (WAVES > 1) {
+        share[wave][lane] = acc;
+        __syncthreads();
+        if (own != 0) return;
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) acc += share[wave + i][lane];
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t* p = a.out.data + token * a.out.row + head * a.out.head + lane * kEach;
     if constexpr (kEach == 2)
-        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(acc[0] * inv, acc[kEach - 1] * inv);
     else
         *p = (uint16_t)pack_bf16x2(acc[0] * inv, 0.0f);
 }
@@ -764,33 +806,50 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
 AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len) {
     const int32_t group = q_heads / kv_heads;
     AttentionPlan p;
-    // pieces until two workgroups for each of 256 CUs are in flight, at least 4
-    // blocks (one a wave) to a piece
-    int64_t tiles = (M * group + kRows - 1) / kRows;
+    // 128-row tiles from 96 rows a sequence (on average) on
+    p.wide = M * group >= 96 * B;
+    const int64_t T = p.wide ? kWideRows : kRows;
+    // The keys are cut into pieces until two workgroups for each of 256 CUs are
+    // in flight, but not below 8 blocks to a piece of a narrow tile (2 a wave;
+    // none below 32 blocks) and 4 of a wide one.  One token of 32 query and 8
+    // key/value heads over 16,384 keys: 12.2 us with pieces of 8, 18 of 16, 20 of
+    // 32; over 1024 keys 9.9 us in one piece, 10.4 in two.  40 tokens over 2048
+    // keys: 16 us with pieces of 4, 20 of 8.
+    int64_t tiles = (M * group + T - 1) / T;
     tiles = tiles < B ? B : tiles;
     const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock;
-    const int64_t want = 512 / (tiles * kv_heads), most = blocks / 4;
-    p.wide = M * group >= 96 * B;
-    p.parts = p.wide ? 1 : (int32_t)clamp64(want < most ? want : most, 1, 64);
+    const int64_t want = 512 / (tiles * kv_heads), most = p.wide ? blocks / 4 : blocks >= 32 ? blocks / 8 : 1;
+    p.parts = (int32_t)clamp64(want < most ? want : most, 1, kMaxParts);
     p.workspace_bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)(M * q_heads) * (size_t)(dim + 2) * sizeof(float);
     return p;
 }
 
 template <int D>
 static void attention_of(const AttentionArgs& a, hipStream_t s) {
+    const int64_t units = tile_units(a.seqs.M, a.seqs.B, a.group, a.wide ? kWideRows : kRows);
     if (a.wide) {
-        const int64_t units = tile_units(a.seqs.M, a.seqs.B, a.group, kWideRows);
         const bool flat = units * a.cache.heads < ((int64_t)1 << 23);  // workgroups x threads below 2^32
-        const dim3 grid((unsigned)(flat ? units * a.cache.heads : units), flat ? 1u : (unsigned)a.cache.heads);
+        const dim3 grid((unsigned)(flat ? units * a.cache.heads : units), flat ? 1u : (unsigned)a.cache.heads,
+                        (unsigned)a.parts);
         attention_wide_kernel<D><<<grid, dim3(64 * kWideWaves), 0, s>>>(a);
-        return;
+    } else {
+        const dim3 grid((unsigned)units, (unsigned)a.cache.heads, (unsigned)a.parts);
+        attention_narrow_kernel<D><<<grid, dim3(64 * kNarrowWaves), 0, s>>>(a);
     }
-    const dim3 grid((unsigned)tile_units(a.seqs.M, a.seqs.B, a.group, kRows), (unsigned)a.cache.heads, (unsigned)a.parts);
-    attention_narrow_kernel<D><<<grid, dim3(64 * kNarrowWaves), 0, s>>>(a);
-    if (a.parts > 1) {
-        const int64_t rows = a.seqs.M * a.q_heads;
-        attention_join_kernel<D><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s>>>(a);
-    }
+    const int64_t rows = a.seqs.M * a.q_heads;
+    const dim3 four((unsigned)((rows + 3) / 4)), one((unsigned)rows), threads(256);
+    if (a.parts > 32)
+        attention_join_kernel<D, 4, 16><<<one, threads, 0, s>>>(a);
+    else if (a.parts > 16)
+        attention_join_kernel<D, 4, 8><<<one, threads, 0, s>>>(a);
+    else if (a.parts > 8)
+        attention_join_kernel<D, 4, 4><<<one, threads, 0, s>>>(a);
+    else if (a.parts > 4)
+        attention_join_kernel<D, 1, 8><<<four, threads, 0, s>>>(a);
+    else if (a.parts > 2)
+        attention_join_kernel<D, 1, 4><<<four, threads, 0, s>>>(a);
+    else if (a.parts > 1)
+        attention_join_kernel<D, 1, 2><<<four, threads, 0, s>>>(a);
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {
