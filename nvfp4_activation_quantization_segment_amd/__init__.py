@@ -557,33 +557,29 @@ def _heads(name: str, x: torch.Tensor, shape=None) -> Heads:
     return Heads(x.data_ptr(), row if got[0] > 1 else 0, head if got[1] > 1 else 0)
 
 
-def _int32(name: str, t: torch.Tensor, dims: int):
-    """The tensor's shape and strides, once it is found to be what the library takes."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name}: expected int32, got {t.dtype}")
-    if len(shape) != dims or (stride[-1] != 1 and shape[-1] > 1):
-        raise ValueError(f"{name} must have {dims} dimension(s) and unit stride along the last")
-    return shape, stride
-
-
 def _rope_params(tables, positions: torch.Tensor, rows: int, split: bool, dev: torch.device) -> RopeParams:
     axes = len(tables)
     if not 1 <= axes <= ROPE_MAX_AXES:
         raise ValueError(f"expected 1 to {ROPE_MAX_AXES} tables, got {axes}")
-    shape, stride = _int32("positions", positions, 2)
-    if shape != (rows, axes):
-        raise ValueError(f"positions: expected [{rows}, {axes}], got {list(shape)}")
-    _same_device(dev, positions, *tables)
-    p = RopeParams(axes, 1 if split else 0)
-    for a, t in enumerate(tables):
+    if positions.dtype != torch.int32:
+        raise TypeError(f"positions: expected int32, got {positions.dtype}")
+    if positions.shape != (rows, axes) or (axes > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions: expected [{rows}, {axes}] with unit stride along the last, got "
+                         f"{list(positions.shape)}, strides {positions.stride()}")
+    if positions.device != dev:
+        raise ValueError(f"positions are on {positions.device}, expected {dev}")
+    sizes, pairs, data = [], [], []
+    for t in tables:
         shape = t.shape
         if t.dtype != torch.float32 or len(shape) != 3 or shape[2] != 2 or not t.is_contiguous():
             raise ValueError("a rope table is a contiguous fp32 [positions, pairs, 2]")
-        p.rows[a], p.pairs[a], _ = shape
-        p.table[a] = t.data_ptr()
-    p.positions, p.ld_positions = positions.data_ptr(), stride[0] if rows > 1 else axes
-    return p
+        if t.device != dev:
+            raise ValueError(f"a rope table is on {t.device}, expected {dev}")
+        sizes.append(shape[0])
+        pairs.append(shape[1])
+        data.append(t.data_ptr())
+    return RopeParams(axes, 1 if split else 0, tuple(pairs), tuple(sizes), tuple(data), positions.data_ptr(),
+                      positions.stride(0) if rows > 1 else axes)
 
 
 def _empty(dev: torch.device, stream, shape, dtype=torch.bfloat16) -> torch.Tensor:
@@ -652,17 +648,18 @@ class KvCache:
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_power: torch.Tensor, v_power: torch.Tensor):
         if k.dim() != 5:
             raise ValueError("k must be [blocks, heads, dim / 16, 64, 16]")
-        blocks, heads, groups, _, _ = shape = k.shape
-        dim = 16 * groups
-        for name, t, want in (("k", k, (blocks, heads, groups, KV_BLOCK, 16)), ("v", v, (blocks, heads, 4, dim, 16)),
-                              ("k_power", k_power, shape[:2]), ("v_power", v_power, shape[:2])):
-            if t.dtype != torch.uint8:
-                raise TypeError(f"{name}: expected uint8, got {t.dtype}")
-            if t.shape != want or not t.is_contiguous():
-                raise ValueError(f"{name}: expected contiguous {list(want)}, got {list(t.shape)}")
-        _same_device(k.device, v, k_power, v_power)
+        blocks, heads, groups, block, sixteen = k.shape
+        dim, dev, u8 = 16 * groups, k.device, torch.uint8
+        if not (k.dtype == v.dtype == k_power.dtype == v_power.dtype == u8):
+            raise TypeError(f"expected uint8, got {[t.dtype for t in (k, v, k_power, v_power)]}")
+        if (block != KV_BLOCK or sixteen != 16 or v.shape != (blocks, heads, 4, dim, 16) or
+                k_power.shape != (blocks, heads) or v_power.shape != (blocks, heads) or
+                not (k.is_contiguous() and v.is_contiguous() and k_power.is_contiguous() and v_power.is_contiguous())):
+            raise ValueError(f"expected contiguous {[blocks, heads, groups, KV_BLOCK, 16]}, {[blocks, heads, 4, dim, 16]} "
+                             f"and twice {[blocks, heads]}, got {[list(t.shape) for t in (k, v, k_power, v_power)]}")
+        _same_device(dev, v, k_power, v_power)
         self.k, self.v, self.k_power, self.v_power = k, v, k_power, v_power
-        self.blocks, self.heads, self.dim, self.device = blocks, heads, dim, k.device
+        self.blocks, self.heads, self.dim, self.device = blocks, heads, dim, dev
         self._struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_power.data_ptr(), v_power.data_ptr(), blocks, heads,
                                      dim)
 
@@ -676,12 +673,20 @@ class KvCache:
 
 
 def _sequences(row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, dev: torch.device) -> KvSequences:
-    _same_device(dev, row_start, lens, table)
-    (starts,), _ = _int32("row_start", row_start, 1)
-    (n,), _ = _int32("lens", lens, 1)
-    (rows, blocks), (ld, _) = _int32("table", table, 2)
-    if starts != n + 1 or rows != n:
-        raise ValueError(f"{n} lengths need {n + 1} row starts and {n} table rows, got {starts} and {rows}")
+    if not (row_start.dtype == lens.dtype == table.dtype == torch.int32):
+        raise TypeError(f"row_start, lens and table: expected int32, got {row_start.dtype}, {lens.dtype} and {table.dtype}")
+    if row_start.device != dev or lens.device != dev or table.device != dev:
+        raise ValueError(f"row_start, lens and table are on {row_start.device}, {lens.device} and {table.device}, expected "
+                         f"{dev}")
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [sequences, blocks], got {list(table.shape)}")
+    n, blocks = table.shape
+    ld, unit = table.stride()
+    if row_start.shape != (n + 1,) or lens.shape != (n,):
+        raise ValueError(f"a table of {n} sequences needs {n + 1} row starts and {n} lengths, got {list(row_start.shape)} "
+                         f"and {list(lens.shape)}")
+    if (unit != 1 and blocks > 1) or row_start.stride(0) != 1 or (n > 1 and lens.stride(0) != 1):
+        raise ValueError("row_start, lens and table must have unit stride along the last dimension")
     return KvSequences(n, row_start.data_ptr(), lens.data_ptr(), table.data_ptr(), ld if n > 1 else blocks, blocks)
 
 

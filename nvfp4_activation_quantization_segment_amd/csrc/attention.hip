@@ -818,7 +818,12 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
     int64_t tiles = (M * group + T - 1) / T;
     tiles = tiles < B ? B : tiles;
     const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock;
-    const int64_t want = 512 / (tiles * kv_heads), most = p.wide ? blocks / 4 : blocks >= 32 ? blocks / 8 : 1;
+    int64_t want = 512 / (tiles * kv_heads);
+    // Many sequences are of many lengths, which the host does not know: pieces
+    // half as long even the workgroups out (32 sequences of 1 to 16,384 keys: 123
+    // -> 115 us; 32 of 8192: 113 -> 110; 4 of 16,384: 27 -> 30, so few are left).
+    if (!p.wide && B >= 16 && want >= 2) want *= 2;
+    const int64_t most = p.wide ? blocks / 4 : blocks >= 32 ? blocks / 8 : 1;
     p.parts = (int32_t)clamp64(want < most ? want : most, 1, kMaxParts);
     p.workspace_bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)(M * q_heads) * (size_t)(dim + 2) * sizeof(float);
     return p;
