@@ -489,7 +489,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences
  * a query is split into two E4M3 numbers that together hold each bf16 element
  * to its last bit, or to 2^-21 of the row's largest element where that is
  * more.  Probabilities are rounded to bf16 for the product with the values, and
- * the output once to bf16.  The order of the sums depends on the sizes and
+ * the output once to bf16.  (The sums run against a reference that may lie a few
+ * powers of two below the maximum; values above 2^96 can overflow them.)  The order of the sums depends on the sizes and
  * max_len only: the same call gives the same bytes.
  * max_len is the host's bound on the lengths, used to decide how far the keys
  * of few rows are shared out over workgroups (results for longer sequences are

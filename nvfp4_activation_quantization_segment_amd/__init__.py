@@ -615,6 +615,8 @@ def rope_table(positions: int, pairs: int, theta: float = 10000.0, device=None, 
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     _same_device(dev)
+    if not (0 < positions < 2**31 and 0 < pairs < 2**31):
+        raise ValueError(f"expected positions and pairs of 1 to 2^31 - 1, got {positions} and {pairs}")
     table = _empty(dev, stream, (positions, pairs, 2), torch.float32)
     _call("nvfp4_rope_table", lib.nvfp4_rope_table, dev, stream, table.data_ptr(), positions, pairs, float(theta))
     return table
@@ -750,6 +752,8 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
     s = _sequences(row_start, lens, table, dev)
     if max_len is None:
         max_len = table.shape[1] * KV_BLOCK
+    if not 0 <= causal_block < 2**31:
+        raise ValueError(f"causal_block: expected 0 to 2^31 - 1, got {causal_block}")
     if out is None:
         out = _empty(dev, stream, shape)
     if workspace is None and rows:

@@ -806,7 +806,10 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
 AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len) {
     const int32_t group = q_heads / kv_heads;
     AttentionPlan p;
-    // 128-row tiles from 96 rows a sequence (on average) on
+    // 128-row tiles from 96 rows a sequence (on average) on.  8 sequences, 32 query
+    // and 8 key/value heads: 128 rows over 30,000 keys 212 us (narrow tiles 328),
+    // over 3000 keys 49 (45), 96 rows over 3000 37 (35); 32 sequences of 100 rows
+    // and keys, 16 heads of 64: 12 us (25).
     p.wide = M * group >= 96 * B;
     const int64_t T = p.wide ? kWideRows : kRows;
     // The keys are cut into pieces until two workgroups for each of 256 CUs are

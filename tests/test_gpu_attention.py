@@ -454,11 +454,12 @@ def test_rows_that_see_nothing(nv, rows):
         assert bool((out[rs[1]:rs[2] - 5] == 0).all())
 
 
-@pytest.mark.parametrize("dim,group,news", [(64, 1, [1, 1]), (128, 2, [40, 3]), (128, 1, [150, 130]), (64, 4, [200, 70])])
-def test_what_is_hidden_has_no_effect(nv, dim, group, news):
+@pytest.mark.parametrize("dim,group,news,past", [
+    (64, 1, [1, 1], [70, 100]), (128, 2, [40, 3], [70, 100]), (128, 1, [150, 130], [70, 100]), (64, 4, [200, 70], [70, 100]),
+    (128, 2, [3, 1], [2500, 3001]), (64, 1, [150, 99], [2500, 1900])])  # the last two share the keys out
+def test_what_is_hidden_has_no_effect(nv, dim, group, news, past):
     """NaN codes behind the last position and in masked places: the outputs' bytes do not change.  A NaN that a row
     sees reaches that row, and no other."""
-    past = [70, 100]
     lens = [p + n for p, n in zip(past, news)]
     pool = Pool(nv, 84, 2, dim, lens)
     q = normal(gen(85), sum(news), 2 * group, dim)
@@ -553,6 +554,78 @@ def test_scores_far_apart(nv):
     got = nv.kv_attention(q.cuda(), pool.gpu, i32([0, 5]), pool.lens, pool.tab, scale=1.0)
     want, tol = kv_ref.attention(q.double().numpy(), pool.ref, [0, 5], [n], pool.table, 1.0, 0, bounds=True)
     check(got, want, tol)
+
+
+@pytest.mark.parametrize("count", [62, 63, 64, 65, 300, 4200])
+def test_many_sequences(nv, count):
+    """Counts around and above the 64 that are looked up at once: written, read back and attended, each sequence by
+    itself; some have no rows."""
+    heads, dim = 1, 64
+    g = gen(count)
+    news = torch.randint(0, 4, (count,), generator=g).tolist()
+    past = torch.randint(0, 70, (count,), generator=g).tolist()
+    lens = [p + n for p, n in zip(past, news)]
+    pool = Pool(nv, count, heads, dim, lens)
+    rows, rs = sum(news), starts(news)
+    k, v, q = (normal(g, rows, n, dim) for n in (heads, heads, 2))
+    nv.kv_write(pool.gpu, k.cuda(), v.cuda(), i32(rs), pool.lens, pool.tab)
+    pool.ref.write((k.double().numpy(), v.double().numpy()), rs, lens, pool.table)
+    pool.same()
+    back = nv.kv_read(pool.gpu, rows, i32(rs), pool.lens, pool.tab)
+    want = [np.concatenate([pool.ref.sequence(kind, 0, pool.table[b], lens[b])[past[b]:] for b in range(count)]) for kind in range(2)]
+    for kind in range(2):
+        assert np.array_equal(back[kind][:, 0].cpu().double().numpy(), want[kind])
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1)
+    ref, tol = kv_ref.attention(q.double().numpy(), pool.ref, rs, lens, pool.table, np.float64(np.float32(0.125)), 1, bounds=True)
+    check(got, ref, tol)
+
+
+def test_a_pool_past_4_gib(nv):
+    """Blocks whose offsets pass 32 bits: the same rows through the pool's first and last blocks."""
+    heads, dim, n = 8, 128, 200
+    blocks = 2**32 // (heads * 64 * dim) + 100  # 4 GiB of keys and as much of values
+    pool = nv.KvCache.empty(blocks, heads, dim)
+    g = gen(7)
+    k, v, q = (normal(g, n, h, dim).cuda() for h in (heads, heads, 2 * heads))
+    rs, lens = i32([0, n]), i32([n])
+    got = []
+    for table in ([0, 1, 2, 3], [blocks - 1, blocks - 90, blocks - 2, blocks - 50]):
+        tab = i32([table])
+        nv.kv_write(pool, k, v, rs, lens, tab)
+        got.append([*nv.kv_read(pool, n, rs, lens, tab), nv.kv_attention(q, pool, rs, lens, tab, causal_block=1),
+                    nv.kv_attention(q[-1:], pool, i32([0, 1]), lens, tab, causal_block=1)])
+    for a, b in zip(*got):
+        assert same(a, b)
+    assert float(got[0][0].double().abs().max()) > 1
+
+
+def test_rows_further_apart_than_2_gib(nv):
+    """Row strides of 2^31 elements: inputs and outputs of each operator spread over one allocation."""
+    heads, dim, stride = 2, 64, 2**31
+    store = torch.zeros(2 * stride + heads * dim, dtype=torch.bfloat16, device="cuda")
+    far = torch.as_strided(store, (3, heads, dim), (stride, dim, 1))
+    g = gen(8)
+    x = normal(g, 3, heads, dim).cuda()
+    tables = [nv.rope_table(9, 16)]
+    pos = i32([[1], [8], [0]])
+    near = nv.rope(x, tables, pos)
+    far.copy_(x)
+    assert same(nv.rope(far, tables, pos), near)
+    nv.rope(far, tables, pos, out=far)
+    assert same(far, near)
+    one, two = (Pool(nv, 9, heads, dim, [3], filled=False) for _ in range(2))
+    rs = i32([0, 3])
+    nv.kv_write(one.gpu, near, near, rs, one.lens, one.tab)
+    nv.kv_write(two.gpu, far, far, rs, two.lens, two.tab)
+    for a, b in zip(one.pulled(), two.pulled()):
+        assert np.array_equal(a, b)
+    want = nv.kv_attention(near, one.gpu, rs, one.lens, one.tab)
+    assert same(nv.kv_attention(far, one.gpu, rs, one.lens, one.tab), want)
+    back = nv.kv_read(one.gpu, 3, rs, one.lens, one.tab)
+    nv.kv_attention(near, one.gpu, rs, one.lens, one.tab, out=far)
+    assert same(far, want)
+    nv.kv_read(one.gpu, 3, rs, one.lens, one.tab, k=far, v=torch.empty_like(near))
+    assert same(far, back[0])
 
 
 # ---------------------------------------------------------------------------
@@ -683,6 +756,11 @@ def test_another_devices_or_types_are_refused(nv):
         nv.kv_attention(q.cuda(), pool.gpu, rs.long(), pool.lens, pool.tab)
     with pytest.raises(nv.Nvfp4Error):
         nv.kv_attention(q.cuda(), pool.gpu, rs, pool.lens, pool.tab, scale=0.0)
+    for c in (-1, 2**31, 2**32):
+        with pytest.raises(ValueError):
+            nv.kv_attention(q.cuda(), pool.gpu, rs, pool.lens, pool.tab, causal_block=c)
+    with pytest.raises(ValueError):
+        nv.rope_table(4, 2**32 + 8)
     with pytest.raises(nv.Nvfp4Error):  # an output whose heads overlap
         nv.kv_attention(q.cuda(), pool.gpu, rs, pool.lens, pool.tab, out=torch.empty_like(q.cuda()[:1]).expand(4, 1, 64))
     with pytest.raises(ValueError):
