@@ -263,11 +263,11 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     const int c = lane & 31, h = lane >> 5;
     const int kv_head = blockIdx.y, part = blockIdx.z;
     const Row row = find_row(a, t, t.first + c, kv_head);
-    // blocks that the tile's last row sees, and keys that all its rows see
-    const int seen = limit_of_row(a, t, t.first + kRows - 1);
-    const int all = limit_of_row(a, t, t.first);
+    // keys that the tile's last row sees, and keys that all its rows see: limits
+    // do not fall from row to row
+    const int seen = __builtin_amdgcn_readlane(row.limit, kRows - 1), all = __builtin_amdgcn_readlane(row.limit, 0);
     const BlockRange range = kv_part((seen + kKvBlock - 1) / kKvBlock, part, a.parts);
-    const int64_t at0 = range.first + wave;
+    const int at0 = range.first + wave;
     u32x4 qw[D / 16];
     fetch_query<D>(qw, a, row);
 
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     // looked at when they are needed: a wait for one of them would be a wait for
     // every load before it.
     const int32_t* table = a.seqs.table + t.b * a.seqs.ld_table;
-    const auto entry = [&](int64_t at) { return table[at < range.last ? at : range.last - 1]; };
+    const auto entry = [&](int at) { return table[at < range.last ? at : range.last - 1]; };
     const auto page_of = [&](int32_t loaded) -> int64_t {
         const int32_t p = __builtin_amdgcn_readfirstlane(loaded);
         return p >= 0 && p < a.cache.blocks ? p : -1;
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     f32x16 o[kDT];
 #pragma unroll
     for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
-    for (int64_t at = at0; at < range.last; at += kNarrowWaves) {
+    for (int at = at0; at < range.last; at += kNarrowWaves) {
         const bool good = page >= 0;
         u32x4 vf[kDT][2];
         {
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
             next = entry(at + 2 * kNarrowWaves);
         }
 
-        const int first_key = (int)at * kKvBlock;
+        const int first_key = at * kKvBlock;
         const bool edge = first_key + kKvBlock > all;
         if (edge) {
             mask_scores(s[0], row.limit - first_key);
@@ -527,12 +527,12 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     const Row row = find_row(a, t, row0 + c, kv_head);
     // keys that the tile's last row and this wave's last row see, and keys that
     // all rows of the tile and of the wave see
-    const int tile_seen = limit_of_row(a, t, t.first + kWideRows - 1);
-    const int seen = row0 < t.rows ? limit_of_row(a, t, row0 + kRows - 1) : 0;
-    const int tile_all = limit_of_row(a, t, t.first), all = limit_of_row(a, t, row0);
+    const int tile_seen = limit_of_row(a, t, t.first + kWideRows - 1), tile_all = limit_of_row(a, t, t.first);
+    const int seen = row0 < t.rows ? __builtin_amdgcn_readlane(row.limit, kRows - 1) : 0;
+    const int all = __builtin_amdgcn_readlane(row.limit, 0);
     const int part = blockIdx.z;
     const BlockRange range = kv_part((tile_seen + kKvBlock - 1) / kKvBlock, part, a.parts);
-    const int at0 = (int)range.first, end = (int)range.last;
+    const int at0 = range.first, end = range.last;
 
     u32x4 qw[D / 16];
     fetch_query<D>(qw, a, row);

@@ -73,14 +73,16 @@ constexpr int32_t kv_limit(int32_t pos, int32_t len, int32_t causal) {
     return left > len - pos ? len : pos + left;
 }
 
-// Blocks [first, last) of part s of S of a row tile that sees n blocks.
+// Blocks [first, last) of part s of S of a row tile that sees n blocks (n below
+// 2^25, S at most 64).
 struct BlockRange {
-    int64_t first, last;
+    int32_t first, last;
 };
-constexpr BlockRange kv_part(int64_t n, int64_t s, int64_t S) {
-    const int64_t per = (n + S - 1) / S;
-    const int64_t a = clamp64(s * per, 0, n);
-    return BlockRange{a, clamp64(a + per, a, n)};
+constexpr BlockRange kv_part(int32_t n, int32_t s, int32_t S) {
+    if (S == 1) return BlockRange{0, n};
+    const int32_t per = (n + S - 1) / S;
+    const int32_t a = s * per < n ? s * per : n;
+    return BlockRange{a, a + per < n ? a + per : n};
 }
 
 }  // namespace nvfp4
