@@ -336,6 +336,36 @@ def nvfp4_modulate_gemm_ring(x, M, K, ldx, seg, ws, tensor_scale, amax_out, ring
                                         gemm_workspace_bytes, _stream(stream)))
 
 
+# The rotary, cache and attention entry points take the structures Heads,
+# RopeParams, KvCacheStruct and KvSequences (make_heads, make_rope_params,
+# KvCache.struct, make_kv_sequences); their tensors must outlive the call.
+def nvfp4_rope_table(table, rows, pairs, theta, stream=None):
+    _check("nvfp4_rope_table", lib.nvfp4_rope_table(_ptr(table), rows, pairs, theta, _stream(stream)))
+
+
+def nvfp4_rope(x, M, heads, dim, rope, out, stream=None):
+    _check("nvfp4_rope", lib.nvfp4_rope(x, M, heads, dim, rope, out, _stream(stream)))
+
+
+def nvfp4_kv_write(cache, seqs, M, k, v, rope=None, stream=None):
+    _check("nvfp4_kv_write", lib.nvfp4_kv_write(cache, seqs, M, k, v, rope, _stream(stream)))
+
+
+def nvfp4_kv_read(cache, seqs, M, k, v, stream=None):
+    _check("nvfp4_kv_read", lib.nvfp4_kv_read(cache, seqs, M, k, v, _stream(stream)))
+
+
+def nvfp4_kv_attention_workspace_bytes(M, count, q_heads, heads, dim, max_len):
+    return int(lib.nvfp4_kv_attention_workspace_bytes(M, count, q_heads, heads, dim, max_len))
+
+
+def nvfp4_kv_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len, out, workspace, workspace_bytes,
+                       stream=None):
+    _check("nvfp4_kv_attention",
+           lib.nvfp4_kv_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len, out, _ptr(workspace),
+                                  workspace_bytes, _stream(stream)))
+
+
 def nvfp4_step_modulate(x, scale, shift, y, n, stream=None):
     _check("nvfp4_step_modulate",
            lib.nvfp4_step_modulate(_ptr(x), _ptr(scale), _ptr(shift), _ptr(y), n, _stream(stream)))
@@ -544,7 +574,8 @@ def _same_device(dev: torch.device, *tensors):
             raise ValueError(f"a tensor is on {t.device}, expected {dev}")
 
 
-def _heads(name: str, x: torch.Tensor, shape=None) -> Heads:
+def make_heads(name: str, x: torch.Tensor, shape=None) -> Heads:
+    """The C description of heads [rows, heads, dim] (bf16, unit stride along dim); `name` is for its messages."""
     got = x.shape
     if x.dtype != torch.bfloat16:
         raise TypeError(f"{name}: expected bf16, got {x.dtype}")
@@ -557,7 +588,8 @@ def _heads(name: str, x: torch.Tensor, shape=None) -> Heads:
     return Heads(x.data_ptr(), row if got[0] > 1 else 0, head if got[1] > 1 else 0)
 
 
-def _rope_params(tables, positions: torch.Tensor, rows: int, split: bool, dev: torch.device) -> RopeParams:
+def make_rope_params(tables, positions: torch.Tensor, rows: int, split: bool, dev: torch.device) -> RopeParams:
+    """The C description of rotary positions: one [positions, pairs, 2] table for each axis, positions [rows, axes]."""
     axes = len(tables)
     if not 1 <= axes <= ROPE_MAX_AXES:
         raise ValueError(f"expected 1 to {ROPE_MAX_AXES} tables, got {axes}")
@@ -584,10 +616,18 @@ def _rope_params(tables, positions: torch.Tensor, rows: int, split: bool, dev: t
 
 def _empty(dev: torch.device, stream, shape, dtype=torch.bfloat16) -> torch.Tensor:
     """A new tensor of the stream that the call runs on."""
-    if stream is None and dev.index == torch.cuda.current_device():
+    if stream is None and dev.index == torch._C._cuda_getDevice():
         return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(_torch_stream(stream, dev)):
         return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _output(name: str, t, dev: torch.device, stream, shape):
+    """The caller's output once checked, or a new one, and its description."""
+    if t is not None:
+        return t, make_heads(name, t, shape)
+    t = _empty(dev, stream, shape)
+    return t, Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
 
 
 def _call(name: str, fn, dev: torch.device, stream, *args):
@@ -599,7 +639,7 @@ def _call(name: str, fn, dev: torch.device, stream, *args):
         if st.device != dev:
             raise ValueError(f"the stream is on {st.device}, the tensors on {dev}")
         raw = st.cuda_stream
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             status = fn(*args, raw)
     else:
@@ -630,12 +670,10 @@ def rope(x: torch.Tensor, tables, positions: torch.Tensor, split: bool = False, 
     Pairs are neighbouring dims, or with split dims half of the rotated part apart.  out may be x."""
     dev = x.device
     _same_device(dev, out)
-    hx = _heads("x", x)
+    hx = make_heads("x", x)
     rows, heads, dim = shape = x.shape
-    r = _rope_params(tables, positions, rows, split, dev)
-    if out is None:
-        out = _empty(dev, stream, shape)
-    ho = _heads("out", out, shape)
+    r = make_rope_params(tables, positions, rows, split, dev)
+    out, ho = _output("out", out, dev, stream, shape)
     if rows:
         _call("nvfp4_rope", lib.nvfp4_rope, dev, stream, hx, rows, heads, dim, r, ho)
     return out
@@ -662,7 +700,7 @@ class KvCache:
         _same_device(dev, v, k_power, v_power)
         self.k, self.v, self.k_power, self.v_power = k, v, k_power, v_power
         self.blocks, self.heads, self.dim, self.device = blocks, heads, dim, dev
-        self._struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_power.data_ptr(), v_power.data_ptr(), blocks, heads,
+        self.struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_power.data_ptr(), v_power.data_ptr(), blocks, heads,
                                      dim)
 
     @classmethod
@@ -674,7 +712,8 @@ class KvCache:
                    make(blocks, heads))
 
 
-def _sequences(row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, dev: torch.device) -> KvSequences:
+def make_kv_sequences(row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, dev: torch.device) -> KvSequences:
+    """The C description of sequences: row_start [n + 1], lens [n] and table [n, blocks], int32."""
     if not (row_start.dtype == lens.dtype == table.dtype == torch.int32):
         raise TypeError(f"row_start, lens and table: expected int32, got {row_start.dtype}, {lens.dtype} and {table.dtype}")
     if row_start.device != dev or lens.device != dev or table.device != dev:
@@ -703,15 +742,15 @@ def kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, row_start: torch.
     _same_device(dev, k, v)
     rows = k.shape[0]
     shape = (rows, cache.heads, cache.dim)
-    hk, hv = _heads("k", k, shape), _heads("v", v, shape)
-    q = _sequences(row_start, lens, table, dev)
+    hk, hv = make_heads("k", k, shape), make_heads("v", v, shape)
+    q = make_kv_sequences(row_start, lens, table, dev)
     r = None
     if len(tables):
         if positions is None:
             raise ValueError("rotating the keys needs their positions")
-        r = _rope_params(tables, positions, rows, split, dev)
+        r = make_rope_params(tables, positions, rows, split, dev)
     if rows:
-        _call("nvfp4_kv_write", lib.nvfp4_kv_write, dev, stream, cache._struct, q, rows, hk, hv, r)
+        _call("nvfp4_kv_write", lib.nvfp4_kv_write, dev, stream, cache.struct, q, rows, hk, hv, r)
 
 
 def kv_read(cache: KvCache, rows: int, row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
@@ -719,18 +758,13 @@ def kv_read(cache: KvCache, rows: int, row_start: torch.Tensor, lens: torch.Tens
     """Reads the positions of `rows` rows (as kv_write addresses them) back: k and v, bf16 [rows, heads, dim]."""
     dev = cache.device
     _same_device(dev, k, v)
-    q = _sequences(row_start, lens, table, dev)
+    q = make_kv_sequences(row_start, lens, table, dev)
     shape = (rows, cache.heads, cache.dim)
-    k = _empty(dev, stream, shape) if k is None else k
-    v = _empty(dev, stream, shape) if v is None else v
-    hk, hv = _heads("k", k, shape), _heads("v", v, shape)
+    k, hk = _output("k", k, dev, stream, shape)
+    v, hv = _output("v", v, dev, stream, shape)
     if rows:
-        _call("nvfp4_kv_read", lib.nvfp4_kv_read, dev, stream, cache._struct, q, rows, hk, hv)
+        _call("nvfp4_kv_read", lib.nvfp4_kv_read, dev, stream, cache.struct, q, rows, hk, hv)
     return k, v
-
-
-def nvfp4_kv_attention_workspace_bytes(M, count, q_heads, heads, dim, max_len):
-    return int(lib.nvfp4_kv_attention_workspace_bytes(M, count, q_heads, heads, dim, max_len))
 
 
 def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
@@ -745,25 +779,25 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
     on the stream that the call runs on."""
     dev = cache.device
     _same_device(dev, q, out, workspace)
-    hq = _heads("q", q)
+    hq = make_heads("q", q)
     rows, q_heads, dim = shape = q.shape
     if dim != cache.dim:
         raise ValueError(f"q has heads of {dim}, the cache of {cache.dim}")
-    s = _sequences(row_start, lens, table, dev)
+    s = make_kv_sequences(row_start, lens, table, dev)
     if max_len is None:
         max_len = table.shape[1] * KV_BLOCK
     if not 0 <= causal_block < 2**31:
         raise ValueError(f"causal_block: expected 0 to 2^31 - 1, got {causal_block}")
-    if out is None:
-        out = _empty(dev, stream, shape)
+    out, ho = _output("out", out, dev, stream, shape)
     if workspace is None and rows:
         need = lib.nvfp4_kv_attention_workspace_bytes(rows, s.count, q_heads, cache.heads, dim, max_len)
         if need:
             workspace = _empty(dev, stream, (need,), torch.uint8)
-    ho = _heads("out", out, shape)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if rows:
-        _call("nvfp4_kv_attention", lib.nvfp4_kv_attention, dev, stream, hq, rows, q_heads, cache._struct, s,
+        _call("nvfp4_kv_attention", lib.nvfp4_kv_attention, dev, stream, hq, rows, q_heads, cache.struct, s,
               dim ** -0.5 if scale is None else float(scale), causal_block, max_len, ho,
               None if workspace is None else workspace.data_ptr(), size)
     return out

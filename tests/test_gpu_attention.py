@@ -742,6 +742,46 @@ def test_from_projection_to_projection(nv):
         assert tuple(y.shape) == (rows, width) and bool(y.isfinite().all())
 
 
+def test_c_entry_points_by_name(nv):
+    """The functions named like the C entry points, on the structures that the conveniences build, with a workspace of
+    the caller's: the same bytes."""
+    heads, dim, n = 2, 64, 3000
+    g = gen(104)
+    k, v, q = (normal(g, n, h, dim).cuda() for h in (heads, heads, 4))
+    dev = k.device
+    one, two = (Pool(nv, 105, heads, dim, [n], filled=False) for _ in range(2))
+    table = torch.empty(50, 32, 2, device="cuda")
+    nv.nvfp4_rope_table(table, 50, 32, 10000.0)
+    assert torch.equal(table, nv.rope_table(50, 32))
+    pos = (torch.arange(n).int() % 50)[:, None].cuda()
+    rs, lens = i32([0, n]), i32([n])
+    r, s = nv.make_rope_params([table], pos, n, True, dev), nv.make_kv_sequences(rs, lens, two.tab, dev)
+    turned = nv.rope(q, [table], pos, split=True)
+    out = torch.empty_like(q)
+    nv.nvfp4_rope(nv.make_heads("q", q), n, 4, dim, r, nv.make_heads("out", out))
+    assert same(out, turned)
+    nv.kv_write(one.gpu, k, v, rs, lens, one.tab, tables=[table], positions=pos, split=True)
+    nv.nvfp4_kv_write(two.gpu.struct, s, n, nv.make_heads("k", k), nv.make_heads("v", v), r)
+    for a, b in zip(one.pulled(), two.pulled()):
+        assert np.array_equal(a, b)
+    back = torch.empty_like(k), torch.empty_like(v)
+    nv.nvfp4_kv_read(two.gpu.struct, s, n, nv.make_heads("k", back[0]), nv.make_heads("v", back[1]))
+    for a, b in zip(back, nv.kv_read(one.gpu, n, rs, lens, one.tab)):
+        assert same(a, b)
+    last = i32([0, 1])
+    want = nv.kv_attention(turned[-1:], one.gpu, last, lens, one.tab)
+    need = nv.nvfp4_kv_attention_workspace_bytes(1, 1, 4, heads, dim, 64 * one.table.shape[1])
+    assert need > 0
+    ws, got = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.empty_like(want)
+    s1 = nv.make_kv_sequences(last, lens, two.tab, dev)
+    nv.nvfp4_kv_attention(nv.make_heads("q", turned[-1:]), 1, 4, two.gpu.struct, s1, dim ** -0.5, 0, 64 * one.table.shape[1],
+                          nv.make_heads("out", got), ws, need)
+    assert same(got, want)
+    assert same(nv.kv_attention(turned[-1:], one.gpu, last, lens, one.tab, workspace=ws), want)
+    with pytest.raises(nv.Nvfp4Error):
+        nv.kv_attention(turned[-1:], one.gpu, last, lens, one.tab, workspace=ws[:need // 2])
+
+
 def test_another_devices_or_types_are_refused(nv):
     pool = Pool(nv, 103, 1, 64, [64])
     q = normal(gen(1), 4, 1, 64)
