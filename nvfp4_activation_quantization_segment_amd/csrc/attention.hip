@@ -246,7 +246,9 @@ __device__ __forceinline__ void mask_scores(f32x16& s, int32_t left) {
 // and other short row tiles.  Every lane loads its operands from the cache
 // itself, 1 KB of neighbouring bytes a wave and load; keys of the next block
 // are in flight while this one's softmax runs, values while its scores are
-// formed.
+// formed.  Bound by memory: 32 single tokens of 32 query and 8 key/value heads
+// over 1 to 16,384 keys each, 539 MB, take 114 us and 5 for the join, 4.6 TB/s
+// of cache read; four over 65,536 keys 102 us, 5.3 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kNarrowWaves = 4;
 
@@ -468,6 +470,13 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
 // before it is worked on (two buffers, one barrier a block): keys as they are,
 // values as bf16, converted once for all four waves.  Both lie in LDS in the
 // order the lanes read them, 16 neighbouring bytes each, free of conflicts.
+//
+// 4096 rows of 56 heads over 37,810 keys: 3.8 to 4.0 ms on different cards, 1110
+// to 1170 TFLOP/s, where a library product of 8192^3 in bf16 reaches 1229.  The
+// matrix pipes are busy 56% of the cycles, and the card is at its power limit:
+// with 10% fewer cycles for the same work its clock fell from 2.05 to 1.9 GHz.
+// Wave priorities (raised for the products, or for every other wave) changed
+// nothing; one workgroup to a CU instead of two took 5.2 ms.
 // ---------------------------------------------------------------------------
 constexpr int kWideWaves = 4;
 constexpr int kWideRows = kWideWaves * kRows;
@@ -861,7 +870,6 @@ static void attention_of(const AttentionArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {
-    (void)hipGetLastError();
     if (a.cache.dim == 128)
         attention_of<128>(a, s);
     else
