@@ -490,7 +490,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences
  * to its last bit, or to 2^-21 of the row's largest element where that is
  * more.  Probabilities are rounded to bf16 for the product with the values, and
  * the output once to bf16.  (The sums run against a reference that may lie a few
- * powers of two below the maximum; values above 2^96 can overflow them.)  The order of the sums depends on the sizes and
+ * powers of two below the maximum; values above 2^96, or scaled scores above 2^30,
+ * can overflow them.)  The order of the sums depends on the sizes and
  * max_len only: the same call gives the same bytes.
  * max_len is the host's bound on the lengths, used to decide how far the keys
  * of few rows are shared out over workgroups (results for longer sequences are
@@ -498,8 +499,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences
  * nvfp4_kv_attention_workspace_bytes(...) bytes for the same sizes (16-byte
  * aligned; may be NULL when that is 0); calls that can overlap must not share
  * it.  scale > 0 and finite; causal_block, max_len >= 0; q_heads a multiple of
- * cache->heads, M * q_heads < 2^31, M * (q_heads / heads) <= 2^28; out may be q
- * itself. */
+ * cache->heads, M * q_heads <= 2^28; out may be q itself. */
 size_t nvfp4_kv_attention_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
                                           int64_t max_len);
 nvfp4_status nvfp4_kv_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads, const nvfp4_kv_cache* cache,

@@ -80,8 +80,7 @@ nvfp4_status check_sequences(const nvfp4_kv_sequences* s, int64_t M, SeqArgs* a)
 
 bool attention_sizes_ok(int64_t M, int64_t count, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_len) {
     return M >= 1 && M <= kMaxRows && count >= 1 && count <= kMaxSeqs && heads >= 1 && heads <= kMaxHeads &&
-           q_heads >= 1 && q_heads % heads == 0 && M * q_heads < INT32_MAX &&
-           M * (q_heads / heads) <= ((int64_t)1 << 28) && (dim == 64 || dim == 128) && max_len >= 0;
+           q_heads >= 1 && q_heads % heads == 0 && M * q_heads <= ((int64_t)1 << 28) && (dim == 64 || dim == 128) && max_len >= 0;
 }
 
 HeadsIn in(const nvfp4_heads* h) { return HeadsIn{h->data, h->row_stride, h->head_stride}; }

@@ -487,11 +487,6 @@ constexpr int kWideRows = kWideWaves * kRows;
 // go from the last to the first: under a causal mask the later ones take
 // longer, and the short ones fill the end.
 __device__ __forceinline__ void wide_place(const AttentionArgs& a, int& unit, int& kv_head) {
-    if (gridDim.y > 1) {
-        unit = gridDim.x - 1 - blockIdx.x;
-        kv_head = blockIdx.y;
-        return;
-    }
     const uint32_t heads = a.cache.heads, units = gridDim.x / heads;
     if (heads % 8 == 0) {
         const uint32_t at = blockIdx.x / 8, head = at / units;
@@ -845,9 +840,9 @@ template <int D>
 static void attention_of(const AttentionArgs& a, hipStream_t s) {
     const int64_t units = tile_units(a.seqs.M, a.seqs.B, a.group, a.wide ? kWideRows : kRows);
     if (a.wide) {
-        const bool flat = units * a.cache.heads < ((int64_t)1 << 23);  // workgroups x threads below 2^32
-        const dim3 grid((unsigned)(flat ? units * a.cache.heads : units), flat ? 1u : (unsigned)a.cache.heads,
-                        (unsigned)a.parts);
+        // below 2^23, so that the threads of a dimension stay below 2^32: the heads
+        // times M group / 128 + B, where B <= M group / 96 and M q_heads <= 2^28
+        const dim3 grid((unsigned)(units * a.cache.heads), 1, (unsigned)a.parts);
         attention_wide_kernel<D><<<grid, dim3(64 * kWideWaves), 0, s>>>(a);
     } else {
         const dim3 grid((unsigned)units, (unsigned)a.cache.heads, (unsigned)a.parts);

@@ -77,6 +77,8 @@ def tables_for(pairs, size, theta=100.0):
     (3, 300, 64, [16], True, "plain"),
     (2, 2, 512, [100, 100], False, "plain"),
     (300, 1, 96, [24, 16], True, "qkv"),
+    (8195, 40, 64, [8, 12, 12], False, "plain"),  # several rows to a workgroup although one fills it
+    (8192, 20, 64, [24], True, "qkv"),
 ])
 def test_rope_is_the_formula_bit_for_bit(nv, rows, heads, dim, pairs, split, layout):
     g = gen(rows * dim + heads)
@@ -424,14 +426,33 @@ def test_attention_of_longer_rows(nv, dim, heads, group, c, seqs):
     check(got, want, tol)
 
 
-@pytest.mark.parametrize("max_len", [0, 64, 1000, 5000, 200000])
-def test_attention_is_right_for_any_bound_on_the_lengths(nv, max_len):
-    """max_len decides the number of parts only; below and above the true lengths the result stays right."""
-    pool = Pool(nv, 80, 2, 128, [2000, 1, 130])
-    q = normal(gen(81), 3, 8, 128)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("max_len", [0, 64, 1000, 2100, 4000, 5000, 12000, 200000])
+def test_attention_is_right_for_any_bound_on_the_lengths(nv, max_len, dim):
+    """max_len decides the number of parts only (1, 4, 7, 9, 23 and 64 here); below and above the true lengths the
+    result stays right."""
+    pool = Pool(nv, 80, 2, dim, [2000, 1, 130])
+    q = normal(gen(81), 3, 8, dim)
     want, tol = kv_ref.attention(q.double().numpy(), pool.ref, [0, 1, 2, 3], [2000, 1, 130], pool.table,
-                                 np.float64(np.float32(128 ** -0.5)), 1, bounds=True)
+                                 np.float64(np.float32(dim ** -0.5)), 1, bounds=True)
     got = nv.kv_attention(q.cuda(), pool.gpu, i32([0, 1, 2, 3]), pool.lens, pool.tab, causal_block=1, max_len=max_len)
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("dim,count", [(64, 12), (128, 12), (64, 16)])
+def test_attention_in_two_parts(nv, dim, count):
+    """Many workgroups already: the keys in two parts only, or from 16 sequences on in four."""
+    heads = 16
+    r = np.random.RandomState(count)
+    lens = [2100] + r.randint(1, 2100, count - 1).tolist()
+    pool = Pool(nv, 106, heads, dim, lens)
+    rs = list(range(count + 1))
+    parts = 2 if count < 16 else 4
+    assert nv.nvfp4_kv_attention_workspace_bytes(count, count, heads, heads, dim, 2112) == parts * count * heads * (dim + 2) * 4
+    q = normal(gen(107), count, heads, dim)
+    want, tol = kv_ref.attention(q.double().numpy(), pool.ref, rs, lens, pool.table, np.float64(np.float32(dim ** -0.5)), 1,
+                                 bounds=True)
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1)
     check(got, want, tol)
 
 
@@ -578,6 +599,18 @@ def test_many_sequences(nv, count):
     got = nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1)
     ref, tol = kv_ref.attention(q.double().numpy(), pool.ref, rs, lens, pool.table, np.float64(np.float32(0.125)), 1, bounds=True)
     check(got, ref, tol)
+
+
+def test_sequences_that_share_blocks(nv):
+    """A prefix's blocks in several tables, and a block twice in one: read only, each sequence as if alone."""
+    pool = Pool(nv, 108, 2, 64, [300, 300, 300])
+    pool.table[1, :3] = pool.table[0, :3]
+    pool.table[2] = pool.table[2, 0]
+    lens, rs = [300, 250, 300], [0, 1, 41, 241]
+    q = normal(gen(109), 241, 4, 64)
+    want, tol = kv_ref.attention(q.double().numpy(), pool.ref, rs, lens, pool.table, np.float64(np.float32(0.125)), 1, bounds=True)
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32(rs), i32(lens), i32(pool.table.tolist()), causal_block=1)
+    check(got, want, tol)
 
 
 def test_a_pool_past_4_gib(nv):
