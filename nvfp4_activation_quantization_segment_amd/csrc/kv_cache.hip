@@ -504,6 +504,134 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
     }
 }
 
+// The writer for a few rows a sequence: a lane has 2 dims, a wave takes one new
+// position after another (twice: for the maximum and for the codes), and WAVES
+// waves share out a block's where there are several.  The same bytes as the
+// writer above, from a sixth of its code and a fifth of its registers: a call
+// this short is a chain of waits, for memory and for instructions.  32 single
+// tokens of 8 heads 4.3 us (8.8 with the writer above), 256 of 56 heads 21 (108).
+template <int D, int MODE, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqArgs q, HeadsIn kx, HeadsIn vx, RopeArgs r) {
+    constexpr int kBytes = kKvBlock * D;
+    __shared__ uint32_t red[2][WAVES];
+    const BlockUnit u = block_unit(q, c.blocks, blockIdx.x);
+    if (!u.any) return;
+    const int lo = (int)(u.first > u.start ? u.first - u.start : 0);
+    const int hi = (int)(u.len - u.start < kKvBlock ? u.len - u.start : kKvBlock);
+    const int h = blockIdx.y, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const bool several = WAVES > 1 && hi - lo > 1;
+    if (!several && wave > 0) return;
+    const int step = several ? WAVES : 1;  // the others of a single one's waves are done
+    const bool mine = 2 * lane < D;
+    const int d = mine ? 2 * lane : 0;  // idle lanes load dims 0 and 1, count as zero and store nothing
+    const int64_t row = u.row0 + (u.start - u.first);
+    const Axes axes = axes_of(r);
+    // this lane's pair is (d, d + 1), or its two are (d, d + 1) with the dims
+    // r.total away, in the other half of the rotated part
+    const bool turns = MODE != ROPE_NONE && d < 2 * r.total, upper = MODE == ROPE_SPLIT && d >= r.total;
+    const int pair = !turns ? 0 : MODE == ROPE_SPLIT ? d - (upper ? r.total : 0) : d / 2;
+    const int partner = MODE == ROPE_SPLIT && turns && mine ? lane + (upper ? -(r.total / 2) : r.total / 2) : lane;
+    const auto key_of = [&](int t) -> uint32_t {
+        uint32_t w = *reinterpret_cast<const uint32_t*>(kx.data + (row + t) * kx.row + h * kx.head + d);
+        if constexpr (MODE == ROPE_PAIRS) {
+            const float2 a = rope_turn(axes, positions_of(r, row + t), pair);
+            const float x1 = bf16_lo(w), x2 = bf16_hi(w);
+            const uint32_t y = pack_bf16x2(x1 * a.x - x2 * a.y, x2 * a.x + x1 * a.y);
+            w = turns ? y : w;
+        } else if constexpr (MODE == ROPE_SPLIT) {
+            const Positions pos = positions_of(r, row + t);
+            float2 a = rope_turn(axes, pos, pair), b = rope_turn(axes, pos, turns ? pair + 1 : 0);
+            const uint32_t p = (uint32_t)__shfl((int)w, partner);
+            a.y = upper ? a.y : -a.y;
+            b.y = upper ? b.y : -b.y;
+            const uint32_t y = pack_bf16x2(bf16_lo(w) * a.x + bf16_lo(p) * a.y, bf16_hi(w) * b.x + bf16_hi(p) * b.y);
+            w = turns ? y : w;
+        }
+        return mine ? w : 0u;  // (an idle lane's partner is itself: its pair means nothing)
+    };
+    const auto value_of = [&](int t) -> uint32_t {
+        return *reinterpret_cast<const uint32_t*>(vx.data + (row + t) * vx.row + h * vx.head + d);
+    };
+    // a wave's last position stays in registers: most calls have one
+    uint32_t kw = 0, vw = 0, mk = 0, mv = 0, fk = 0, fv = 0;  // m: magnitudes, f: the finite ones
+    int last = -1;
+    for (int t = lo + wave; t < hi; t += step) {
+        last = t;
+        vw = value_of(t);
+        kw = key_of(t);
+        mk = pk_max_u16(mk, mag2(kw));
+        mv = pk_max_u16(mv, mag2(vw));
+        fk = pk_max_u16(fk, drop_nonfinite(mag2(kw)));
+        fv = pk_max_u16(fv, drop_nonfinite(mag2(vw)));
+    }
+    if (!u.good) return;
+    const int64_t at = u.page * c.heads + h;
+    uint8_t* const kb = c.k + at * kBytes;
+    uint8_t* const vb = c.v + at * kBytes;
+    const uint32_t had_k = lo > 0 ? clamp_power(c.k_power[at]) : 0u, had_v = lo > 0 ? clamp_power(c.v_power[at]) : 0u;
+    uint32_t any = (fold_max(mk) << 16) | fold_max(mv), top = (fold_max(fk) << 16) | fold_max(fv);
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) {
+        any = pk_max_u16(any, (uint32_t)__shfl_xor((int)any, s));
+        top = pk_max_u16(top, (uint32_t)__shfl_xor((int)top, s));
+    }
+    if (several) {
+        if (lane == 0) {
+            red[0][wave] = any;
+            red[1][wave] = top;
+        }
+        __syncthreads();  // also: all have read the block's powers
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            any = pk_max_u16(any, red[0][w]);
+            top = pk_max_u16(top, red[1][w]);
+        }
+    }
+    const bool odd = (any & 0xFFFFu) > 0x7F60u || (any >> 16) > 0x7F60u;
+    uint32_t pk = power_for(top >> 16), pv = power_for(top & 0xFFFFu);
+    pk = pk > had_k ? pk : had_k;
+    pv = pv > had_v ? pv : had_v;
+    if (mine && had_k && pk > had_k) {
+        const float f = power_value(127u - (pk - had_k < 126u ? pk - had_k : 126u));
+        for (int t = wave; t < lo; t += step) {
+            uint16_t* p = reinterpret_cast<uint16_t*>(kb + kv_key_offset(t, d));
+            *p = (uint16_t)shrink4(*p, f);
+        }
+    }
+    if (mine && had_v && pv > had_v) {
+        const float f = power_value(127u - (pv - had_v < 126u ? pv - had_v : 126u));
+        for (int t = wave; t < lo; t += step)
+            for (int i = 0; i < 2; ++i) {
+                uint8_t* p = vb + kv_value_offset(t, d + i, D);
+                *p = (uint8_t)shrink4(*p, f);
+            }
+    }
+    for (int t = last; t >= lo; t -= step) {
+        if (t != last) {
+            vw = value_of(t);
+            kw = key_of(t);
+        }
+        uint32_t kc, vc;
+        if (!odd) {
+            const float ik = power_inverse(pk), iv = power_inverse(pv);
+            kc = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(kw) * ik, bf16_hi(kw) * ik, 0, false);
+            vc = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(bf16_lo(vw) * iv, bf16_hi(vw) * iv, 0, false);
+        } else {
+            kc = encode_any(bf16_lo(kw), pk) | encode_any(bf16_hi(kw), pk) << 8;
+            vc = encode_any(bf16_lo(vw), pv) | encode_any(bf16_hi(vw), pv) << 8;
+        }
+        if (mine) {
+            *reinterpret_cast<uint16_t*>(kb + kv_key_offset(t, d)) = (uint16_t)kc;
+            vb[kv_value_offset(t, d, D)] = (uint8_t)vc;
+            vb[kv_value_offset(t, d + 1, D)] = (uint8_t)(vc >> 8);
+        }
+    }
+    if (threadIdx.x == 0) {
+        c.k_power[at] = (uint8_t)pk;
+        c.v_power[at] = (uint8_t)pv;
+    }
+}
+
 // The inverse of the writer: the same ownership, the same rows.
 template <int D>
 __global__ __launch_bounds__(2 * D) void kv_read_kernel(CacheArgs c, SeqArgs q, HeadsOut kx, HeadsOut vx,
@@ -595,6 +723,13 @@ __global__ __launch_bounds__(2 * D) void kv_read_kernel(CacheArgs c, SeqArgs q, 
 constexpr int kWriteHeads = 16, kReadHeads = 2;
 int heads_each(int64_t units, int32_t heads, int most) { return (int)clamp64(units * heads / 2048, 1, most); }
 
+// Rows a sequence (on average) up to which the short writer is taken, with one
+// wave up to one row and four above.  8 heads, 32 sequences of 4 rows: 5.4 us with
+// four waves, 6.9 with one, 8.8 with the long writer; of 16 rows 8.8, 17 and 10.
+// One of 60 rows and 63 of one: 13 us with four waves, 15 with the long writer;
+// one of 100 and 15 of one (7 on average): 19 and 9.
+constexpr int64_t kAppendRows = 4;
+
 }  // namespace
 
 hipError_t launch_rope_table(float2* table, int64_t rows, int32_t pairs, double theta, hipStream_t s) {
@@ -626,10 +761,24 @@ hipError_t launch_rope(const HeadsIn& x, const HeadsOut& out, int64_t M, int32_t
     return hipGetLastError();
 }
 
+template <int D, int WAVES>
+static void kv_append_of(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, const HeadsIn& v, const RopeArgs& r,
+                         hipStream_t s) {
+    const dim3 grid((unsigned)block_units(q.M, q.B), (unsigned)c.heads), block(64 * WAVES);
+    if (r.axes == 0)
+        kv_append_kernel<D, ROPE_NONE, WAVES><<<grid, block, 0, s>>>(c, q, k, v, r);
+    else if (r.split)
+        kv_append_kernel<D, ROPE_SPLIT, WAVES><<<grid, block, 0, s>>>(c, q, k, v, r);
+    else
+        kv_append_kernel<D, ROPE_PAIRS, WAVES><<<grid, block, 0, s>>>(c, q, k, v, r);
+}
+
 template <int D>
 static void kv_write_of(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, const HeadsIn& v, const RopeArgs& r,
                         hipStream_t s) {
     const int64_t units = block_units(q.M, q.B);
+    if (q.M <= q.B) return kv_append_of<D, 1>(c, q, k, v, r, s);
+    if (q.M <= kAppendRows * q.B) return kv_append_of<D, 4>(c, q, k, v, r, s);
     const int each = heads_each(units, c.heads, kWriteHeads);
     const dim3 grid((unsigned)units, (unsigned)((c.heads + each - 1) / each)), block(2 * D);
     if (r.axes == 0)

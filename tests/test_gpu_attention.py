@@ -198,6 +198,11 @@ WRITES = [
     (2, 64, [(1, 62), (1, 63), (1, 64), (1, 200)]),
     (9, 64, [(37, 5), (0, 0), (130, 3), (190, 70)]),
     (17, 128, [(77, 301), (5, 3)]),
+    # at most one row a sequence on average, and at most four: the short writer
+    (5, 128, [(63, 1), (0, 1), (64, 1), (150, 1), (7, 0), (200, 1)]),
+    (2, 64, [(100, 150)] + [(i, 0) for i in range(150)]),
+    (3, 128, [(30, 100)] + [(i, 1) for i in range(40)]),
+    (2, 64, [(60, 9), (126, 3), (0, 2), (5, 1), (64, 4)]),
 ]
 
 
@@ -256,6 +261,28 @@ def test_kv_write_of_special_values(nv):
             assert np.array_equal(back[kind][:, h].cpu().double().numpy(), want, equal_nan=True)
 
 
+@pytest.mark.parametrize("rows", [1, 3])
+def test_short_write_of_special_values(nv, rows):
+    """The special values one or three rows at a time, over what other rows left in the block."""
+    dim, heads = 128, 6
+    pool = Pool(nv, 13, heads, dim, [66])
+    for i in range(0, 66, rows):
+        k = normal(gen(400 + i), rows, heads, dim)
+        k[:, 0] = 0.0
+        k[:, 1] = 2.0 ** -133
+        if i > 30:
+            k[0, 1, 3] = -(2.0 ** (i - 130))
+            k[:, 2, 1] = torch.finfo(torch.bfloat16).max
+            k[0, 3, 5], k[-1, 4, 127] = float("inf"), float("nan")
+            k[:, 4, :9] = float("-inf")
+        k[:, 5, ::2], k[:, 5, 1::2] = -0.0, 448.0 * 2.0 ** (i // 9)
+        v = k.flip(1)
+        lens = [i + rows]
+        pool.ref.write((k.double().numpy(), v.double().numpy()), [0, rows], lens, pool.table)
+        nv.kv_write(pool.gpu, k.cuda(), v.cuda(), i32([0, rows]), i32(lens), pool.tab)
+    pool.same()
+
+
 @pytest.mark.parametrize("fraction", range(128))
 def test_power_of_every_fraction(nv, fraction):
     """amax = (1 + f/128) 2^e for every bf16 fraction: the power steps at 1.75, and codes stay at most 448."""
@@ -287,8 +314,9 @@ def test_tokens_appended_one_by_one(nv):
 @pytest.mark.parametrize("dim,pairs,split", [(64, [32], True), (64, [8], True), (64, [3, 5], False), (128, [16, 24, 24], False),
                                              (128, [22, 21, 21], True), (128, [8, 8], True), (128, [40], True),
                                              (64, [1, 2, 3, 2], True)])
-def test_kv_write_rotates_the_keys_as_rope_does(nv, dim, pairs, split):
-    heads, seqs = 5, [(0, 130), (37, 1), (60, 70)]
+@pytest.mark.parametrize("seqs", [[(0, 130), (37, 1), (60, 70)], [(0, 1), (63, 1), (64, 1)], [(0, 3), (37, 1), (62, 5)]])
+def test_kv_write_rotates_the_keys_as_rope_does(nv, dim, pairs, split, seqs):
+    heads = 5
     news = [n for _, n in seqs]
     rows = sum(news)
     g = gen(20)
