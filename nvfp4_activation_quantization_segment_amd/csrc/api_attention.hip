@@ -92,7 +92,7 @@ extern "C" {
 
 nvfp4_status nvfp4_rope_table(float* table, int64_t rows, int32_t pairs, double theta, void* stream) {
     if (!table || rows < 1 || pairs < 1 || !(theta > 0.0) || !isfinite(theta)) return NVFP4_ERR_INVALID_ARGUMENT;
-    if (rows >= ((int64_t)1 << 28) / pairs) return NVFP4_ERR_SHAPE;
+    if (rows > (((int64_t)1 << 28) - 1) / pairs) return NVFP4_ERR_SHAPE;
     if (!aligned(table, 8)) return NVFP4_ERR_ALIGNMENT;
     return report_hip(launch_rope_table(reinterpret_cast<float2*>(table), rows, pairs, theta, (hipStream_t)stream));
 }

@@ -87,6 +87,10 @@ def test_rope_table_refusals(nv):
         assert f(FAKE, 4, 4, theta, None) == INVALID
     assert f(FAKE, 1 << 30, 4, 1e4, None) == SHAPE
     assert f(FAKE + 4, 4, 4, 1e4, None) == ALIGNMENT
+    # rows * pairs < 2^28 exactly: 3 * 89478485 = 2^28 - 1 gets as far as the pointer
+    for rows, pairs in ((89478485, 3), ((1 << 28) - 1, 1), (1, (1 << 28) - 1)):
+        assert f(FAKE + 4, rows, pairs, 1e4, None) == ALIGNMENT
+        assert f(FAKE + 4, rows + 1, pairs, 1e4, None) == SHAPE
 
 
 def test_cache_refusals(nv):
