@@ -824,7 +824,7 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
     // keys: 16 us with pieces of 4, 20 of 8.
     int64_t tiles = (M * group + T - 1) / T;
     tiles = tiles < B ? B : tiles;
-    const int64_t blocks = (max_len + kKvBlock - 1) / kKvBlock;
+    const int64_t blocks = clamp64(max_len, 0, (int64_t)1 << 31) / kKvBlock + (max_len % kKvBlock != 0);
     int64_t want = 512 / (tiles * kv_heads);
     // Many sequences are of many lengths, which the host does not know: pieces
     // half as long even the workgroups out (32 sequences of 1 to 16,384 keys: 123

@@ -279,3 +279,13 @@ def test_structs_match_the_header(nv, tmp_path):
         t = names[name]
         assert ctypes.sizeof(t) == int(size)
         assert [getattr(t, f[0]).offset for f in t._fields_] == [int(a) for a in at]
+
+
+def test_any_bound_on_the_lengths(nv):
+    """Lengths are below 2^31; a bound past that, up to the largest number, cuts like a long one."""
+    f = nv.lib.nvfp4_kv_attention_workspace_bytes
+    for M, count, q_heads in ((1, 1, 8), (40, 1, 32), (32, 32, 32)):
+        want = f(M, count, q_heads, 8, 128, 1 << 31)
+        assert want > 0
+        for max_len in (1 << 40, (1 << 63) - 64, (1 << 63) - 1):
+            assert f(M, count, q_heads, 8, 128, max_len) == want
