@@ -463,7 +463,9 @@ typedef struct {
  * block that already holds positions of the sequence before the new ones keeps
  * them: its power becomes the larger of the old and what the new values need,
  * and where it grew the held codes are re-encoded, E4M3(code * 2^(old - new)).
- * Bytes of positions after the last are left as they were.  Rows whose block
+ * Bytes of positions after the last are left as they were, but for the values'
+ * in a block that new values give the largest power, b = 247: they become 0,
+ * since what an earlier use of the block left there may not be finite with it.  Rows whose block
  * does not exist (an entry outside the pool, a length that the table cannot
  * hold, a position before 0) are skipped.  Two sequences must not write to the
  * same block in one call.  1 <= M <= 2^23. */

@@ -234,11 +234,14 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m, uint32_t* slot) {
     return m;
 }
 
+// The largest power's byte: that of finite bf16 values above 1.75 * 2^127.
+constexpr uint32_t kLargestPower = 247;
+
 // Code of one value: the nearest E4M3 of x / p, or the NaN code for what is not
 // finite.  With the largest power, 2^120, codes stop at 240: 256 * 2^120 = 2^128,
 // the nearest to values above 1.9375 * 2^127, would not be finite any more.
 __device__ __forceinline__ uint32_t encode_any(float x, uint32_t power) {
-    const float most = power >= 247u ? 240.0f : 448.0f;
+    const float most = power >= kLargestPower ? 240.0f : 448.0f;
     const float y = fminf(fmaxf(x * power_inverse(power), -most), most);
     const uint32_t bits = __float_as_uint(x) & 0x7F800000u;
     return bits == 0x7F800000u ? 0x7Fu : (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, 0.0f, 0, false) & 0xFFu;
@@ -403,6 +406,7 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
             top = group_max<Own::kWaves>((fold_max(mk) << 16) | fold_max(mv), red2[parity]);
         }
         uint32_t pk = power_for(top >> 16), pv = power_for(top & 0xFFFFu);
+        const bool clear = pv >= kLargestPower;
         pk = pk > had_k ? pk : had_k;
         pv = pv > had_v ? pv : had_v;
         const float ik = power_inverse(pk), iv = power_inverse(pv);
@@ -482,18 +486,23 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
                     *p = make_uint2(shrink4(w.x, fk), shrink4(w.y, fk));
                 }
             }
-            uint32_t keep = 0, old = 0;  // bytes that stay, and those of them that are positions before lo
+            // bytes that stay, and those of them that are positions before lo.
+            // Behind the last position an earlier use may have left codes that are
+            // not finite with the largest power: they would make 0 p of the rows
+            // that do not see them NaN, so with that power they become 0.
+            uint32_t keep = 0, old = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (!fresh[j]) keep |= 0xFFu << (8 * j);
                 if (o.t0 + j < lo) old |= 0xFFu << (8 * j);
             }
-            if (keep != 0xFFFFFFFFu || (grew_v && old)) {
+            const uint32_t stay = clear ? old : keep;
+            if (stay != 0xFFFFFFFFu || (grew_v && old)) {
 #pragma unroll
                 for (int d = 0; d < 8; ++d) {
                     uint32_t w = was[d];
                     if (grew_v) w = (shrink4(w, fv) & old) | (w & ~old);
-                    vp[4 * d] = (w & keep) | (vc[d] & ~keep);
+                    vp[4 * d] = (w & stay) | (vc[d] & ~keep);
                 }
             }
         }
@@ -589,6 +598,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqA
     }
     const bool odd = (any & 0xFFFFu) > 0x7F60u || (any >> 16) > 0x7F60u;
     uint32_t pk = power_for(top >> 16), pv = power_for(top & 0xFFFFu);
+    const bool clear = pv >= kLargestPower;
     pk = pk > had_k ? pk : had_k;
     pv = pv > had_v ? pv : had_v;
     if (mine && had_k && pk > had_k) {
@@ -606,6 +616,10 @@ __global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqA
                 *p = (uint8_t)shrink4(*p, f);
             }
     }
+    // with the largest power, codes behind the last position become 0 (see the other writer)
+    if (mine && clear)
+        for (int t = hi + wave; t < kKvBlock; t += step)
+            for (int i = 0; i < 2; ++i) vb[kv_value_offset(t, d + i, D)] = 0;
     for (int t = last; t >= lo; t -= step) {
         if (t != last) {
             vw = value_of(t);

@@ -108,6 +108,8 @@ class Cache:
                                 old = codes[kept]
                                 again = nearest_code(E4M3[old] * 2.0 ** (had - p))
                                 codes[kept] = np.where((old & 0x7F) == 0x7F, old, again)
+                        if kind == 1 and power_for(x) >= 247:  # what an earlier use left may not be finite
+                            codes[off[hi - at * BLOCK:]] = 0
                         most = 240.0 if p >= 247 else 448.0
                         y = np.where(np.isfinite(x), np.clip(x * 2.0 ** (127 - p), -most, most), x)
                         codes[off[lo - at * BLOCK:hi - at * BLOCK]] = nearest_code(y)

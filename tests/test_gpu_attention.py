@@ -541,6 +541,29 @@ def test_what_is_hidden_has_no_effect(nv, dim, group, news, past):
         clean = call()
 
 
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("dim,rows", [(64, 1), (128, 1), (64, 3), (128, 5), (64, 66), (128, 130), (64, 201)])
+def test_codes_left_behind_the_largest_values(nv, dim, rows, causal):
+    """A block whose values need the largest power, 2^120, with the codes of an earlier use (448, which times 2^120
+    is not finite) behind the last position: they have no effect.  Zero keys, so all probabilities are 1 before the
+    division; the largest value is the only one of its block that is not rounded to 0, so every sum is finite."""
+    v = torch.ones(rows, 2, dim, dtype=torch.bfloat16)
+    v[-1, 0, 3] = torch.finfo(torch.bfloat16).max
+    v[-1, 1, dim - 1] = -torch.finfo(torch.bfloat16).max
+    q = normal(gen(dim + rows), rows, 4, dim)
+    blocks = -(-rows // BLOCK)
+    got = []
+    for left in (0, 0x7E):
+        cache = nv.KvCache.empty(blocks, 2, dim)
+        for t in (cache.k, cache.v):
+            t.fill_(left)
+        args = i32([0, rows]), i32([rows]), i32([list(range(blocks))])
+        nv.kv_write(cache, torch.zeros_like(v).cuda(), v.cuda(), *args)
+        got.append(nv.kv_attention(q.cuda(), cache, *args, causal_block=causal))
+    assert bool(torch.isfinite(got[0]).all()) and bool((got[0][-1, :2, 3] > 2.0 ** 110).all())
+    assert same(got[1], got[0])
+
+
 @pytest.mark.parametrize("rows", [1, 50, 200])
 def test_blocks_and_lengths_that_do_not_exist(nv, rows):
     pool = Pool(nv, 86, 2, 64, [300, 300, 300, 300])
