@@ -566,9 +566,10 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
         vp_raw = a.cache.v_power[at];
     };
     // stages the fetched block; edge: some row of the tile does not see all of
-    // it, or it stands in for one that does not exist
-    const auto stage = [&](int buffer, bool edge) {
-        const float scale = power_value(clamp_power(vp_raw));
+    // it, or it stands in for one that does not exist (!good: then its power may
+    // be anything and is not used, so that the rows that do not see it get 0 p)
+    const auto stage = [&](int buffer, bool edge, bool good) {
+        const float scale = power_value(good ? clamp_power(vp_raw) : 127u);
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int at = i * kThreads + threadIdx.x;
@@ -615,7 +616,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
 #pragma unroll
     for (int d = 0; d < kDT; ++d) o[d] = f32x16{};
     if (at0 < end) {
-        stage(0, edge_now);
+        stage(0, edge_now, first_good);
         kp = key_power(kp_raw, first_good);
     }
     __syncthreads();
@@ -703,7 +704,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
         if (more) {
             const bool good = page >= 0;
             edge_now = !good || first_key + 2 * kKvBlock > tile_all;
-            stage(1 - b, edge_now);
+            stage(1 - b, edge_now, good);
             kp = key_power(kp_raw, good);
         }
         __syncthreads();

@@ -578,6 +578,29 @@ def test_blocks_and_lengths_that_do_not_exist(nv, rows):
     assert np.isnan(want[3 * rows:]).all() and not np.isnan(want[:rows]).any()
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [30, 130])
+def test_missing_blocks_beside_unwritten_ones(nv, dim, rows):
+    """Rows that do not see a missing block, in a tile whose other rows do: they are what they are without it, also
+    where the pool's first block, never written, holds what is not finite."""
+    past = 40  # the first 24 rows end before the missing block 1
+    n = past + rows
+    blocks = -(-n // BLOCK)
+    k, v, q = (normal(gen(700 + i), *s) for i, s in enumerate(((n, 2, dim), (n, 2, dim), (rows, 2, dim))))
+    table = [list(range(1, blocks + 1))]
+    cache = nv.KvCache.empty(blocks + 1, 2, dim)
+    nv.kv_write(cache, k.cuda(), v.cuda(), i32([0, n]), i32([n]), i32(table))
+    table[0][1] = -1
+    got = []
+    for code, power in ((0, 1), (0x7E, 254), (0x7F, 255)):
+        for t, x in ((cache.k, code), (cache.v, code), (cache.k_power, power), (cache.v_power, power)):
+            t[0] = x
+        got.append(nv.kv_attention(q.cuda(), cache, i32([0, rows]), i32([n]), i32(table), causal_block=1))
+    for x in got:
+        assert bool(torch.isfinite(x[:24]).all()) and bool(x[24:].isnan().all())
+        assert same(x[:24], got[0][:24])
+
+
 def test_queries_that_are_not_finite_and_large_and_small_ones(nv):
     pool = Pool(nv, 88, 1, 128, [100, 100])
     q = normal(gen(89), 40, 1, 128)
