@@ -467,14 +467,15 @@ typedef struct {
  * in a block that new values give the largest power, b = 247: they become 0,
  * since what an earlier use of the block left there may not be finite with it.  Rows whose block
  * does not exist (an entry outside the pool, a length that the table cannot
- * hold, a position before 0) are skipped.  Two sequences must not write to the
- * same block in one call.  1 <= M <= 2^23. */
+ * hold, a position before 0) are skipped.  No block may be written twice in one
+ * call, by two sequences or by one whose table names it twice (the bytes that it
+ * would hold are not defined).  1 <= M <= 2^23. */
 nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences* seqs, int64_t M,
                             const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_rope_params* rope, void* stream);
 
 /* Reads the positions of the M rows back: k and v [M, heads, dim] = code *
  * power, exact in bf16.  A row before position 0 is 0; one whose block does not
- * exist, NaN. */
+ * exist, NaN.  k and v must not overlap; sequences may share blocks. */
 nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences* seqs, int64_t M,
                            const nvfp4_heads* k, const nvfp4_heads* v, void* stream);
 
