@@ -471,8 +471,8 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
 // values as bf16, converted once for all four waves.  Both lie in LDS in the
 // order the lanes read them, 16 neighbouring bytes each, free of conflicts.
 //
-// 4096 rows of 56 heads over 37,810 keys: 3.8 to 4.0 ms on different cards, 1110
-// to 1170 TFLOP/s, where a library product of 8192^3 in bf16 reaches 1229.  The
+// 4096 rows of 56 heads over 37,810 keys: 3.7 to 4.1 ms on different cards, 1080
+// to 1195 TFLOP/s, where a library product of 8192^3 in bf16 reaches 1229.  The
 // matrix pipes are busy 56% of the cycles, and the card is at its power limit:
 // with 10% fewer cycles for the same work its clock fell from 2.05 to 1.9 GHz.
 // Wave priorities (raised for the products, or for every other wave) changed
