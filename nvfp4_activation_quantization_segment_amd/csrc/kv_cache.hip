@@ -516,9 +516,9 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
 // The writer for a few rows a sequence: a lane has 2 dims, a wave takes one new
 // position after another (twice: for the maximum and for the codes), and WAVES
 // waves share out a block's where there are several.  The same bytes as the
-// writer above, from a sixth of its code and a fifth of its registers: a call
-// this short is a chain of waits, for memory and for instructions.  32 single
-// tokens of 8 heads 4.3 us (8.8 with the writer above), 256 of 56 heads 21 (108).
+// writer above, from less code and a third of its registers: a call this short
+// is a chain of waits, for memory and for instructions.  32 single tokens of 8
+// heads 4.3 us (8.8 with the writer above), 256 of 56 heads 20 (110).
 template <int D, int MODE, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqArgs q, HeadsIn kx, HeadsIn vx, RopeArgs r) {
     constexpr int kBytes = kKvBlock * D;
@@ -561,17 +561,35 @@ __global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqA
     const auto value_of = [&](int t) -> uint32_t {
         return *reinterpret_cast<const uint32_t*>(vx.data + (row + t) * vx.row + h * vx.head + d);
     };
-    // a wave's last position stays in registers: most calls have one
-    uint32_t kw = 0, vw = 0, mk = 0, mv = 0, fk = 0, fv = 0;  // m: magnitudes, f: the finite ones
-    int last = -1;
-    for (int t = lo + wave; t < hi; t += step) {
-        last = t;
-        vw = value_of(t);
-        kw = key_of(t);
+    uint32_t mk = 0, mv = 0, fk = 0, fv = 0;  // m: magnitudes, f: the finite ones
+    const auto look_at = [&](uint32_t kw, uint32_t vw) {
         mk = pk_max_u16(mk, mag2(kw));
         mv = pk_max_u16(mv, mag2(vw));
         fk = pk_max_u16(fk, drop_nonfinite(mag2(kw)));
         fv = pk_max_u16(fv, drop_nonfinite(mag2(vw)));
+    };
+    // a wave's last position stays in registers: most calls have one.  The others
+    // are taken kBatch at a time, their loads in flight together (one sequence of
+    // 60 rows and 63 of none, one wave a head: 27 us, 33 one by one; 8 at a time
+    // the same)
+    constexpr int kBatch = 4;
+    uint32_t kw = 0, vw = 0;
+    int last = -1, t = lo + wave;
+    for (; t + kBatch * step < hi; t += kBatch * step) {
+        uint32_t k[kBatch], v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            v[i] = value_of(t + i * step);
+            k[i] = key_of(t + i * step);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) look_at(k[i], v[i]);
+    }
+    for (; t < hi; t += step) {
+        last = t;
+        vw = value_of(t);
+        kw = key_of(t);
+        look_at(kw, vw);
     }
     if (!u.good) return;
     const int64_t at = u.page * c.heads + h;
@@ -620,11 +638,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqA
     if (mine && clear)
         for (int t = hi + wave; t < kKvBlock; t += step)
             for (int i = 0; i < 2; ++i) vb[kv_value_offset(t, d + i, D)] = 0;
-    for (int t = last; t >= lo; t -= step) {
-        if (t != last) {
-            vw = value_of(t);
-            kw = key_of(t);
-        }
+    const auto store = [&](int t, uint32_t kw, uint32_t vw) {
         uint32_t kc, vc;
         if (!odd) {
             const float ik = power_inverse(pk), iv = power_inverse(pv);
@@ -639,7 +653,19 @@ __global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqA
             vb[kv_value_offset(t, d, D)] = (uint8_t)vc;
             vb[kv_value_offset(t, d + 1, D)] = (uint8_t)(vc >> 8);
         }
+    };
+    if (last >= 0) store(last, kw, vw);
+    for (t = lo + wave; t + kBatch * step <= last; t += kBatch * step) {
+        uint32_t k[kBatch], v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            v[i] = value_of(t + i * step);
+            k[i] = key_of(t + i * step);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) store(t + i * step, k[i], v[i]);
     }
+    for (; t < last; t += step) store(t, key_of(t), value_of(t));
     if (threadIdx.x == 0) {
         c.k_power[at] = (uint8_t)pk;
         c.v_power[at] = (uint8_t)pv;
@@ -738,10 +764,12 @@ constexpr int kWriteHeads = 16, kReadHeads = 2;
 int heads_each(int64_t units, int32_t heads, int most) { return (int)clamp64(units * heads / 2048, 1, most); }
 
 // Rows a sequence (on average) up to which the short writer is taken, with one
-// wave up to one row and four above.  8 heads, 32 sequences of 4 rows: 5.4 us with
-// four waves, 6.9 with one, 8.8 with the long writer; of 16 rows 8.8, 17 and 10.
-// One of 60 rows and 63 of one: 13 us with four waves, 15 with the long writer;
-// one of 100 and 15 of one (7 on average): 19 and 9.
+// wave up to one row and four above.  256 single tokens of 56 heads: 21 us with
+// one wave, 48 with four, 110 with the long writer.  8 heads, 32 sequences of 4
+// rows: 5.1 us with four waves, 8.9 with the long writer.  One of 60 rows and 63
+// of one: 10 and 15 us; one of 100 and 15 of one (7 on average): 19 and 9.  What
+// the rule costs where the rows are one sequence's: 60 rows beside 63 sequences
+// of none take 27 us, 10 with the long writer.
 constexpr int64_t kAppendRows = 4;
 
 }  // namespace

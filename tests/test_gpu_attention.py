@@ -296,6 +296,22 @@ def test_power_of_every_fraction(nv, fraction):
     pool.same()
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("count,rows,past", [(80, 60, 0), (80, 75, 37), (201, 200, 63), (20, 70, 60), (9, 33, 1)])
+def test_one_sequence_among_empty_ones(nv, dim, count, rows, past):
+    """Many rows of one sequence although there are few rows a sequence: every length of a wave's share."""
+    news, pasts = [0] * count, [5] * count
+    news[count // 2], pasts[count // 2] = rows, past
+    lens = [p + n for p, n in zip(pasts, news)]
+    pool = Pool(nv, 500 + rows, 3, dim, lens)
+    g = gen(501 + rows)
+    k, v = normal(g, rows, 3, dim), normal(g, rows, 3, dim, sigma=30.0)
+    rs = starts(news)
+    nv.kv_write(pool.gpu, k.cuda(), v.cuda(), i32(rs), pool.lens, pool.tab)
+    pool.ref.write((k.double().numpy(), v.double().numpy()), rs, lens, pool.table)
+    pool.same()
+
+
 def test_tokens_appended_one_by_one(nv):
     """150 single appends: each step equals the formula, whatever grew on the way."""
     heads, dim = 3, 128
