@@ -74,7 +74,7 @@ nvfp4_status check_sequences(const nvfp4_kv_sequences* s, int64_t M, SeqArgs* a)
     if (s->table_blocks < 1 || s->ld_table < s->table_blocks) return NVFP4_ERR_INVALID_ARGUMENT;
     if (M > kMaxRows || s->count > kMaxSeqs || s->table_blocks > INT32_MAX / kKvBlock) return NVFP4_ERR_SHAPE;
     if (!aligned(s->row_start, 4) || !aligned(s->lens, 4) || !aligned(s->table, 4)) return NVFP4_ERR_ALIGNMENT;
-    *a = SeqArgs{M, s->count, s->row_start, s->lens, s->table, s->ld_table, s->table_blocks};
+    *a = SeqArgs{M, s->count, s->row_start, s->lens, s->table, s->ld_table, s->table_blocks, 0};
     return NVFP4_OK;
 }
 

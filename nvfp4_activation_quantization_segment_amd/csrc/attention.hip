@@ -50,10 +50,10 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int64_t unit, 
     Tile t;
     t.any = false;
     const SeqArgs& q = a.seqs;
-    const Located at = locate(q, unit, [&](int64_t row, int64_t b) { return tile_base(row, b, a.group, T); });
+    const Located at = locate(q, unit, [&](int64_t row, int64_t b) { return tile_first(row, b, a.group, T, q.per_row); });
     t.b = at.b;
     const RowRange r = row_range(at.start, at.end, q.M);
-    const int64_t n = r.last - r.first, local = unit - tile_base(r.first, t.b, a.group, T);
+    const int64_t n = r.last - r.first, local = unit - tile_first(r.first, t.b, a.group, T, q.per_row);
     if (local < 0 || local * T >= n * a.group) return t;
     t.any = true;
     t.row0 = r.first;
@@ -259,11 +259,16 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     constexpr int kLd = D + 4;
     __shared__ __align__(16) float so[kNarrowWaves][kRows][kLd];
     __shared__ float sm[kNarrowWaves][kRows], sl[kNarrowWaves][kRows];
-    const Tile t = find_tile(a, blockIdx.x, kRows);
+    const int kv_head = blockIdx.y, part = blockIdx.z;
+    // Workgroups go to the 8 XCDs in turn: with a multiple of 8 units, all of a
+    // long sequence's would go to one of them, were heads and parts not turned
+    // against each other (32 sequences of 1 to 16,384 keys: 118 us, 124 without).
+    uint32_t unit = blockIdx.x + (blockIdx.y + blockIdx.z) % gridDim.x;
+    unit = unit < gridDim.x ? unit : unit - gridDim.x;
+    const Tile t = find_tile(a, unit, kRows);
     if (!t.any) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int c = lane & 31, h = lane >> 5;
-    const int kv_head = blockIdx.y, part = blockIdx.z;
     const Row row = find_row(a, t, t.first + c, kv_head);
     // keys that the tile's last row sees, and keys that all its rows see: limits
     // do not fall from row to row
@@ -824,13 +829,16 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
     // 32; over 1024 keys 9.9 us in one piece, 10.4 in two.  40 tokens over 2048
     // keys: 16 us with pieces of 4, 20 of 8.
     int64_t tiles = (M * group + T - 1) / T;
-    tiles = tiles < B ? B : tiles;
+    // Slots without rows are not tiles: one token over 16,384 keys among 255 empty
+    // slots 13 us, 117 when they counted.
+    const int64_t most_seqs = B < M ? B : M;
+    tiles = tiles < most_seqs ? most_seqs : tiles;
     const int64_t blocks = clamp64(max_len, 0, (int64_t)1 << 31) / kKvBlock + (max_len % kKvBlock != 0);
     int64_t want = 512 / (tiles * kv_heads);
     // Many sequences are of many lengths, which the host does not know: pieces
     // half as long even the workgroups out (32 sequences of 1 to 16,384 keys: 123
     // -> 115 us; 32 of 8192: 113 -> 110; 4 of 16,384: 27 -> 30, so few are left).
-    if (!p.wide && B >= 16 && want >= 2) want *= 2;
+    if (!p.wide && most_seqs >= 16 && want >= 2) want *= 2;
     const int64_t most = p.wide ? blocks / 4 : blocks >= 32 ? blocks / 8 : 1;
     p.parts = (int32_t)clamp64(want < most ? want : most, 1, kMaxParts);
     p.workspace_bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)(M * q_heads) * (size_t)(dim + 2) * sizeof(float);
@@ -838,8 +846,11 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
 }
 
 template <int D>
-static void attention_of(const AttentionArgs& a, hipStream_t s) {
-    const int64_t units = tile_units(a.seqs.M, a.seqs.B, a.group, a.wide ? kWideRows : kRows);
+static void attention_of(const AttentionArgs& args, hipStream_t s) {
+    AttentionArgs a = args;
+    const int64_t T = a.wide ? kWideRows : kRows;
+    a.seqs.per_row = tiles_per_row(a.seqs.M, a.seqs.B, a.group, T);
+    const int64_t units = tile_first(a.seqs.M, a.seqs.B, a.group, T, a.seqs.per_row);
     if (a.wide) {
         // below 2^23, so that the threads of a dimension stay below 2^32: the heads
         // times M group / 128 + B, where B <= M group / 96 and M q_heads <= 2^28

@@ -196,9 +196,9 @@ struct BlockUnit {
 __device__ __forceinline__ BlockUnit block_unit(const SeqArgs& q, int64_t blocks, int64_t unit) {
     BlockUnit u;
     u.any = false;
-    const Located s = locate(q, unit, [](int64_t row, int64_t b) { return block_base(row, b); });
+    const Located s = locate(q, unit, [&](int64_t row, int64_t b) { return block_first(row, b, q.per_row); });
     const RowRange r = row_range(s.start, s.end, q.M);
-    const int64_t n = r.last - r.first, local = unit - block_base(r.first, s.b);
+    const int64_t n = r.last - r.first, local = unit - block_first(r.first, s.b, q.per_row);
     if (n <= 0 || local < 0) return u;
     u.len = s.len;
     u.first = u.len - n;
@@ -518,7 +518,7 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
 // waves share out a block's where there are several.  The same bytes as the
 // writer above, from less code and a third of its registers: a call this short
 // is a chain of waits, for memory and for instructions.  32 single tokens of 8
-// heads 4.3 us (8.8 with the writer above), 256 of 56 heads 20 (110).
+// heads 4.2 us (8.8 with the writer above), 256 of 56 heads 17 (110).
 template <int D, int MODE, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqArgs q, HeadsIn kx, HeadsIn vx, RopeArgs r) {
     constexpr int kBytes = kKvBlock * D;
@@ -806,7 +806,7 @@ hipError_t launch_rope(const HeadsIn& x, const HeadsOut& out, int64_t M, int32_t
 template <int D, int WAVES>
 static void kv_append_of(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, const HeadsIn& v, const RopeArgs& r,
                          hipStream_t s) {
-    const dim3 grid((unsigned)block_units(q.M, q.B), (unsigned)c.heads), block(64 * WAVES);
+    const dim3 grid((unsigned)block_first(q.M, q.B, q.per_row), (unsigned)c.heads), block(64 * WAVES);
     if (r.axes == 0)
         kv_append_kernel<D, ROPE_NONE, WAVES><<<grid, block, 0, s>>>(c, q, k, v, r);
     else if (r.split)
@@ -818,7 +818,7 @@ static void kv_append_of(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k,
 template <int D>
 static void kv_write_of(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, const HeadsIn& v, const RopeArgs& r,
                         hipStream_t s) {
-    const int64_t units = block_units(q.M, q.B);
+    const int64_t units = block_first(q.M, q.B, q.per_row);
     if (q.M <= q.B) return kv_append_of<D, 1>(c, q, k, v, r, s);
     if (q.M <= kAppendRows * q.B) return kv_append_of<D, 4>(c, q, k, v, r, s);
     const int each = heads_each(units, c.heads, kWriteHeads);
@@ -831,8 +831,10 @@ static void kv_write_of(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, 
         kv_write_kernel<D, ROPE_PAIRS><<<grid, block, 0, s>>>(c, q, k, v, r, each);
 }
 
-hipError_t launch_kv_write(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, const HeadsIn& v, const RopeArgs& r,
+hipError_t launch_kv_write(const CacheArgs& c, const SeqArgs& seqs, const HeadsIn& k, const HeadsIn& v, const RopeArgs& r,
                            hipStream_t s) {
+    SeqArgs q = seqs;
+    q.per_row = blocks_per_row(q.M, q.B);
     if (c.dim == 128)
         kv_write_of<128>(c, q, k, v, r, s);
     else
@@ -840,8 +842,10 @@ hipError_t launch_kv_write(const CacheArgs& c, const SeqArgs& q, const HeadsIn& 
     return hipGetLastError();
 }
 
-hipError_t launch_kv_read(const CacheArgs& c, const SeqArgs& q, const HeadsOut& k, const HeadsOut& v, hipStream_t s) {
-    const int64_t units = block_units(q.M, q.B);
+hipError_t launch_kv_read(const CacheArgs& c, const SeqArgs& seqs, const HeadsOut& k, const HeadsOut& v, hipStream_t s) {
+    SeqArgs q = seqs;
+    q.per_row = blocks_per_row(q.M, q.B);
+    const int64_t units = block_first(q.M, q.B, q.per_row);
     const int each = heads_each(units, c.heads, kReadHeads);
     const dim3 grid((unsigned)units, (unsigned)((c.heads + each - 1) / each));
     if (c.dim == 128)

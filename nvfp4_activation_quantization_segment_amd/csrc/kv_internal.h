@@ -50,6 +50,7 @@ struct SeqArgs {
     const int32_t* table;
     int64_t ld_table;
     int64_t table_blocks;
+    int32_t per_row;   // work units of a row, 0: counted by sequences (kv_layout.h)
 };
 
 struct AttentionArgs {

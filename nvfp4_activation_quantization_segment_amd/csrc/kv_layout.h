@@ -44,11 +44,28 @@ constexpr int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0 ? 
 // floor(n per / T) + 1 is never less.
 // Blocks of 64 positions: n positions starting anywhere touch at most
 // (n + 62) / 64 + 1 <= floor(n / 64) + 2 of them.
+//
+// With few rows a sequence (single tokens, slots that are mostly empty) fewer
+// units do: n tokens have at most n ceil(per / T) tiles and n blocks, so every
+// row can have that many of its own.  per_row is that number, or 0 where the
+// count above is the smaller one; it is picked on the host.  (256 single tokens
+// of 56 heads: written in 17 us instead of 21, attended over 1000 keys and 8
+// heads in 102 to 110 instead of 113.)
 // ---------------------------------------------------------------------------
 constexpr int64_t tile_base(int64_t row, int64_t b, int64_t per, int64_t T) { return row * per / T + b; }
 constexpr int64_t tile_units(int64_t M, int64_t B, int64_t per, int64_t T) { return M * per / T + B; }
 constexpr int64_t block_base(int64_t row, int64_t b) { return row / kKvBlock + 2 * b; }
 constexpr int64_t block_units(int64_t M, int64_t B) { return M / kKvBlock + 2 * B; }
+constexpr int32_t tiles_per_row(int64_t M, int64_t B, int64_t per, int64_t T) {
+    const int64_t each = (per + T - 1) / T;
+    return M * each < tile_units(M, B, per, T) ? (int32_t)each : 0;
+}
+constexpr int32_t blocks_per_row(int64_t M, int64_t B) { return M < block_units(M, B) ? 1 : 0; }
+// First unit of the sequence b whose first row is `row`; of M and B: how many.
+constexpr int64_t tile_first(int64_t row, int64_t b, int64_t per, int64_t T, int32_t per_row) {
+    return per_row ? row * per_row : tile_base(row, b, per, T);
+}
+constexpr int64_t block_first(int64_t row, int64_t b, int32_t per_row) { return per_row ? row : block_base(row, b); }
 
 // Rows [first, last) of sequence b of row_start, whatever the array holds.
 struct RowRange {

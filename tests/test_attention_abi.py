@@ -207,6 +207,40 @@ int main() {
             need(touched <= bend - block_base(r.first, b), "blocks");
         }
     }
+    // every tile and block has one unit, found as the kernels find it (the last sequence that starts at or before
+    // it), whichever way the units are counted; the other units find nothing
+    for (int round = 0; round < 20000; ++round) {
+        const int B = 1 + rand() % 9;
+        const int64_t per = rand() % 4 ? 1 + rand() % 9 : 1 + rand() % 300, T = (round & 1) ? 32 : 128;
+        const int most = rand() % 2 ? 2 : 200;
+        std::vector<int64_t> start(1, rand() % 3 ? 0 : rand() % 5), pos;
+        for (int b = 0; b < B; ++b) start.push_back(start.back() + (rand() % 2 ? rand() % (most + 1) : 0));
+        for (int b = 0; b < B; ++b) pos.push_back(rand() % 300 - 100);
+        const int64_t M = start.back() + rand() % 3 + (start.back() == 0);
+        const auto check = [&](int64_t units, auto first, auto wanted, const char* what) {
+            std::vector<int64_t> found(B);
+            for (int64_t u = 0; u < units; ++u) {
+                int b = 0;
+                for (int i = 1; i < B; ++i)
+                    if (first(start[i], i) <= u) b = i;
+                const int64_t local = u - first(start[b], b);
+                if (local >= 0 && local < wanted(b)) need(found[b]++ == local, what);
+            }
+            for (int b = 0; b < B; ++b) need(found[b] == wanted(b), what);
+        };
+        const auto rows = [&](int b) { return start[b + 1] - start[b]; };
+        const auto tiles = [&](int b) { return (rows(b) * per + T - 1) / T; };
+        const auto blocks = [&](int b) {
+            return rows(b) ? floor_div(pos[b] + rows(b) - 1, 64) - floor_div(pos[b], 64) + 1 : 0;
+        };
+        const int32_t t = tiles_per_row(M, B, per, T), k = blocks_per_row(M, B);
+        need(tile_first(M, B, per, T, t) <= tile_units(M, B, per, T), "fewer tiles");
+        need(block_first(M, B, k) <= block_units(M, B), "fewer blocks");
+        for (int32_t each : {0, (int32_t)((per + T - 1) / T)})
+            check(tile_first(M, B, per, T, each), [&](int64_t r, int b) { return tile_first(r, b, per, T, each); }, tiles, "tile units");
+        for (int32_t each : {0, 1})
+            check(block_first(M, B, each), [&](int64_t r, int b) { return block_first(r, b, each); }, blocks, "block units");
+    }
     // any row starts stay inside the rows
     const int64_t odd[] = {INT32_MIN, -5, 0, 3, 7, 100, INT32_MAX};
     for (int64_t a : odd)

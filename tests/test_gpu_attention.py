@@ -691,6 +691,38 @@ def test_many_sequences(nv, count):
     check(got, ref, tol)
 
 
+@pytest.mark.parametrize("count,rows,group,dim,longest", [
+    (70, {0: 1}, 1, 64, 2500), (70, {69: 1}, 4, 128, 2500), (300, {3: 1, 150: 2, 151: 1, 299: 1}, 2, 64, 1500),
+    (9, {2: 1, 7: 1}, 40, 64, 2500), (12, {0: 1, 5: 2}, 70, 128, 600), (12, {1: 1, 2: 1, 11: 1}, 130, 64, 1100),
+    (8, {b: 1 for b in range(8)}, 300, 64, 700), (64, {b: 1 for b in range(64)}, 3, 64, 300), (40, {9: 35}, 3, 64, 900)])
+def test_slots_that_are_mostly_empty(nv, count, rows, group, dim, longest):
+    """A few sequences with rows among many without, one to several tiles a row, rows before the first sequence and
+    after the last: written, read back and attended."""
+    g = gen(count + group)
+    news = [rows.get(b, 0) for b in range(count)]
+    lens = [int(torch.randint(news[b], longest if news[b] else 60, (1,), generator=g)) for b in range(count)]
+    lens[max(rows)] = longest
+    pool = Pool(nv, count + dim, 1, dim, lens)
+    lead, n = 2, sum(news)
+    M, rs = lead + n + 3, [lead + r for r in starts(news)]
+    k, v, q = (normal(g, M, h, dim) for h in (1, 1, group))
+    nv.kv_write(pool.gpu, k.cuda(), v.cuda(), i32(rs), pool.lens, pool.tab)
+    pool.ref.write((k.double().numpy(), v.double().numpy()), rs, lens, pool.table)
+    pool.same()
+    out = [torch.full((M, h, dim), 5.0, dtype=torch.bfloat16, device="cuda") for h in (1, 1, group)]
+    nv.kv_read(pool.gpu, M, i32(rs), pool.lens, pool.tab, k=out[0], v=out[1])
+    nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1, out=out[2])
+    for x in out:
+        assert bool((x[:lead] == 5).all()) and bool((x[lead + n:] == 5).all())
+    for kind in range(2):
+        want = np.concatenate([pool.ref.sequence(kind, 0, pool.table[b], lens[b])[lens[b] - news[b]:] for b in range(count)])
+        assert np.array_equal(out[kind][lead:lead + n, 0].cpu().double().numpy(), want)
+    mid = slice(lead, lead + n)
+    want, tol = kv_ref.attention(q[mid].double().numpy(), pool.ref, starts(news), lens, pool.table,
+                                 np.float64(np.float32(dim ** -0.5)), 1, bounds=True)
+    check(out[2][mid], want, tol)
+
+
 def test_sequences_that_share_blocks(nv):
     """A prefix's blocks in several tables, and a block twice in one: read only, each sequence as if alone."""
     pool = Pool(nv, 108, 2, 64, [300, 300, 300])
