@@ -496,9 +496,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences
  * powers of two below the maximum; values above 2^96, or scaled scores above 2^30,
  * can overflow them.)  The order of the sums depends on the sizes and
  * max_len only: the same call gives the same bytes.
- * max_len is the host's bound on the lengths, used to decide how far the keys
- * of few rows are shared out over workgroups (results for longer sequences are
- * right all the same).  The workspace needs
+ * max_len is the host's bound on the lengths, used to decide how many rows a
+ * workgroup takes and how far the keys of few rows are shared out over
+ * workgroups (results for longer sequences are right all the same).  The workspace needs
  * nvfp4_kv_attention_workspace_bytes(...) bytes for the same sizes (16-byte
  * aligned; may be NULL when that is 0); calls that can overlap must not share
  * it.  scale > 0 and finite; causal_block, max_len >= 0; q_heads a multiple of

@@ -774,8 +774,8 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
 
     Rows and positions as in kv_write.  causal_block: 0 for no mask, 1 for causal, c for runs of c positions that
     see one another and all before them.  scale: dim^-0.5 by default.  max_len: a bound on the lengths known to the
-    host (default: what the table holds), which decides how far the keys of few rows are shared out over
-    workgroups.  A workspace of nvfp4_kv_attention_workspace_bytes(...) is allocated with torch when none is given,
+    host (default: what the table holds), which decides how many rows a workgroup takes and how far the keys of
+    few rows are shared out over workgroups.  A workspace of nvfp4_kv_attention_workspace_bytes(...) is allocated with torch when none is given,
     on the stream that the call runs on."""
     dev = cache.device
     _same_device(dev, q, out, workspace)

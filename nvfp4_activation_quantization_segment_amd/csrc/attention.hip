@@ -816,11 +816,21 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
 AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len) {
     const int32_t group = q_heads / kv_heads;
     AttentionPlan p;
-    // 128-row tiles from 96 rows a sequence (on average) on.  8 sequences, 32 query
-    // and 8 key/value heads: 128 rows over 30,000 keys 212 us (narrow tiles 328),
-    // over 3000 keys 49 (45), 96 rows over 3000 37 (35); 32 sequences of 100 rows
-    // and keys, 16 heads of 64: 12 us (25).
-    p.wide = M * group >= 96 * B;
+    const int64_t blocks = clamp64(max_len, 0, (int64_t)1 << 31) / kKvBlock + (max_len % kKvBlock != 0);
+    // 128-row tiles from 64 rows a sequence (on average) on.  8 sequences, 32 query
+    // and 8 key/value heads: 128 rows over 30,000 keys 212 us (narrow tiles 328);
+    // 16 sequences of 64 rows and keys, 56 heads: 20 (35), 16 heads: 10 (16).
+    // But where they are no more than one for each CU, one after the other of
+    // their blocks of keys is what takes the time, and a narrow tile's four waves
+    // share them out without a join: one prompt of 1000 rows and 16 heads 35 us
+    // (17), 56 heads and 512 rows 34 (24).  Over more than 8192 keys pieces of
+    // them fill the chip again (16 heads, 512 rows after 16,000: 94, narrow 135),
+    // and over very few a narrow tile's own start and end are most of it (32 and 8
+    // heads, 4 sequences of 256 rows: 15, narrow 24).  Over 351 shapes of 64 to
+    // 4000 rows and both dims the rule is 1% slower on average than the better of
+    // the two, and 32% at most; always wide 9%, and 102%.
+    const int64_t wide_tiles = (M * group + kWideRows - 1) / kWideRows * kv_heads;
+    p.wide = M * group >= 64 * B && !(wide_tiles <= 256 && blocks <= 128 && wide_tiles <= 32 * blocks);
     const int64_t T = p.wide ? kWideRows : kRows;
     // The keys are cut into pieces until two workgroups for each of 256 CUs are
     // in flight, but not below 8 blocks to a piece of a narrow tile (2 a wave;
@@ -833,7 +843,6 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
     // slots 13 us, 117 when they counted.
     const int64_t most_seqs = B < M ? B : M;
     tiles = tiles < most_seqs ? most_seqs : tiles;
-    const int64_t blocks = clamp64(max_len, 0, (int64_t)1 << 31) / kKvBlock + (max_len % kKvBlock != 0);
     int64_t want = 512 / (tiles * kv_heads);
     // Many sequences are of many lengths, which the host does not know: pieces
     // half as long even the workgroups out (32 sequences of 1 to 16,384 keys: 123
@@ -853,7 +862,7 @@ static void attention_of(const AttentionArgs& args, hipStream_t s) {
     const int64_t units = tile_first(a.seqs.M, a.seqs.B, a.group, T, a.seqs.per_row);
     if (a.wide) {
         // below 2^23, so that the threads of a dimension stay below 2^32: the heads
-        // times M group / 128 + B, where B <= M group / 96 and M q_heads <= 2^28
+        // times M group / 128 + B, where B <= M group / 64 and M q_heads <= 2^28
         const dim3 grid((unsigned)(units * a.cache.heads), 1, (unsigned)a.parts);
         attention_wide_kernel<D><<<grid, dim3(64 * kWideWaves), 0, s>>>(a);
     } else {

@@ -1,4 +1,7 @@
 """Rotary positions, the 8-bit key/value cache and attention over it, against plain references (tests/kv_ref.py)."""
+import functools
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -11,11 +14,20 @@ BLOCK = 64
 
 
 @pytest.fixture(scope="module")
-def nv():
+def nv(request):
     import nvfp4_activation_quantization_segment_amd as m
 
     device()
-    return m
+    bound = getattr(request, "param", None)
+    if bound is None:
+        return m
+    return types.SimpleNamespace(**dict(vars(m), kv_attention=functools.partial(m.kv_attention, max_len=bound)))
+
+
+# The bound on the lengths decides between 32-row and 128-row tiles and how far the keys are cut: what the table
+# holds mostly gives 32 rows at these sizes, 0 gives 128 rows in one piece (from 64 rows a sequence on), a large
+# one 128 rows in many pieces.  The results have to be right with all of them.
+BOUNDS = pytest.mark.parametrize("nv", [None, 0, 1 << 20], indirect=True, ids=["fits", "one-piece", "pieces"])
 
 
 def gen(seed):
@@ -374,6 +386,7 @@ def test_kv_write_and_read_past_the_ends(nv):
         assert np.isnan(got[43:73]).all()
 
 
+@BOUNDS
 @pytest.mark.parametrize("rs,lens", [([5, 2, 9], [4, 4]), ([-3, 40, 2000], [64, 64]), ([0, 0, 0], [0, 0]),
                                      ([10, 10, 3], [2**31 - 1, -2**31]), ([2**31 - 1, -2**31, 5], [64, -1])])
 def test_arrays_that_make_no_sense_stay_in_bounds(nv, rs, lens):
@@ -438,6 +451,7 @@ ATTENTION = [
 ]
 
 
+@BOUNDS
 @pytest.mark.parametrize("case", range(len(ATTENTION)))
 def test_attention(nv, case):
     dim, heads, group, c, seqs = ATTENTION[case]
@@ -458,6 +472,7 @@ def test_attention(nv, case):
     assert same(inplace, got)
 
 
+@BOUNDS
 @pytest.mark.parametrize("dim,heads,group,c,seqs", [(128, 2, 4, 1, [(0, 700), (333, 500)]), (64, 3, 1, 0, [(900, 601)]),
                                                     (128, 4, 1, 256, [(100, 1100)]), (64, 2, 7, 1, [(0, 300), (0, 301)])])
 def test_attention_of_longer_rows(nv, dim, heads, group, c, seqs):
@@ -500,6 +515,7 @@ def test_attention_in_two_parts(nv, dim, count):
     check(got, want, tol)
 
 
+@BOUNDS
 @pytest.mark.parametrize("rows", [1, 40, 300])
 def test_rows_that_see_nothing(nv, rows):
     """A sequence of no positions, and more rows than positions under a causal mask: those rows are 0, and rows of no
@@ -519,6 +535,7 @@ def test_rows_that_see_nothing(nv, rows):
         assert bool((out[rs[1]:rs[2] - 5] == 0).all())
 
 
+@BOUNDS
 @pytest.mark.parametrize("dim,group,news,past", [
     (64, 1, [1, 1], [70, 100]), (128, 2, [40, 3], [70, 100]), (128, 1, [150, 130], [70, 100]), (64, 4, [200, 70], [70, 100]),
     (128, 2, [3, 1], [2500, 3001]), (64, 1, [150, 99], [2500, 1900])])  # the last two share the keys out
@@ -557,6 +574,7 @@ def test_what_is_hidden_has_no_effect(nv, dim, group, news, past):
         clean = call()
 
 
+@BOUNDS
 @pytest.mark.parametrize("causal", [0, 1])
 @pytest.mark.parametrize("dim,rows", [(64, 1), (128, 1), (64, 3), (128, 5), (64, 66), (128, 130), (64, 201)])
 def test_codes_left_behind_the_largest_values(nv, dim, rows, causal):
@@ -580,6 +598,7 @@ def test_codes_left_behind_the_largest_values(nv, dim, rows, causal):
     assert same(got[1], got[0])
 
 
+@BOUNDS
 @pytest.mark.parametrize("rows", [1, 50, 200])
 def test_blocks_and_lengths_that_do_not_exist(nv, rows):
     pool = Pool(nv, 86, 2, 64, [300, 300, 300, 300])
@@ -594,6 +613,7 @@ def test_blocks_and_lengths_that_do_not_exist(nv, rows):
     assert np.isnan(want[3 * rows:]).all() and not np.isnan(want[:rows]).any()
 
 
+@BOUNDS
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("rows", [30, 130])
 def test_missing_blocks_beside_unwritten_ones(nv, dim, rows):
@@ -617,6 +637,7 @@ def test_missing_blocks_beside_unwritten_ones(nv, dim, rows):
         assert same(x[:24], got[0][:24])
 
 
+@BOUNDS
 def test_queries_that_are_not_finite_and_large_and_small_ones(nv):
     pool = Pool(nv, 88, 1, 128, [100, 100])
     q = normal(gen(89), 40, 1, 128)
@@ -636,6 +657,7 @@ def test_queries_that_are_not_finite_and_large_and_small_ones(nv):
     check(got, want, tol)
 
 
+@BOUNDS
 def test_values_of_very_different_powers(nv):
     """Blocks whose values differ by powers of two up to 2^60, and values near the ends of the range."""
     for low, high in ((90, 150), (10, 30), (200, 240)):
@@ -650,6 +672,7 @@ def test_values_of_very_different_powers(nv):
         check(got, want, tol)
 
 
+@BOUNDS
 def test_scores_far_apart(nv):
     """A growing row of scores (each block above the last by hundreds), a falling one, and one that stays."""
     heads, dim, n = 3, 64, 640
@@ -667,6 +690,7 @@ def test_scores_far_apart(nv):
     check(got, want, tol)
 
 
+@BOUNDS
 @pytest.mark.parametrize("count", [62, 63, 64, 65, 300, 4200])
 def test_many_sequences(nv, count):
     """Counts around and above the 64 that are looked up at once: written, read back and attended, each sequence by
@@ -691,6 +715,7 @@ def test_many_sequences(nv, count):
     check(got, ref, tol)
 
 
+@BOUNDS
 @pytest.mark.parametrize("count,rows,group,dim,longest", [
     (70, {0: 1}, 1, 64, 2500), (70, {69: 1}, 4, 128, 2500), (300, {3: 1, 150: 2, 151: 1, 299: 1}, 2, 64, 1500),
     (9, {2: 1, 7: 1}, 40, 64, 2500), (12, {0: 1, 5: 2}, 70, 128, 600), (12, {1: 1, 2: 1, 11: 1}, 130, 64, 1100),
@@ -723,6 +748,7 @@ def test_slots_that_are_mostly_empty(nv, count, rows, group, dim, longest):
     check(out[2][mid], want, tol)
 
 
+@BOUNDS
 def test_sequences_that_share_blocks(nv):
     """A prefix's blocks in several tables, and a block twice in one: read only, each sequence as if alone."""
     pool = Pool(nv, 108, 2, 64, [300, 300, 300])
@@ -794,6 +820,7 @@ def _serving_state(nv, seed, lens, heads=2, group=4, dim=128):
     return pool
 
 
+@BOUNDS
 def test_captured_tokens_replay(nv):
     """Append and attend for four sequences captured once and replayed with new inputs and lengths, eager work in
     between, two graphs alive at once: every replay equals the eager calls."""
@@ -851,6 +878,7 @@ def test_other_streams(nv):
         assert same(o, want)
 
 
+@BOUNDS
 def test_same_call_same_bytes(nv):
     pool = Pool(nv, 99, 4, 64, [5000, 4000])
     q = normal(gen(98), 300, 8, 64).cuda()
