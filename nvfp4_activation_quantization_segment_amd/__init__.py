@@ -737,7 +737,10 @@ def kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, row_start: torch.
 
     Sequence b's rows are row_start[b] .. row_start[b + 1], its last positions once it holds lens[b] of them;
     table [sequences, blocks] names its cache blocks (all int32 on the GPU).  With tables and positions the keys
-    are rotated on the way, as `rope` does."""
+    are rotated on the way, as `rope` does; one without the other is refused."""
+    if (positions is None) != (len(tables) == 0):
+        raise ValueError("rotating the keys needs their tables and positions, got " +
+                         ("tables" if positions is None else "positions") + " alone")
     dev = cache.device
     _same_device(dev, k, v)
     rows = k.shape[0]
@@ -745,9 +748,7 @@ def kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, row_start: torch.
     hk, hv = make_heads("k", k, shape), make_heads("v", v, shape)
     q = make_kv_sequences(row_start, lens, table, dev)
     r = None
-    if len(tables):
-        if positions is None:
-            raise ValueError("rotating the keys needs their positions")
+    if positions is not None:
         r = make_rope_params(tables, positions, rows, split, dev)
     if rows:
         _call("nvfp4_kv_write", lib.nvfp4_kv_write, dev, stream, cache.struct, q, rows, hk, hv, r)

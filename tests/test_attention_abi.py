@@ -323,3 +323,18 @@ def test_any_bound_on_the_lengths(nv):
         assert want > 0
         for max_len in (1 << 40, (1 << 63) - 64, (1 << 63) - 1):
             assert f(M, count, q_heads, 8, 128, max_len) == want
+
+
+def test_positions_without_tables_are_refused(nv):
+    """Positions say that the keys are to be rotated: without tables they were written as they are."""
+    import types
+
+    import torch
+
+    cpu = torch.device("cpu")
+    x = torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32)  # noqa: E731
+    pool = types.SimpleNamespace(device=cpu, heads=1, dim=64, struct=None)
+    for tables in ((), []):
+        with pytest.raises(ValueError, match="tables"):
+            nv.kv_write(pool, x, x, i32(0, 2), i32(2), i32([0]), tables=tables, positions=torch.zeros(2, 1, dtype=torch.int32))
