@@ -683,13 +683,19 @@ class KvCache:
     """A pool of 8-bit key/value cache blocks of 64 positions, as four uint8 tensors:
 
     k [blocks, heads, dim / 16, 64, 16] and v [blocks, heads, 4, dim, 16], E4M3 codes in the order that the
-    attention kernels read them; k_power and v_power [blocks, heads], byte b standing for 2^(b - 127)."""
+    attention kernels read them; k_power and v_power [blocks, heads], byte b standing for 2^(b - 127).
+    The tensors stay the same for the cache's life; calls take the memory that they have then."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_power: torch.Tensor, v_power: torch.Tensor):
+        self._tensors = k, v, k_power, v_power
+        self._describe()
+
+    def _describe(self):
+        k, v, k_power, v_power = self._tensors
         if k.dim() != 5:
             raise ValueError("k must be [blocks, heads, dim / 16, 64, 16]")
         blocks, heads, groups, block, sixteen = k.shape
-        dim, dev, u8 = 16 * groups, k.device, torch.uint8
+        dim, u8 = 16 * groups, torch.uint8
         if not (k.dtype == v.dtype == k_power.dtype == v_power.dtype == u8):
             raise TypeError(f"expected uint8, got {[t.dtype for t in (k, v, k_power, v_power)]}")
         if (block != KV_BLOCK or sixteen != 16 or v.shape != (blocks, heads, 4, dim, 16) or
@@ -697,11 +703,26 @@ class KvCache:
                 not (k.is_contiguous() and v.is_contiguous() and k_power.is_contiguous() and v_power.is_contiguous())):
             raise ValueError(f"expected contiguous {[blocks, heads, groups, KV_BLOCK, 16]}, {[blocks, heads, 4, dim, 16]} "
                              f"and twice {[blocks, heads]}, got {[list(t.shape) for t in (k, v, k_power, v_power)]}")
-        _same_device(dev, v, k_power, v_power)
-        self.k, self.v, self.k_power, self.v_power = k, v, k_power, v_power
-        self.blocks, self.heads, self.dim, self.device = blocks, heads, dim, dev
-        self.struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_power.data_ptr(), v_power.data_ptr(), blocks, heads,
-                                     dim)
+        _same_device(k.device, v, k_power, v_power)
+        self._memory = k.data_ptr(), v.data_ptr(), k_power.data_ptr(), v_power.data_ptr()
+        self._struct = KvCacheStruct(*self._memory, blocks, heads, dim)
+
+    @property
+    def struct(self) -> KvCacheStruct:
+        """The C description, of the memory that the tensors have now."""
+        k, v, k_power, v_power = self._tensors
+        if (k.data_ptr(), v.data_ptr(), k_power.data_ptr(), v_power.data_ptr()) != self._memory:
+            self._describe()
+        return self._struct
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_power = property(lambda self: self._tensors[2])
+    v_power = property(lambda self: self._tensors[3])
+    device = property(lambda self: self._tensors[0].device)
+    blocks = property(lambda self: self.struct.blocks)
+    heads = property(lambda self: self.struct.heads)
+    dim = property(lambda self: self.struct.dim)
 
     @classmethod
     def empty(cls, blocks: int, heads: int, dim: int, device=None) -> "KvCache":
@@ -741,30 +762,30 @@ def kv_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, row_start: torch.
     if (positions is None) != (len(tables) == 0):
         raise ValueError("rotating the keys needs their tables and positions, got " +
                          ("tables" if positions is None else "positions") + " alone")
-    dev = cache.device
+    dev, c = cache.device, cache.struct
     _same_device(dev, k, v)
     rows = k.shape[0]
-    shape = (rows, cache.heads, cache.dim)
+    shape = (rows, c.heads, c.dim)
     hk, hv = make_heads("k", k, shape), make_heads("v", v, shape)
     q = make_kv_sequences(row_start, lens, table, dev)
     r = None
     if positions is not None:
         r = make_rope_params(tables, positions, rows, split, dev)
     if rows:
-        _call("nvfp4_kv_write", lib.nvfp4_kv_write, dev, stream, cache.struct, q, rows, hk, hv, r)
+        _call("nvfp4_kv_write", lib.nvfp4_kv_write, dev, stream, c, q, rows, hk, hv, r)
 
 
 def kv_read(cache: KvCache, rows: int, row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
             k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
     """Reads the positions of `rows` rows (as kv_write addresses them) back: k and v, bf16 [rows, heads, dim]."""
-    dev = cache.device
+    dev, c = cache.device, cache.struct
     _same_device(dev, k, v)
     q = make_kv_sequences(row_start, lens, table, dev)
-    shape = (rows, cache.heads, cache.dim)
+    shape = (rows, c.heads, c.dim)
     k, hk = _output("k", k, dev, stream, shape)
     v, hv = _output("v", v, dev, stream, shape)
     if rows:
-        _call("nvfp4_kv_read", lib.nvfp4_kv_read, dev, stream, cache.struct, q, rows, hk, hv)
+        _call("nvfp4_kv_read", lib.nvfp4_kv_read, dev, stream, c, q, rows, hk, hv)
     return k, v
 
 
@@ -778,12 +799,12 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
     host (default: what the table holds), which decides how many rows a workgroup takes and how far the keys of
     few rows are shared out over workgroups.  A workspace of nvfp4_kv_attention_workspace_bytes(...) is allocated with torch when none is given,
     on the stream that the call runs on."""
-    dev = cache.device
+    dev, c = cache.device, cache.struct
     _same_device(dev, q, out, workspace)
     hq = make_heads("q", q)
     rows, q_heads, dim = shape = q.shape
-    if dim != cache.dim:
-        raise ValueError(f"q has heads of {dim}, the cache of {cache.dim}")
+    if dim != c.dim:
+        raise ValueError(f"q has heads of {dim}, the cache of {c.dim}")
     s = make_kv_sequences(row_start, lens, table, dev)
     if max_len is None:
         max_len = table.shape[1] * KV_BLOCK
@@ -791,14 +812,14 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
         raise ValueError(f"causal_block: expected 0 to 2^31 - 1, got {causal_block}")
     out, ho = _output("out", out, dev, stream, shape)
     if workspace is None and rows:
-        need = lib.nvfp4_kv_attention_workspace_bytes(rows, s.count, q_heads, cache.heads, dim, max_len)
+        need = lib.nvfp4_kv_attention_workspace_bytes(rows, s.count, q_heads, c.heads, dim, max_len)
         if need:
             workspace = _empty(dev, stream, (need,), torch.uint8)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if rows:
-        _call("nvfp4_kv_attention", lib.nvfp4_kv_attention, dev, stream, hq, rows, q_heads, cache.struct, s,
+        _call("nvfp4_kv_attention", lib.nvfp4_kv_attention, dev, stream, hq, rows, q_heads, c, s,
               dim ** -0.5 if scale is None else float(scale), causal_block, max_len, ho,
               None if workspace is None else workspace.data_ptr(), size)
     return out

@@ -338,3 +338,29 @@ def test_positions_without_tables_are_refused(nv):
     for tables in ((), []):
         with pytest.raises(ValueError, match="tables"):
             nv.kv_write(pool, x, x, i32(0, 2), i32(2), i32([0]), tables=tables, positions=torch.zeros(2, 1, dtype=torch.int32))
+
+
+def test_a_cache_describes_the_memory_that_it_has(nv, monkeypatch):
+    """Calls get the pointers that the tensors have then, and nothing of a cache can be assigned."""
+    import torch
+
+    monkeypatch.setattr(nv, "_same_device", lambda dev, *tensors: None)
+    shapes = (3, 2, 4, 64, 16), (3, 2, 4, 64, 16), (3, 2), (3, 2)
+    make = lambda: [torch.zeros(s, dtype=torch.uint8) for s in shapes]  # noqa: E731
+    tensors, other = make(), make()
+    c = nv.KvCache(*tensors)
+    described = lambda: [getattr(c.struct, n) for n in ("k", "v", "k_power", "v_power")]  # noqa: E731
+    assert described() == [t.data_ptr() for t in tensors] and (c.struct.blocks, c.struct.heads, c.struct.dim) == (3, 2, 64)
+    for name, value in zip(("k", "v", "k_power", "v_power", "blocks", "heads", "dim", "device", "struct"), other + [9, 9, 9, None, None]):
+        with pytest.raises(AttributeError):
+            setattr(c, name, value)
+    for t, o in zip(tensors, other):  # the same tensors with other memory
+        t.data = o
+        assert described() == [t.data_ptr() for t in tensors]
+    tensors[0].data = torch.zeros(1, 2, 4, 64, 16, dtype=torch.uint8)  # and of another size
+    with pytest.raises(ValueError, match="contiguous"):
+        c.struct
+    four = [torch.zeros((4, *s[1:]), dtype=torch.uint8) for s in shapes]
+    for t, o in zip(tensors, four):
+        t.data = o
+    assert described() == [t.data_ptr() for t in four] and c.struct.blocks == c.blocks == 4
