@@ -371,8 +371,9 @@ nvfp4_status nvfp4_modulate_gemm_ring(const uint16_t* x, int64_t M, int64_t K, i
 
 /* Heads [rows, heads, dim] in device memory, bf16, unit stride along dim: head
  * h of row m starts at data + m * row_stride + h * head_stride (elements, both
- * multiples of 8 and not negative; data 16-byte aligned).  A third of a QKV
- * product and [heads, rows, dim] are both of this form.  As an output no two
+ * multiples of 8 and not negative, at most 2^38; data 16-byte aligned; neither
+ * (rows - 1) * row_stride nor (heads - 1) * head_stride past 2^60).  A third of a
+ * QKV product and [heads, rows, dim] are both of this form.  As an output no two
  * heads may overlap: row_stride >= (heads - 1) * head_stride + dim with
  * head_stride >= dim, or head_stride >= (rows - 1) * row_stride + dim with
  * row_stride >= dim. */

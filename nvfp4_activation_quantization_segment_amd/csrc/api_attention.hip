@@ -20,9 +20,11 @@ nvfp4_status check_heads(const nvfp4_heads* x, int64_t M, int64_t heads, int64_t
     if (!x || !x->data) return NVFP4_ERR_INVALID_ARGUMENT;
     if (x->row_stride < 0 || x->head_stride < 0) return NVFP4_ERR_INVALID_ARGUMENT;
     if (!aligned(x->data, 16) || x->row_stride % 8 != 0 || x->head_stride % 8 != 0) return NVFP4_ERR_ALIGNMENT;
-    // element offsets of the last head stay far inside 64 bits
-    constexpr int64_t kMost = (int64_t)1 << 38;
+    // the last head's offset stays inside 64 bits, in elements and in bytes
+    constexpr int64_t kMost = (int64_t)1 << 38, kReach = (int64_t)1 << 60;
     if (x->row_stride > kMost || x->head_stride > kMost) return NVFP4_ERR_SHAPE;
+    if ((M > 1 && x->row_stride > kReach / (M - 1)) || (heads > 1 && x->head_stride > kReach / (heads - 1)))
+        return NVFP4_ERR_SHAPE;
     if (output) {
         const bool by_row = (heads == 1 || x->head_stride >= dim) &&
                             (M == 1 || x->row_stride >= (heads - 1) * x->head_stride + dim);

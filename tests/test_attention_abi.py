@@ -364,3 +364,20 @@ def test_a_cache_describes_the_memory_that_it_has(nv, monkeypatch):
     for t, o in zip(tensors, four):
         t.data = o
     assert described() == [t.data_ptr() for t in four] and c.struct.blocks == c.blocks == 4
+
+
+def test_heads_too_far_apart_are_refused(nv):
+    """Attention takes up to 2^28 query heads a call: the last one's offset has to fit 64 bits, in elements and bytes."""
+    def call(M, q_heads, q, out):
+        return nv.lib.nvfp4_kv_attention(q, M, q_heads, cache(nv, heads=1), seqs(nv, count=1), 0.1, 1, 64, out, FAKE, 1 << 40, None)
+
+    misaligned = heads(nv, FAKE + 8)  # as the output: the queries have passed
+    for M, q_heads, stride in ((1, 1 << 28, 1 << 38), (2, 1 << 27, 1 << 37), (2, 1 << 27, 1 << 36), (1, 1 << 28, 1 << 33)):
+        far = heads(nv, head=stride)
+        assert call(M, q_heads, far, misaligned) == SHAPE
+        # as an output, rows 8 elements apart overlap; (2^27 - 1) 2^37 is negative in 64 bits
+        assert call(M, q_heads, heads(nv), heads(nv, row=8, head=stride)) == SHAPE
+    for M, q_heads, stride in ((1, 1 << 20, 1 << 38), (1, 1, 1 << 38), (1 << 23, 32, 1 << 38)):
+        assert call(M, q_heads, heads(nv, head=stride), misaligned) == ALIGNMENT
+    assert call(1 << 23, 32, heads(nv, row=1 << 38), misaligned) == SHAPE
+    assert call(1 << 22, 32, heads(nv, row=1 << 38), misaligned) == ALIGNMENT
