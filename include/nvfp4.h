@@ -502,8 +502,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences
  * workgroups (results for longer sequences are right all the same).  The workspace needs
  * nvfp4_kv_attention_workspace_bytes(...) bytes for the same sizes (16-byte
  * aligned; may be NULL when that is 0); calls that can overlap must not share
- * it.  scale > 0 and finite; causal_block, max_len >= 0; q_heads a multiple of
- * cache->heads, M * q_heads <= 2^28; out may be q itself. */
+ * it.  scale > 0, and scale * log2(e) finite in binary32; causal_block, max_len
+ * >= 0; q_heads a multiple of cache->heads, M * q_heads <= 2^28; out may be q
+ * itself. */
 size_t nvfp4_kv_attention_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
                                           int64_t max_len);
 nvfp4_status nvfp4_kv_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads, const nvfp4_kv_cache* cache,

@@ -153,7 +153,8 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads
     if ((st = check_cache(cache, &a.cache)) != NVFP4_OK) return st;
     if ((st = check_sequences(seqs, M, &a.seqs)) != NVFP4_OK) return st;
     if (q_heads < 1 || causal_block < 0 || max_len < 0) return NVFP4_ERR_INVALID_ARGUMENT;
-    if (!(scale > 0.0f) || !isfinite(scale)) return NVFP4_ERR_INVALID_ARGUMENT;
+    const float scale_log2 = scale * 1.44269504088896340736f;
+    if (!(scale > 0.0f) || !isfinite(scale_log2)) return NVFP4_ERR_INVALID_ARGUMENT;
     if (!attention_sizes_ok(M, seqs->count, q_heads, cache->heads, cache->dim, max_len)) return NVFP4_ERR_SHAPE;
     if ((st = check_heads(q, M, q_heads, cache->dim, false)) != NVFP4_OK) return st;
     if ((st = check_heads(out, M, q_heads, cache->dim, true)) != NVFP4_OK) return st;
@@ -164,7 +165,7 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads
     a.out = out_of(out);
     a.q_heads = q_heads;
     a.group = q_heads / cache->heads;
-    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.scale_log2 = scale_log2;
     a.causal = causal_block;
     a.wide = p.wide;
     a.parts = p.parts;

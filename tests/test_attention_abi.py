@@ -381,3 +381,14 @@ def test_heads_too_far_apart_are_refused(nv):
         assert call(M, q_heads, heads(nv, head=stride), misaligned) == ALIGNMENT
     assert call(1 << 23, 32, heads(nv, row=1 << 38), misaligned) == SHAPE
     assert call(1 << 22, 32, heads(nv, row=1 << 38), misaligned) == ALIGNMENT
+
+
+def test_scales_past_binary32_are_refused(nv):
+    """Scores are taken in base 2: scale * log2(e) has to be finite (times a score of 0 it gave NaN)."""
+    def call(scale):  # a misaligned output: a good scale gets that far
+        return nv.lib.nvfp4_kv_attention(heads(nv), 10, 8, cache(nv), seqs(nv), scale, 1, 64, heads(nv, FAKE + 8), FAKE, 1 << 40, None)
+
+    for scale in (3.4e38, 2.4e38, 2.36e38):
+        assert call(scale) == INVALID
+    for scale in (2.35e38, 1e30, 0.1, 1e-38, 1e-45):
+        assert call(scale) == ALIGNMENT

@@ -996,3 +996,15 @@ def test_another_devices_or_types_are_refused(nv):
         nv.rope(q.cuda(), [nv.rope_table(4, 8)], torch.zeros(1, 1, dtype=torch.int32, device="cuda").expand(4, 1))
     empty = nv.kv_attention(q.cuda()[:0], pool.gpu, i32([0, 0]), pool.lens, pool.tab)
     assert tuple(empty.shape) == (0, 1, 64)
+
+
+@BOUNDS
+@pytest.mark.parametrize("rows", [1, 90])
+def test_the_smallest_scale(nv, rows):
+    """The smallest number of binary32, not a normal one: all scores are equal, and what is masked stays so."""
+    pool = Pool(nv, 110, 2, 64, [200])
+    q = normal(gen(111), rows, 4, 64)
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32([0, rows]), pool.lens, pool.tab, scale=1e-45, causal_block=1)
+    want, tol = kv_ref.attention(q.double().numpy(), pool.ref, [0, rows], [200], pool.table, np.float64(np.float32(1e-45)), 1,
+                                 bounds=True)
+    check(got, want, tol)
