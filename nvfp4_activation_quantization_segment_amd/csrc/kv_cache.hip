@@ -755,14 +755,6 @@ __global__ __launch_bounds__(2 * D) void kv_read_kernel(CacheArgs c, SeqArgs q, 
     }
 }
 
-// Heads that one workgroup takes: as many as leave about 8 workgroups for each
-// of 256 CUs, so that a short call still fills the chip, and at most `most`.
-// The writer looks its angles up once for all of them (37,810 x 56 heads: 340 us
-// with 16, 346 with 8, 387 with 2); the reader keeps nothing from one to the
-// next (352 us with 2, 356 with 8, 363 with 16).
-constexpr int kWriteHeads = 16, kReadHeads = 2;
-int heads_each(int64_t units, int32_t heads, int most) { return (int)clamp64(units * heads / 2048, 1, most); }
-
 // Rows a sequence (on average) up to which the short writer is taken, with one
 // wave up to one row and four above.  256 single tokens of 56 heads: 21 us with
 // one wave, 48 with four, 110 with the long writer.  8 heads, 32 sequences of 4
@@ -821,7 +813,7 @@ static void kv_write_of(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, 
     const int64_t units = block_first(q.M, q.B, q.per_row);
     if (q.M <= q.B) return kv_append_of<D, 1>(c, q, k, v, r, s);
     if (q.M <= kAppendRows * q.B) return kv_append_of<D, 4>(c, q, k, v, r, s);
-    const int each = heads_each(units, c.heads, kWriteHeads);
+    const int each = kv_heads_each(units, c.heads, kKvWriteHeads);
     const dim3 grid((unsigned)units, (unsigned)((c.heads + each - 1) / each)), block(2 * D);
     if (r.axes == 0)
         kv_write_kernel<D, ROPE_NONE><<<grid, block, 0, s>>>(c, q, k, v, r, each);
@@ -846,7 +838,7 @@ hipError_t launch_kv_read(const CacheArgs& c, const SeqArgs& seqs, const HeadsOu
     SeqArgs q = seqs;
     q.per_row = blocks_per_row(q.M, q.B);
     const int64_t units = block_first(q.M, q.B, q.per_row);
-    const int each = heads_each(units, c.heads, kReadHeads);
+    const int each = kv_heads_each(units, c.heads, kKvReadHeads);
     const dim3 grid((unsigned)units, (unsigned)((c.heads + each - 1) / each));
     if (c.dim == 128)
         kv_read_kernel<128><<<grid, dim3(256), 0, s>>>(c, q, k, v, each);

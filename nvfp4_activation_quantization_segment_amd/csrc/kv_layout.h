@@ -67,6 +67,17 @@ constexpr int64_t tile_first(int64_t row, int64_t b, int64_t per, int64_t T, int
 }
 constexpr int64_t block_first(int64_t row, int64_t b, int32_t per_row) { return per_row ? row : block_base(row, b); }
 
+// Heads that one workgroup of the cache's long writer or reader takes: as many
+// as leave about 8 workgroups for each of 256 CUs, so that a short call still
+// fills the chip, and at most `most`.  The writer looks its angles up once for
+// all of them (37,810 x 56 heads: 340 us with 16, 346 with 8, 387 with 2); the
+// reader keeps nothing from one to the next (352 us with 2, 356 with 8, 363 with
+// 16).
+constexpr int kKvWriteHeads = 16, kKvReadHeads = 2;
+constexpr int32_t kv_heads_each(int64_t units, int32_t heads, int32_t most) {
+    return (int32_t)clamp64(units * heads / 2048, 1, most);
+}
+
 // Rows [first, last) of sequence b of row_start, whatever the array holds.
 struct RowRange {
     int64_t first, last;

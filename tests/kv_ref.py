@@ -205,3 +205,14 @@ def attention_fast(q, cache, row_start, lens, table, scale, c):
             out[rows, g] = o
             tol[rows, g] = (2.0 ** -8 + 2 * ds) * a + 2.0 ** -8 * (np.abs(o) + (2.0 ** -8 + 2 * ds) * a) + 1e-38
     return out, tol
+
+
+# Calls whose long writer and reader take several heads to a workgroup, the last of them fewer: heads, dim,
+# [(past, new)] and the heads that a workgroup takes, written and read.
+HEAD_LOOPS = [
+    (53, 128, [(37, 5000), (0, 4000)], 3, 2),
+    (57, 64, [(1, 63), (100, 8900), (0, 37)], 4, 2),
+    (41, 64, [(0, 20000), (17, 10001)], 9, 2),
+    (37, 64, [(63, 60001)], 16, 2),
+    (35, 128, [(5, 60002)], 16, 2),
+]

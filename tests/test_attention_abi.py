@@ -392,3 +392,22 @@ def test_scales_past_binary32_are_refused(nv):
         assert call(scale) == INVALID
     for scale in (2.35e38, 1e30, 0.1, 1e-38, 1e-45):
         assert call(scale) == ALIGNMENT
+
+
+def test_heads_of_a_workgroup(tmp_path):
+    """The shapes that the head loops are tested with take as many heads as they say, the last workgroup fewer."""
+    lines = []
+    for heads, _, seqs, write, read in kv_ref.HEAD_LOOPS:
+        M = sum(n for _, n in seqs)
+        assert M > 4 * len(seqs)  # the long writer
+        lines.append(f"need({heads}, block_first({M}, {len(seqs)}, blocks_per_row({M}, {len(seqs)})), {write}, {read});")
+    src, exe = tmp_path / "each.cpp", tmp_path / "each"
+    src.write_text('#include <cstdio>\n#include <cstdlib>\n#include "kv_layout.h"\nusing namespace nvfp4;\n'
+                   "static void need(int heads, int64_t units, int write, int read) {\n"
+                   "    const int w = kv_heads_each(units, heads, kKvWriteHeads), r = kv_heads_each(units, heads, kKvReadHeads);\n"
+                   "    if (w != write || r != read || w < 2 || r < 2 || heads % w == 0 || heads % r == 0) {\n"
+                   '        printf("%d heads: %d and %d a workgroup", heads, w, r);\n        exit(1);\n    }\n}\n'
+                   "int main() {\n" + "\n".join(lines) + "\n}\n")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert got.returncode == 0, got.stdout

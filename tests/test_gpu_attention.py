@@ -1008,3 +1008,53 @@ def test_the_smallest_scale(nv, rows):
     want, tol = kv_ref.attention(q.double().numpy(), pool.ref, [0, rows], [200], pool.table, np.float64(np.float32(1e-45)), 1,
                                  bounds=True)
     check(got, want, tol)
+
+
+@pytest.mark.parametrize("rope", ["none", "pairs", "split"])
+@pytest.mark.parametrize("case", range(len(kv_ref.HEAD_LOOPS)))
+def test_several_heads_to_a_workgroup(nv, case, rope):
+    """Long writes and reads whose workgroups go over several heads, the last of them over fewer, equal the same rows
+    one head at a time: partial first and last blocks over what is there, powers that grow, and rows that are not
+    finite in neighbouring heads, in single ones and in none."""
+    heads, dim, seqs, _, _ = kv_ref.HEAD_LOOPS[case]
+    news, lens = [n for _, n in seqs], [p + n for p, n in seqs]
+    M, rs = sum(news), i32(starts(news))
+    g = torch.Generator("cuda")
+    g.manual_seed(case)
+    k, v = (torch.randn(M, heads, dim, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    for x in (k, v):  # sizes of their own for heads and stretches of rows
+        x *= torch.exp2(torch.randint(-6, 7, (M // 50 + 1, heads, 1), generator=g, device="cuda")
+                        .repeat_interleave(50, 0)[:M].float()).to(torch.bfloat16)
+    for h, first, step in ((1, 3, 401), (2, 5, 401), (3, 0, 1009), (7, M - 1, 1), (heads - 1, 2, 333)):
+        k[first::step, h, h % dim] = float("inf")
+        v[first + 1::step, h, 5] = float("nan")
+        v[first::step, h + 1 if h + 1 < heads else 0, 9] = torch.finfo(torch.bfloat16).max
+    rot = {}
+    if rope != "none":
+        pairs = [16, 8, 8] if dim == 64 else [24, 16]
+        rot = dict(tables=[t.cuda() for t in tables_for(pairs, [50] * len(pairs))], split=rope == "split",
+                   positions=torch.randint(0, 50, (M, len(pairs)), generator=g, device="cuda", dtype=torch.int32))
+    need = [-(-n // BLOCK) for n in lens]
+    blocks = sum(need) + 1
+    order = torch.randperm(blocks, generator=g, device="cuda").int()
+    tab = torch.full((len(lens), max(need)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(need):
+        tab[b, :n] = order[at:at + n]
+        at += n
+    pool = nv.KvCache.empty(blocks, heads, dim)
+    for t in (pool.k, pool.v):
+        t.copy_(torch.randint(0, 0x7F, t.shape, generator=g, device="cuda", dtype=torch.uint8))
+    for t in (pool.k_power, pool.v_power):
+        t.copy_(torch.randint(118, 126, t.shape, generator=g, device="cuda", dtype=torch.uint8))
+    ones = [nv.KvCache(*(t[:, h:h + 1].contiguous() for t in (pool.k, pool.v, pool.k_power, pool.v_power))) for h in range(heads)]
+    nv.kv_write(pool, k, v, rs, i32(lens), tab, **rot)
+    back = nv.kv_read(pool, M, rs, i32(lens), tab)
+    for h, one in enumerate(ones):
+        nv.kv_write(one, k[:, h:h + 1].contiguous(), v[:, h:h + 1].contiguous(), rs, i32(lens), tab, **rot)
+        for name in ("k", "v", "k_power", "v_power"):
+            assert torch.equal(getattr(pool, name)[:, h], getattr(one, name)[:, 0]), f"head {h}: {name}"
+        for got, want in zip(back, nv.kv_read(one, M, rs, i32(lens), tab)):
+            assert torch.equal(got[:, h].view(torch.int16), want[:, 0].view(torch.int16)), f"head {h}"
+    bad = torch.isnan(back[1]).any(0).any(1)
+    assert bool(bad[1]) and bool(bad[2]) and not bool(bad[10])
