@@ -27,7 +27,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kRows = 32;  // rows of a wave
+constexpr int kRows = kNarrowRows;  // rows of a wave
 // Probabilities are taken against a reference that need not be the maximum:
 // while the sum of a lane's 16 new ones stays below this, the reference stays.
 constexpr float kMost = 256.0f;
@@ -484,7 +484,7 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
 // nothing; one workgroup to a CU instead of two took 5.2 ms.
 // ---------------------------------------------------------------------------
 constexpr int kWideWaves = 4;
-constexpr int kWideRows = kWideWaves * kRows;
+static_assert(kWideRows == kWideWaves * kRows, "32 rows to a wave");
 
 // Which tile and key/value head a workgroup takes.  Workgroups go to the 8 XCDs
 // in turn; where the heads divide evenly over them, each XCD takes whole heads,
@@ -817,20 +817,7 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
     const int32_t group = q_heads / kv_heads;
     AttentionPlan p;
     const int64_t blocks = clamp64(max_len, 0, (int64_t)1 << 31) / kKvBlock + (max_len % kKvBlock != 0);
-    // 128-row tiles from 64 rows a sequence (on average) on.  8 sequences, 32 query
-    // and 8 key/value heads: 128 rows over 30,000 keys 212 us (narrow tiles 328);
-    // 16 sequences of 64 rows and keys, 56 heads: 20 (35), 16 heads: 10 (16).
-    // But where they are no more than one for each CU, one after the other of
-    // their blocks of keys is what takes the time, and a narrow tile's four waves
-    // share them out without a join: one prompt of 1000 rows and 16 heads 35 us
-    // (17), 56 heads and 512 rows 34 (24).  Over more than 8192 keys pieces of
-    // them fill the chip again (16 heads, 512 rows after 16,000: 94, narrow 135),
-    // and over very few a narrow tile's own start and end are most of it (32 and 8
-    // heads, 4 sequences of 256 rows: 15, narrow 24).  Over 351 shapes of 64 to
-    // 4000 rows and both dims the rule is 1% slower on average than the better of
-    // the two, and 32% at most; always wide 9%, and 102%.
-    const int64_t wide_tiles = (M * group + kWideRows - 1) / kWideRows * kv_heads;
-    p.wide = M * group >= 64 * B && !(wide_tiles <= 256 && blocks <= 128 && wide_tiles <= 32 * blocks);
+    p.wide = attention_wide(M, B, group, kv_heads, blocks);
     const int64_t T = p.wide ? kWideRows : kRows;
     // The keys are cut into pieces until two workgroups for each of 256 CUs are
     // in flight, but not below 8 blocks to a piece of a narrow tile (2 a wave;

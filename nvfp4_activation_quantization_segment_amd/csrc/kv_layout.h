@@ -78,6 +78,26 @@ constexpr int32_t kv_heads_each(int64_t units, int32_t heads, int32_t most) {
     return (int32_t)clamp64(units * heads / 2048, 1, most);
 }
 
+// Rows of an attention tile, and which of the two a call takes.  B counts all
+// sequences, those without rows too.
+// 128-row tiles from 64 rows a sequence (on average) on.  8 sequences, 32 query
+// and 8 key/value heads: 128 rows over 30,000 keys 212 us (narrow tiles 328);
+// 16 sequences of 64 rows and keys, 56 heads: 20 (35), 16 heads: 10 (16).
+// But where they are no more than one for each CU, one after the other of
+// their blocks of keys is what takes the time, and a narrow tile's four waves
+// share them out without a join: one prompt of 1000 rows and 16 heads 35 us
+// (17), 56 heads and 512 rows 34 (24).  Over more than 8192 keys pieces of
+// them fill the chip again (16 heads, 512 rows after 16,000: 94, narrow 135),
+// and over very few a narrow tile's own start and end are most of it (32 and 8
+// heads, 4 sequences of 256 rows: 15, narrow 24).  Over 351 shapes of 64 to
+// 4000 rows and both dims the rule is 1% slower on average than the better of
+// the two, and 32% at most; always wide 9%, and 102%.
+constexpr int kNarrowRows = 32, kWideRows = 128;
+constexpr bool attention_wide(int64_t M, int64_t B, int64_t group, int64_t kv_heads, int64_t blocks) {
+    const int64_t wide_tiles = (M * group + kWideRows - 1) / kWideRows * kv_heads;
+    return M * group >= 64 * B && !(wide_tiles <= 256 && blocks <= 128 && wide_tiles <= 32 * blocks);
+}
+
 // Rows [first, last) of sequence b of row_start, whatever the array holds.
 struct RowRange {
     int64_t first, last;

@@ -216,3 +216,13 @@ HEAD_LOOPS = [
     (37, 64, [(63, 60001)], 16, 2),
     (35, 128, [(5, 60002)], 16, 2),
 ]
+
+# Attention calls with key/value heads in multiples of 8 that take 128-row tiles with a bound of 0 or 2^20 on the
+# lengths: dim, heads, query heads per key/value head, causal block, [(past, new)]; so many rows of no sequence before
+# the first and after the last.
+WIDE_HEADS = [
+    (128, 8, 1, 1, [(0, 300), (77, 130), (0, 0), (500, 65)]), (64, 8, 3, 1, [(10, 200), (0, 129)]),
+    (64, 8, 2, 1, [(30, 190), (0, 70)]), (64, 16, 1, 0, [(64, 257)]), (128, 16, 2, 100, [(0, 140), (200, 70)]),
+    (64, 24, 1, 1, [(0, 100), (0, 400), (3, 90)]),
+]
+WIDE_LEAD = 3

@@ -411,3 +411,23 @@ def test_heads_of_a_workgroup(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-Wall", "-I", CSRC, str(src), "-o", str(exe)], check=True)
     got = subprocess.run([str(exe)], capture_output=True, text=True)
     assert got.returncode == 0, got.stdout
+
+
+def test_shapes_that_take_wide_tiles(tmp_path):
+    """The shapes that the placement of 128-row tiles is tested with take them, with odd and even numbers of units."""
+    lines = []
+    for _, heads, group, _, seqs in kv_ref.WIDE_HEADS:
+        assert heads % 8 == 0
+        M, B = sum(n for _, n in seqs) + 2 * kv_ref.WIDE_LEAD, len(seqs)
+        lines.append(f"need({M}, {B}, {group}, {heads});")
+    src, exe = tmp_path / "wide.cpp", tmp_path / "wide"
+    src.write_text('#include <cstdlib>\n#include <initializer_list>\n#include "kv_layout.h"\nusing namespace nvfp4;\n'
+                   "static int odd = 0, even = 0;\n"
+                   "static void need(int64_t M, int64_t B, int64_t group, int64_t heads) {\n"
+                   "    for (int blocks : {0, (1 << 20) / kKvBlock})\n"
+                   "        if (!attention_wide(M, B, group, heads, blocks)) exit(1);\n"
+                   "    const int64_t units = tile_first(M, B, group, kWideRows, tiles_per_row(M, B, group, kWideRows));\n"
+                   "    ++(units % 2 ? odd : even);\n}\n"
+                   "int main() {\n" + "\n".join(lines) + "\nreturn odd && even ? 0 : 2;\n}\n")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0

@@ -1058,3 +1058,22 @@ def test_several_heads_to_a_workgroup(nv, case, rope):
             assert torch.equal(got[:, h].view(torch.int16), want[:, 0].view(torch.int16)), f"head {h}"
     bad = torch.isnan(back[1]).any(0).any(1)
     assert bool(bad[1]) and bool(bad[2]) and not bool(bad[10])
+
+
+@BOUNDS
+@pytest.mark.parametrize("dim,heads,group,c,seqs", kv_ref.WIDE_HEADS)
+def test_attention_with_heads_for_every_xcd(nv, dim, heads, group, c, seqs):
+    """Key/value heads in multiples of 8, which 128-row tiles are laid out by: every row of every head, with odd and
+    even numbers of tiles, and no row but those."""
+    news = [n for _, n in seqs]
+    lens = [p + n for p, n in seqs]
+    pool = Pool(nv, 120 + heads, heads, dim, lens)
+    lead, n = kv_ref.WIDE_LEAD, sum(news)
+    M, rs = n + 2 * lead, [lead + r for r in starts(news)]
+    q = normal(gen(121), M, heads * group, dim)
+    scale = np.float64(np.float32(dim ** -0.5))
+    want, tol = kv_ref.attention_fast(q.double().numpy(), pool.ref, rs, lens, pool.table, scale, c)
+    out = torch.full(q.shape, 77.0, dtype=torch.bfloat16, device="cuda")
+    nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=c, out=out)
+    assert bool((out[:lead] == 77).all()) and bool((out[lead + n:] == 77).all())
+    check(out[lead:lead + n], want[lead:lead + n], tol[lead:lead + n])
