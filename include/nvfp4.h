@@ -494,8 +494,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences
  * to its last bit, or to 2^-21 of the row's largest element where that is
  * more.  Probabilities are rounded to bf16 for the product with the values, and
  * the output once to bf16.  (The sums run against a reference that may lie a few
- * powers of two below the maximum; values above 2^96, or scaled scores above 2^30,
- * can overflow them.)  The order of the sums depends on the sizes and
+ * powers of two below the maximum and is itself a binary32 number: values above
+ * 2^96, or scaled scores above 2^26, can overflow them, and so can q.k past
+ * binary32 before it is scaled.)  The order of the sums depends on the sizes and
  * max_len only: the same call gives the same bytes.
  * max_len is the host's bound on the lengths, used to decide how many rows a
  * workgroup takes and how far the keys of few rows are shared out over

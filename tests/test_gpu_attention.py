@@ -1077,3 +1077,31 @@ def test_attention_with_heads_for_every_xcd(nv, dim, heads, group, c, seqs):
     nv.kv_attention(q.cuda(), pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=c, out=out)
     assert bool((out[:lead] == 77).all()) and bool((out[lead + n:] == 77).all())
     check(out[lead:lead + n], want[lead:lead + n], tol[lead:lead + n])
+
+
+@BOUNDS
+@pytest.mark.parametrize("dim,rows", [(64, 1), (128, 1), (64, 40), (128, 200)])
+def test_scores_and_values_at_their_documented_ends(nv, dim, rows):
+    """Scaled scores up to 2^26, where the reference is off by up to 4 in the exponent, and values up to 2^96: each row
+    sees the mean of one block's values, all others being too far below.
+
+    Those 64 probabilities are equal, so their rounding to bf16 (half a step, 2^-8) is one factor of the products that
+    their sum does not have; the output's is 2^-8 more, and the sums of 64 terms and the division some 2^-24 each."""
+    blocks, heads = 6, 2
+    pool = Pool(nv, 130 + dim, heads, dim, [blocks * BLOCK])
+    pool.ref.codes[0][:] = 0x38  # 1.0
+    pool.ref.powers[1][:] = 127 + 87  # up to 448 * 2^87 < 2^96
+    top = (4, 2)
+    for h in range(heads):
+        for at in range(blocks):
+            pool.ref.powers[0][pool.table[0, at], h] = 127 + (10 if at == top[h] else at)
+    pool.push()
+    # the largest score is dim * 2^20, and scaled 0.61 * 2^26
+    q = torch.full((rows, heads, dim), 2.0 ** 10, dtype=torch.bfloat16)
+    scale = np.float32(0.61 * 2.0 ** 26 / (dim * 2.0 ** 20))
+    got = nv.kv_attention(q.cuda(), pool.gpu, i32([0, rows]), pool.lens, pool.tab, scale=float(scale)).cpu().double().numpy()
+    for h in range(heads):
+        v = pool.ref.sequence(1, h, pool.table[0], blocks * BLOCK)[top[h] * BLOCK:(top[h] + 1) * BLOCK]
+        want, a = v.mean(0), np.abs(v).mean(0)
+        off = (2.0 ** -8 + 128 * 2.0 ** -24) * a
+        assert (np.abs(got[:, h] - want) <= off + 2.0 ** -8 * (np.abs(want) + off)).all()
