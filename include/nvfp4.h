@@ -500,7 +500,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences
  * max_len only: the same call gives the same bytes.
  * max_len is the host's bound on the lengths, used to decide how many rows a
  * workgroup takes and how far the keys of few rows are shared out over
- * workgroups (results for longer sequences are right all the same).  The workspace needs
+ * workgroups (results for longer sequences are right all the same).  Both are
+ * decided once for all sequences of a call: single tokens over long contexts are
+ * faster apart from prompts.  The workspace needs
  * nvfp4_kv_attention_workspace_bytes(...) bytes for the same sizes (16-byte
  * aligned; may be NULL when that is 0); calls that can overlap must not share
  * it.  scale > 0, and scale * log2(e) finite in binary32; causal_block, max_len

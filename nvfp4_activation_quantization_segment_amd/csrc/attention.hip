@@ -15,8 +15,11 @@
 // rate cost what one bf16 product would, and the keys need no conversion.
 //
 // Values become bf16 (exact: code times a power of two) and are multiplied with
-// probabilities rounded to bf16 (half a step is 2^-9 of each p, and their sum
-// is taken before that rounding).  Scores, maxima, sums and outputs are held in
+// probabilities rounded to bf16 (half a step is at most 2^-8 of each p; their
+// sum is taken before that rounding).  Two bf16 halves of each p would double
+// these products; as it is the outputs' error against 64 bits is 0.0021 to 0.0023
+// of their size, where binary32 probabilities and the output's own rounding give
+// 0.0016 to 0.0017.  Scores, maxima, sums and outputs are held in
 // binary32.
 #include "kv_device.h"
 
@@ -248,7 +251,10 @@ __device__ __forceinline__ void mask_scores(f32x16& s, int32_t left) {
 // are in flight while this one's softmax runs, values while its scores are
 // formed.  Bound by memory: 32 single tokens of 32 query and 8 key/value heads
 // over 1 to 16,384 keys each, 539 MB, take 114 us and 5 for the join, 4.6 TB/s
-// of cache read; four over 65,536 keys 102 us, 5.3 TB/s.
+// of cache read; four over 65,536 keys 102 us, 5.3 TB/s.  With D = 128 all 256
+// vector registers are in use and 2 spill (12 bytes of scratch a lane), with
+// 41 scalar ones that go to lanes of a vector register; D = 64 spills 46 scalar
+// ones only.
 // ---------------------------------------------------------------------------
 constexpr int kNarrowWaves = 4;
 

@@ -518,7 +518,10 @@ __global__ __launch_bounds__(2 * D) void kv_write_kernel(CacheArgs c, SeqArgs q,
 // waves share out a block's where there are several.  The same bytes as the
 // writer above, from less code and a third of its registers: a call this short
 // is a chain of waits, for memory and for instructions.  32 single tokens of 8
-// heads 4.2 us (8.8 with the writer above), 256 of 56 heads 17 (110).
+// heads, rotated, 4.2 us (8.8 with the writer above), 256 of 56 heads 18 (110).
+// Further rows of a sequence cost more than their bytes: single bytes of values
+// are stored, and all but a wave's last row are loaded and rotated twice (4 rows
+// of 256 sequences and 56 heads 55 to 65 us, 9 at a copy's bandwidth).
 template <int D, int MODE, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqArgs q, HeadsIn kx, HeadsIn vx, RopeArgs r) {
     constexpr int kBytes = kKvBlock * D;
@@ -532,7 +535,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv_append_kernel(CacheArgs c, SeqA
     if (!several && wave > 0) return;
     const int step = several ? WAVES : 1;  // the others of a single one's waves are done
     const bool mine = 2 * lane < D;
-    const int d = mine ? 2 * lane : 0;  // idle lanes load dims 0 and 1, count as zero and store nothing
+    const int d = mine ? 2 * lane : 0;  // idle lanes load dims 0 and 1 (their keys count as zero) and store nothing
     const int64_t row = u.row0 + (u.start - u.first);
     const Axes axes = axes_of(r);
     // this lane's pair is (d, d + 1), or its two are (d, d + 1) with the dims
@@ -756,12 +759,14 @@ __global__ __launch_bounds__(2 * D) void kv_read_kernel(CacheArgs c, SeqArgs q, 
 }
 
 // Rows a sequence (on average) up to which the short writer is taken, with one
-// wave up to one row and four above.  256 single tokens of 56 heads: 21 us with
-// one wave, 48 with four, 110 with the long writer.  8 heads, 32 sequences of 4
-// rows: 5.1 us with four waves, 8.9 with the long writer.  One of 60 rows and 63
-// of one: 10 and 15 us; one of 100 and 15 of one (7 on average): 19 and 9.  What
-// the rule costs where the rows are one sequence's: 60 rows beside 63 sequences
-// of none take 27 us, 10 with the long writer.
+// wave up to one row and four above.  256 single tokens of 56 heads, when units
+// were still counted by sequences: 21 us with one wave (15 now), 48 with four,
+// 110 with the long writer.  8 heads, 32 sequences of 4 rows: 5.1 us with four
+// waves, 8.9 with the long writer.  One of 60 rows and 63 of one: 10 and 15 us;
+// one of 100 and 15 of one (7 on average): 19 and 9.  What the rule costs where
+// the rows are one sequence's: 60 rows beside 63 sequences of none take 20 to 27
+// us, 10 with the long writer; 1000 rows among 255 empty slots 17 us for 8 heads
+// (6 alone, with the long writer), 50 for 56 (12).
 constexpr int64_t kAppendRows = 4;
 
 }  // namespace
