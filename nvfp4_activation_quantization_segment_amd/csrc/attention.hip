@@ -832,8 +832,10 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
     // 32; over 1024 keys 9.9 us in one piece, 10.4 in two.  40 tokens over 2048
     // keys: 16 us with pieces of 4, 20 of 8.
     int64_t tiles = (M * group + T - 1) / T;
-    // Slots without rows are not tiles: one token over 16,384 keys among 255 empty
-    // slots 13 us, 117 when they counted.
+    // At most M of the slots have rows, the others are not tiles: one token over
+    // 16,384 keys among 255 empty slots 13 us, 117 when they counted.  (Several rows
+    // of one slot still count as several: 40 over 65,536 keys take 72 us alone and
+    // 274 among 255 empty slots, where the keys are not cut.)
     const int64_t most_seqs = B < M ? B : M;
     tiles = tiles < most_seqs ? most_seqs : tiles;
     int64_t want = 512 / (tiles * kv_heads);
