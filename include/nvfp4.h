@@ -514,6 +514,75 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads
                                 const nvfp4_kv_sequences* seqs, float scale, int32_t causal_block, int64_t max_len,
                                 const nvfp4_heads* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Around the cache ------------------------------------------------------
+ * What a serving step does besides: norms of the heads, the tables that the
+ * cache's calls take, attention that sees a part of the past, and attention over
+ * a prefix that the sequences of a batch share.  As above: kernels only, no state
+ * between calls, and replays under graph capture are right. */
+
+/* Root-mean-square norms of query and key heads, with rotary positions:
+ *   n_i = x_i w_i / sqrt(mean_j x_j^2 + eps),  j over the head's dim elements,
+ *   y1 = n1 cos - n2 sin,  y2 = n2 cos + n1 sin  for the rotated pairs, y = n else,
+ * in binary32, rounded once to bf16.  Squares that leave binary32 do no harm; an
+ * element that is not finite does what the formula says.  q [M, q_heads, dim] and
+ * k [M, k_heads, dim] with weights [dim] (bf16, 16-byte aligned; NULL: ones), both
+ * in one launch; k_heads = 0: no keys (k, k_out NULL).  rope as in nvfp4_rope, or
+ * NULL for no rotation.  Each output may be its own input (same data and strides);
+ * otherwise no two of them overlap.  2^-126 <= eps <= 1; dim a multiple of 16, at
+ * most 512; 1 <= M <= 2^23. */
+nvfp4_status nvfp4_norm_rope(const nvfp4_heads* q, int32_t q_heads, const uint16_t* q_weight, const nvfp4_heads* k,
+                             int32_t k_heads, const uint16_t* k_weight, int64_t M, int32_t dim, float eps,
+                             const nvfp4_rope_params* rope, const nvfp4_heads* q_out, const nvfp4_heads* k_out,
+                             void* stream);
+
+/* The block tables of `count` requests and a stack of the pool's free blocks,
+ * DEVICE int32.  table[b][j] is request b's cache block of positions 64 j .. 64 j +
+ * 63 (row stride ld_table >= table_blocks); the stack's top is free_blocks[n - 1]
+ * where n, at most `capacity`, is held apart.  1 <= count <= 2^20. */
+typedef struct {
+    int64_t count;
+    int32_t* table;
+    int64_t ld_table;
+    int64_t table_blocks;
+    int32_t* free_blocks;
+    int64_t capacity;
+} nvfp4_kv_tables;
+
+/* Gives every request its next rows, positions and blocks.  Request b holds past[b]
+ * positions and asks for more[b] (below 0: none).  In order of b:
+ *   n = more[b], cut to the rows left of M and to a length below 2^31;
+ *   row_start[b] = the rows of the requests before, row_start[count] all of them;
+ *   lens[b] = past[b] + n;
+ *   blocks ceil(past / 64) .. ceil(lens / 64) - 1 of its table (as far as the table
+ *   goes) are taken from the top of the stack; where that is empty, the entry
+ *   becomes -1 and *missing, the number of these, grows.
+ * *free_left is the stack's size after it; the stack's own entries stay as they are.
+ * The m-th row's position goes to positions[m] (int32) and its slot, block * 64 +
+ * position % 64, to slots[m] (int64; -1 where there is no block); rows of no request
+ * get -1 in both.  Either may be NULL.  row_start, lens, table and positions are what
+ * nvfp4_kv_write, nvfp4_rope and nvfp4_kv_attention take: nothing of a step's tables
+ * passes the host.  lens may be past and free_left may be free_count (a step in
+ * place); otherwise outputs must not overlap one another or the inputs.  *free_count
+ * is taken as at least 0 and at most capacity.  1 <= M <= 2^23.  The workspace needs
+ * nvfp4_kv_extend_workspace_bytes(count) bytes (16-byte aligned). */
+size_t nvfp4_kv_extend_workspace_bytes(int64_t count);
+nvfp4_status nvfp4_kv_extend(const nvfp4_kv_tables* tables, const int32_t* past, const int32_t* more,
+                             const int32_t* free_count, int64_t M, int32_t* row_start, int32_t* lens, int32_t* free_left,
+                             int32_t* missing, int32_t* positions, int64_t* slots, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Takes the blocks of finished requests back: of each b with done[b] != 0, in order,
+ * the entries keep .. ceil(lens[b] / 64) - 1 of its table that are not negative go on
+ * top of the stack (what would pass its capacity is dropped), and lens_out[b] = 0;
+ * the other lengths are copied.  *free_left is the stack's size after it.  The table
+ * stays as it is.  keep: the first entries of every table that are not the request's
+ * own (a shared prefix).  lens_out may be lens and free_left may be free_count.  The
+ * workspace needs nvfp4_kv_release_workspace_bytes(count) bytes (16-byte aligned). */
+size_t nvfp4_kv_release_workspace_bytes(int64_t count);
+nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens, const int32_t* done, int64_t keep,
+                              const int32_t* free_count, int32_t* lens_out, int32_t* free_left, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* ---- Single-step entry points ------------------------------------------
  * Elementwise versions of single producer steps, running the very device
  * functions the producer kernels use, so that each step can be checked over

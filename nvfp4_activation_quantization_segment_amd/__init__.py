@@ -10,7 +10,9 @@ torch tensors and the same arguments as the C ABI (``include/nvfp4.h``);
 ``modulate_quantize``, ``swiglu_quantize`` and ``gemm`` are conveniences that
 allocate their outputs with torch, and so are ``rope_table``, ``rope``,
 ``KvCache``, ``kv_write``, ``kv_read`` and ``kv_attention`` for what lies between
-the QKV projection and the attention output's quantizer.
+the QKV projection and the attention output's quantizer, with ``norm_rope`` for
+the norms of its heads and ``KvStep``, ``kv_extend`` and ``kv_release`` for the
+tables that the cache's calls take.
 """
 from __future__ import annotations
 
@@ -72,6 +74,11 @@ class KvSequences(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("table_blocks", ctypes.c_int64)]
 
 
+class KvTables(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+                ("table_blocks", ctypes.c_int64), ("free_blocks", ctypes.c_void_p), ("capacity", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run nvfp4_activation_quantization_segment_amd/build.py")
@@ -80,7 +87,7 @@ def _load():
     SEG = ctypes.POINTER(Segments)
     GATES = ctypes.POINTER(RowGates)
     HEADS, ROPE = ctypes.POINTER(Heads), ctypes.POINTER(RopeParams)
-    CACHE, SEQS = ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvSequences)
+    CACHE, SEQS, TABLES = ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvSequences), ctypes.POINTER(KvTables)
     sigs = {
         "nvfp4_padded_rows": (I64, [I64]),
         "nvfp4_absmax_workspace_bytes": (ctypes.c_size_t, []),
@@ -110,6 +117,11 @@ def _load():
         "nvfp4_kv_attention_workspace_bytes": (ctypes.c_size_t, [I64, I64, I32, I32, I32, I64]),
         "nvfp4_kv_attention": (I32, [HEADS, I64, I32, CACHE, SEQS, ctypes.c_float, I32, I64, HEADS, P,
                                      ctypes.c_size_t, V]),
+        "nvfp4_norm_rope": (I32, [HEADS, I32, P, HEADS, I32, P, I64, I32, ctypes.c_float, ROPE, HEADS, HEADS, V]),
+        "nvfp4_kv_extend_workspace_bytes": (ctypes.c_size_t, [I64]),
+        "nvfp4_kv_extend": (I32, [TABLES, P, P, P, I64, P, P, P, P, P, P, P, ctypes.c_size_t, V]),
+        "nvfp4_kv_release_workspace_bytes": (ctypes.c_size_t, [I64]),
+        "nvfp4_kv_release": (I32, [TABLES, P, P, I64, P, P, P, P, ctypes.c_size_t, V]),
         "nvfp4_step_modulate": (I32, [P, P, P, P, I64, V]),
         "nvfp4_step_swiglu": (I32, [P, P, P, I64, V]),
         "nvfp4_step_block_scale": (I32, [P, P, P, I64, V]),
@@ -337,8 +349,9 @@ def nvfp4_modulate_gemm_ring(x, M, K, ldx, seg, ws, tensor_scale, amax_out, ring
 
 
 # The rotary, cache and attention entry points take the structures Heads,
-# RopeParams, KvCacheStruct and KvSequences (make_heads, make_rope_params,
-# KvCache.struct, make_kv_sequences); their tensors must outlive the call.
+# RopeParams, KvCacheStruct, KvSequences and KvTables (make_heads,
+# make_rope_params, KvCache.struct, make_kv_sequences, make_kv_tables); their
+# tensors must outlive the call.
 def nvfp4_rope_table(table, rows, pairs, theta, stream=None):
     _check("nvfp4_rope_table", lib.nvfp4_rope_table(_ptr(table), rows, pairs, theta, _stream(stream)))
 
@@ -364,6 +377,34 @@ def nvfp4_kv_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len,
     _check("nvfp4_kv_attention",
            lib.nvfp4_kv_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len, out, _ptr(workspace),
                                   workspace_bytes, _stream(stream)))
+
+
+def nvfp4_norm_rope(q, q_heads, q_weight, k, k_heads, k_weight, M, dim, eps, rope, q_out, k_out, stream=None):
+    _check("nvfp4_norm_rope",
+           lib.nvfp4_norm_rope(q, q_heads, _ptr(q_weight), k, k_heads, _ptr(k_weight), M, dim, eps, rope, q_out, k_out,
+                               _stream(stream)))
+
+
+def nvfp4_kv_extend_workspace_bytes(count):
+    return int(lib.nvfp4_kv_extend_workspace_bytes(count))
+
+
+def nvfp4_kv_extend(tables, past, more, free_count, M, row_start, lens, free_left, missing, positions, slots, workspace,
+                    workspace_bytes, stream=None):
+    _check("nvfp4_kv_extend",
+           lib.nvfp4_kv_extend(tables, _ptr(past), _ptr(more), _ptr(free_count), M, _ptr(row_start), _ptr(lens),
+                               _ptr(free_left), _ptr(missing), _ptr(positions), _ptr(slots), _ptr(workspace),
+                               workspace_bytes, _stream(stream)))
+
+
+def nvfp4_kv_release_workspace_bytes(count):
+    return int(lib.nvfp4_kv_release_workspace_bytes(count))
+
+
+def nvfp4_kv_release(tables, lens, done, keep, free_count, lens_out, free_left, workspace, workspace_bytes, stream=None):
+    _check("nvfp4_kv_release",
+           lib.nvfp4_kv_release(tables, _ptr(lens), _ptr(done), keep, _ptr(free_count), _ptr(lens_out), _ptr(free_left),
+                                _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def nvfp4_step_modulate(x, scale, shift, y, n, stream=None):
@@ -679,6 +720,53 @@ def rope(x: torch.Tensor, tables, positions: torch.Tensor, split: bool = False, 
     return out
 
 
+def _norm_weight(name: str, w, dim: int, dev: torch.device):
+    if w is None:
+        return None
+    if w.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected bf16, got {w.dtype}")
+    if w.shape != (dim,) or w.stride(0) != 1:
+        raise ValueError(f"{name}: expected [{dim}] with unit stride, got {list(w.shape)}")
+    if w.device != dev:
+        raise ValueError(f"{name} is on {w.device}, expected {dev}")
+    return w.data_ptr()
+
+
+def norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+              k_weight: torch.Tensor | None = None, eps: float = 1e-6, tables=(), positions: torch.Tensor | None = None,
+              split: bool = False, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norms of the heads q [rows, q_heads, dim] and k [rows, k_heads, dim] (bf16, any row and head
+    strides), times their weights [dim] (bf16; none: ones), rotated as `rope` does where tables and positions are given.
+
+    One launch for both; formed in binary32 and rounded once.  Returns the normed queries, with k the pair of queries
+    and keys.  q_out may be q and k_out k; otherwise they overlap nothing."""
+    if (positions is None) != (len(tables) == 0):
+        raise ValueError("rotating the heads needs tables and positions, got " +
+                         ("tables" if positions is None else "positions") + " alone")
+    if k is None and (k_weight is not None or k_out is not None):
+        raise ValueError("a weight or an output of the keys without keys")
+    dev = q.device
+    _same_device(dev, k, q_out, k_out)
+    hq = make_heads("q", q)
+    rows, heads, dim = shape = q.shape
+    hk = ko = None
+    k_heads = 0
+    if k is not None:
+        hk = make_heads("k", k)
+        k_heads = k.shape[1]
+        if k.shape[0] != rows or k.shape[2] != dim:
+            raise ValueError(f"k: expected [{rows}, heads, {dim}], got {list(k.shape)}")
+    wq, wk = _norm_weight("q_weight", q_weight, dim, dev), _norm_weight("k_weight", k_weight, dim, dev)
+    r = None if positions is None else make_rope_params(tables, positions, rows, split, dev)
+    q_out, ho = _output("q_out", q_out, dev, stream, shape)
+    if k is not None:
+        k_out, ko = _output("k_out", k_out, dev, stream, k.shape)
+    if rows:
+        _call("nvfp4_norm_rope", lib.nvfp4_norm_rope, dev, stream, hq, heads, wq, hk, k_heads, wk, rows, dim, float(eps), r,
+              ho, ko)
+    return q_out if k is None else (q_out, k_out)
+
+
 class KvCache:
     """A pool of 8-bit key/value cache blocks of 64 positions, as four uint8 tensors:
 
@@ -823,3 +911,113 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
               dim ** -0.5 if scale is None else float(scale), causal_block, max_len, ho,
               None if workspace is None else workspace.data_ptr(), size)
     return out
+
+
+# ---------------------------------------------------------------------------
+# the tables of a step, built on the GPU
+# ---------------------------------------------------------------------------
+def _int32s(dev: torch.device, **tensors):
+    """Checks int32 vectors on `dev`: name=(tensor, elements or None for any number)."""
+    for name, (t, n) in tensors.items():
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name}: expected int32, got {t.dtype}")
+        if t.dim() != 1 or (n is not None and t.shape[0] != n):
+            raise ValueError(f"{name}: expected {'a vector' if n is None else [n]}, got {list(t.shape)}")
+        if t.stride(0) != 1 and t.shape[0] > 1:
+            raise ValueError(f"{name} must have unit stride")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def make_kv_tables(table: torch.Tensor, free: torch.Tensor) -> KvTables:
+    """The C description of block tables [requests, blocks] and a stack of free blocks [capacity], int32."""
+    dev = table.device
+    if table.dtype != torch.int32:
+        raise TypeError(f"table: expected int32, got {table.dtype}")
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [requests, blocks], got {list(table.shape)}")
+    _int32s(dev, free=(free, None))
+    n, blocks = table.shape
+    ld, unit = table.stride()
+    if unit != 1 and blocks > 1:
+        raise ValueError("table must have unit stride along its last dimension")
+    return KvTables(n, table.data_ptr(), ld if n > 1 else blocks, blocks, free.data_ptr(), free.shape[0])
+
+
+class KvStep:
+    """What kv_extend writes, for up to `rows` rows: row_start [requests + 1], lens [requests], free_count [1] and
+    missing [1], positions [rows, 1] (all int32) and slots [rows] (int64), as tensors that can serve step after step."""
+
+    __slots__ = ("row_start", "lens", "free_count", "missing", "positions", "slots", "workspace")
+
+    def __init__(self, row_start, lens, free_count, missing, positions, slots, workspace):
+        self.row_start, self.lens, self.free_count, self.missing = row_start, lens, free_count, missing
+        self.positions, self.slots, self.workspace = positions, slots, workspace
+
+    @classmethod
+    def empty(cls, requests: int, rows: int, device=None, stream=None) -> "KvStep":
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        make = lambda *shape: _empty(dev, stream, shape, torch.int32)  # noqa: E731
+        return cls(make(requests + 1), make(requests), make(1), make(1), make(rows, 1),
+                   _empty(dev, stream, (rows,), torch.int64),
+                   _empty(dev, stream, (nvfp4_kv_extend_workspace_bytes(requests),), torch.uint8))
+
+
+def kv_extend(past: torch.Tensor, more: torch.Tensor, table: torch.Tensor, free: torch.Tensor, free_count: torch.Tensor,
+              step: KvStep, stream=None) -> KvStep:
+    """Gives every request its next rows, positions and cache blocks, on the GPU: returns `step`, written.
+
+    Request b holds past[b] positions and asks for more[b].  Their rows follow one another in order, cut to the rows of
+    the step; the blocks they need come from the top of the stack free[:free_count], into the table [requests, blocks]
+    (in place; an entry is -1 where the stack is empty, and `missing` counts those).  step.row_start, step.lens, the
+    table and step.positions are what kv_write, rope and kv_attention take; step.slots is each row's block * 64 +
+    position % 64.  Rows of no request get -1 in both.  step.lens may be `past` and step.free_count `free_count`."""
+    dev = table.device
+    if dev.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {dev}")
+    t = make_kv_tables(table, free)
+    n, rows = t.count, step.positions.shape[0]
+    _int32s(dev, past=(past, n), more=(more, n), free_count=(free_count, 1), row_start=(step.row_start, n + 1),
+            lens=(step.lens, n), left=(step.free_count, 1), missing=(step.missing, 1), positions=(step.positions.view(-1), rows))
+    slots, ws = step.slots, step.workspace
+    if slots.dtype != torch.int64 or slots.shape != (rows,) or not slots.is_contiguous():
+        raise ValueError(f"slots: expected a contiguous int64 [{rows}], got {slots.dtype} {list(slots.shape)}")
+    _same_device(dev, slots, ws)
+    if not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    _call("nvfp4_kv_extend", lib.nvfp4_kv_extend, dev, stream, t, past.data_ptr(), more.data_ptr(), free_count.data_ptr(),
+          rows, step.row_start.data_ptr(), step.lens.data_ptr(), step.free_count.data_ptr(), step.missing.data_ptr(),
+          step.positions.data_ptr(), slots.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    return step
+
+
+def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free: torch.Tensor, free_count: torch.Tensor,
+               keep: int = 0, lens_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None):
+    """Takes the blocks of finished requests (done[b] != 0) back onto the stack free[:free_count], on the GPU: returns the
+    lengths, 0 for those, and the stack's size after it.
+
+    keep: the first entries of every table that are not the request's own (a shared prefix).  The stack grows in place;
+    lens_out may be `lens` and free_count_out `free_count`."""
+    dev = table.device
+    if dev.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {dev}")
+    t = make_kv_tables(table, free)
+    n = t.count
+    if lens_out is None:
+        lens_out = _empty(dev, stream, (n,), torch.int32)
+    if free_count_out is None:
+        free_count_out = _empty(dev, stream, (1,), torch.int32)
+    _int32s(dev, lens=(lens, n), done=(done, n), free_count=(free_count, 1), lens_out=(lens_out, n),
+            free_count_out=(free_count_out, 1))
+    if workspace is None:
+        workspace = _empty(dev, stream, (nvfp4_kv_release_workspace_bytes(n),), torch.uint8)
+    _same_device(dev, workspace)
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    _call("nvfp4_kv_release", lib.nvfp4_kv_release, dev, stream, t, lens.data_ptr(), done.data_ptr(), keep,
+          free_count.data_ptr(), lens_out.data_ptr(), free_count_out.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return lens_out, free_count_out

@@ -1,4 +1,5 @@
-// C ABI of the rotary, cache and attention entry points: argument validation.
+// C ABI of the rotary, norm, cache, table and attention entry points: argument
+// validation.
 // Every check happens before anything is enqueued.
 #include <math.h>
 #include <string.h>
@@ -80,6 +81,19 @@ nvfp4_status check_sequences(const nvfp4_kv_sequences* s, int64_t M, SeqArgs* a)
     return NVFP4_OK;
 }
 
+constexpr size_t kStateBytes = 16;  // what a table call's launches hand on
+
+nvfp4_status check_tables(const nvfp4_kv_tables* t) {
+    if (!t || !t->table || !t->free_blocks || t->count < 1 || t->table_blocks < 1 || t->capacity < 1 ||
+        t->ld_table < t->table_blocks)
+        return NVFP4_ERR_INVALID_ARGUMENT;
+    if (t->count > kMaxSeqs || t->table_blocks > INT32_MAX / kKvBlock || t->capacity > INT32_MAX ||
+        t->ld_table > ((int64_t)1 << 60) / t->count)
+        return NVFP4_ERR_SHAPE;
+    if (!aligned(t->table, 4) || !aligned(t->free_blocks, 4)) return NVFP4_ERR_ALIGNMENT;
+    return NVFP4_OK;
+}
+
 bool attention_sizes_ok(int64_t M, int64_t count, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_len) {
     return M >= 1 && M <= kMaxRows && count >= 1 && count <= kMaxSeqs && heads >= 1 && heads <= kMaxHeads &&
            q_heads >= 1 && q_heads % heads == 0 && M * q_heads <= ((int64_t)1 << 28) && (dim == 64 || dim == 128) && max_len >= 0;
@@ -111,6 +125,38 @@ nvfp4_status nvfp4_rope(const nvfp4_heads* x, int64_t M, int32_t heads, int32_t 
     return report_hip(launch_rope(in(x), out_of(out), M, heads, dim, r, (hipStream_t)stream));
 }
 
+nvfp4_status nvfp4_norm_rope(const nvfp4_heads* q, int32_t q_heads, const uint16_t* q_weight, const nvfp4_heads* k,
+                             int32_t k_heads, const uint16_t* k_weight, int64_t M, int32_t dim, float eps,
+                             const nvfp4_rope_params* rope, const nvfp4_heads* q_out, const nvfp4_heads* k_out,
+                             void* stream) {
+    if (M < 1 || q_heads < 1 || k_heads < 0 || dim < 1) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (!(eps >= 0x1p-126f && eps <= 1.0f)) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (dim % 16 != 0 || dim > 512 || M > kMaxRows || q_heads > kMaxHeads || k_heads > kMaxHeads) return NVFP4_ERR_SHAPE;
+    if (k_heads == 0 && (k || k_out || k_weight)) return NVFP4_ERR_INVALID_ARGUMENT;
+    NormArgs a;
+    memset(&a, 0, sizeof(a));
+    const nvfp4_heads* xs[2] = {q, k};
+    const nvfp4_heads* outs[2] = {q_out, k_out};
+    const uint16_t* weights[2] = {q_weight, k_weight};
+    const int32_t heads[2] = {q_heads, k_heads};
+    nvfp4_status st;
+    for (int i = 0; i < 2 && heads[i] > 0; ++i) {
+        if ((st = check_heads(xs[i], M, heads[i], dim, false)) != NVFP4_OK) return st;
+        if ((st = check_heads(outs[i], M, heads[i], dim, true)) != NVFP4_OK) return st;
+        if (!aligned(weights[i], 16)) return NVFP4_ERR_ALIGNMENT;
+        a.part[i].x = in(xs[i]);
+        a.part[i].out = out_of(outs[i]);
+        a.part[i].weight = weights[i];
+        a.part[i].heads = heads[i];
+    }
+    if (rope && (st = check_rope(rope, dim, &a.rope)) != NVFP4_OK) return st;
+    a.M = M;
+    a.units = dim / 16;
+    a.inverse_dim = 1.0f / (float)dim;
+    a.eps = eps;
+    return report_hip(launch_norm_rope(a, (hipStream_t)stream));
+}
+
 nvfp4_status nvfp4_kv_write(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences* seqs, int64_t M,
                             const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_rope_params* rope, void* stream) {
     CacheArgs c;
@@ -136,6 +182,80 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const nvfp4_kv_sequences
     if ((st = check_heads(k, M, c.heads, c.dim, true)) != NVFP4_OK) return st;
     if ((st = check_heads(v, M, c.heads, c.dim, true)) != NVFP4_OK) return st;
     return report_hip(launch_kv_read(c, q, out_of(k), out_of(v), (hipStream_t)stream));
+}
+
+size_t nvfp4_kv_extend_workspace_bytes(int64_t count) {
+    return count < 1 || count > kMaxSeqs ? 0 : kStateBytes + (size_t)count * sizeof(int32_t);
+}
+
+nvfp4_status nvfp4_kv_extend(const nvfp4_kv_tables* tables, const int32_t* past, const int32_t* more,
+                             const int32_t* free_count, int64_t M, int32_t* row_start, int32_t* lens, int32_t* free_left,
+                             int32_t* missing, int32_t* positions, int64_t* slots, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    nvfp4_status st;
+    if ((st = check_tables(tables)) != NVFP4_OK) return st;
+    if (!past || !more || !free_count || !row_start || !lens || !free_left || !missing || M < 1)
+        return NVFP4_ERR_INVALID_ARGUMENT;
+    if (M > kMaxRows) return NVFP4_ERR_SHAPE;
+    if (!aligned(past, 4) || !aligned(more, 4) || !aligned(free_count, 4) || !aligned(row_start, 4) || !aligned(lens, 4) ||
+        !aligned(free_left, 4) || !aligned(missing, 4) || !aligned(positions, 4) || !aligned(slots, 8))
+        return NVFP4_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < nvfp4_kv_extend_workspace_bytes(tables->count)) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
+    ExtendArgs a;
+    a.B = tables->count;
+    a.M = M;
+    a.past = past;
+    a.more = more;
+    a.table = tables->table;
+    a.ld_table = tables->ld_table;
+    a.table_blocks = tables->table_blocks;
+    a.free_blocks = tables->free_blocks;
+    a.capacity = tables->capacity;
+    a.free_count = free_count;
+    a.row_start = row_start;
+    a.lens = lens;
+    a.free_left = free_left;
+    a.missing = missing;
+    a.positions = positions;
+    a.slots = slots;
+    a.state = (int32_t*)workspace;
+    a.taken = (int32_t*)((char*)workspace + kStateBytes);
+    return report_hip(launch_kv_extend(a, (hipStream_t)stream));
+}
+
+size_t nvfp4_kv_release_workspace_bytes(int64_t count) {
+    if (count < 1 || count > kMaxSeqs) return 0;
+    return kStateBytes + (size_t)kv_release_groups(count) * sizeof(int64_t) + (size_t)count * sizeof(int32_t);
+}
+
+nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens, const int32_t* done, int64_t keep,
+                              const int32_t* free_count, int32_t* lens_out, int32_t* free_left, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    nvfp4_status st;
+    if ((st = check_tables(tables)) != NVFP4_OK) return st;
+    if (!lens || !done || !free_count || !lens_out || !free_left || keep < 0) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (!aligned(lens, 4) || !aligned(done, 4) || !aligned(free_count, 4) || !aligned(lens_out, 4) || !aligned(free_left, 4))
+        return NVFP4_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < nvfp4_kv_release_workspace_bytes(tables->count)) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
+    ReleaseArgs a;
+    a.B = tables->count;
+    a.lens = lens;
+    a.done = done;
+    a.table = tables->table;
+    a.ld_table = tables->ld_table;
+    a.table_blocks = tables->table_blocks;
+    a.keep = keep;
+    a.free_blocks = tables->free_blocks;
+    a.capacity = tables->capacity;
+    a.free_count = free_count;
+    a.lens_out = lens_out;
+    a.free_left = free_left;
+    a.state = (int32_t*)workspace;
+    a.totals = (int64_t*)((char*)workspace + kStateBytes);
+    a.counts = (int32_t*)(a.totals + kv_release_groups(a.B));
+    return report_hip(launch_kv_release(a, (hipStream_t)stream));
 }
 
 size_t nvfp4_kv_attention_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,

@@ -32,6 +32,26 @@ struct RopeArgs {
     int32_t split;
 };
 
+// One of the two inputs of the norms (queries, keys), and how its rows are
+// shared out (set by the launcher).
+struct NormPart {
+    HeadsIn x;
+    HeadsOut out;
+    const uint16_t* weight;          // null: ones
+    int32_t heads;                   // 0: none
+    int32_t rows;                    // rows of a workgroup
+    int32_t step_heads, step_rows;   // from one head of a lane to its next
+    uint32_t groups;
+};
+struct NormArgs {
+    NormPart part[2];
+    RopeArgs rope;       // total = 0: not rotated
+    int64_t M;
+    int32_t units;       // of 16 dims in a head
+    int32_t log_lanes;   // lanes of a head: the next power of two (set by the launcher)
+    float inverse_dim, eps;
+};
+
 struct CacheArgs {
     uint8_t* k;
     uint8_t* v;
@@ -53,6 +73,41 @@ struct SeqArgs {
     int32_t per_row;   // work units of a row, 0: counted by sequences (kv_layout.h)
 };
 
+struct ExtendArgs {
+    int64_t B, M;
+    const int32_t* past;
+    const int32_t* more;
+    int32_t* table;
+    int64_t ld_table, table_blocks;
+    const int32_t* free_blocks;
+    int64_t capacity;
+    const int32_t* free_count;
+    int32_t* row_start;
+    int32_t* lens;
+    int32_t* free_left;
+    int32_t* missing;
+    int32_t* positions;   // or null
+    int64_t* slots;       // or null
+    int32_t* state;       // workspace: free blocks before
+    int32_t* taken;       // workspace: [B] blocks that the requests before take
+};
+
+struct ReleaseArgs {
+    int64_t B;
+    const int32_t* lens;
+    const int32_t* done;
+    const int32_t* table;
+    int64_t ld_table, table_blocks, keep;
+    int32_t* free_blocks;
+    int64_t capacity;
+    const int32_t* free_count;
+    int32_t* lens_out;
+    int32_t* free_left;
+    int32_t* state;       // workspace: free blocks before
+    int64_t* totals;      // workspace: blocks of each workgroup's requests
+    int32_t* counts;      // workspace: [B] blocks of each request
+};
+
 struct AttentionArgs {
     HeadsIn q;
     HeadsOut out;
@@ -70,10 +125,15 @@ struct AttentionArgs {
 hipError_t launch_rope_table(float2* table, int64_t rows, int32_t pairs, double theta, hipStream_t s);
 hipError_t launch_rope(const HeadsIn& x, const HeadsOut& out, int64_t M, int32_t heads, int32_t dim, const RopeArgs& r,
                        hipStream_t s);
+hipError_t launch_norm_rope(const NormArgs& a, hipStream_t s);
 // r.axes = 0: the keys are not rotated.
 hipError_t launch_kv_write(const CacheArgs& c, const SeqArgs& q, const HeadsIn& k, const HeadsIn& v, const RopeArgs& r,
                            hipStream_t s);
 hipError_t launch_kv_read(const CacheArgs& c, const SeqArgs& q, const HeadsOut& k, const HeadsOut& v, hipStream_t s);
+
+hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t s);
+int64_t kv_release_groups(int64_t B);  // workgroups of a release
+hipError_t launch_kv_release(const ReleaseArgs& a, hipStream_t s);
 
 // How an attention call is cut: from sizes the host knows.
 struct AttentionPlan {
