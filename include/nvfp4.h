@@ -583,6 +583,39 @@ nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens
                               const int32_t* free_count, int32_t* lens_out, int32_t* free_left, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* nvfp4_kv_attention through a window: of the positions below its limit, the row at
+ * position p sees those above p - window and the first `sinks`; the others' blocks
+ * are not read.  causal_block bounds what a row sees ahead of it, as there (with 0 all
+ * of its sequence).  window >= 1, sinks >= 0.  What hidden positions hold has no
+ * effect; everything else as nvfp4_kv_attention has it.  The workspace needs
+ * nvfp4_kv_attention_window_workspace_bytes(...) bytes for the same sizes (16-byte
+ * aligned; may be NULL when that is 0). */
+size_t nvfp4_kv_attention_window_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
+                                                 int32_t causal_block, int32_t window, int32_t sinks, int64_t max_len);
+nvfp4_status nvfp4_kv_attention_window(const nvfp4_heads* q, int64_t M, int32_t q_heads, const nvfp4_kv_cache* cache,
+                                       const nvfp4_kv_sequences* seqs, float scale, int32_t causal_block, int32_t window,
+                                       int32_t sinks, int64_t max_len, const nvfp4_heads* out, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* nvfp4_kv_attention of sequences whose first 64 * shared_blocks positions are the
+ * same: the blocks shared[0 .. shared_blocks) (DEVICE int32) stand for the first
+ * entries of every sequence's table, which are not read.  All rows of the batch are
+ * taken against them together, so that a long prefix is read and multiplied in tiles
+ * of many sequences' rows, and against their own sequence's further positions apart;
+ * the two are joined by their maxima and sums, so that a row's result is that of one
+ * softmax.  The new rows of every sequence lie behind the prefix: rows of one with
+ * lens[b] - n < 64 * shared_blocks give NaN.  max_len bounds the lengths, prefix
+ * included.  1 <= shared_blocks <= (2^31 - 1) / 64; the tables hold the prefix too
+ * (lens[b] <= 64 * table_blocks).  Everything else as nvfp4_kv_attention has it.  The
+ * workspace needs nvfp4_kv_attention_shared_workspace_bytes(...) bytes for the same
+ * sizes (16-byte aligned). */
+size_t nvfp4_kv_attention_shared_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
+                                                 int64_t shared_blocks, int64_t max_len);
+nvfp4_status nvfp4_kv_attention_shared(const nvfp4_heads* q, int64_t M, int32_t q_heads, const nvfp4_kv_cache* cache,
+                                       const nvfp4_kv_sequences* seqs, const int32_t* shared, int64_t shared_blocks,
+                                       float scale, int32_t causal_block, int64_t max_len, const nvfp4_heads* out,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- Single-step entry points ------------------------------------------
  * Elementwise versions of single producer steps, running the very device
  * functions the producer kernels use, so that each step can be checked over

@@ -117,6 +117,12 @@ def _load():
         "nvfp4_kv_attention_workspace_bytes": (ctypes.c_size_t, [I64, I64, I32, I32, I32, I64]),
         "nvfp4_kv_attention": (I32, [HEADS, I64, I32, CACHE, SEQS, ctypes.c_float, I32, I64, HEADS, P,
                                      ctypes.c_size_t, V]),
+        "nvfp4_kv_attention_window_workspace_bytes": (ctypes.c_size_t, [I64, I64, I32, I32, I32, I32, I32, I32, I64]),
+        "nvfp4_kv_attention_window": (I32, [HEADS, I64, I32, CACHE, SEQS, ctypes.c_float, I32, I32, I32, I64, HEADS, P,
+                                            ctypes.c_size_t, V]),
+        "nvfp4_kv_attention_shared_workspace_bytes": (ctypes.c_size_t, [I64, I64, I32, I32, I32, I64, I64]),
+        "nvfp4_kv_attention_shared": (I32, [HEADS, I64, I32, CACHE, SEQS, P, I64, ctypes.c_float, I32, I64, HEADS, P,
+                                            ctypes.c_size_t, V]),
         "nvfp4_norm_rope": (I32, [HEADS, I32, P, HEADS, I32, P, I64, I32, ctypes.c_float, ROPE, HEADS, HEADS, V]),
         "nvfp4_kv_extend_workspace_bytes": (ctypes.c_size_t, [I64]),
         "nvfp4_kv_extend": (I32, [TABLES, P, P, P, I64, P, P, P, P, P, P, P, ctypes.c_size_t, V]),
@@ -377,6 +383,29 @@ def nvfp4_kv_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len,
     _check("nvfp4_kv_attention",
            lib.nvfp4_kv_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len, out, _ptr(workspace),
                                   workspace_bytes, _stream(stream)))
+
+
+def nvfp4_kv_attention_window_workspace_bytes(M, count, q_heads, heads, dim, causal_block, window, sinks, max_len):
+    return int(lib.nvfp4_kv_attention_window_workspace_bytes(M, count, q_heads, heads, dim, causal_block, window, sinks,
+                                                             max_len))
+
+
+def nvfp4_kv_attention_window(q, M, q_heads, cache, seqs, scale, causal_block, window, sinks, max_len, out, workspace,
+                              workspace_bytes, stream=None):
+    _check("nvfp4_kv_attention_window",
+           lib.nvfp4_kv_attention_window(q, M, q_heads, cache, seqs, scale, causal_block, window, sinks, max_len, out,
+                                         _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def nvfp4_kv_attention_shared_workspace_bytes(M, count, q_heads, heads, dim, shared_blocks, max_len):
+    return int(lib.nvfp4_kv_attention_shared_workspace_bytes(M, count, q_heads, heads, dim, shared_blocks, max_len))
+
+
+def nvfp4_kv_attention_shared(q, M, q_heads, cache, seqs, shared, shared_blocks, scale, causal_block, max_len, out,
+                              workspace, workspace_bytes, stream=None):
+    _check("nvfp4_kv_attention_shared",
+           lib.nvfp4_kv_attention_shared(q, M, q_heads, cache, seqs, _ptr(shared), shared_blocks, scale, causal_block,
+                                         max_len, out, _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def nvfp4_norm_rope(q, q_heads, q_weight, k, k_heads, k_weight, M, dim, eps, rope, q_out, k_out, stream=None):
@@ -879,14 +908,21 @@ def kv_read(cache: KvCache, rows: int, row_start: torch.Tensor, lens: torch.Tens
 
 def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
                  scale: float | None = None, causal_block: int = 0, max_len: int | None = None,
-                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None, window: int = 0,
+                 sinks: int = 0, shared: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of the queries q [rows, q_heads, dim] (bf16) over their sequences' cached keys and values.
 
     Rows and positions as in kv_write.  causal_block: 0 for no mask, 1 for causal, c for runs of c positions that
     see one another and all before them.  scale: dim^-0.5 by default.  max_len: a bound on the lengths known to the
     host (default: what the table holds), which decides how many rows a workgroup takes and how far the keys of
     few rows are shared out over workgroups.  A workspace of nvfp4_kv_attention_workspace_bytes(...) is allocated with torch when none is given,
-    on the stream that the call runs on."""
+    on the stream that the call runs on.
+
+    window: a row sees only its last `window` positions and the first `sinks` of the sequence (0: all; sinks need a
+    window).  shared: int32 [blocks] on the GPU, the cache blocks of a prefix that all sequences begin with; they stand
+    for the first entries of every table, and the rows of all sequences are taken against them together.  The new rows
+    lie behind it (NaN where they do not).  Not both at once.  Their workspaces are those of
+    nvfp4_kv_attention_window_workspace_bytes and nvfp4_kv_attention_shared_workspace_bytes."""
     dev, c = cache.device, cache.struct
     _same_device(dev, q, out, workspace)
     hq = make_heads("q", q)
@@ -898,18 +934,36 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
         max_len = table.shape[1] * KV_BLOCK
     if not 0 <= causal_block < 2**31:
         raise ValueError(f"causal_block: expected 0 to 2^31 - 1, got {causal_block}")
+    if not 0 <= window < 2**31 or not 0 <= sinks < 2**31:
+        raise ValueError(f"window and sinks: expected 0 to 2^31 - 1, got {window} and {sinks}")
+    if sinks and not window:
+        raise ValueError("first positions without a window: a row sees them anyway")
+    scale = dim ** -0.5 if scale is None else float(scale)
+    if shared is not None:
+        if window:
+            raise ValueError("a window and a shared prefix in one call")
+        _int32s(dev, shared=(shared, None))
+        name, fn, size_of = "nvfp4_kv_attention_shared", lib.nvfp4_kv_attention_shared, \
+            lib.nvfp4_kv_attention_shared_workspace_bytes
+        sizes, args = (shared.shape[0], max_len), (shared.data_ptr(), shared.shape[0], scale, causal_block, max_len)
+    elif window:
+        name, fn, size_of = "nvfp4_kv_attention_window", lib.nvfp4_kv_attention_window, \
+            lib.nvfp4_kv_attention_window_workspace_bytes
+        sizes, args = (causal_block, window, sinks, max_len), (scale, causal_block, window, sinks, max_len)
+    else:
+        name, fn, size_of = "nvfp4_kv_attention", lib.nvfp4_kv_attention, lib.nvfp4_kv_attention_workspace_bytes
+        sizes, args = (max_len,), (scale, causal_block, max_len)
     out, ho = _output("out", out, dev, stream, shape)
     if workspace is None and rows:
-        need = lib.nvfp4_kv_attention_workspace_bytes(rows, s.count, q_heads, c.heads, dim, max_len)
+        need = size_of(rows, s.count, q_heads, c.heads, dim, *sizes)
         if need:
             workspace = _empty(dev, stream, (need,), torch.uint8)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if rows:
-        _call("nvfp4_kv_attention", lib.nvfp4_kv_attention, dev, stream, hq, rows, q_heads, c, s,
-              dim ** -0.5 if scale is None else float(scale), causal_block, max_len, ho,
-              None if workspace is None else workspace.data_ptr(), size)
+        _call(name, fn, dev, stream, hq, rows, q_heads, c, s, *args, ho, None if workspace is None else workspace.data_ptr(),
+              size)
     return out
 
 

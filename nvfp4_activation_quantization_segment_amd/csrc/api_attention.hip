@@ -14,6 +14,7 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t)1 << 23;   // rows x threads of a row stay below 2^32
 constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
 constexpr int32_t kMaxHeads = 65535;             // second dimension of a grid
+constexpr int64_t kMaxTableBlocks = INT32_MAX / kKvBlock;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -75,7 +76,7 @@ nvfp4_status check_cache(const nvfp4_kv_cache* c, CacheArgs* a) {
 nvfp4_status check_sequences(const nvfp4_kv_sequences* s, int64_t M, SeqArgs* a) {
     if (!s || !s->row_start || !s->lens || !s->table || M < 1 || s->count < 1) return NVFP4_ERR_INVALID_ARGUMENT;
     if (s->table_blocks < 1 || s->ld_table < s->table_blocks) return NVFP4_ERR_INVALID_ARGUMENT;
-    if (M > kMaxRows || s->count > kMaxSeqs || s->table_blocks > INT32_MAX / kKvBlock) return NVFP4_ERR_SHAPE;
+    if (M > kMaxRows || s->count > kMaxSeqs || s->table_blocks > kMaxTableBlocks) return NVFP4_ERR_SHAPE;
     if (!aligned(s->row_start, 4) || !aligned(s->lens, 4) || !aligned(s->table, 4)) return NVFP4_ERR_ALIGNMENT;
     *a = SeqArgs{M, s->count, s->row_start, s->lens, s->table, s->ld_table, s->table_blocks, 0};
     return NVFP4_OK;
@@ -87,7 +88,7 @@ nvfp4_status check_tables(const nvfp4_kv_tables* t) {
     if (!t || !t->table || !t->free_blocks || t->count < 1 || t->table_blocks < 1 || t->capacity < 1 ||
         t->ld_table < t->table_blocks)
         return NVFP4_ERR_INVALID_ARGUMENT;
-    if (t->count > kMaxSeqs || t->table_blocks > INT32_MAX / kKvBlock || t->capacity > INT32_MAX ||
+    if (t->count > kMaxSeqs || t->table_blocks > kMaxTableBlocks || t->capacity > INT32_MAX ||
         t->ld_table > ((int64_t)1 << 60) / t->count)
         return NVFP4_ERR_SHAPE;
     if (!aligned(t->table, 4) || !aligned(t->free_blocks, 4)) return NVFP4_ERR_ALIGNMENT;
@@ -101,6 +102,40 @@ bool attention_sizes_ok(int64_t M, int64_t count, int64_t q_heads, int64_t heads
 
 HeadsIn in(const nvfp4_heads* h) { return HeadsIn{h->data, h->row_stride, h->head_stride}; }
 HeadsOut out_of(const nvfp4_heads* h) { return HeadsOut{h->data, h->row_stride, h->head_stride}; }
+
+// The checks that every attention call makes, and what they describe.
+nvfp4_status check_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads, const nvfp4_kv_cache* cache,
+                             const nvfp4_kv_sequences* seqs, float scale, int32_t causal_block, int64_t max_len,
+                             const nvfp4_heads* out, AttentionArgs* a) {
+    memset(a, 0, sizeof(*a));
+    nvfp4_status st;
+    if ((st = check_cache(cache, &a->cache)) != NVFP4_OK) return st;
+    if ((st = check_sequences(seqs, M, &a->seqs)) != NVFP4_OK) return st;
+    if (q_heads < 1 || causal_block < 0 || max_len < 0) return NVFP4_ERR_INVALID_ARGUMENT;
+    const float scale_log2 = scale * 1.44269504088896340736f;
+    if (!(scale > 0.0f) || !isfinite(scale_log2)) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (!attention_sizes_ok(M, seqs->count, q_heads, cache->heads, cache->dim, max_len)) return NVFP4_ERR_SHAPE;
+    if ((st = check_heads(q, M, q_heads, cache->dim, false)) != NVFP4_OK) return st;
+    if ((st = check_heads(out, M, q_heads, cache->dim, true)) != NVFP4_OK) return st;
+    a->q = in(q);
+    a->out = out_of(out);
+    a->q_heads = q_heads;
+    a->group = q_heads / cache->heads;
+    a->scale_log2 = scale_log2;
+    a->causal = causal_block;
+    return NVFP4_OK;
+}
+
+// One launch over the sequences' keys (and the join), cut for at most `bound` of them a row.
+nvfp4_status run_attention(AttentionArgs& a, int64_t bound, void* workspace, size_t workspace_bytes, void* stream) {
+    const AttentionPlan p = attention_plan(a.seqs.M, a.seqs.B, a.q_heads, a.cache.heads, a.cache.dim, bound);
+    if (p.workspace_bytes > 0 && (!workspace || workspace_bytes < p.workspace_bytes)) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (p.workspace_bytes > 0 && !aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
+    a.wide = p.wide;
+    a.parts = a.all_parts = p.parts;
+    a.partial = (float*)workspace;
+    return report_hip(launch_attention(a, (hipStream_t)stream));
+}
 
 }  // namespace
 
@@ -268,29 +303,54 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads
                                 const nvfp4_kv_sequences* seqs, float scale, int32_t causal_block, int64_t max_len,
                                 const nvfp4_heads* out, void* workspace, size_t workspace_bytes, void* stream) {
     AttentionArgs a;
-    memset(&a, 0, sizeof(a));
-    nvfp4_status st;
-    if ((st = check_cache(cache, &a.cache)) != NVFP4_OK) return st;
-    if ((st = check_sequences(seqs, M, &a.seqs)) != NVFP4_OK) return st;
-    if (q_heads < 1 || causal_block < 0 || max_len < 0) return NVFP4_ERR_INVALID_ARGUMENT;
-    const float scale_log2 = scale * 1.44269504088896340736f;
-    if (!(scale > 0.0f) || !isfinite(scale_log2)) return NVFP4_ERR_INVALID_ARGUMENT;
-    if (!attention_sizes_ok(M, seqs->count, q_heads, cache->heads, cache->dim, max_len)) return NVFP4_ERR_SHAPE;
-    if ((st = check_heads(q, M, q_heads, cache->dim, false)) != NVFP4_OK) return st;
-    if ((st = check_heads(out, M, q_heads, cache->dim, true)) != NVFP4_OK) return st;
-    const AttentionPlan p = attention_plan(M, seqs->count, q_heads, cache->heads, cache->dim, max_len);
-    if (p.workspace_bytes > 0 && (!workspace || workspace_bytes < p.workspace_bytes)) return NVFP4_ERR_INVALID_ARGUMENT;
-    if (p.workspace_bytes > 0 && !aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
-    a.q = in(q);
-    a.out = out_of(out);
-    a.q_heads = q_heads;
-    a.group = q_heads / cache->heads;
-    a.scale_log2 = scale_log2;
-    a.causal = causal_block;
-    a.wide = p.wide;
-    a.parts = p.parts;
+    const nvfp4_status st = check_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len, out, &a);
+    if (st != NVFP4_OK) return st;
+    return run_attention(a, max_len, workspace, workspace_bytes, stream);
+}
+
+size_t nvfp4_kv_attention_window_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
+                                                 int32_t causal_block, int32_t window, int32_t sinks, int64_t max_len) {
+    if (!attention_sizes_ok(M, count, q_heads, heads, dim, max_len) || causal_block < 0 || window < 1 || sinks < 0) return 0;
+    return attention_plan(M, count, q_heads, heads, dim, window_bound(max_len, causal_block, window, sinks)).workspace_bytes;
+}
+
+nvfp4_status nvfp4_kv_attention_window(const nvfp4_heads* q, int64_t M, int32_t q_heads, const nvfp4_kv_cache* cache,
+                                       const nvfp4_kv_sequences* seqs, float scale, int32_t causal_block, int32_t window,
+                                       int32_t sinks, int64_t max_len, const nvfp4_heads* out, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    AttentionArgs a;
+    const nvfp4_status st = check_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len, out, &a);
+    if (st != NVFP4_OK) return st;
+    if (window < 1 || sinks < 0) return NVFP4_ERR_INVALID_ARGUMENT;
+    a.window = window;
+    a.sinks = sinks;
+    return run_attention(a, window_bound(max_len, causal_block, window, sinks), workspace, workspace_bytes, stream);
+}
+
+size_t nvfp4_kv_attention_shared_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
+                                                 int64_t shared_blocks, int64_t max_len) {
+    if (!attention_sizes_ok(M, count, q_heads, heads, dim, max_len) || shared_blocks < 1 || shared_blocks > kMaxTableBlocks)
+        return 0;
+    return shared_plan(M, count, q_heads, heads, dim, max_len, shared_blocks).workspace_bytes;
+}
+
+nvfp4_status nvfp4_kv_attention_shared(const nvfp4_heads* q, int64_t M, int32_t q_heads, const nvfp4_kv_cache* cache,
+                                       const nvfp4_kv_sequences* seqs, const int32_t* shared, int64_t shared_blocks,
+                                       float scale, int32_t causal_block, int64_t max_len, const nvfp4_heads* out,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+    AttentionArgs a;
+    const nvfp4_status st = check_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len, out, &a);
+    if (st != NVFP4_OK) return st;
+    if (!shared || shared_blocks < 1) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (shared_blocks > kMaxTableBlocks) return NVFP4_ERR_SHAPE;
+    if (!aligned(shared, 4)) return NVFP4_ERR_ALIGNMENT;
+    const SharedPlan p = shared_plan(M, seqs->count, q_heads, cache->heads, cache->dim, max_len, shared_blocks);
+    if (!workspace || workspace_bytes < p.workspace_bytes) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
+    a.shared = shared_blocks;
+    a.all_parts = p.prefix.parts + p.own.parts;
     a.partial = (float*)workspace;
-    return report_hip(launch_attention(a, (hipStream_t)stream));
+    return report_hip(launch_attention_shared(a, p, shared, (hipStream_t)stream));
 }
 
 }  // extern "C"

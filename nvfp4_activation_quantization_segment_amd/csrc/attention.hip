@@ -21,6 +21,8 @@
 // of their size, where binary32 probabilities and the output's own rounding give
 // 0.0016 to 0.0017.  Scores, maxima, sums and outputs are held in
 // binary32.
+#include <type_traits>
+
 #include "kv_device.h"
 
 namespace nvfp4 {
@@ -38,9 +40,16 @@ constexpr float kMost = 256.0f;
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
 
+// What the rows of a launch see of the past.
+//   PLAIN   every key below their limit
+//   WINDOW  of these, the last `window` positions and the first `sinks`
+//   PREFIX  rows of all sequences against the blocks that they share
+//   OWN     rows against their own sequence's keys behind the shared blocks
+enum Mode { PLAIN, WINDOW, PREFIX, OWN };
+
 struct Tile {
     bool any;
-    bool bad;         // a length that the table cannot hold
+    bool bad;         // a length that the table cannot hold, or that ends inside the shared blocks
     int64_t b;
     int64_t row0;     // first row of the sequence
     int32_t n;        // its new tokens
@@ -49,10 +58,26 @@ struct Tile {
     int64_t len;
 };
 
+template <int MODE>
 __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int64_t unit, int64_t T) {
     Tile t;
     t.any = false;
     const SeqArgs& q = a.seqs;
+    if constexpr (MODE == PREFIX) {
+        // one run of rows, from the first sequence's to the last's
+        const RowRange r = row_range(q.row_start[0], q.row_start[q.B], q.M);
+        const int64_t rows = (r.last - r.first) * a.group;
+        if (unit * T >= rows) return t;
+        t.any = true;
+        t.bad = false;
+        t.b = 0;
+        t.row0 = r.first;
+        t.n = (int32_t)(r.last - r.first);
+        t.first = (int32_t)(unit * T);
+        t.rows = (int32_t)rows;
+        t.len = a.shared * kKvBlock;
+        return t;
+    }
     const Located at = locate(q, unit, [&](int64_t row, int64_t b) { return tile_first(row, b, a.group, T, q.per_row); });
     t.b = at.b;
     const RowRange r = row_range(at.start, at.end, q.M);
@@ -65,6 +90,7 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int64_t unit, 
     t.rows = (int32_t)(n * a.group);
     t.len = at.len;
     t.bad = kv_length_bad(t.len, q.table_blocks);
+    if constexpr (MODE == OWN) t.bad = t.bad || t.len - t.n < a.shared * kKvBlock;
     return t;
 }
 
@@ -74,6 +100,7 @@ struct Row {
     int64_t token;   // row of q and out
     int32_t head;    // query head
     int32_t limit;   // keys it sees
+    int32_t low;     // WINDOW: the first of them that need not be one of the first positions
 };
 
 // Keys that token i of the sequence sees.
@@ -86,6 +113,51 @@ __device__ __forceinline__ int32_t limit_of_row(const AttentionArgs& a, const Ti
     return limit_of(a, t, __builtin_amdgcn_readfirstlane(at / a.group));
 }
 
+// WINDOW: the first key inside the window of token i of the sequence, and of row
+// rr, the last row's past it.
+__device__ __forceinline__ int32_t low_of(const AttentionArgs& a, const Tile& t, int32_t i) {
+    return t.bad ? 0 : kv_window_low((int32_t)t.len - t.n + i, a.window);
+}
+__device__ __forceinline__ int32_t low_of_row(const AttentionArgs& a, const Tile& t, int32_t rr) {
+    const int32_t at = rr < t.rows ? rr : t.rows - 1;
+    return low_of(a, t, __builtin_amdgcn_readfirstlane(at / a.group));
+}
+
+// The blocks that a tile goes over, in order: what it sees of the first ones, and
+// then those from the one where `jump` leads.
+struct Blocks {
+    int32_t count, jump_at, jump;
+    __device__ __forceinline__ int32_t operator[](int32_t i) const { return i < jump_at ? i : i + jump; }
+};
+// Of a tile whose last row sees `seen` keys and whose first row's window starts at low.
+template <int MODE>
+__device__ __forceinline__ Blocks blocks_of(const AttentionArgs& a, int32_t seen, int32_t low) {
+    const int32_t n = (seen + kKvBlock - 1) / kKvBlock;
+    if constexpr (MODE == WINDOW) {
+        const KvWindowBlocks w = kv_window_blocks(n, low, a.sinks);
+        return Blocks{w.count, w.first, w.skipped};
+    }
+    if constexpr (MODE == OWN) {
+        const int32_t shared = (int32_t)a.shared;
+        return Blocks{n > shared ? n - shared : 0, 0, shared};
+    }
+    return Blocks{n, n, 0};
+}
+
+// Whether some row whose window starts at `low` or before does not see all of the
+// 64 keys from first_key that are below its limit.
+__device__ __forceinline__ bool window_hides(const AttentionArgs& a, int32_t first_key, int32_t low) {
+    const int32_t from = first_key > a.sinks ? first_key : a.sinks;
+    return from < low && from < first_key + kKvBlock;
+}
+
+// Bits of the 64 keys from first_key that a row sees.
+__device__ __forceinline__ uint64_t bits_below(int32_t n) { return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1; }
+__device__ __forceinline__ uint64_t window_bits(const AttentionArgs& a, const Row& r, int32_t first_key) {
+    return bits_below(r.limit - first_key) & (~bits_below(r.low - first_key) | bits_below(a.sinks - first_key));
+}
+
+template <int MODE>
 __device__ __forceinline__ Row find_row(const AttentionArgs& a, const Tile& t, int32_t rr, int32_t kv_head) {
     Row r;
     r.valid = rr < t.rows;
@@ -94,6 +166,7 @@ __device__ __forceinline__ Row find_row(const AttentionArgs& a, const Tile& t, i
     r.token = t.row0 + i;
     r.head = kv_head * a.group + (at - i * a.group);
     r.limit = limit_of(a, t, i);
+    r.low = MODE == WINDOW ? low_of(a, t, i) : 0;
     return r;
 }
 
@@ -242,6 +315,43 @@ __device__ __forceinline__ void mask_scores(f32x16& s, int32_t left) {
         if (8 * (i / 4) + i % 4 >= mine) s[i] = neg_inf();
 }
 
+// WINDOW: and so do those before its window that are not among the first
+// positions.  low, sinks: counted from the tile's first key too.
+__device__ __forceinline__ void mask_window(f32x16& s, int32_t left, int32_t low, int32_t sinks) {
+    const int h = 4 * (int)((threadIdx.x & 63) >> 5);
+    const int last = left - h, from = sinks - h, to = low - h;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int k = 8 * (i / 4) + i % 4;
+        if (k >= last || (k < to && k >= from)) s[i] = neg_inf();
+    }
+}
+// 1 in each byte that is one of E4M3's NaN codes, as bf16 ones for the products,
+// and a one for each key that is not masked.
+__device__ __forceinline__ uint32_t fp8_nan_bytes(uint32_t w) {
+    return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+}
+__device__ __forceinline__ bf16x8 ones_bf16(uint32_t a, uint32_t b) {
+    constexpr uint32_t kOne = 0x3F80u;
+    const auto two = [](uint32_t w) { return (w & 1u) * kOne | ((w >> 8) & 1u) * (kOne << 16); };
+    return __builtin_bit_cast(bf16x8, u32x4{two(a), two(a >> 16), two(b), two(b >> 16)});
+}
+__device__ __forceinline__ bf16x8 seen_ones(const f32x16& s, int k) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (s[8 * k + 2 * i] != neg_inf() ? 0x3F80u : 0u) | (s[8 * k + 2 * i + 1] != neg_inf() ? 0x3F800000u : 0u);
+    return __builtin_bit_cast(bf16x8, w);
+}
+
+template <int MODE>
+__device__ __forceinline__ void mask_tile(f32x16& s, const AttentionArgs& a, const Row& r, int32_t first_key) {
+    if constexpr (MODE == WINDOW)
+        mask_window(s, r.limit - first_key, r.low - first_key, a.sinks - first_key);
+    else
+        mask_scores(s, r.limit - first_key);
+}
+
 // ---------------------------------------------------------------------------
 // Narrow tiles: 32 rows to a workgroup of 4 waves that share out the blocks of
 // keys, each with its own softmax, joined at the end through LDS; the keys of
@@ -258,7 +368,7 @@ __device__ __forceinline__ void mask_scores(f32x16& s, int32_t left) {
 // ---------------------------------------------------------------------------
 constexpr int kNarrowWaves = 4;
 
-template <int D>
+template <int D, int MODE>
 __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(AttentionArgs a) {
     constexpr int kDT = D / 32, kK = D / 64;
     constexpr int kBytes = kKvBlock * D;
@@ -271,15 +381,17 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     // against each other (32 sequences of 1 to 16,384 keys: 118 us, 124 without).
     uint32_t unit = blockIdx.x + (blockIdx.y + blockIdx.z) % gridDim.x;
     unit = unit < gridDim.x ? unit : unit - gridDim.x;
-    const Tile t = find_tile(a, unit, kRows);
+    const Tile t = find_tile<MODE>(a, unit, kRows);
     if (!t.any) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int c = lane & 31, h = lane >> 5;
-    const Row row = find_row(a, t, t.first + c, kv_head);
+    const Row row = find_row<MODE>(a, t, t.first + c, kv_head);
     // keys that the tile's last row sees, and keys that all its rows see: limits
     // do not fall from row to row
     const int seen = __builtin_amdgcn_readlane(row.limit, kRows - 1), all = __builtin_amdgcn_readlane(row.limit, 0);
-    const BlockRange range = kv_part((seen + kKvBlock - 1) / kKvBlock, part, a.parts);
+    const Blocks blocks = blocks_of<MODE>(a, seen, MODE == WINDOW ? __builtin_amdgcn_readlane(row.low, 0) : 0);
+    const int low_last = MODE == WINDOW ? __builtin_amdgcn_readlane(row.low, kRows - 1) : 0;
+    const BlockRange range = kv_part(blocks.count, part, a.parts);
     const int at0 = range.first + wave;
     u32x4 qw[D / 16];
     fetch_query<D>(qw, a, row);
@@ -288,7 +400,7 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     // looked at when they are needed: a wait for one of them would be a wait for
     // every load before it.
     const int32_t* table = a.seqs.table + t.b * a.seqs.ld_table;
-    const auto entry = [&](int at) { return table[at < range.last ? at : range.last - 1]; };
+    const auto entry = [&](int at) { return table[blocks[at < range.last ? at : range.last - 1]]; };
     const auto page_of = [&](int32_t loaded) -> int64_t {
         const int32_t p = __builtin_amdgcn_readfirstlane(loaded);
         return p >= 0 && p < a.cache.blocks ? p : -1;
@@ -356,11 +468,11 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
             next = entry(at + 2 * kNarrowWaves);
         }
 
-        const int first_key = at * kKvBlock;
-        const bool edge = first_key + kKvBlock > all;
+        const int first_key = blocks[at] * kKvBlock;
+        const bool edge = first_key + kKvBlock > all || (MODE == WINDOW && window_hides(a, first_key, low_last));
         if (edge) {
-            mask_scores(s[0], row.limit - first_key);
-            mask_scores(s[1], row.limit - first_key - 32);
+            mask_tile<MODE>(s[0], a, row, first_key);
+            mask_tile<MODE>(s[1], a, row, first_key + 32);
         }
         if (edge) {
             // A masked key has p = 0, but 0 times a NaN value is NaN: NaN codes
@@ -372,7 +484,29 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
                 for (int u = 0; u < 2; ++u)
                     nan |= fp8_any_nan(vf[d][u].x) || fp8_any_nan(vf[d][u].y) || fp8_any_nan(vf[d][u].z) ||
                            fp8_any_nan(vf[d][u].w);
-            if (__any(nan)) {
+            if (MODE == WINDOW && __any(nan)) {
+                // what a row sees is not all keys below a limit: which of them it
+                // sees, times which are NaN, tells it
+#pragma unroll
+                for (int d = 0; d < kDT; ++d) {
+                    f32x16 hit = f32x16{};
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        u32x4 nans;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            nans[i] = fp8_nan_bytes(vf[d][u][i]);
+                            vf[d][u][i] &= ~(nans[i] * 0xFFu);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ones_bf16(nans[2 * k], nans[2 * k + 1]),
+                                                                          seen_ones(s[u], k), hit, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[d][i] = hit[i] > 0.0f ? quiet_nan() : o[d][i];
+                }
+            } else if (__any(nan)) {
                 int half = h;  // opaque: nothing of this rare path is worth registers in the loop
                 asm volatile("" : "+v"(half));
 #pragma unroll
@@ -434,7 +568,7 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     __syncthreads();
     constexpr int kEach = D / 8;  // dims of a thread: 8 threads a row
     const int rr = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * kEach;
-    const Row mine = find_row(a, t, t.first + rr, kv_head);
+    const Row mine = find_row<MODE>(a, t, t.first + rr, kv_head);
     if (!mine.valid) return;
     float m = sm[0][rr];
 #pragma unroll
@@ -452,7 +586,7 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
         for (int i = 0; i < kEach; ++i) acc[i] += f * so[w][rr][d0 + i];
     }
     const int64_t at = mine.token * a.q_heads + mine.head;
-    if (a.parts == 1) {
+    if (a.all_parts == 1) {
         // no key: 0; a length that the table cannot hold: NaN
         const float inv = t.bad ? quiet_nan() : l == 0.0f ? 0.0f : 1.0f / l;
         uint16_t* p = a.out.data + mine.token * a.out.row + mine.head * a.out.head + d0;
@@ -463,8 +597,9 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
                            pack_bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), pack_bf16x2(acc[i + 6] * inv, acc[i + 7] * inv)};
     } else {
         const int64_t all_rows = a.seqs.M * a.q_heads;
-        float* po = a.partial + ((int64_t)part * all_rows + at) * D + d0;
-        float* pm = a.partial + (int64_t)a.parts * all_rows * D + ((int64_t)part * all_rows + at) * 2;
+        const int64_t piece = (int64_t)(a.first_part + part) * all_rows + at;
+        float* po = a.partial + piece * D + d0;
+        float* pm = a.partial + (int64_t)a.all_parts * all_rows * D + piece * 2;
 #pragma unroll
         for (int i = 0; i < kEach; i += 4)
             *reinterpret_cast<float4*>(po + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
@@ -521,7 +656,7 @@ __device__ __forceinline__ void alternate() {
     }
 }
 
-template <int D>
+template <int D, int MODE>
 __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(AttentionArgs a) {
     constexpr int kDT = D / 32, kK = D / 64;
     constexpr int kBytes = kKvBlock * D;
@@ -530,34 +665,51 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     constexpr int kEach = kPieces / kThreads;             // of them a thread's
     __shared__ __align__(16) u32x4 sk[2][kPieces];
     __shared__ __align__(16) u32x4 sv[2][2 * kPieces];    // [k-step][half][dim] of 8 keys
-    __shared__ int nan_key[2][D];                         // first key whose value is a NaN code, by dim
+    // by dim, the first key whose value is a NaN code; WINDOW: the bits of all of them
+    using Mark = std::conditional_t<MODE == WINDOW, unsigned long long, int>;
+    constexpr Mark kNoMark = MODE == WINDOW ? 0 : kKvBlock;
+    __shared__ Mark nan_key[2][D];
     __shared__ int nan_any[2];
     int unit, kv_head;
     wide_place(a, unit, kv_head);
-    const Tile t = find_tile(a, unit, kWideRows);
+    const Tile t = find_tile<MODE>(a, unit, kWideRows);
     if (!t.any) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int c = lane & 31, h = lane >> 5;
     const int row0 = t.first + wave * kRows;
-    const Row row = find_row(a, t, row0 + c, kv_head);
+    const Row row = find_row<MODE>(a, t, row0 + c, kv_head);
     // keys that the tile's last row and this wave's last row see, and keys that
     // all rows of the tile and of the wave see
     const int tile_seen = limit_of_row(a, t, t.first + kWideRows - 1), tile_all = limit_of_row(a, t, t.first);
     const int seen = row0 < t.rows ? __builtin_amdgcn_readlane(row.limit, kRows - 1) : 0;
     const int all = __builtin_amdgcn_readlane(row.limit, 0);
+    // where the windows of the tile's first and last rows and of this wave's start
+    const int tile_low = MODE == WINDOW ? low_of_row(a, t, t.first) : 0;
+    const int tile_low_last = MODE == WINDOW ? low_of_row(a, t, t.first + kWideRows - 1) : 0;
+    const int low_first = MODE == WINDOW ? __builtin_amdgcn_readlane(row.low, 0) : 0;
+    const int low_last = MODE == WINDOW ? __builtin_amdgcn_readlane(row.low, kRows - 1) : 0;
     const int part = blockIdx.z;
-    const BlockRange range = kv_part((tile_seen + kKvBlock - 1) / kKvBlock, part, a.parts);
+    const Blocks blocks = blocks_of<MODE>(a, tile_seen, tile_low);
+    const BlockRange range = kv_part(blocks.count, part, a.parts);
     const int at0 = range.first, end = range.last;
+    // whether some row of the tile does not see all of block i, and whether some row of this wave sees any of it
+    const auto edge_of = [&](int i) {
+        const int first_key = blocks[i] * kKvBlock;
+        return first_key + kKvBlock > tile_all || (MODE == WINDOW && window_hides(a, first_key, tile_low_last));
+    };
+    const auto sees = [&](int first_key) {
+        return first_key < seen && (MODE != WINDOW || first_key + kKvBlock > low_first || first_key < a.sinks);
+    };
 
     u32x4 qw[D / 16];
     fetch_query<D>(qw, a, row);
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) nan_key[i / D][i % D] = kKvBlock;
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) nan_key[i / D][i % D] = kNoMark;
     if (threadIdx.x < 2) nan_any[threadIdx.x] = 0;
 
     // table entries and powers are looked at a block after they are asked for,
     // as in the narrow kernel
     const int32_t* table = a.seqs.table + t.b * a.seqs.ld_table;
-    const auto entry = [&](int at) { return table[at < end ? at : end - 1]; };
+    const auto entry = [&](int at) { return table[blocks[at < end ? at : end - 1]]; };
     const auto page_of = [&](int32_t loaded) -> int64_t {
         const int32_t p = __builtin_amdgcn_readfirstlane(loaded);
         return p >= 0 && p < a.cache.blocks ? p : -1;
@@ -590,16 +742,22 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
                 // as in the narrow kernel: NaN codes are taken out, and given
                 // back to the rows that see their key
                 uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                int lowest = kKvBlock;
+                Mark mark = kNoMark;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     if (((x[j / 4] >> (8 * (j % 4))) & 0x7Fu) == 0x7Fu) {
                         const int key = 32 * (piece / 2) + 16 * (j / 8) + 8 * (j / 4 % 2) + 4 * (piece % 2) + j % 4;
-                        lowest = key < lowest ? key : lowest;
+                        if constexpr (MODE == WINDOW)
+                            mark |= (Mark)1 << key;
+                        else
+                            mark = key < mark ? key : mark;
                         x[j / 4] &= ~(0xFFu << (8 * (j % 4)));
                     }
                 w = u32x4{x[0], x[1], x[2], x[3]};
-                atomicMin(&nan_key[buffer][d], lowest);
+                if constexpr (MODE == WINDOW)
+                    atomicOr(&nan_key[buffer][d], mark);
+                else
+                    atomicMin(&nan_key[buffer][d], mark);
                 nan_any[buffer] = 1;
             }
             sk[buffer][at] = kr[i];
@@ -616,7 +774,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
         const int64_t page = page_of(entry(at0));
         fetch(page);
         next = entry(at0 + 1);
-        edge_now = page < 0 || (at0 + 1) * kKvBlock > tile_all;
+        edge_now = page < 0 || edge_of(at0);
         first_good = page >= 0;
     }
     // the first block is on its way while the queries are split
@@ -632,14 +790,14 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     }
     __syncthreads();
     for (int at = at0; at < end; ++at) {
-        const int b = (at - at0) & 1, first_key = at * kKvBlock;
+        const int b = (at - at0) & 1, first_key = blocks[at] * kKvBlock;
         const bool more = at + 1 < end;
         const int64_t page = page_of(next);
         if (more) {
             fetch(page);
             next = entry(at + 2);
         }
-        if (first_key < seen) {
+        if (sees(first_key)) {
             u32x4 kf[2][2 * kK];
 #pragma unroll
             for (int k = 0; k < kK; ++k)
@@ -652,7 +810,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
             // first's exponentials are taken, and the first's products with the
             // values while the second's are: matrix and vector instructions of
             // one wave overlap where they alternate.
-            const bool edge = first_key + kKvBlock > all;
+            const bool edge = first_key + kKvBlock > all || (MODE == WINDOW && window_hides(a, first_key, low_last));
             f32x16 s[2] = {f32x16{}, f32x16{}};
             const auto scores = [&](int tt) {
 #pragma unroll
@@ -678,14 +836,14 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
             scores(0);
             values(0);
             __builtin_amdgcn_sched_barrier(0);
-            if (edge) mask_scores(s[0], row.limit - first_key);
+            if (edge) mask_tile<MODE>(s[0], a, row, first_key);
             scores(1);
             const float sum0 = probabilities(s[0], a.scale_log2, st.m, p0);
             values(1);
             alternate<2 * kK, 56>();
             asm volatile("" : "+v"(s[1]));  // issued here, not after the branch below
             accept<kDT>(s[0], a.scale_log2, sum0, st, o, p0);
-            if (edge) mask_scores(s[1], row.limit - first_key - 32);
+            if (edge) mask_tile<MODE>(s[1], a, row, first_key + 32);
             multiply(0, p0[0]);
             values(2);
             multiply(1, p0[1]);
@@ -697,24 +855,28 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
             multiply(3, p1[1]);
         }
         if (edge_now && nan_any[b]) {  // the same for all waves
-            if (first_key < seen) {
+            if (sees(first_key)) {
                 int half = h;
                 asm volatile("" : "+v"(half));
 #pragma unroll
                 for (int d = 0; d < kDT; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int key = nan_key[b][32 * d + 8 * (i / 4) + 4 * half + i % 4];
-                        if (key < kKvBlock && key < row.limit - first_key) o[d][i] = quiet_nan();
+                        const Mark key = nan_key[b][32 * d + 8 * (i / 4) + 4 * half + i % 4];
+                        if constexpr (MODE == WINDOW) {
+                            if (key & window_bits(a, row, first_key)) o[d][i] = quiet_nan();
+                        } else {
+                            if (key < kKvBlock && key < row.limit - first_key) o[d][i] = quiet_nan();
+                        }
                     }
             }
             __syncthreads();
-            for (int i = threadIdx.x; i < D; i += kThreads) nan_key[b][i] = kKvBlock;
+            for (int i = threadIdx.x; i < D; i += kThreads) nan_key[b][i] = kNoMark;
             if (threadIdx.x == 0) nan_any[b] = 0;
         }
         if (more) {
             const bool good = page >= 0;
-            edge_now = !good || first_key + 2 * kKvBlock > tile_all;
+            edge_now = !good || edge_of(at + 1);
             stage(1 - b, edge_now, good);
             kp = key_power(kp_raw, good);
         }
@@ -727,8 +889,9 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     float l = st.l + __shfl_xor(st.l, 32);
     if (q.nan && row.limit > 0) l = quiet_nan();
     if (t.bad) l = quiet_nan();
-    if (a.parts > 1) {
-        const int64_t all_rows = a.seqs.M * a.q_heads, mine = (int64_t)part * all_rows + row.token * a.q_heads + row.head;
+    if (a.all_parts > 1) {
+        const int64_t all_rows = a.seqs.M * a.q_heads;
+        const int64_t mine = (int64_t)(a.first_part + part) * all_rows + row.token * a.q_heads + row.head;
         float* po = a.partial + mine * D + 4 * h;
 #pragma unroll
         for (int d = 0; d < kDT; ++d)
@@ -737,7 +900,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
                 *reinterpret_cast<float4*>(po + 32 * d + 8 * i) =
                     make_float4(o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]);
         if (h == 0)
-            *reinterpret_cast<float2*>(a.partial + (int64_t)a.parts * all_rows * D + mine * 2) = make_float2(st.m, l);
+            *reinterpret_cast<float2*>(a.partial + (int64_t)a.all_parts * all_rows * D + mine * 2) = make_float2(st.m, l);
         return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -765,6 +928,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
 // the waves.  (64 parts of one wave's, eight loads at a time, took 12 us where
 // the attention before it takes 25.)
 constexpr int kMaxParts = 64;
+constexpr int kOwnParts = 16;  // of them the sequences' own, behind a shared prefix
 
 template <int D, int WAVES, int EACH>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
@@ -778,21 +942,21 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
     const int64_t token = at / a.q_heads;
     const int32_t head = (int32_t)(at - token * a.q_heads);
     const int32_t first = a.seqs.row_start[0], last = a.seqs.row_start[a.seqs.B];
-    const int mine = lane < a.parts ? lane : 0, own = wave % WAVES;
-    const float2 ml = *reinterpret_cast<const float2*>(a.partial + a.parts * all_rows * D + (mine * all_rows + at) * 2);
+    const int mine = lane < a.all_parts ? lane : 0, own = wave % WAVES;
+    const float2 ml = *reinterpret_cast<const float2*>(a.partial + a.all_parts * all_rows * D + (mine * all_rows + at) * 2);
     const float* po = a.partial + at * D + lane * kEach;
     Dims v[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int s = own + i * WAVES;
-        v[i] = *reinterpret_cast<const Dims*>(po + (s < a.parts ? s : 0) * all_rows * D);
+        v[i] = *reinterpret_cast<const Dims*>(po + (s < a.all_parts ? s : 0) * all_rows * D);
     }
     if (token < first || token >= last) return;
-    float m = lane < a.parts ? ml.x : neg_inf();
+    float m = lane < a.all_parts ? ml.x : neg_inf();
 #pragma unroll
     for (int s = 32; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
-    const float w = lane < a.parts ? __builtin_amdgcn_exp2f(ml.x - (m == neg_inf() ? 0.0f : m)) : 0.0f;
-    float l = lane >= a.parts ? 0.0f : ml.y != ml.y ? ml.y : w * ml.y;
+    const float w = lane < a.all_parts ? __builtin_amdgcn_exp2f(ml.x - (m == neg_inf() ? 0.0f : m)) : 0.0f;
+    float l = lane >= a.all_parts ? 0.0f : ml.y != ml.y ? ml.y : w * ml.y;
 #pragma unroll
     for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s);
     Dims acc = {};
@@ -800,7 +964,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
     for (int i = 0; i < EACH; ++i) {
         const int s = own + i * WAVES;
         const Dims more = __shfl(w, s & 63) * v[i];
-        acc += s < a.parts ? more : Dims{};
+        acc += s < a.all_parts ? more : Dims{};
     }
     if constexpr (WAVES > 1) {
         share[wave][lane] = acc;
@@ -849,35 +1013,90 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
     return p;
 }
 
-template <int D>
-static void attention_of(const AttentionArgs& args, hipStream_t s) {
-    AttentionArgs a = args;
+// The first positions, the window and a tile's rows, each with what a cut inside a
+// block adds: so much of the past can 128 rows see (all of it without a causal mask).
+int64_t window_bound(int64_t max_len, int32_t causal, int32_t window, int32_t sinks) {
+    if (causal == 0) return max_len;
+    const int64_t most = (int64_t)sinks + window + causal + kWideRows + 2 * kKvBlock;
+    return max_len < most ? max_len : most;
+}
+
+SharedPlan shared_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len, int64_t shared) {
+    SharedPlan p;
+    const int64_t common = shared * kKvBlock;
+    p.own = attention_plan(M, B, q_heads, kv_heads, dim, max_len > common ? max_len - common : 0);
+    p.own.parts = p.own.parts < kOwnParts ? p.own.parts : kOwnParts;
+    const int64_t rows = M * (q_heads / kv_heads);
+    p.prefix.wide = rows > kRows;
+    const int64_t T = p.prefix.wide ? kWideRows : kRows, tiles = (rows + T - 1) / T;
+    const int64_t want = 512 / (tiles * kv_heads), most = p.prefix.wide ? shared / 4 : shared / 8;
+    p.prefix.parts = (int32_t)clamp64(want < most ? want : most, 1, kMaxParts - kOwnParts);
+    p.workspace_bytes = (size_t)(p.prefix.parts + p.own.parts) * (size_t)(M * q_heads) * (size_t)(dim + 2) * sizeof(float);
+    return p;
+}
+
+template <int D, int MODE>
+static void attention_tiles(AttentionArgs a, hipStream_t s) {
     const int64_t T = a.wide ? kWideRows : kRows;
-    a.seqs.per_row = tiles_per_row(a.seqs.M, a.seqs.B, a.group, T);
-    const int64_t units = tile_first(a.seqs.M, a.seqs.B, a.group, T, a.seqs.per_row);
+    int64_t units;
+    if (MODE == PREFIX) {
+        units = (a.seqs.M * a.group + T - 1) / T;
+    } else {
+        a.seqs.per_row = tiles_per_row(a.seqs.M, a.seqs.B, a.group, T);
+        units = tile_first(a.seqs.M, a.seqs.B, a.group, T, a.seqs.per_row);
+    }
     if (a.wide) {
         // below 2^23, so that the threads of a dimension stay below 2^32: the heads
         // times M group / 128 + B, where B <= M group / 64 and M q_heads <= 2^28
         const dim3 grid((unsigned)(units * a.cache.heads), 1, (unsigned)a.parts);
-        attention_wide_kernel<D><<<grid, dim3(64 * kWideWaves), 0, s>>>(a);
+        attention_wide_kernel<D, MODE><<<grid, dim3(64 * kWideWaves), 0, s>>>(a);
     } else {
         const dim3 grid((unsigned)units, (unsigned)a.cache.heads, (unsigned)a.parts);
-        attention_narrow_kernel<D><<<grid, dim3(64 * kNarrowWaves), 0, s>>>(a);
+        attention_narrow_kernel<D, MODE><<<grid, dim3(64 * kNarrowWaves), 0, s>>>(a);
     }
+}
+
+template <int D>
+static void attention_join(const AttentionArgs& a, hipStream_t s) {
     const int64_t rows = a.seqs.M * a.q_heads;
     const dim3 four((unsigned)((rows + 3) / 4)), one((unsigned)rows), threads(256);
-    if (a.parts > 32)
+    if (a.all_parts > 32)
         attention_join_kernel<D, 4, 16><<<one, threads, 0, s>>>(a);
-    else if (a.parts > 16)
+    else if (a.all_parts > 16)
         attention_join_kernel<D, 4, 8><<<one, threads, 0, s>>>(a);
-    else if (a.parts > 8)
+    else if (a.all_parts > 8)
         attention_join_kernel<D, 4, 4><<<one, threads, 0, s>>>(a);
-    else if (a.parts > 4)
+    else if (a.all_parts > 4)
         attention_join_kernel<D, 1, 8><<<four, threads, 0, s>>>(a);
-    else if (a.parts > 2)
+    else if (a.all_parts > 2)
         attention_join_kernel<D, 1, 4><<<four, threads, 0, s>>>(a);
-    else if (a.parts > 1)
+    else if (a.all_parts > 1)
         attention_join_kernel<D, 1, 2><<<four, threads, 0, s>>>(a);
+}
+
+template <int D>
+static void attention_of(const AttentionArgs& a, hipStream_t s) {
+    if (a.window > 0)
+        attention_tiles<D, WINDOW>(a, s);
+    else
+        attention_tiles<D, PLAIN>(a, s);
+    attention_join<D>(a, s);
+}
+
+template <int D>
+static void attention_shared_of(const AttentionArgs& a, const SharedPlan& p, const int32_t* shared, hipStream_t s) {
+    AttentionArgs prefix = a;
+    prefix.seqs.table = shared;
+    prefix.causal = 0;
+    prefix.wide = p.prefix.wide;
+    prefix.parts = p.prefix.parts;
+    attention_tiles<D, PREFIX>(prefix, s);
+    AttentionArgs own = a;
+    own.wide = p.own.wide;
+    own.parts = p.own.parts;
+    own.first_part = p.prefix.parts;
+    attention_tiles<D, OWN>(own, s);
+    attention_join<D>(a, s);
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {
@@ -885,6 +1104,14 @@ hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {
         attention_of<128>(a, s);
     else
         attention_of<64>(a, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_attention_shared(const AttentionArgs& a, const SharedPlan& p, const int32_t* shared, hipStream_t s) {
+    if (a.cache.dim == 128)
+        attention_shared_of<128>(a, p, shared, s);
+    else
+        attention_shared_of<64>(a, p, shared, s);
     return hipGetLastError();
 }
 

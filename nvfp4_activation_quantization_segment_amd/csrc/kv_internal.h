@@ -119,7 +119,11 @@ struct AttentionArgs {
     int32_t causal;
     int32_t wide;      // 128 rows to a workgroup (else 32)
     int32_t parts;     // pieces the keys of a row tile are cut into
-    float* partial;    // parts x (M q_heads) x D, then parts x (M q_heads) x 2
+    int32_t first_part, all_parts;  // the first of them, and how many are joined
+    float* partial;    // all_parts x (M q_heads) x D, then all_parts x (M q_heads) x 2
+    int32_t window;    // last positions that a row sees, 0: all
+    int32_t sinks;     // and first ones
+    int64_t shared;    // blocks of the shared prefix
 };
 
 hipError_t launch_rope_table(float2* table, int64_t rows, int32_t pairs, double theta, hipStream_t s);
@@ -143,5 +147,17 @@ struct AttentionPlan {
 };
 AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s);
+
+// A bound on the keys that a tile sees through a window, for attention_plan.
+int64_t window_bound(int64_t max_len, int32_t causal, int32_t window, int32_t sinks);
+
+// How a call over a shared prefix is cut: all rows against it, and each sequence's
+// against its own keys.
+struct SharedPlan {
+    AttentionPlan prefix, own;
+    size_t workspace_bytes;
+};
+SharedPlan shared_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len, int64_t shared);
+hipError_t launch_attention_shared(const AttentionArgs& a, const SharedPlan& p, const int32_t* shared, hipStream_t s);
 
 }  // namespace nvfp4

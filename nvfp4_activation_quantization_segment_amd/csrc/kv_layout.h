@@ -124,6 +124,20 @@ constexpr int32_t kv_limit(int32_t pos, int32_t len, int32_t causal) {
     return left > len - pos ? len : pos + left;
 }
 
+// First key of the last `window` positions (at least 1) up to pos.
+constexpr int32_t kv_window_low(int32_t pos, int32_t window) { return pos >= window ? pos - window + 1 : 0; }
+
+// Of n blocks, those with keys from `low` on or among the first `sinks` keys: the
+// first `first` of them and then all but `skipped`.
+struct KvWindowBlocks {
+    int32_t count, first, skipped;
+};
+constexpr KvWindowBlocks kv_window_blocks(int32_t n, int32_t low, int32_t sinks) {
+    const int32_t at = low / kKvBlock, all = sinks / kKvBlock + (sinks % kKvBlock != 0);
+    const int32_t first = all < at ? all : at;
+    return KvWindowBlocks{n - (at - first), first, at - first};
+}
+
 // Blocks [first, last) of part s of S of a row tile that sees n blocks (n below
 // 2^25, S at most 64).
 struct BlockRange {

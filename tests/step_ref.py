@@ -86,7 +86,7 @@ def attention(q, cache, row_start, lens, table, scale, c, window=0, sinks=0, sha
     common = 0 if shared is None else len(shared) * BLOCK
     for b in range(len(lens)):
         n, length = row_start[b + 1] - row_start[b], int(lens[b])
-        if n <= 0 or length < 0 or length > table.shape[1] * BLOCK or length - n < common:
+        if n <= 0 or length < 0 or length > table.shape[1] * BLOCK or (common and length - n < common):
             continue
         blocks = np.array(table[b])
         if shared is not None:

@@ -8,7 +8,7 @@ import torch
 
 from tests import kv_ref, step_ref
 from tests.gpu_util import device
-from tests.test_gpu_attention import gen, i32, normal, same, strided, tables_for
+from tests.test_gpu_attention import Pool, bits, check, gen, i32, normal, same, starts, strided, tables_for
 
 pytestmark = pytest.mark.gpu
 BLOCK = 64
@@ -276,3 +276,389 @@ def test_a_pool_through_many_steps_in_place(nv):
         past = want["lens"]
         held = [p for b in range(count) for p in table[b][:-(-past[b] // BLOCK)] if p >= 0]
         assert sorted(held + stack) == list(range(pool))
+
+
+# ---------------------------------------------------------------------------
+# attention through a window
+# ---------------------------------------------------------------------------
+# A bound on the lengths decides between 32-row and 128-row tiles and how far the keys are cut; the results have to be
+# right with all of them.
+BOUND = pytest.mark.parametrize("bound", [None, 0, 1 << 20], ids=["fits", "one-piece", "pieces"])
+
+WINDOWS = [
+    # dim, kv heads, group, causal block, window, sinks, [(past, new)]
+    (64, 1, 1, 1, 1, 0, [(0, 1)]),
+    (128, 1, 1, 1, 1, 1, [(0, 70)]),
+    (128, 2, 4, 1, 100, 4, [(516, 1)]),
+    (64, 3, 1, 1, 64, 64, [(63, 1), (64, 1), (65, 1), (0, 1), (300, 1)]),
+    (128, 2, 5, 1, 63, 1, [(300, 1), (0, 1), (77, 1), (900, 1)]),
+    (64, 2, 8, 1, 5, 3, [(100, 3), (10, 2), (0, 3), (5, 0)]),
+    (128, 2, 3, 1, 17, 40, [(0, 65), (17, 100)]),
+    (64, 2, 2, 0, 30, 0, [(40, 90), (0, 129)]),
+    (128, 1, 4, 16, 20, 7, [(5, 60), (64, 48)]),
+    (64, 2, 1, 100, 33, 65, [(0, 250)]),
+    (128, 3, 1, 0, 129, 2, [(1, 200)]),
+    (64, 1, 40, 1, 40, 0, [(70, 3)]),
+    (128, 1, 1, 1, 1000, 200, [(3000, 1)]),
+    (128, 2, 4, 1, 128, 0, [(0, 400), (333, 200)]),
+    (64, 1, 1, 1, 2, 2, [(600, 300)]),
+    (64, 2, 7, 1, 200, 130, [(0, 300), (0, 301)]),
+    (128, 8, 1, 1, 90, 5, [(0, 300), (77, 130), (0, 0), (500, 65)]),
+    (128, 4, 1, 256, 300, 256, [(100, 700)]),
+]
+
+
+@BOUND
+@pytest.mark.parametrize("case", range(len(WINDOWS)))
+def test_window(nv, case, bound):
+    dim, heads, group, c, window, sinks, seqs = WINDOWS[case]
+    news = [n for _, n in seqs]
+    pool = Pool(nv, 250 + case, heads, dim, [p + n for p, n in seqs])
+    q = normal(gen(260 + case), sum(news), heads * group, dim, sigma=1.0 + case % 3)
+    rs = starts(news)
+    want, tol = step_ref.attention(q.double().numpy(), pool.ref, rs, pool.lens.tolist(), pool.table,
+                                   np.float64(np.float32(dim ** -0.5)), c, window, sinks)
+    call = lambda x, **kw: nv.kv_attention(x, pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=c, max_len=bound,  # noqa: E731
+                                           window=window, sinks=sinks, **kw)
+    for layout in ("plain", "qkv", "heads"):
+        got = call(strided(q, layout))
+        check(got, want, tol)
+    out = strided(torch.zeros_like(q), "heads")
+    call(q.cuda(), out=out)
+    assert same(out, got)
+    inplace = q.cuda()
+    call(inplace, out=inplace)
+    assert same(inplace, got)
+
+
+@BOUND
+@pytest.mark.parametrize("rows", [1, 60, 300])
+def test_a_window_past_everything_is_none(nv, bound, rows):
+    """The same bytes as without one where the keys are cut alike, which is what the smaller of the two bounds on what a
+    row sees decides; else the same sums in other pieces."""
+    lens = [900 + rows, 70]
+    pool = Pool(nv, 281, 2, 128, lens)
+    q = normal(gen(282), rows + 3, 8, 128)
+    args = (q.cuda(), pool.gpu, i32([0, rows, rows + 3]), pool.lens, pool.tab)
+    exact, tol = step_ref.attention(q.double().numpy(), pool.ref, [0, rows, rows + 3], lens, pool.table,
+                                    np.float64(np.float32(128 ** -0.5)), 1)
+    want = nv.kv_attention(*args, causal_block=1, max_len=bound)
+    most = pool.tab.shape[1] * BLOCK if bound is None else bound
+    for window, sinks in ((2000, 0), (2000, 2000), (1 << 20, 0), (2**31 - 1, 2**31 - 1)):
+        got = nv.kv_attention(*args, causal_block=1, max_len=bound, window=window, sinks=sinks)
+        check(got, exact, tol)
+        alike = same(got, want)
+        assert alike or window < most
+
+
+@BOUND
+@pytest.mark.parametrize("dim,group,rows,past,window,sinks", [
+    (64, 1, 1, 300, 70, 3), (128, 2, 40, 200, 20, 5), (128, 1, 150, 100, 64, 0), (64, 4, 200, 70, 30, 100),
+    (128, 2, 3, 2500, 700, 65), (64, 1, 150, 2500, 300, 1), (128, 1, 129, 500, 1, 1)])
+def test_what_a_window_hides_has_no_effect(nv, bound, dim, group, rows, past, window, sinks):
+    """NaN codes in places that no row sees, and blocks that none sees missing from the table: the outputs' bytes do not
+    change.  A NaN that some rows see reaches those rows, and no other."""
+    length = past + rows
+    pool = Pool(nv, 284, 2, dim, [length])
+    q = normal(gen(285), rows, 2 * group, dim)
+    call = lambda: nv.kv_attention(q.cuda(), pool.gpu, i32([0, rows]), pool.lens, pool.tab, causal_block=1,  # noqa: E731
+                                   max_len=bound, window=window, sinks=sinks)
+    clean = call()
+    seen = np.stack([step_ref.visible(past + i, length, 1, window, sinks) for i in range(rows)])
+    ever = np.concatenate([seen.any(0), np.zeros(-length % BLOCK, bool)])
+    for kind in range(2):
+        for at in range(len(ever) // BLOCK):
+            hidden = ~ever[at * BLOCK:(at + 1) * BLOCK]
+            pool.ref.codes[kind][pool.table[0, at]][:, pool.ref.off[kind][hidden]] = 0x7F
+    pool.push()
+    for at in range(len(ever) // BLOCK):
+        if not ever[at * BLOCK:(at + 1) * BLOCK].any():
+            pool.tab[0, at] = -3 if at % 2 else 2**31 - 1
+    assert same(call(), clean)
+    r = random.Random(past)
+    for at in {past, length - 1, max(0, past - window), past + rows // 2, max(0, past + 1 - window + rows // 2), 0,
+               max(0, sinks - 1), sinks, r.randrange(length)}:
+        for kind in range(2):
+            if not seen[:, at].any():
+                continue
+            place = pool.table[0, at // BLOCK], 1, pool.ref.off[kind][at % BLOCK, 3]
+            was = pool.ref.codes[kind][place]
+            pool.ref.codes[kind][place] = 0xFF
+            pool.push()
+            got, nan = call().cpu(), torch.zeros(q.shape, dtype=torch.bool)
+            i = torch.from_numpy(seen[:, at].nonzero()[0])
+            if kind == 0:
+                nan[i, group:] = True
+            else:
+                nan[i, group:, 3] = True
+            assert torch.equal(got.isnan(), nan), (at, kind)
+            assert np.array_equal(bits(got)[~nan.numpy()], bits(clean)[~nan.numpy()])
+            pool.ref.codes[kind][place] = was
+    pool.push()
+    # a block that some rows see is missing: those rows are NaN, the others as they were
+    at = min(length - 1, past + rows // 2) // BLOCK
+    pool.tab[0, at] = -1
+    nan = torch.from_numpy(seen[:, at * BLOCK:(at + 1) * BLOCK].any(1))
+    got = call().cpu()
+    assert torch.equal(got.isnan(), nan[:, None, None].expand_as(got))
+    assert same(got[~nan], clean.cpu()[~nan])
+
+
+@BOUND
+@pytest.mark.parametrize("rows", [1, 40, 300])
+def test_window_rows_that_see_nothing(nv, bound, rows):
+    """Sequences of no positions, rows before position 0, a length that the table cannot hold, rows of no sequence."""
+    pool = Pool(nv, 286, 1, 64, [0, 5, 70, 64])
+    rs = [2, 2 + rows, 2 + 2 * rows, 2 + 3 * rows, 2 + 4 * rows]
+    lens = [0, 5, 70, 10**6]
+    q = normal(gen(287), rs[-1] + 3, 2, 64)
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    nv.kv_attention(q.cuda(), pool.gpu, i32(rs), i32(lens), pool.tab, causal_block=1, out=out, window=20, sinks=3, max_len=bound)
+    want, tol = step_ref.attention(q.double().numpy(), pool.ref, rs, lens, pool.table, np.float64(np.float32(0.125)), 1, 20, 3)
+    inside = slice(rs[0], rs[-1])
+    check(out[inside], want[inside], tol[inside])
+    assert bool((out[:rs[0]] == 5).all()) and bool((out[rs[-1]:] == 5).all())
+    assert bool((out[rs[0]:rs[1]] == 0).all()) and bool(out[rs[3]:rs[4]].isnan().all())
+
+
+# ---------------------------------------------------------------------------
+# attention over a shared prefix
+# ---------------------------------------------------------------------------
+SHARED = [
+    # dim, kv heads, group, causal block, prefix blocks, [(past behind the prefix, new)]
+    (64, 1, 1, 1, 1, [(0, 1)]),
+    (128, 1, 1, 1, 1, [(63, 1), (64, 1)]),
+    (128, 2, 4, 1, 3, [(16, 1), (0, 1), (100, 1), (5, 1)]),
+    (64, 3, 1, 1, 7, [(0, 1), (64, 1), (0, 0), (65, 3), (200, 1)]),
+    (64, 2, 8, 1, 2, [(100, 3), (10, 2), (0, 3), (5, 0), (0, 9)]),
+    (128, 2, 3, 1, 5, [(0, 65), (17, 100)]),
+    (64, 2, 2, 0, 4, [(40, 90), (0, 29)]),
+    (128, 1, 4, 16, 2, [(5, 60), (64, 48)]),
+    (64, 1, 40, 1, 3, [(70, 3)]),
+    (128, 1, 1, 1, 50, [(300, 1), (0, 1)]),
+    (128, 8, 1, 1, 3, [(0, 30), (77, 30), (0, 0), (50, 65)]),
+    (64, 2, 2, 1, 40, [(i % 9, 1 + i % 2) for i in range(70)]),
+]
+
+
+def shared_pool(nv, seed, heads, dim, blocks, seqs):
+    """A pool whose sequences begin with the first one's blocks; the other tables name none there."""
+    pool = Pool(nv, seed, heads, dim, [blocks * BLOCK + p + n for p, n in seqs])
+    common = pool.table[0, :blocks].copy()
+    pool.table[:, :blocks] = -9
+    pool.tab = i32(pool.table.tolist())
+    return pool, common
+
+
+@BOUND
+@pytest.mark.parametrize("case", range(len(SHARED)))
+def test_shared_prefix(nv, case, bound):
+    dim, heads, group, c, blocks, seqs = SHARED[case]
+    news = [n for _, n in seqs]
+    pool, common = shared_pool(nv, 300 + case, heads, dim, blocks, seqs)
+    q = normal(gen(310 + case), sum(news) + 5, heads * group, dim, sigma=1.0 + case % 3)
+    rs = [3 + r for r in starts(news)]
+    want, tol = step_ref.attention(q.double().numpy(), pool.ref, rs, pool.lens.tolist(), pool.table,
+                                   np.float64(np.float32(dim ** -0.5)), c, shared=common)
+    inside = slice(rs[0], rs[-1])
+    call = lambda x, **kw: nv.kv_attention(x, pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=c, max_len=bound,  # noqa: E731
+                                           shared=i32(common.tolist()), **kw)
+    for layout in ("plain", "qkv", "heads"):
+        got = call(strided(q, layout), out=torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda"))
+        check(got[inside], want[inside], tol[inside])
+        assert bool((got[:rs[0]] == 5).all()) and bool((got[rs[-1]:] == 5).all())
+    out = strided(torch.zeros_like(q), "heads")
+    call(q.cuda(), out=out)
+    assert same(out[inside], got[inside])
+    inplace = q.cuda()
+    call(inplace, out=inplace)
+    assert same(inplace[inside], got[inside]) and same(inplace[:3], q[:3]) and same(inplace[-2:], q[-2:])
+
+
+@BOUND
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("blocks,rows,count", [(100, 1, 9), (33, 3, 40), (300, 1, 1), (130, 40, 5)])
+def test_a_longer_shared_prefix(nv, bound, dim, blocks, rows, count):
+    """Against the sequences' own tables that name the same blocks: one softmax, whatever the pieces."""
+    seqs = [(7 * i % 150, rows) for i in range(count)]
+    pool, common = shared_pool(nv, 330, 2, dim, blocks, seqs)
+    q = normal(gen(331), rows * count, 8, dim).cuda()
+    rs = i32(starts([rows] * count))
+    got = nv.kv_attention(q, pool.gpu, rs, pool.lens, pool.tab, causal_block=1, max_len=bound, shared=i32(common.tolist()))
+    pool.tab[:, :blocks] = i32(common.tolist())
+    want = nv.kv_attention(q, pool.gpu, rs, pool.lens, pool.tab, causal_block=1).double()
+    # each is one rounding of bf16 probabilities (2^-8 of the sums of p |v|, values of order 1) and one of the output
+    assert float((got.double() - want).abs().max()) <= 2 * (2.0 ** -8 + 2.0 ** -8) * float(want.abs().max().clamp(min=1))
+
+
+@BOUND
+def test_shared_prefix_errors_of_single_sequences(nv, bound):
+    """A sequence whose rows begin inside the prefix, whose length the table cannot hold, or one of whose own blocks is
+    missing is NaN, the others as they were; a missing or NaN block of the prefix reaches every row that there is."""
+    seqs = [(10, 2), (70, 3), (0, 1), (30, 40)]
+    pool, common = shared_pool(nv, 340, 2, 128, 4, seqs)
+    q = normal(gen(341), 46, 4, 128).cuda()
+    rs, shared = i32([0, 2, 5, 6, 46]), i32(common.tolist())
+    call = lambda lens, tab, sh: nv.kv_attention(q, pool.gpu, rs, lens, tab, causal_block=1, max_len=bound, shared=sh).cpu()  # noqa: E731
+    clean = call(pool.lens, pool.tab, shared)
+    assert bool(clean.isfinite().all())
+    for b, length in ((0, 257), (1, 10**6), (2, 0), (1, 258), (3, 255), (3, -1)):
+        lens = pool.lens.clone()
+        lens[b] = length
+        got = call(lens, pool.tab, shared)
+        rows = torch.zeros(46, dtype=torch.bool)
+        rows[int(rs[b]):int(rs[b + 1])] = True
+        assert bool(got[rows].isnan().all()) and same(got[~rows], clean[~rows])
+    tab = pool.tab.clone()
+    tab[1, 5] = -1
+    got = call(pool.lens, tab, shared)
+    assert bool(got[2:5].isnan().all())  # position 70 and on: the block of positions 64 .. 127 behind the prefix
+    assert same(got[:2], clean[:2]) and same(got[5:], clean[5:])
+    for bad in (-1, 10**6):
+        assert bool(call(pool.lens, pool.tab, i32([common[0], bad, common[2], common[3]])).isnan().all())
+    pool.ref.codes[1][common[2], 1, pool.ref.off[1][5, 9]] = 0x7F
+    pool.push()
+    got = call(pool.lens, pool.tab, shared)
+    nan = torch.zeros_like(got, dtype=torch.bool)
+    nan[:, 2:, 9] = True
+    assert torch.equal(got.isnan(), nan) and same(got[~nan], clean[~nan])
+
+
+def test_shared_prefix_with_rows_that_make_no_sense_stays_in_bounds(nv):
+    pool, common = shared_pool(nv, 342, 1, 64, 2, [(10, 2), (70, 3)])
+    q = normal(gen(343), 60, 2, 64).cuda()
+    for rs in ([5, 2, 9], [-3, 40, 2000], [0, 0, 0], [60, 60, 60], [2**31 - 1, -2**31, 7], [40, 50, 45]):
+        for bound in (None, 0, 1 << 20):
+            nv.kv_attention(q, pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1, max_len=bound, shared=i32(common.tolist()))
+            nv.kv_attention(q, pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1, max_len=bound, window=9, sinks=2)
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+class Serving:
+    """A few requests over one pool: what a program keeps from step to step, and one step of it."""
+
+    def __init__(self, nv, shared_blocks=0):
+        self.nv, self.count, self.heads, self.dim, self.rows, self.pool = nv, 5, 2, 128, 130, 64
+        self.cache = nv.KvCache.empty(self.pool, self.heads, self.dim)
+        self.table = torch.full((self.count, 12), -1, dtype=torch.int32, device="cuda")
+        self.shared = i32(list(range(shared_blocks))) if shared_blocks else None
+        self.keep = shared_blocks
+        if shared_blocks:
+            g = gen(77)
+            n = shared_blocks * BLOCK
+            k, v = normal(g, n, self.heads, self.dim).cuda(), normal(g, n, self.heads, self.dim).cuda()
+            nv.kv_write(self.cache, k, v, i32([0, n]), i32([n]), self.shared[None])
+            self.table[:, :shared_blocks] = self.shared
+        self.lens = i32([shared_blocks * BLOCK] * self.count)
+        self.free = i32(list(range(shared_blocks, self.pool)))
+        self.n_free = i32([self.pool - shared_blocks])
+        self.step_arrays = nv.KvStep.empty(self.count, self.rows)
+        self.step_arrays.lens, self.step_arrays.free_count = self.lens, self.n_free
+        self.tables = [nv.rope_table(2048, 64)]
+        g = gen(78)
+        self.weights = [(1 + normal(g, self.dim, sigma=0.1).float()).bfloat16().cuda() for _ in range(2)]
+        self.more, self.done = i32([0] * self.count), i32([0] * self.count)
+        self.base = i32([shared_blocks * BLOCK] * self.count)
+        self.x = torch.zeros(self.rows, 12, self.dim, dtype=torch.bfloat16, device="cuda")
+
+    def step(self):
+        nv, h = self.nv, self.heads
+        nv.kv_release(self.lens, self.done, self.table, self.free, self.n_free, keep=self.keep, lens_out=self.lens,
+                      free_count_out=self.n_free)
+        torch.maximum(self.lens, self.base, out=self.lens)  # a new request begins behind the prefix
+        s = nv.kv_extend(self.lens, self.more, self.table, self.free, self.n_free, self.step_arrays)
+        q, k = nv.norm_rope(self.x[:, :4 * h], self.x[:, 4 * h:5 * h], *self.weights, tables=self.tables, positions=s.positions,
+                            split=True)
+        nv.kv_write(self.cache, k, self.x[:, 5 * h:], s.row_start, s.lens, self.table)
+        if self.shared is not None:
+            o = nv.kv_attention(q, self.cache, s.row_start, s.lens, self.table, causal_block=1, shared=self.shared)
+        else:
+            o = nv.kv_attention(q, self.cache, s.row_start, s.lens, self.table, causal_block=1, window=100, sinks=4)
+        self.o = o
+        return nv.quantize(o.reshape(self.rows, -1))
+
+
+@pytest.mark.parametrize("shared", [0, 3])
+def test_a_serving_step_eager_and_captured(nv, shared):
+    """Release, extend, norms and rotation, cache, attention, quantizer: eager steps against the references, and the same
+    step captured once and replayed with new inputs, eager work between: every replay equals the eager step."""
+    eager, captured = Serving(nv, shared), Serving(nv, shared)
+    side = torch.cuda.Stream()
+    Serving(nv, shared).step()  # what a first call sets up stays out of the capture
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        graph_out = captured.step()
+    r, g = random.Random(shared), gen(79)
+    ref = kv_ref.Cache(eager.pool, eager.heads, eager.dim)
+    for c, t in zip(ref.codes + ref.powers, (eager.cache.k, eager.cache.v, eager.cache.k_power, eager.cache.v_power)):
+        c[:] = t.cpu().numpy().reshape(c.shape)
+    lens = [shared * BLOCK] * 5
+    table, stack = eager.table.tolist(), eager.free.tolist()
+    tables = [t.cpu() for t in eager.tables]
+    weights = [w.cpu() for w in eager.weights]
+    for turn in range(6):
+        x = normal(g, eager.rows, 12, eager.dim)
+        done = [int(turn > 1 and r.random() < 0.3) for _ in range(5)]
+        more = [r.choice([1, 1, 20, 40, 0]) for _ in range(5)]
+        for s in (eager, captured):
+            s.x.copy_(x), s.done.copy_(i32(done)), s.more.copy_(i32(more))
+        out = [t.clone() for t in eager.step()]
+        graph.replay()
+        torch.cuda.synchronize()
+        now = step_ref.release(lens, done, table, stack, shared, eager.pool - shared)
+        now = [max(n, shared * BLOCK) for n in now]
+        want = step_ref.extend(now, more, table, stack, eager.rows)
+        lens, rs = want["lens"], want["row_start"]
+        assert eager.lens.tolist() == lens and eager.table.tolist() == table and eager.n_free.tolist() == [len(stack)]
+        used = rs[-1]
+        positions = torch.tensor(want["positions"], dtype=torch.int32)[:, None]
+        q, k = (step_ref.norm_rope(x[:used, a:b], w, 1e-6, tables, positions[:used], True)[0]
+                for a, b, w in ((0, 8, weights[0]), (8, 10, weights[1])))
+        # what the kernels themselves made of the rows goes on: the cache as it stands, the queries as they were rounded
+        for c, t in zip(ref.codes + ref.powers, (eager.cache.k, eager.cache.v, eager.cache.k_power, eager.cache.v_power)):
+            c[:] = t.cpu().numpy().reshape(c.shape)
+        made = nv.norm_rope(eager.x[:, :8], None, eager.weights[0], tables=eager.tables, positions=eager.step_arrays.positions,
+                            split=True).cpu()
+        assert float((made[:used].double() - q).abs().max()) <= 2.0 ** -8 * float(q.abs().max()) * 1.01
+        for b in range(5):  # keys in the cache: 8-bit codes of the normed ones (2^-4 of the value, 2^-10 of the block's largest)
+            for h in range(2):
+                held = ref.sequence(0, h, np.array(table[b]), lens[b])[lens[b] - (rs[b + 1] - rs[b]):]
+                mine = k[rs[b]:rs[b + 1], h].numpy()
+                if len(mine):
+                    assert np.all(np.abs(held - mine) <= 2.0 ** -3 * np.abs(mine) + 2.0 ** -8 * np.abs(k).max().item())
+        o, tol = step_ref.attention(made.double().numpy(), ref, rs, lens, np.array(table), np.float64(np.float32(128 ** -0.5)), 1,
+                                    *((0, 0) if shared else (100, 4)), shared=np.arange(shared) if shared else None)
+        check(eager.o[:used], o[:used], tol[:used])
+        assert all(a.shape == b.shape for a, b in zip(out, graph_out))
+        assert same(eager.o[:used], captured.o[:used]), f"replay {turn}"
+        for name in ("lens", "table", "n_free", "free"):
+            assert torch.equal(getattr(eager, name), getattr(captured, name)), name
+        for a, b in ((eager.cache.k, captured.cache.k), (eager.cache.v, captured.cache.v)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kw", [dict(window=200, sinks=5), "shared"])
+def test_other_streams_and_the_same_bytes(nv, kw):
+    """Calls on side streams, two at once with workspaces of their own, equal the calls on the main one."""
+    pool, common = shared_pool(nv, 350, 2, 128, 20, [(700, 1), (50, 1)])
+    if kw == "shared":
+        kw = dict(shared=i32(common.tolist()))
+    else:
+        pool.tab[:, :20] = i32(common.tolist())
+    q = normal(gen(351), 2, 8, 128).cuda()
+    rs = i32([0, 1, 2])
+    want = nv.kv_attention(q, pool.gpu, rs, pool.lens, pool.tab, causal_block=1, **kw)
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for s in side:
+            got.append(nv.kv_attention(q, pool.gpu, rs, pool.lens, pool.tab, causal_block=1, stream=s, **kw))
+    for s in side:
+        s.synchronize()
+    for o in got:
+        assert same(o, want)
