@@ -250,6 +250,7 @@ struct Softmax {
 
 // Probabilities of a tile of 32 keys in bf16, the second operands of two
 // k-steps of the products with the values, and their sum.
+template <int MODE>
 __device__ __forceinline__ float probabilities(const f32x16& s, float scale_log2, float ref, bf16x8 (&p)[2]) {
     float sum[2];
 #pragma unroll
@@ -263,7 +264,18 @@ __device__ __forceinline__ float probabilities(const f32x16& s, float scale_log2
             part[i] = x + y;
             w[i] = pack_bf16x2(x, y);
         }
-        sum[k] = (part[0] + part[1]) + (part[2] + part[3]);
+        if constexpr (MODE == PLAIN) {
+            sum[k] = (part[0] + part[1]) + (part[2] + part[3]);
+        } else {
+            // what the products take is what is summed: where a few keys have most
+            // of the weight, their roundings then cancel in the quotient (a key
+            // alone gives its value exactly).  Two at an instruction
+            sum[k] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sum[k] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[i]),
+                                                         __builtin_bit_cast(bf16x2, 0x3F803F80u), sum[k], false);
+        }
         p[k] = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
     }
     return sum[0] + sum[1];
@@ -275,7 +287,7 @@ __device__ __forceinline__ float probabilities(const f32x16& s, float scale_log2
 // is there anyway, tells when the reference is too low (more than kMost, or
 // infinite, or NaN for the first tile, whose reference is -inf).  p and the sums
 // are floating-point numbers: a reference below the maximum costs no precision.
-template <int NO>
+template <int MODE, int NO>
 __device__ __forceinline__ void accept(const f32x16& s, float scale_log2, float sum, Softmax& st, f32x16 (&o)[NO],
                                        bf16x8 (&p)[2]) {
     const uint64_t over = __ballot(!(sum <= kMost));
@@ -296,7 +308,7 @@ __device__ __forceinline__ void accept(const f32x16& s, float scale_log2, float 
         for (int d = 0; d < NO; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] *= alpha;
-        sum = probabilities(s, scale_log2, m == neg_inf() ? 0.0f : m, p);  // nothing seen yet: all 0
+        sum = probabilities<MODE>(s, scale_log2, m == neg_inf() ? 0.0f : m, p);  // nothing seen yet: all 0
     }
     st.l += sum;
 }
@@ -539,8 +551,8 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
             bf16x8 p[2];
-            const float sum = probabilities(s[tt], a.scale_log2, st.m, p);
-            accept<kDT>(s[tt], a.scale_log2, sum, st, o, p);
+            const float sum = probabilities<MODE>(s[tt], a.scale_log2, st.m, p);
+            accept<MODE, kDT>(s[tt], a.scale_log2, sum, st, o, p);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -838,19 +850,19 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
             __builtin_amdgcn_sched_barrier(0);
             if (edge) mask_tile<MODE>(s[0], a, row, first_key);
             scores(1);
-            const float sum0 = probabilities(s[0], a.scale_log2, st.m, p0);
+            const float sum0 = probabilities<MODE>(s[0], a.scale_log2, st.m, p0);
             values(1);
             alternate<2 * kK, 56>();
             asm volatile("" : "+v"(s[1]));  // issued here, not after the branch below
-            accept<kDT>(s[0], a.scale_log2, sum0, st, o, p0);
+            accept<MODE, kDT>(s[0], a.scale_log2, sum0, st, o, p0);
             if (edge) mask_tile<MODE>(s[1], a, row, first_key + 32);
             multiply(0, p0[0]);
             values(2);
             multiply(1, p0[1]);
-            const float sum1 = probabilities(s[1], a.scale_log2, st.m, p1);
+            const float sum1 = probabilities<MODE>(s[1], a.scale_log2, st.m, p1);
             values(3);
             alternate<2 * kDT, 56>();
-            accept<kDT>(s[1], a.scale_log2, sum1, st, o, p1);
+            accept<MODE, kDT>(s[1], a.scale_log2, sum1, st, o, p1);
             multiply(2, p1[0]);
             multiply(3, p1[1]);
         }

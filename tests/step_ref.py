@@ -78,7 +78,9 @@ def visible(pos, length, causal, window, sinks, columns=None):
 
 def attention(q, cache, row_start, lens, table, scale, c, window=0, sinks=0, shared=None):
     """out [M, heads, dim] in 64 bits (NaN in rows of no sequence), and the largest error that the kernel's own roundings
-    allow each element: kv_ref.attention's bound, over the keys that a row sees."""
+    allow each element: kv_ref.attention's bound, over the keys that a row sees.  But through a window or over a prefix
+    the rounded p are summed, so that with p' = p (1 + d), |d| <= 2^-8, the quotient is off by sum p d (v - o) / sum p',
+    at most 2^-8 / (1 - 2^-8) of sum p |v - o| / sum p <= a + |o|: 1.01 * 2^-8 |o| more than with the exact sum."""
     M, Hq, D = q.shape
     G = Hq // cache.heads
     out = np.full((M, Hq, D), np.nan)
@@ -111,5 +113,6 @@ def attention(q, cache, row_start, lens, table, scale, c, window=0, sinks=0, sha
                 ds = ds + 4 * 2.0 ** -24 * (2 * np.abs(np.where(seen, s, 0)).max(1, keepdims=True, initial=0) + 16) + \
                     (length + 64) * 2.0 ** -24
             out[rows, g] = np.where(poison, np.nan, o)
-            tol[rows, g] = (2.0 ** -8 + 2 * ds) * a + 2.0 ** -8 * (np.abs(o) + (2.0 ** -8 + 2 * ds) * a) + 1e-38
+            before = (1.01 * 2.0 ** -8 + 2 * ds) * a + 1.01 * 2.0 ** -8 * np.abs(o)
+            tol[rows, g] = before + 2.0 ** -8 * (np.abs(o) + before) + 1e-38
     return out, tol
