@@ -21,8 +21,6 @@
 // of their size, where binary32 probabilities and the output's own rounding give
 // 0.0016 to 0.0017.  Scores, maxima, sums and outputs are held in
 // binary32.
-#include <type_traits>
-
 #include "kv_device.h"
 
 namespace nvfp4 {
@@ -328,16 +326,21 @@ __device__ __forceinline__ void mask_scores(f32x16& s, int32_t left) {
 }
 
 // WINDOW: and so do those before its window that are not among the first
-// positions.  low, sinks: counted from the tile's first key too.
-__device__ __forceinline__ void mask_window(f32x16& s, int32_t left, int32_t low, int32_t sinks) {
-    const int h = 4 * (int)((threadIdx.x & 63) >> 5);
-    const int last = left - h, from = sinks - h, to = low - h;
+// positions.  Bit k: whether the row sees the tile's key k.
+__device__ __forceinline__ void mask_window(f32x16& s, uint32_t visible) {
+    visible >>= 4 * ((threadIdx.x & 63) >> 5);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int k = 8 * (i / 4) + i % 4;
-        if (k >= last || (k < to && k >= from)) s[i] = neg_inf();
-    }
+    for (int i = 0; i < 16; ++i) s[i] = visible & (1u << (8 * (i / 4) + i % 4)) ? s[i] : neg_inf();
 }
+// Of tile t of the 64 keys from first_key.
+template <int MODE>
+__device__ __forceinline__ void mask_tile(f32x16& s, const AttentionArgs& a, const Row& r, int32_t first_key, int t) {
+    if constexpr (MODE == WINDOW)
+        mask_window(s, (uint32_t)(window_bits(a, r, first_key) >> (32 * t)));
+    else
+        mask_scores(s, r.limit - first_key - 32 * t);
+}
+
 // 1 in each byte that is one of E4M3's NaN codes, as bf16 ones for the products,
 // and a one for each key that is not masked.
 __device__ __forceinline__ uint32_t fp8_nan_bytes(uint32_t w) {
@@ -354,14 +357,6 @@ __device__ __forceinline__ bf16x8 seen_ones(const f32x16& s, int k) {
     for (int i = 0; i < 4; ++i)
         w[i] = (s[8 * k + 2 * i] != neg_inf() ? 0x3F80u : 0u) | (s[8 * k + 2 * i + 1] != neg_inf() ? 0x3F800000u : 0u);
     return __builtin_bit_cast(bf16x8, w);
-}
-
-template <int MODE>
-__device__ __forceinline__ void mask_tile(f32x16& s, const AttentionArgs& a, const Row& r, int32_t first_key) {
-    if constexpr (MODE == WINDOW)
-        mask_window(s, r.limit - first_key, r.low - first_key, a.sinks - first_key);
-    else
-        mask_scores(s, r.limit - first_key);
 }
 
 // ---------------------------------------------------------------------------
@@ -483,8 +478,8 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
         const int first_key = blocks[at] * kKvBlock;
         const bool edge = first_key + kKvBlock > all || (MODE == WINDOW && window_hides(a, first_key, low_last));
         if (edge) {
-            mask_tile<MODE>(s[0], a, row, first_key);
-            mask_tile<MODE>(s[1], a, row, first_key + 32);
+            mask_tile<MODE>(s[0], a, row, first_key, 0);
+            mask_tile<MODE>(s[1], a, row, first_key, 1);
         }
         if (edge) {
             // A masked key has p = 0, but 0 times a NaN value is NaN: NaN codes
@@ -496,9 +491,10 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
                 for (int u = 0; u < 2; ++u)
                     nan |= fp8_any_nan(vf[d][u].x) || fp8_any_nan(vf[d][u].y) || fp8_any_nan(vf[d][u].z) ||
                            fp8_any_nan(vf[d][u].w);
-            if (MODE == WINDOW && __any(nan)) {
-                // what a row sees is not all keys below a limit: which of them it
-                // sees, times which are NaN, tells it
+            if (!__any(nan)) {
+                // as almost always
+            } else if constexpr (MODE != PLAIN) {
+                // which keys a row sees, times which are NaN, tells it
 #pragma unroll
                 for (int d = 0; d < kDT; ++d) {
                     f32x16 hit = f32x16{};
@@ -518,7 +514,7 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[d][i] = hit[i] > 0.0f ? quiet_nan() : o[d][i];
                 }
-            } else if (__any(nan)) {
+            } else {
                 int half = h;  // opaque: nothing of this rare path is worth registers in the loop
                 asm volatile("" : "+v"(half));
 #pragma unroll
@@ -677,10 +673,11 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     constexpr int kEach = kPieces / kThreads;             // of them a thread's
     __shared__ __align__(16) u32x4 sk[2][kPieces];
     __shared__ __align__(16) u32x4 sv[2][2 * kPieces];    // [k-step][half][dim] of 8 keys
-    // by dim, the first key whose value is a NaN code; WINDOW: the bits of all of them
-    using Mark = std::conditional_t<MODE == WINDOW, unsigned long long, int>;
-    constexpr Mark kNoMark = MODE == WINDOW ? 0 : kKvBlock;
-    __shared__ Mark nan_key[2][D];
+    // by dim, which keys' values are NaN codes: PLAIN the first of them, else the
+    // bits of all, [half of the block][dim]
+    constexpr int kMarks = MODE == PLAIN ? 1 : 2;
+    constexpr int kNoMark = MODE == PLAIN ? kKvBlock : 0;
+    __shared__ int nan_key[2][kMarks * D];
     __shared__ int nan_any[2];
     int unit, kv_head;
     wide_place(a, unit, kv_head);
@@ -715,7 +712,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
 
     u32x4 qw[D / 16];
     fetch_query<D>(qw, a, row);
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) nan_key[i / D][i % D] = kNoMark;
+    for (int i = threadIdx.x; i < 2 * kMarks * D; i += kThreads) nan_key[i / (kMarks * D)][i % (kMarks * D)] = kNoMark;
     if (threadIdx.x < 2) nan_any[threadIdx.x] = 0;
 
     // table entries and powers are looked at a block after they are asked for,
@@ -753,23 +750,29 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
             if (edge && (fp8_any_nan(w.x) || fp8_any_nan(w.y) || fp8_any_nan(w.z) || fp8_any_nan(w.w))) {
                 // as in the narrow kernel: NaN codes are taken out, and given
                 // back to the rows that see their key
-                uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                Mark mark = kNoMark;
+                if constexpr (MODE != PLAIN) {
+                    // dword i holds keys 8i + 4 (piece % 2) .. + 3 of half piece / 2
+                    uint32_t mark = 0;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (((x[j / 4] >> (8 * (j % 4))) & 0x7Fu) == 0x7Fu) {
-                        const int key = 32 * (piece / 2) + 16 * (j / 8) + 8 * (j / 4 % 2) + 4 * (piece % 2) + j % 4;
-                        if constexpr (MODE == WINDOW)
-                            mark |= (Mark)1 << key;
-                        else
-                            mark = key < mark ? key : mark;
-                        x[j / 4] &= ~(0xFFu << (8 * (j % 4)));
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t nans = fp8_nan_bytes(w[j]);
+                        w[j] &= ~(nans * 0xFFu);
+                        mark |= ((nans | nans >> 7 | nans >> 14 | nans >> 21) & 0xFu) << (8 * j);
                     }
-                w = u32x4{x[0], x[1], x[2], x[3]};
-                if constexpr (MODE == WINDOW)
-                    atomicOr(&nan_key[buffer][d], mark);
-                else
-                    atomicMin(&nan_key[buffer][d], mark);
+                    atomicOr(&nan_key[buffer][(piece / 2) * D + d], (int)(mark << (4 * (piece % 2))));
+                } else {
+                    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                    int lowest = kKvBlock;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (((x[j / 4] >> (8 * (j % 4))) & 0x7Fu) == 0x7Fu) {
+                            const int key = 32 * (piece / 2) + 16 * (j / 8) + 8 * (j / 4 % 2) + 4 * (piece % 2) + j % 4;
+                            lowest = key < lowest ? key : lowest;
+                            x[j / 4] &= ~(0xFFu << (8 * (j % 4)));
+                        }
+                    w = u32x4{x[0], x[1], x[2], x[3]};
+                    atomicMin(&nan_key[buffer][d], lowest);
+                }
                 nan_any[buffer] = 1;
             }
             sk[buffer][at] = kr[i];
@@ -848,14 +851,14 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
             scores(0);
             values(0);
             __builtin_amdgcn_sched_barrier(0);
-            if (edge) mask_tile<MODE>(s[0], a, row, first_key);
+            if (edge) mask_tile<MODE>(s[0], a, row, first_key, 0);
             scores(1);
             const float sum0 = probabilities<MODE>(s[0], a.scale_log2, st.m, p0);
             values(1);
             alternate<2 * kK, 56>();
             asm volatile("" : "+v"(s[1]));  // issued here, not after the branch below
             accept<MODE, kDT>(s[0], a.scale_log2, sum0, st, o, p0);
-            if (edge) mask_tile<MODE>(s[1], a, row, first_key + 32);
+            if (edge) mask_tile<MODE>(s[1], a, row, first_key, 1);
             multiply(0, p0[0]);
             values(2);
             multiply(1, p0[1]);
@@ -870,20 +873,24 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
             if (sees(first_key)) {
                 int half = h;
                 asm volatile("" : "+v"(half));
+                const uint64_t visible = MODE == PLAIN ? 0 : window_bits(a, row, first_key);
 #pragma unroll
                 for (int d = 0; d < kDT; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const Mark key = nan_key[b][32 * d + 8 * (i / 4) + 4 * half + i % 4];
-                        if constexpr (MODE == WINDOW) {
-                            if (key & window_bits(a, row, first_key)) o[d][i] = quiet_nan();
+                        const int at_dim = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+                        const int key = nan_key[b][at_dim];
+                        if constexpr (MODE != PLAIN) {
+                            const uint32_t hit = ((uint32_t)key & (uint32_t)visible) |
+                                                 ((uint32_t)nan_key[b][(kMarks - 1) * D + at_dim] & (uint32_t)(visible >> 32));
+                            if (hit) o[d][i] = quiet_nan();
                         } else {
                             if (key < kKvBlock && key < row.limit - first_key) o[d][i] = quiet_nan();
                         }
                     }
             }
             __syncthreads();
-            for (int i = threadIdx.x; i < D; i += kThreads) nan_key[b][i] = kNoMark;
+            for (int i = threadIdx.x; i < kMarks * D; i += kThreads) nan_key[b][i] = kNoMark;
             if (threadIdx.x == 0) nan_any[b] = 0;
         }
         if (more) {
