@@ -538,7 +538,8 @@ nvfp4_status nvfp4_norm_rope(const nvfp4_heads* q, int32_t q_heads, const uint16
 /* The block tables of `count` requests and a stack of the pool's free blocks,
  * DEVICE int32.  table[b][j] is request b's cache block of positions 64 j .. 64 j +
  * 63 (row stride ld_table >= table_blocks); the stack's top is free_blocks[n - 1]
- * where n, at most `capacity`, is held apart.  1 <= count <= 2^20. */
+ * where n, at most `capacity`, is held apart.  1 <= count <= 2^20; 1 <= capacity <=
+ * 2^30. */
 typedef struct {
     int64_t count;
     int32_t* table;
@@ -577,7 +578,8 @@ nvfp4_status nvfp4_kv_extend(const nvfp4_kv_tables* tables, const int32_t* past,
  * the other lengths are copied.  *free_left is the stack's size after it.  The table
  * stays as it is.  keep: the first entries of every table that are not the request's
  * own (a shared prefix).  lens_out may be lens and free_left may be free_count.  The
- * workspace needs nvfp4_kv_release_workspace_bytes(count) bytes (16-byte aligned). */
+ * workspace needs nvfp4_kv_release_workspace_bytes(count) bytes (16-byte aligned; may
+ * be NULL when that is 0). */
 size_t nvfp4_kv_release_workspace_bytes(int64_t count);
 nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens, const int32_t* done, int64_t keep,
                               const int32_t* free_count, int32_t* lens_out, int32_t* free_left, void* workspace,

@@ -942,7 +942,7 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
     if shared is not None:
         if window:
             raise ValueError("a window and a shared prefix in one call")
-        _int32s(dev, shared=(shared, None))
+        _int32("shared", shared, None, dev)
         name, fn, size_of = "nvfp4_kv_attention_shared", lib.nvfp4_kv_attention_shared, \
             lib.nvfp4_kv_attention_shared_workspace_bytes
         sizes, args = (shared.shape[0], max_len), (shared.data_ptr(), shared.shape[0], scale, causal_block, max_len)
@@ -970,17 +970,18 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
 # ---------------------------------------------------------------------------
 # the tables of a step, built on the GPU
 # ---------------------------------------------------------------------------
-def _int32s(dev: torch.device, **tensors):
-    """Checks int32 vectors on `dev`: name=(tensor, elements or None for any number)."""
-    for name, (t, n) in tensors.items():
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name}: expected int32, got {t.dtype}")
-        if t.dim() != 1 or (n is not None and t.shape[0] != n):
-            raise ValueError(f"{name}: expected {'a vector' if n is None else [n]}, got {list(t.shape)}")
-        if t.stride(0) != 1 and t.shape[0] > 1:
-            raise ValueError(f"{name} must have unit stride")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _int32(name: str, t: torch.Tensor, n: int | None, dev: torch.device) -> int:
+    """Where an int32 vector on `dev` of n elements (None: any number) lies, once checked."""
+    shape = t.shape
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name}: expected int32, got {t.dtype}")
+    if len(shape) != 1 or (n is not None and shape[0] != n):
+        raise ValueError(f"{name}: expected {'a vector' if n is None else [n]}, got {list(shape)}")
+    if t.stride(0) != 1 and shape[0] > 1:
+        raise ValueError(f"{name} must have unit stride")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return t.data_ptr()
 
 
 def make_kv_tables(table: torch.Tensor, free: torch.Tensor) -> KvTables:
@@ -990,32 +991,72 @@ def make_kv_tables(table: torch.Tensor, free: torch.Tensor) -> KvTables:
         raise TypeError(f"table: expected int32, got {table.dtype}")
     if table.dim() != 2:
         raise ValueError(f"table: expected [requests, blocks], got {list(table.shape)}")
-    _int32s(dev, free=(free, None))
     n, blocks = table.shape
     ld, unit = table.stride()
     if unit != 1 and blocks > 1:
         raise ValueError("table must have unit stride along its last dimension")
-    return KvTables(n, table.data_ptr(), ld if n > 1 else blocks, blocks, free.data_ptr(), free.shape[0])
+    return KvTables(n, table.data_ptr(), ld if n > 1 else blocks, blocks, _int32("free", free, None, dev), free.shape[0])
 
 
 class KvStep:
     """What kv_extend writes, for up to `rows` rows: row_start [requests + 1], lens [requests], free_count [1] and
-    missing [1], positions [rows, 1] (all int32) and slots [rows] (int64), as tensors that can serve step after step."""
+    missing [1], positions [rows, 1] (all int32) and slots [rows] (int64), contiguous tensors that can serve step after
+    step, and a workspace of nvfp4_kv_extend_workspace_bytes(requests) bytes."""
 
-    __slots__ = ("row_start", "lens", "free_count", "missing", "positions", "slots", "workspace")
+    def __init__(self, row_start: torch.Tensor, lens: torch.Tensor, free_count: torch.Tensor, missing: torch.Tensor,
+                 positions: torch.Tensor, slots: torch.Tensor, workspace: torch.Tensor):
+        self._tensors = row_start, lens, free_count, missing, positions, slots, workspace
+        self._describe()
 
-    def __init__(self, row_start, lens, free_count, missing, positions, slots, workspace):
-        self.row_start, self.lens, self.free_count, self.missing = row_start, lens, free_count, missing
-        self.positions, self.slots, self.workspace = positions, slots, workspace
+    def _describe(self):
+        row_start, lens, free_count, missing, positions, slots, workspace = self._tensors
+        dev, n = lens.device, lens.shape[0]
+        _int32("row_start", row_start, n + 1, dev)
+        _int32("lens", lens, n, dev)
+        _int32("free_count", free_count, 1, dev)
+        _int32("missing", missing, 1, dev)
+        rows = positions.shape[0]
+        if positions.shape != (rows, 1) or not positions.is_contiguous():
+            raise ValueError(f"positions: expected a contiguous [rows, 1], got {list(positions.shape)}")
+        _int32("positions", positions[:, 0], rows, dev)
+        if slots.dtype != torch.int64:
+            raise TypeError(f"slots: expected int64, got {slots.dtype}")
+        if slots.shape != (rows,) or not slots.is_contiguous():
+            raise ValueError(f"slots: expected a contiguous [{rows}], got {list(slots.shape)}")
+        _same_device(dev, slots, workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
+        self.device, self.requests, self.rows = dev, n, rows
+        self._size = workspace.numel() * workspace.element_size()
+        self._memory = tuple(t.data_ptr() for t in self._tensors)
+
+    @property
+    def memory(self) -> tuple:
+        """Where the tensors lie now."""
+        memory = tuple([t.data_ptr() for t in self._tensors])
+        if memory != self._memory:
+            self._describe()
+        return memory
+
+    row_start = property(lambda self: self._tensors[0])
+    lens = property(lambda self: self._tensors[1])
+    free_count = property(lambda self: self._tensors[2])
+    missing = property(lambda self: self._tensors[3])
+    positions = property(lambda self: self._tensors[4])
+    slots = property(lambda self: self._tensors[5])
+    workspace = property(lambda self: self._tensors[6])
 
     @classmethod
-    def empty(cls, requests: int, rows: int, device=None, stream=None) -> "KvStep":
+    def empty(cls, requests: int, rows: int, device=None, lens: torch.Tensor | None = None,
+              free_count: torch.Tensor | None = None, stream=None) -> "KvStep":
+        """New tensors for it on `device` (default: the current GPU).  For steps in place give the lengths, or the count of
+        free blocks, that kv_extend also takes."""
         dev = torch.device("cuda") if device is None else torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         make = lambda *shape: _empty(dev, stream, shape, torch.int32)  # noqa: E731
-        return cls(make(requests + 1), make(requests), make(1), make(1), make(rows, 1),
-                   _empty(dev, stream, (rows,), torch.int64),
+        return cls(make(requests + 1), make(requests) if lens is None else lens, make(1) if free_count is None else free_count,
+                   make(1), make(rows, 1), _empty(dev, stream, (rows,), torch.int64),
                    _empty(dev, stream, (nvfp4_kv_extend_workspace_bytes(requests),), torch.uint8))
 
 
@@ -1028,22 +1069,18 @@ def kv_extend(past: torch.Tensor, more: torch.Tensor, table: torch.Tensor, free:
     (in place; an entry is -1 where the stack is empty, and `missing` counts those).  step.row_start, step.lens, the
     table and step.positions are what kv_write, rope and kv_attention take; step.slots is each row's block * 64 +
     position % 64.  Rows of no request get -1 in both.  step.lens may be `past` and step.free_count `free_count`."""
-    dev = table.device
+    dev = step.device
     if dev.type != "cuda":
         raise ValueError(f"expected tensors on a GPU, got {dev}")
-    t = make_kv_tables(table, free)
-    n, rows = t.count, step.positions.shape[0]
-    _int32s(dev, past=(past, n), more=(more, n), free_count=(free_count, 1), row_start=(step.row_start, n + 1),
-            lens=(step.lens, n), left=(step.free_count, 1), missing=(step.missing, 1), positions=(step.positions.view(-1), rows))
-    slots, ws = step.slots, step.workspace
-    if slots.dtype != torch.int64 or slots.shape != (rows,) or not slots.is_contiguous():
-        raise ValueError(f"slots: expected a contiguous int64 [{rows}], got {slots.dtype} {list(slots.shape)}")
-    _same_device(dev, slots, ws)
-    if not ws.is_contiguous():
-        raise ValueError("the workspace must be contiguous")
-    _call("nvfp4_kv_extend", lib.nvfp4_kv_extend, dev, stream, t, past.data_ptr(), more.data_ptr(), free_count.data_ptr(),
-          rows, step.row_start.data_ptr(), step.lens.data_ptr(), step.free_count.data_ptr(), step.missing.data_ptr(),
-          step.positions.data_ptr(), slots.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    if table.device != dev:
+        raise ValueError(f"table is on {table.device}, expected {dev}")
+    t, n = make_kv_tables(table, free), step.requests
+    if t.count != n:
+        raise ValueError(f"a table of {t.count} requests, a step of {n}")
+    row_start, lens, left, missing, positions, slots, workspace = step.memory
+    _call("nvfp4_kv_extend", lib.nvfp4_kv_extend, dev, stream, t, _int32("past", past, n, dev), _int32("more", more, n, dev),
+          _int32("free_count", free_count, 1, dev), step.rows, row_start, lens, left, missing, positions, slots, workspace,
+          step._size)
     return step
 
 
@@ -1054,24 +1091,29 @@ def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free
     lengths, 0 for those, and the stack's size after it.
 
     keep: the first entries of every table that are not the request's own (a shared prefix).  The stack grows in place;
-    lens_out may be `lens` and free_count_out `free_count`."""
+    lens_out may be `lens` and free_count_out `free_count`.  A workspace of nvfp4_kv_release_workspace_bytes(requests)
+    bytes is allocated with torch when none is given, on the stream that the call runs on."""
     dev = table.device
     if dev.type != "cuda":
         raise ValueError(f"expected tensors on a GPU, got {dev}")
     t = make_kv_tables(table, free)
     n = t.count
+    if not 0 <= keep < 2**31:
+        raise ValueError(f"keep: expected 0 to 2^31 - 1, got {keep}")
+    lens_at, done_at = _int32("lens", lens, n, dev), _int32("done", done, n, dev)
+    count_at = _int32("free_count", free_count, 1, dev)
     if lens_out is None:
         lens_out = _empty(dev, stream, (n,), torch.int32)
     if free_count_out is None:
         free_count_out = _empty(dev, stream, (1,), torch.int32)
-    _int32s(dev, lens=(lens, n), done=(done, n), free_count=(free_count, 1), lens_out=(lens_out, n),
-            free_count_out=(free_count_out, 1))
     if workspace is None:
-        workspace = _empty(dev, stream, (nvfp4_kv_release_workspace_bytes(n),), torch.uint8)
-    _same_device(dev, workspace)
-    if not workspace.is_contiguous():
-        raise ValueError("the workspace must be contiguous")
-    _call("nvfp4_kv_release", lib.nvfp4_kv_release, dev, stream, t, lens.data_ptr(), done.data_ptr(), keep,
-          free_count.data_ptr(), lens_out.data_ptr(), free_count_out.data_ptr(), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+        need = lib.nvfp4_kv_release_workspace_bytes(n)
+        if need:
+            workspace = _empty(dev, stream, (need,), torch.uint8)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on {dev}")
+    _call("nvfp4_kv_release", lib.nvfp4_kv_release, dev, stream, t, lens_at, done_at, keep, count_at,
+          _int32("lens_out", lens_out, n, dev), _int32("free_count_out", free_count_out, 1, dev),
+          None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
     return lens_out, free_count_out

@@ -88,7 +88,7 @@ nvfp4_status check_tables(const nvfp4_kv_tables* t) {
     if (!t || !t->table || !t->free_blocks || t->count < 1 || t->table_blocks < 1 || t->capacity < 1 ||
         t->ld_table < t->table_blocks)
         return NVFP4_ERR_INVALID_ARGUMENT;
-    if (t->count > kMaxSeqs || t->table_blocks > kMaxTableBlocks || t->capacity > INT32_MAX ||
+    if (t->count > kMaxSeqs || t->table_blocks > kMaxTableBlocks || t->capacity > ((int64_t)1 << 30) ||
         t->ld_table > ((int64_t)1 << 60) / t->count)
         return NVFP4_ERR_SHAPE;
     if (!aligned(t->table, 4) || !aligned(t->free_blocks, 4)) return NVFP4_ERR_ALIGNMENT;
@@ -260,8 +260,8 @@ nvfp4_status nvfp4_kv_extend(const nvfp4_kv_tables* tables, const int32_t* past,
 }
 
 size_t nvfp4_kv_release_workspace_bytes(int64_t count) {
-    if (count < 1 || count > kMaxSeqs) return 0;
-    return kStateBytes + (size_t)kv_release_groups(count) * sizeof(int64_t) + (size_t)count * sizeof(int32_t);
+    if (count < 1 || count > kMaxSeqs || kv_release_groups(count) == 1) return 0;
+    return kStateBytes + (size_t)kv_release_groups(count) * sizeof(int64_t);
 }
 
 nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens, const int32_t* done, int64_t keep,
@@ -272,8 +272,9 @@ nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens
     if (!lens || !done || !free_count || !lens_out || !free_left || keep < 0) return NVFP4_ERR_INVALID_ARGUMENT;
     if (!aligned(lens, 4) || !aligned(done, 4) || !aligned(free_count, 4) || !aligned(lens_out, 4) || !aligned(free_left, 4))
         return NVFP4_ERR_ALIGNMENT;
-    if (!workspace || workspace_bytes < nvfp4_kv_release_workspace_bytes(tables->count)) return NVFP4_ERR_INVALID_ARGUMENT;
-    if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
+    const size_t need = nvfp4_kv_release_workspace_bytes(tables->count);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (need > 0 && !aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
     ReleaseArgs a;
     a.B = tables->count;
     a.lens = lens;
@@ -281,7 +282,7 @@ nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens
     a.table = tables->table;
     a.ld_table = tables->ld_table;
     a.table_blocks = tables->table_blocks;
-    a.keep = keep;
+    a.keep = keep < tables->table_blocks ? keep : tables->table_blocks;
     a.free_blocks = tables->free_blocks;
     a.capacity = tables->capacity;
     a.free_count = free_count;
@@ -289,7 +290,6 @@ nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens
     a.free_left = free_left;
     a.state = (int32_t*)workspace;
     a.totals = (int64_t*)((char*)workspace + kStateBytes);
-    a.counts = (int32_t*)(a.totals + kv_release_groups(a.B));
     return report_hip(launch_kv_release(a, (hipStream_t)stream));
 }
 

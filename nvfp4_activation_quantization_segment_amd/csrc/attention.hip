@@ -375,19 +375,27 @@ __device__ __forceinline__ bf16x8 seen_ones(const f32x16& s, int k) {
 // ---------------------------------------------------------------------------
 constexpr int kNarrowWaves = 4;
 
+template <int D>
+struct NarrowShared {
+    alignas(16) float o[kNarrowWaves][kRows][D + 4];
+    float m[kNarrowWaves][kRows], l[kNarrowWaves][kRows];
+};
+
+// Which tile, key/value head and piece of the keys a workgroup takes.
+struct Place {
+    uint32_t unit;
+    int kv_head, part;
+};
+
 template <int D, int MODE>
-__global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(AttentionArgs a) {
+__device__ __forceinline__ void narrow_tile(const AttentionArgs& a, NarrowShared<D>& share, const Place& place) {
     constexpr int kDT = D / 32, kK = D / 64;
     constexpr int kBytes = kKvBlock * D;
-    constexpr int kLd = D + 4;
-    __shared__ __align__(16) float so[kNarrowWaves][kRows][kLd];
-    __shared__ float sm[kNarrowWaves][kRows], sl[kNarrowWaves][kRows];
-    const int kv_head = blockIdx.y, part = blockIdx.z;
-    // Workgroups go to the 8 XCDs in turn: with a multiple of 8 units, all of a
-    // long sequence's would go to one of them, were heads and parts not turned
-    // against each other (32 sequences of 1 to 16,384 keys: 118 us, 124 without).
-    uint32_t unit = blockIdx.x + (blockIdx.y + blockIdx.z) % gridDim.x;
-    unit = unit < gridDim.x ? unit : unit - gridDim.x;
+    auto& so = share.o;
+    auto& sm = share.m;
+    auto& sl = share.l;
+    const int kv_head = place.kv_head, part = place.part;
+    const uint32_t unit = place.unit;
     const Tile t = find_tile<MODE>(a, unit, kRows);
     if (!t.any) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -618,6 +626,20 @@ __global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(
     }
 }
 
+// Workgroups go to the 8 XCDs in turn: with a multiple of 8 units, all of a
+// long sequence's would go to one of them, were heads and parts not turned
+// against each other (32 sequences of 1 to 16,384 keys: 118 us, 124 without).
+__device__ __forceinline__ Place narrow_place(uint32_t x, uint32_t y, uint32_t z, uint32_t units) {
+    const uint32_t unit = x + (y + z) % units;
+    return Place{unit < units ? unit : unit - units, (int)y, (int)z};
+}
+
+template <int D, int MODE>
+__global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(AttentionArgs a) {
+    __shared__ NarrowShared<D> share;
+    narrow_tile<D, MODE>(a, share, narrow_place(blockIdx.x, blockIdx.y, blockIdx.z, gridDim.x));
+}
+
 // ---------------------------------------------------------------------------
 // Wide tiles: 128 rows to a workgroup of 4 waves, 32 rows each, that go over
 // the same blocks of keys together.  A block is staged in LDS while the one
@@ -640,17 +662,13 @@ static_assert(kWideRows == kWideWaves * kRows, "32 rows to a wave");
 // so that the tiles in flight at a time read the same keys from its L2.  Tiles
 // go from the last to the first: under a causal mask the later ones take
 // longer, and the short ones fill the end.
-__device__ __forceinline__ void wide_place(const AttentionArgs& a, int& unit, int& kv_head) {
-    const uint32_t heads = a.cache.heads, units = gridDim.x / heads;
+__device__ __forceinline__ Place wide_place(uint32_t x, uint32_t z, uint32_t units, uint32_t heads) {
     if (heads % 8 == 0) {
-        const uint32_t at = blockIdx.x / 8, head = at / units;
-        kv_head = (int)((blockIdx.x % 8) * (heads / 8) + head);
-        unit = (int)(units - 1 - (at - head * units));
-    } else {
-        const uint32_t at = blockIdx.x / heads;
-        kv_head = (int)(blockIdx.x - at * heads);
-        unit = (int)(units - 1 - at);
+        const uint32_t at = x / 8, head = at / units;
+        return Place{units - 1 - (at - head * units), (int)((x % 8) * (heads / 8) + head), (int)z};
     }
+    const uint32_t at = x / heads;
+    return Place{units - 1 - at, (int)(x - at * heads), (int)z};
 }
 
 // Asks the compiler to lay MATRIX matrix instructions of a stretch of code out
@@ -665,22 +683,31 @@ __device__ __forceinline__ void alternate() {
 }
 
 template <int D, int MODE>
-__global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(AttentionArgs a) {
-    constexpr int kDT = D / 32, kK = D / 64;
-    constexpr int kBytes = kKvBlock * D;
-    constexpr int kPieces = kBytes / 16;                  // 16-byte pieces of a block's keys, and of its values
-    constexpr int kThreads = 64 * kWideWaves;
-    constexpr int kEach = kPieces / kThreads;             // of them a thread's
-    __shared__ __align__(16) u32x4 sk[2][kPieces];
-    __shared__ __align__(16) u32x4 sv[2][2 * kPieces];    // [k-step][half][dim] of 8 keys
+struct WideShared {
+    static constexpr int kPieces = kKvBlock * D / 16;  // 16-byte pieces of a block's keys, and of its values
+    static constexpr int kMarks = MODE == PLAIN ? 1 : 2;
+    alignas(16) u32x4 k[2][kPieces];
+    alignas(16) u32x4 v[2][2 * kPieces];               // [k-step][half][dim] of 8 keys
     // by dim, which keys' values are NaN codes: PLAIN the first of them, else the
     // bits of all, [half of the block][dim]
-    constexpr int kMarks = MODE == PLAIN ? 1 : 2;
+    int nan_key[2][kMarks * D];
+    int nan_any[2];
+};
+
+template <int D, int MODE>
+__device__ __forceinline__ void wide_tile(const AttentionArgs& a, WideShared<D, MODE>& share, const Place& place) {
+    constexpr int kDT = D / 32, kK = D / 64;
+    constexpr int kBytes = kKvBlock * D;
+    constexpr int kThreads = 64 * kWideWaves;
+    constexpr int kEach = WideShared<D, MODE>::kPieces / kThreads;  // pieces of a thread
+    constexpr int kMarks = WideShared<D, MODE>::kMarks;
     constexpr int kNoMark = MODE == PLAIN ? kKvBlock : 0;
-    __shared__ int nan_key[2][kMarks * D];
-    __shared__ int nan_any[2];
-    int unit, kv_head;
-    wide_place(a, unit, kv_head);
+    auto& sk = share.k;
+    auto& sv = share.v;
+    auto& nan_key = share.nan_key;
+    auto& nan_any = share.nan_any;
+    const uint32_t unit = place.unit;
+    const int kv_head = place.kv_head;
     const Tile t = find_tile<MODE>(a, unit, kWideRows);
     if (!t.any) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -697,7 +724,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
     const int tile_low_last = MODE == WINDOW ? low_of_row(a, t, t.first + kWideRows - 1) : 0;
     const int low_first = MODE == WINDOW ? __builtin_amdgcn_readlane(row.low, 0) : 0;
     const int low_last = MODE == WINDOW ? __builtin_amdgcn_readlane(row.low, kRows - 1) : 0;
-    const int part = blockIdx.z;
+    const int part = place.part;
     const Blocks blocks = blocks_of<MODE>(a, tile_seen, tile_low);
     const BlockRange range = kv_part(blocks.count, part, a.parts);
     const int at0 = range.first, end = range.last;
@@ -940,6 +967,47 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
         }
 }
 
+template <int D, int MODE>
+__global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(AttentionArgs a) {
+    __shared__ WideShared<D, MODE> share;
+    wide_tile<D, MODE>(a, share, wide_place(blockIdx.x, blockIdx.z, gridDim.x / a.cache.heads, a.cache.heads));
+}
+
+// ---------------------------------------------------------------------------
+// A batch over a shared prefix: the first workgroups take tiles of all sequences'
+// rows against pieces of the prefix, the others each sequence's rows against its
+// own keys, in one launch, so that the loads of the one fill the waits of the
+// other.
+// ---------------------------------------------------------------------------
+template <int D, bool PREFIX_WIDE, bool OWN_WIDE>
+__global__ __launch_bounds__(64 * kWideWaves, 2) void attention_shared_kernel(AttentionArgs prefix, AttentionArgs own,
+                                                                              SharedGrid g) {
+    static_assert(kNarrowWaves == kWideWaves, "one size of workgroup");
+    __shared__ union {
+        NarrowShared<D> narrow;
+        WideShared<D, PREFIX> prefix_wide;
+        WideShared<D, OWN> own_wide;
+    } share;
+    uint32_t at = blockIdx.y * gridDim.x + blockIdx.x;
+    const uint32_t heads = own.cache.heads;
+    if (at < g.prefix_groups) {
+        const uint32_t each = g.prefix_units * heads, z = at / each, x = at - z * each;
+        if constexpr (PREFIX_WIDE)
+            wide_tile<D, PREFIX>(prefix, share.prefix_wide, wide_place(x, z, g.prefix_units, heads));
+        else
+            narrow_tile<D, PREFIX>(prefix, share.narrow,
+                                   narrow_place(x % g.prefix_units, x / g.prefix_units, z, g.prefix_units));
+        return;
+    }
+    at -= g.prefix_groups;
+    if (at >= g.own_groups) return;
+    const uint32_t each = g.own_units * heads, z = at / each, x = at - z * each;
+    if constexpr (OWN_WIDE)
+        wide_tile<D, OWN>(own, share.own_wide, wide_place(x, z, g.own_units, heads));
+    else
+        narrow_tile<D, OWN>(own, share.narrow, narrow_place(x % g.own_units, x / g.own_units, z, g.own_units));
+}
+
 // Joins the parts of each row; rows that no sequence has are left alone.  WAVES
 // waves take a row: each has the maximum and sum of every part in its lanes
 // (part s in lane s, at most 64), adds up its share of at most EACH parts, D / 64
@@ -1057,13 +1125,8 @@ SharedPlan shared_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, 
 template <int D, int MODE>
 static void attention_tiles(AttentionArgs a, hipStream_t s) {
     const int64_t T = a.wide ? kWideRows : kRows;
-    int64_t units;
-    if (MODE == PREFIX) {
-        units = (a.seqs.M * a.group + T - 1) / T;
-    } else {
-        a.seqs.per_row = tiles_per_row(a.seqs.M, a.seqs.B, a.group, T);
-        units = tile_first(a.seqs.M, a.seqs.B, a.group, T, a.seqs.per_row);
-    }
+    a.seqs.per_row = tiles_per_row(a.seqs.M, a.seqs.B, a.group, T);
+    const int64_t units = tile_first(a.seqs.M, a.seqs.B, a.group, T, a.seqs.per_row);
     if (a.wide) {
         // below 2^23, so that the threads of a dimension stay below 2^32: the heads
         // times M group / 128 + B, where B <= M group / 64 and M q_heads <= 2^28
@@ -1104,17 +1167,30 @@ static void attention_of(const AttentionArgs& a, hipStream_t s) {
 
 template <int D>
 static void attention_shared_of(const AttentionArgs& a, const SharedPlan& p, const int32_t* shared, hipStream_t s) {
-    AttentionArgs prefix = a;
+    const int64_t heads = a.cache.heads, rows = a.seqs.M * a.group;
+    AttentionArgs prefix = a, own = a;
     prefix.seqs.table = shared;
     prefix.causal = 0;
-    prefix.wide = p.prefix.wide;
     prefix.parts = p.prefix.parts;
-    attention_tiles<D, PREFIX>(prefix, s);
-    AttentionArgs own = a;
-    own.wide = p.own.wide;
     own.parts = p.own.parts;
     own.first_part = p.prefix.parts;
-    attention_tiles<D, OWN>(own, s);
+    const int64_t T = p.own.wide ? kWideRows : kRows, PT = p.prefix.wide ? kWideRows : kRows;
+    own.seqs.per_row = tiles_per_row(a.seqs.M, a.seqs.B, a.group, T);
+    // both below 2^30: M q_heads is at most 2^28, tiles are at most 2 a row and
+    // head, and the keys are cut only where there are few of them
+    SharedGrid g;
+    g.prefix_units = (uint32_t)((rows + PT - 1) / PT);
+    g.own_units = (uint32_t)tile_first(a.seqs.M, a.seqs.B, a.group, T, own.seqs.per_row);
+    g.prefix_groups = (uint32_t)(g.prefix_units * heads * p.prefix.parts);
+    g.own_groups = (uint32_t)(g.own_units * heads * p.own.parts);
+    const uint32_t groups = g.prefix_groups + g.own_groups, row = groups < (1u << 20) ? groups : 1u << 20;
+    const dim3 grid(row, (groups + row - 1) / row), block(64 * kWideWaves);
+    if (p.prefix.wide && p.own.wide)
+        attention_shared_kernel<D, true, true><<<grid, block, 0, s>>>(prefix, own, g);
+    else if (p.prefix.wide)
+        attention_shared_kernel<D, true, false><<<grid, block, 0, s>>>(prefix, own, g);
+    else
+        attention_shared_kernel<D, false, false><<<grid, block, 0, s>>>(prefix, own, g);
     attention_join<D>(a, s);
 }
 

@@ -105,7 +105,6 @@ struct ReleaseArgs {
     int32_t* free_left;
     int32_t* state;       // workspace: free blocks before
     int64_t* totals;      // workspace: blocks of each workgroup's requests
-    int32_t* counts;      // workspace: [B] blocks of each request
 };
 
 struct AttentionArgs {
@@ -150,6 +149,11 @@ hipError_t launch_attention(const AttentionArgs& a, hipStream_t s);
 
 // A bound on the keys that a tile sees through a window, for attention_plan.
 int64_t window_bound(int64_t max_len, int32_t causal, int32_t window, int32_t sinks);
+
+// The workgroups of a call over a shared prefix: tiles of a head and all of them.
+struct SharedGrid {
+    uint32_t prefix_units, prefix_groups, own_units, own_groups;
+};
 
 // How a call over a shared prefix is cut: all rows against it, and each sequence's
 // against its own keys.

@@ -8,6 +8,10 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
 
 // Inclusive sum over the workgroup's threads; total: that of all of them.  The
 // slots are read by all before the call returns and written by the next one's
@@ -39,39 +43,222 @@ __device__ __forceinline__ int32_t blocks_of(int64_t len, int64_t table_blocks) 
 }
 
 // ---------------------------------------------------------------------------
-// Extending.  The requests come first: rows and blocks of each, as running sums,
-// by one workgroup (the sums of a few thousand requests are a few rounds of it).
+// Extending.  The requests come first: rows and blocks of each, as running sums.
 // Then the rows: each finds its request, and the row that starts a block writes
 // the table's entry.  A block's number comes from the sums alone, so rows of one
 // block need not wait for one another.
+//
+// Up to 1024 requests, every workgroup takes the sums of all of them by itself,
+// into LDS, and then its 4096 rows: one launch.  What that costs is the chain of
+// loads (past; a request's last block; free blocks), about 3 us whatever the
+// number of rows.  A step in place whose rows need several workgroups, of which
+// one writes what the others read, and more requests than that take a launch for
+// the sums and one for the rows.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void extend_requests(const ExtendArgs& a) {
+// One request's part of a round of sums.
+struct Asked {
+    int64_t past, rows, blocks;  // held; rows given, blocks taken
+    int64_t first, taken;        // its first row, blocks of the requests before
+};
+struct Sums {
+    int64_t rows, blocks;
+};
+
+__device__ __forceinline__ Asked ask(const ExtendArgs& a, int64_t b, Sums& sums, int64_t* slot) {
+    Asked q;
+    q.past = b < a.B ? a.past[b] : 0;
+    const int64_t want = b < a.B ? clamp64(a.more[b], 0, INT32_MAX - clamp64(q.past, 0, INT32_MAX)) : 0;
+    int64_t rows, blocks;
+    const int64_t end = sums.rows + group_scan(want, slot, rows);
+    q.first = clamp64(end - want, 0, a.M);
+    q.rows = clamp64(end, 0, a.M) - q.first;
+    q.blocks = blocks_of(q.past + q.rows, a.table_blocks) - blocks_of(q.past, a.table_blocks);
+    q.taken = sums.blocks + group_scan(q.blocks, slot, blocks) - q.blocks;
+    sums.rows += rows;
+    sums.blocks += blocks;
+    return q;
+}
+
+__device__ __forceinline__ void write_asked(const ExtendArgs& a, int64_t b, const Asked& q) {
+    if (b < a.B) {
+        a.row_start[b + 1] = (int32_t)(q.first + q.rows);
+        a.lens[b] = (int32_t)(q.past + q.rows);
+    }
+}
+__device__ __forceinline__ void write_stack(const ExtendArgs& a, int64_t had, int64_t blocks) {
+    a.row_start[0] = 0;
+    *a.free_left = (int32_t)(had > blocks ? had - blocks : 0);
+    *a.missing = (int32_t)(blocks > had ? blocks - had : 0);
+}
+
+// Position, and slot, of a row of a request; the table's entry where it starts a
+// block.  last: the entry of the request's last block, where that has room left.
+__device__ __forceinline__ void write_row(const ExtendArgs& a, int64_t row, int64_t b, int64_t past, int64_t first,
+                                          int64_t taken, int64_t had, int32_t last) {
+    const int64_t pos = past + row - first, at = floor_div(pos, kKvBlock);
+    int64_t slot = -1;
+    if (pos >= 0 && at < a.table_blocks) {
+        const int64_t fresh = at - blocks_of(past, a.table_blocks), place = had - 1 - taken - fresh;
+        const int32_t page = fresh < 0 ? last : place >= 0 ? a.free_blocks[place] : -1;
+        if (fresh >= 0 && pos % kKvBlock == 0) a.table[b * a.ld_table + at] = page;
+        slot = page < 0 ? -1 : (int64_t)page * kKvBlock + pos % kKvBlock;
+    }
+    if (a.positions) a.positions[row] = (int32_t)pos;
+    if (a.slots) a.slots[row] = slot;
+}
+__device__ __forceinline__ void write_no_row(const ExtendArgs& a, int64_t row) {
+    if (a.positions) a.positions[row] = -1;
+    if (a.slots) a.slots[row] = -1;
+}
+// Column of the block that a request's next position falls into, where it has begun.
+__device__ __forceinline__ int64_t last_column(const ExtendArgs& a, int64_t past) {
+    return past > 0 && past % kKvBlock != 0 && past / kKvBlock < a.table_blocks ? past / kKvBlock : -1;
+}
+
+// Inclusive sum, or maximum, over a wave's lanes of what `combine` joins.
+template <class Combine>
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x, Combine combine) {
+    const auto from = [&](auto control, auto rows) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(control)::value, decltype(rows)::value, 0xF, false);
+    };
+    x = combine(x, from(Int<0x111>(), Int<0xF>()));  // 1, 2, 4 and 8 lanes before, within rows of 16
+    x = combine(x, from(Int<0x112>(), Int<0xF>()));
+    x = combine(x, from(Int<0x114>(), Int<0xF>()));
+    x = combine(x, from(Int<0x118>(), Int<0xF>()));
+    x = combine(x, from(Int<0x142>(), Int<0xA>()));  // the row before's last, then the half before's
+    x = combine(x, from(Int<0x143>(), Int<0xC>()));
+    return x;
+}
+// The same over the workgroup's threads: what comes before each of them, and all.
+// 0 joined to anything is that.  The slots are the scan's own.
+template <class Combine>
+__device__ __forceinline__ uint32_t group_scan32(uint32_t x, uint32_t* slot, uint32_t& all, Combine combine) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t mine = wave_scan(x, combine);
+    if (lane == 63) slot[wave] = mine;
+    const uint32_t up = (uint32_t)__shfl_up((int)mine, 1);
+    __syncthreads();
+    uint32_t before = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const uint32_t v = slot[w];
+        before = w < wave ? combine(before, v) : before;
+        all = combine(all, v);
+    }
+    return lane == 0 ? before : combine(before, up);
+}
+__device__ __forceinline__ uint32_t add_up(uint32_t x, uint32_t y) { return __builtin_elementwise_add_sat(x, y); }
+__device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) { return x > y ? x : y; }
+
+constexpr int kRowsEach = 4;
+constexpr int kGroupRows = kThreads * kRowsEach;
+
+// What a row needs of its request.
+struct __align__(16) Request {
+    int32_t shift;    // its position minus the row
+    int32_t first;    // first column that is not held
+    int32_t top;      // place on the stack of column 0, were it taken like the others
+    int32_t last;     // the entry of the block that has room left
+};
+
+__global__ __launch_bounds__(kThreads) void extend_kernel(ExtendArgs a) {
+    __shared__ uint32_t slot[3][kWaves];
+    __shared__ Request request[kThreads];
+    __shared__ __align__(16) uint32_t mark[kGroupRows];  // request + 1 at its first row here
+    const int32_t had = (int32_t)clamp64(*a.free_count, 0, a.capacity);
+    const int t = threadIdx.x;
+    const int32_t row0 = (int32_t)(blockIdx.x * kGroupRows), M = (int32_t)a.M;
+    *reinterpret_cast<uint4*>(&mark[kRowsEach * t]) = make_uint4(0, 0, 0, 0);
+    const int32_t past = t < a.B ? a.past[t] : 0, asked = t < a.B ? a.more[t] : 0;
+    // a request's last entry is on its way while the sums are taken
+    const int64_t column = last_column(a, past);
+    const int32_t entry = column >= 0 ? a.table[t * a.ld_table + column] : -1;
+    const int32_t room = INT32_MAX - (past > 0 ? past : 0);
+    const uint32_t want = asked < 0 ? 0 : asked < room ? asked : room;
+    uint32_t total, taken_all;
+    const uint32_t start = group_scan32(want, slot[0], total, add_up);  // saturates: far above M
+    const int32_t first = start < (uint32_t)M ? (int32_t)start : M;
+    const int32_t rows = want < (uint32_t)(M - first) ? (int32_t)want : M - first;
+    const int32_t have = blocks_of(past, a.table_blocks);
+    const int32_t take = blocks_of((int64_t)past + rows, a.table_blocks) - have;
+    const int32_t taken = (int32_t)group_scan32((uint32_t)take, slot[1], taken_all, add_up);
+    // a position's shift wraps where past - first leaves 32 bits, and back where the row is added
+    request[t] = Request{(int32_t)((uint32_t)past - (uint32_t)first), have, had - 1 - taken + have, entry};
+    if (rows > 0 && first + rows > row0 && first < row0 + kGroupRows) mark[first > row0 ? first - row0 : 0] = t + 1;
+    if (blockIdx.x == 0) {
+        if (t < a.B) {
+            a.row_start[t + 1] = first + rows;
+            a.lens[t] = past + rows;
+        }
+        if (t == 0) write_stack(a, had, taken_all);
+    }
+    __syncthreads();
+    const uint4 marks = *reinterpret_cast<const uint4*>(&mark[kRowsEach * t]);
+    uint32_t of[kRowsEach] = {marks.x, marks.y, marks.z, marks.w};
+#pragma unroll
+    for (int i = 1; i < kRowsEach; ++i) of[i] = larger(of[i], of[i - 1]);
+    uint32_t none;
+    const uint32_t before = group_scan32(of[kRowsEach - 1], slot[2], none, larger);
+    const int32_t used = total < (uint32_t)M ? (int32_t)total : M;
+    int32_t position[kRowsEach];
+    int64_t where[kRowsEach];
+#pragma unroll
+    for (int i = 0; i < kRowsEach; ++i) {
+        const int32_t row = row0 + kRowsEach * t + i;
+        const uint32_t b = larger(of[i], before);
+        position[i] = -1;
+        where[i] = -1;
+        if (row >= used || b == 0) continue;
+        const Request q = request[b - 1];
+        const int32_t pos = (int32_t)((uint32_t)q.shift + (uint32_t)row), at = pos >> 6;
+        position[i] = pos;
+        if (pos < 0 || at >= a.table_blocks) continue;
+        int32_t page = q.last;
+        if (at >= q.first) {
+            page = q.top - at >= 0 ? a.free_blocks[q.top - at] : -1;
+            if (pos % kKvBlock == 0) a.table[(b - 1) * a.ld_table + at] = page;
+        }
+        where[i] = page < 0 ? -1 : (int64_t)page * kKvBlock + pos % kKvBlock;
+    }
+    const int32_t mine = row0 + kRowsEach * t;
+    const bool whole = mine + kRowsEach <= M;
+    if (a.positions) {
+        if (whole && ((uintptr_t)a.positions & 15) == 0) {
+            *reinterpret_cast<int4*>(a.positions + mine) = make_int4(position[0], position[1], position[2], position[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRowsEach; ++i)
+                if (mine + i < M) a.positions[mine + i] = position[i];
+        }
+    }
+    if (a.slots) {
+        if (whole && ((uintptr_t)a.slots & 15) == 0) {
+            typedef int64_t i64x2 __attribute__((ext_vector_type(2)));
+            i64x2* p = reinterpret_cast<i64x2*>(a.slots + mine);
+            p[0] = i64x2{where[0], where[1]};
+            p[1] = i64x2{where[2], where[3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRowsEach; ++i)
+                if (mine + i < M) a.slots[mine + i] = where[i];
+        }
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void extend_requests_kernel(ExtendArgs a) {
     __shared__ int64_t slot[kWaves];
     const int64_t had = clamp64(*a.free_count, 0, a.capacity);
-    int64_t rows = 0, blocks = 0;  // of the requests before
-    if (threadIdx.x == 0) a.row_start[0] = 0;
+    Sums sums = {0, 0};
     for (int64_t b0 = 0; b0 < a.B; b0 += kThreads) {
         const int64_t b = b0 + threadIdx.x;
-        const int64_t past = b < a.B ? a.past[b] : 0;
-        const int64_t want = b < a.B ? clamp64(a.more[b], 0, INT32_MAX - clamp64(past, 0, INT32_MAX)) : 0;
-        int64_t sum_rows, sum_blocks;
-        const int64_t end = rows + group_scan(want, slot, sum_rows);
-        const int64_t first = clamp64(end - want, 0, a.M), last = clamp64(end, 0, a.M);
-        const int64_t len = past + (last - first);
-        const int64_t take = blocks_of(len, a.table_blocks) - blocks_of(past, a.table_blocks);
-        const int64_t taken = blocks + group_scan(take, slot, sum_blocks) - take;
-        if (b < a.B) {
-            a.row_start[b + 1] = (int32_t)last;
-            a.lens[b] = (int32_t)len;
-            a.taken[b] = (int32_t)taken;
-        }
-        rows += sum_rows;
-        blocks += sum_blocks;
+        const Asked q = ask(a, b, sums, slot);
+        write_asked(a, b, q);
+        if (b < a.B) a.taken[b] = (int32_t)q.taken;
     }
     if (threadIdx.x == 0) {
         a.state[0] = (int32_t)had;
-        *a.free_left = (int32_t)(had > blocks ? had - blocks : 0);
-        *a.missing = (int32_t)(blocks > had ? blocks - had : 0);
+        write_stack(a, had, sums.blocks);
     }
 }
 
@@ -113,140 +300,156 @@ __device__ __forceinline__ int64_t request_of(const ExtendArgs& a, int64_t row, 
     return b;
 }
 
-__device__ __forceinline__ void extend_rows(const ExtendArgs& a, int64_t row0) {
-    const int64_t row = row0 + (threadIdx.x & 63);
+__global__ __launch_bounds__(256) void extend_rows_kernel(ExtendArgs a) {
+    const int64_t row0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 64, row = row0 + (threadIdx.x & 63);
+    if (row0 >= a.M) return;
     const int32_t used = a.row_start[a.B];
     if (row0 >= used) {
-        if (row < a.M) {
-            if (a.positions) a.positions[row] = -1;
-            if (a.slots) a.slots[row] = -1;
-        }
+        if (row < a.M) write_no_row(a, row);
         return;
     }
     const int64_t b = request_of(a, row < used ? row : used - 1, row0);
     if (row >= a.M) return;
-    int64_t pos = -1, slot = -1;
-    if (row < used) {
-        const int64_t first = a.row_start[b], n = a.row_start[b + 1] - first, past = a.lens[b] - n;
-        pos = past + row - first;
-        const int64_t at = floor_div(pos, kKvBlock);
-        if (pos >= 0 && at < a.table_blocks) {
-            const int64_t fresh = at - blocks_of(past, a.table_blocks);
-            int32_t* entry = a.table + b * a.ld_table + at;
-            int32_t page;
-            if (fresh < 0) {
-                page = *entry;
-            } else {
-                const int64_t place = (int64_t)a.state[0] - 1 - a.taken[b] - fresh;
-                page = place >= 0 ? a.free_blocks[place] : -1;
-                if (pos % kKvBlock == 0) *entry = page;
-            }
-            slot = page < 0 ? -1 : (int64_t)page * kKvBlock + pos % kKvBlock;
-        }
+    if (row >= used) {
+        write_no_row(a, row);
+        return;
     }
-    if (a.positions) a.positions[row] = (int32_t)pos;
-    if (a.slots) a.slots[row] = slot;
-}
-
-__global__ __launch_bounds__(kThreads) void extend_requests_kernel(ExtendArgs a) { extend_requests(a); }
-
-__global__ __launch_bounds__(256) void extend_rows_kernel(ExtendArgs a) {
-    const int64_t row0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 64;
-    if (row0 < a.M) extend_rows(a, row0);
-}
-
-__global__ __launch_bounds__(kThreads) void extend_kernel(ExtendArgs a) {
-    extend_requests(a);
-    __threadfence_block();
-    __syncthreads();
-    for (int64_t row0 = (threadIdx.x >> 6) * 64; row0 < a.M; row0 += kThreads) extend_rows(a, row0);
+    const int64_t first = a.row_start[b], past = a.lens[b] - (a.row_start[b + 1] - first), column = last_column(a, past);
+    write_row(a, row, b, past, first, a.taken[b], a.state[0], column >= 0 ? a.table[b * a.ld_table + column] : -1);
 }
 
 // ---------------------------------------------------------------------------
-// Releasing.  A wave takes a request: its table's entries, 64 at a time.  Their
-// places on the stack follow from how many blocks the requests before give back,
-// so a first launch counts and a second one moves.
+// Releasing.  A wave takes a few requests: their tables' entries, 64 at a time,
+// the first ones of all of them in flight together and kept in registers.  Their
+// places on the stack follow from how many blocks the requests before give back:
+// one workgroup finds that out in LDS, several of them by a launch that counts
+// before the one that moves.
 // ---------------------------------------------------------------------------
-constexpr int kEach = 4;                 // requests of a wave
+constexpr int kEach = 2;                 // requests of a wave
+constexpr int kKept = 4;                 // times 64 entries of each that it keeps
 constexpr int kOf = kEach * kWaves;      // requests of a workgroup
 
-__device__ __forceinline__ int32_t release_blocks(const ReleaseArgs& a, int64_t b) {
-    return b < a.B && a.done[b] != 0 ? blocks_of(a.lens[b], a.table_blocks) : 0;
+struct Released {
+    int32_t blocks[kEach];        // entries [keep, blocks) of each
+    int32_t page[kEach][kKept];   // this lane's of the first ones, -1 for none
+    int32_t lens[kEach];          // what is left of each
+    int64_t count[kEach];         // blocks given back
+};
+
+__device__ __forceinline__ int32_t entry_of(const ReleaseArgs& a, int64_t b, int64_t at, int32_t blocks) {
+    const int32_t page = at < blocks ? a.table[b * a.ld_table + at] : -1;
+    return page < 0 ? -1 : page;
 }
 
-// Blocks that the wave's request gives back, counted, and with move() for each.
-template <class Move>
-__device__ __forceinline__ int64_t release_request(const ReleaseArgs& a, int64_t b, Move move) {
+__device__ __forceinline__ Released take(const ReleaseArgs& a, int64_t b0) {
     const int lane = threadIdx.x & 63;
-    const int32_t blocks = release_blocks(a, b);
-    int64_t count = 0;
-    for (int64_t at = a.keep; at < blocks; at += 64) {
-        const int32_t page = at + lane < blocks ? a.table[b * a.ld_table + at + lane] : -1;
-        const uint64_t good = __ballot(page >= 0);
-        if (page >= 0) move(count + __popcll(good & (((uint64_t)1 << lane) - 1)), page);
-        count += __popcll(good);
+    Released r;
+    int32_t done[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        done[i] = b0 + i < a.B ? a.done[b0 + i] : 0;
+        r.lens[i] = b0 + i < a.B ? a.lens[b0 + i] : 0;
     }
-    return count;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        r.blocks[i] = done[i] != 0 ? blocks_of(r.lens[i], a.table_blocks) : 0;
+        r.lens[i] = done[i] != 0 ? 0 : r.lens[i];
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) r.page[i][k] = entry_of(a, b0 + i, a.keep + 64 * k + lane, r.blocks[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        r.count[i] = 0;
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) r.count[i] += __popcll(__ballot(r.page[i][k] >= 0));
+        for (int64_t at = a.keep + 64 * kKept; at < r.blocks[i]; at += 64)
+            r.count[i] += __popcll(__ballot(entry_of(a, b0 + i, at + lane, r.blocks[i]) >= 0));
+    }
+    return r;
+}
+
+// Puts them on the stack from `place` on.
+__device__ __forceinline__ void give(const ReleaseArgs& a, int64_t b0, const Released& r, int64_t place) {
+    const int lane = threadIdx.x & 63;
+    const auto put = [&](int32_t page) {
+        const uint64_t good = __ballot(page >= 0);
+        const int64_t at = place + __popcll(good & (((uint64_t)1 << lane) - 1));
+        if (page >= 0 && at < a.capacity) a.free_blocks[at] = page;
+        place += __popcll(good);
+    };
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) put(r.page[i][k]);
+        for (int64_t at = a.keep + 64 * kKept; at < r.blocks[i]; at += 64) put(entry_of(a, b0 + i, at + lane, r.blocks[i]));
+        if (b0 + i < a.B && lane == 0) a.lens_out[b0 + i] = r.lens[i];
+    }
+}
+
+// What the waves before this one give back, and all of them.
+__device__ __forceinline__ int64_t waves_before(const Released& r, int64_t* share, int64_t& all) {
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    int64_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) mine += r.count[i];
+    if ((threadIdx.x & 63) == 0) share[wave] = mine;
+    __syncthreads();
+    int64_t before = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        before += w < wave ? share[w] : 0;
+        all += share[w];
+    }
+    return before;
+}
+
+__device__ __forceinline__ int64_t first_request() {
+    return (int64_t)blockIdx.x * kOf + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * kEach;
 }
 
 __global__ __launch_bounds__(kThreads) void release_count_kernel(ReleaseArgs a) {
     __shared__ int64_t share[kWaves];
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int64_t b0 = (int64_t)blockIdx.x * kOf + wave * kEach;
-    int64_t mine = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int64_t count = release_request(a, b0 + i, [](int64_t, int32_t) {});
-        if (b0 + i < a.B && (threadIdx.x & 63) == 0) a.counts[b0 + i] = (int32_t)count;
-        mine += count;
-    }
-    if ((threadIdx.x & 63) == 0) share[wave] = mine;
-    __syncthreads();
+    int64_t all;
+    waves_before(take(a, first_request()), share, all);
     if (threadIdx.x == 0) {
-        int64_t all = 0;
-        for (int w = 0; w < kWaves; ++w) all += share[w];
         a.totals[blockIdx.x] = all;
         if (blockIdx.x == 0) a.state[0] = *a.free_count;
     }
 }
 
-__global__ __launch_bounds__(kThreads) void release_move_kernel(ReleaseArgs a) {
-    __shared__ int64_t slot[kWaves];
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    // what the workgroups before give back, and all of them
-    int64_t before = 0, all = 0;
-    for (int64_t i = threadIdx.x; i < gridDim.x; i += kThreads) {
-        const int64_t t = a.totals[i];
-        before += i < blockIdx.x ? t : 0;
-        all += t;
+// count: where the stack's size is, a copy of it where several workgroups read it.
+__global__ __launch_bounds__(kThreads) void release_move_kernel(ReleaseArgs a, const int32_t* count) {
+    __shared__ int64_t share[kWaves], slot[kWaves];
+    const int64_t had = clamp64(*count, 0, a.capacity);
+    // what the workgroups before give back, and all that are launched
+    int64_t before = 0, others = 0;
+    if (gridDim.x > 1) {
+        for (int64_t i = threadIdx.x; i < gridDim.x; i += kThreads) {
+            const int64_t n = a.totals[i];
+            before += i < blockIdx.x ? n : 0;
+            others += i != blockIdx.x ? n : 0;
+        }
+        int64_t sum;
+        group_scan(before, slot, sum);
+        before = sum;
+        group_scan(others, slot, sum);
+        others = sum;
     }
-    int64_t sum;
-    group_scan(before, slot, sum);
-    const int64_t had = clamp64(a.state[0], 0, a.capacity);
-    int64_t place = had + sum;
-    group_scan(all, slot, sum);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.free_left = (int32_t)clamp64(had + sum, 0, a.capacity);
-    // and the waves before
-    const int64_t b0 = (int64_t)blockIdx.x * kOf;
-    for (int i = 0; i < wave * kEach; ++i) place += b0 + i < a.B ? a.counts[b0 + i] : 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int64_t b = b0 + wave * kEach + i;
-        place += release_request(a, b, [&](int64_t at, int32_t page) {
-            if (place + at < a.capacity) a.free_blocks[place + at] = page;
-        });
-        if (b < a.B && (threadIdx.x & 63) == 0) a.lens_out[b] = a.done[b] != 0 ? 0 : a.lens[b];
-    }
+    const Released r = take(a, first_request());
+    int64_t all;
+    const int64_t waves = waves_before(r, share, all);
+    give(a, first_request(), r, had + before + waves);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.free_left = (int32_t)clamp64(had + others + all, 0, a.capacity);
 }
 
 }  // namespace
 
-// Up to so many rows one workgroup does all of it, in one launch.
-constexpr int64_t kOneGroupRows = 4096;
-
 hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t s) {
-    if (a.M <= kOneGroupRows) {
-        extend_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(a);
+    const unsigned groups = (unsigned)((a.M + kGroupRows - 1) / kGroupRows);
+    const bool in_place = a.lens == a.past || a.free_left == a.free_count;
+    if (a.B <= kThreads && (groups == 1 || !in_place)) {
+        extend_kernel<<<dim3(groups), dim3(kThreads), 0, s>>>(a);
     } else {
         extend_requests_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(a);
         extend_rows_kernel<<<dim3((unsigned)((a.M + 255) / 256)), dim3(256), 0, s>>>(a);
@@ -258,8 +461,8 @@ int64_t kv_release_groups(int64_t B) { return (B + kOf - 1) / kOf; }
 
 hipError_t launch_kv_release(const ReleaseArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)kv_release_groups(a.B)), block(kThreads);
-    release_count_kernel<<<grid, block, 0, s>>>(a);
-    release_move_kernel<<<grid, block, 0, s>>>(a);
+    if (grid.x > 1) release_count_kernel<<<grid, block, 0, s>>>(a);
+    release_move_kernel<<<grid, block, 0, s>>>(a, grid.x > 1 ? a.state : a.free_count);
     return hipGetLastError();
 }
 

@@ -152,9 +152,7 @@ def run_extend(nv, past, more, table, stack, rows, capacity=None, in_place=False
     t = wide[:, :columns]
     free = i32(stack + [-5] * (capacity - len(stack)))
     count, p = i32([len(stack)]), i32(past)
-    step = nv.KvStep.empty(n, rows)
-    if in_place:
-        step.lens, step.free_count = p, count
+    step = nv.KvStep.empty(n, rows, **(dict(lens=p, free_count=count) if in_place else {}))
     got = nv.kv_extend(p, i32(more), t, free, count, step)
     assert got is step
     if not in_place:
@@ -262,8 +260,7 @@ def test_a_pool_through_many_steps_in_place(nv):
     count, columns, pool = 40, 12, 300
     past, table, stack = [0] * count, [[-1] * columns for _ in range(count)], list(range(pool))
     lens, free, n_free, t = i32(past), i32(stack), i32([pool]), i32(table)
-    step = nv.KvStep.empty(count, 900)
-    step.lens, step.free_count = lens, n_free
+    step = nv.KvStep.empty(count, 900, lens=lens, free_count=n_free)
     for turn in range(30):
         done = [int(r.random() < 0.2) for _ in range(count)]
         more = [r.choice([0, 1, 1, 1, 30, 90]) for _ in range(count)]
@@ -556,8 +553,7 @@ class Serving:
         self.lens = i32([shared_blocks * BLOCK] * self.count)
         self.free = i32(list(range(shared_blocks, self.pool)))
         self.n_free = i32([self.pool - shared_blocks])
-        self.step_arrays = nv.KvStep.empty(self.count, self.rows)
-        self.step_arrays.lens, self.step_arrays.free_count = self.lens, self.n_free
+        self.step_arrays = nv.KvStep.empty(self.count, self.rows, lens=self.lens, free_count=self.n_free)
         self.tables = [nv.rope_table(2048, 64)]
         g = gen(78)
         self.weights = [(1 + normal(g, self.dim, sigma=0.1).float()).bfloat16().cuda() for _ in range(2)]
@@ -630,7 +626,7 @@ def test_a_serving_step_eager_and_captured(nv, shared):
                 held = ref.sequence(0, h, np.array(table[b]), lens[b])[lens[b] - (rs[b + 1] - rs[b]):]
                 mine = k[rs[b]:rs[b + 1], h].numpy()
                 if len(mine):
-                    assert np.all(np.abs(held - mine) <= 2.0 ** -3 * np.abs(mine) + 2.0 ** -8 * np.abs(k).max().item())
+                    assert np.all(np.abs(held - mine) <= 2.0 ** -3 * np.abs(mine) + 2.0 ** -8 * float(k.abs().max()))
         o, tol = step_ref.attention(made.double().numpy(), ref, rs, lens, np.array(table), np.float64(np.float32(128 ** -0.5)), 1,
                                     *((0, 0) if shared else (100, 4)), shared=np.arange(shared) if shared else None)
         check(eager.o[:used], o[:used], tol[:used])
