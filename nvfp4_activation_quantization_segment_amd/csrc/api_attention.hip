@@ -126,9 +126,8 @@ nvfp4_status check_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads, c
     return NVFP4_OK;
 }
 
-// One launch over the sequences' keys (and the join), cut for at most `bound` of them a row.
-nvfp4_status run_attention(AttentionArgs& a, int64_t bound, void* workspace, size_t workspace_bytes, void* stream) {
-    const AttentionPlan p = attention_plan(a.seqs.M, a.seqs.B, a.q_heads, a.cache.heads, a.cache.dim, bound);
+// One launch over the sequences' keys (and the join), cut as planned.
+nvfp4_status run_attention(AttentionArgs& a, const AttentionPlan& p, void* workspace, size_t workspace_bytes, void* stream) {
     if (p.workspace_bytes > 0 && (!workspace || workspace_bytes < p.workspace_bytes)) return NVFP4_ERR_INVALID_ARGUMENT;
     if (p.workspace_bytes > 0 && !aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
     a.wide = p.wide;
@@ -305,13 +304,14 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_heads* q, int64_t M, int32_t q_heads
     AttentionArgs a;
     const nvfp4_status st = check_attention(q, M, q_heads, cache, seqs, scale, causal_block, max_len, out, &a);
     if (st != NVFP4_OK) return st;
-    return run_attention(a, max_len, workspace, workspace_bytes, stream);
+    return run_attention(a, attention_plan(M, seqs->count, q_heads, cache->heads, cache->dim, max_len), workspace,
+                         workspace_bytes, stream);
 }
 
 size_t nvfp4_kv_attention_window_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
                                                  int32_t causal_block, int32_t window, int32_t sinks, int64_t max_len) {
     if (!attention_sizes_ok(M, count, q_heads, heads, dim, max_len) || causal_block < 0 || window < 1 || sinks < 0) return 0;
-    return attention_plan(M, count, q_heads, heads, dim, window_bound(max_len, causal_block, window, sinks)).workspace_bytes;
+    return window_plan(M, count, q_heads, heads, dim, max_len, causal_block, window, sinks).workspace_bytes;
 }
 
 nvfp4_status nvfp4_kv_attention_window(const nvfp4_heads* q, int64_t M, int32_t q_heads, const nvfp4_kv_cache* cache,
@@ -324,7 +324,8 @@ nvfp4_status nvfp4_kv_attention_window(const nvfp4_heads* q, int64_t M, int32_t 
     if (window < 1 || sinks < 0) return NVFP4_ERR_INVALID_ARGUMENT;
     a.window = window;
     a.sinks = sinks;
-    return run_attention(a, window_bound(max_len, causal_block, window, sinks), workspace, workspace_bytes, stream);
+    return run_attention(a, window_plan(M, seqs->count, q_heads, cache->heads, cache->dim, max_len, causal_block, window, sinks),
+                         workspace, workspace_bytes, stream);
 }
 
 size_t nvfp4_kv_attention_shared_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,

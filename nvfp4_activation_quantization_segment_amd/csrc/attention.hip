@@ -1070,7 +1070,10 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
 
 }  // namespace
 
-AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len) {
+constexpr int64_t kSlots = 512;  // workgroups that are in flight at a time, two on each CU
+
+static AttentionPlan plan_for(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len,
+                              int64_t slots) {
     const int32_t group = q_heads / kv_heads;
     AttentionPlan p;
     const int64_t blocks = clamp64(max_len, 0, (int64_t)1 << 31) / kKvBlock + (max_len % kKvBlock != 0);
@@ -1089,35 +1092,95 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
     // 274 among 255 empty slots, where the keys are not cut.)
     const int64_t most_seqs = B < M ? B : M;
     tiles = tiles < most_seqs ? most_seqs : tiles;
-    int64_t want = 512 / (tiles * kv_heads);
+    int64_t want = slots / (tiles * kv_heads);
     // Many sequences are of many lengths, which the host does not know: pieces
     // half as long even the workgroups out (32 sequences of 1 to 16,384 keys: 123
     // -> 115 us; 32 of 8192: 113 -> 110; 4 of 16,384: 27 -> 30, so few are left).
-    if (!p.wide && most_seqs >= 16 && want >= 2) want *= 2;
+    if (!p.wide && most_seqs >= 16 && want >= 2 && slots == kSlots) want *= 2;
     const int64_t most = p.wide ? blocks / 4 : blocks >= 32 ? blocks / 8 : 1;
     p.parts = (int32_t)clamp64(want < most ? want : most, 1, kMaxParts);
     p.workspace_bytes = p.parts == 1 ? 0 : (size_t)p.parts * (size_t)(M * q_heads) * (size_t)(dim + 2) * sizeof(float);
     return p;
 }
 
+AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len) {
+    return plan_for(M, B, q_heads, kv_heads, dim, max_len, kSlots);
+}
+
+// Where no sequence sees many more keys than the others (through a window, or
+// behind a prefix), fewer pieces: until one workgroup for each CU.  The last 4096
+// of 16,384 keys, 32 and 8 heads: 32 tokens 63 us in one piece, 70 in four and
+// their join; 8 tokens 29 in four, 30 in eight.  Behind a prefix they take the
+// CUs' other places (64 tokens, up to 1024 own keys: 45 us in one piece, 57 in four).
+static AttentionPlan few_parts_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len) {
+    const bool wide = plan_for(M, B, q_heads, kv_heads, dim, max_len, kSlots).wide;
+    return plan_for(M, B, q_heads, kv_heads, dim, max_len, wide ? kSlots : kSlots / 2);
+}
+
 // The first positions, the window and a tile's rows, each with what a cut inside a
 // block adds: so much of the past can 128 rows see (all of it without a causal mask).
-int64_t window_bound(int64_t max_len, int32_t causal, int32_t window, int32_t sinks) {
-    if (causal == 0) return max_len;
+AttentionPlan window_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len,
+                          int32_t causal, int32_t window, int32_t sinks) {
     const int64_t most = (int64_t)sinks + window + causal + kWideRows + 2 * kKvBlock;
-    return max_len < most ? max_len : most;
+    if (causal == 0 || max_len <= most) return attention_plan(M, B, q_heads, kv_heads, dim, max_len);
+    return few_parts_plan(M, B, q_heads, kv_heads, dim, most);
+}
+
+// The tiles and pieces of a prefix of n blocks for `rows` rows of a key/value
+// head: those of the smallest cost, in microseconds, of
+//   a workgroup's steps (a block of a wide tile, four of a narrow one, and one
+//   more to begin), longer where two workgroups share a CU, and
+//   the pieces' sums, written and read once.
+// Measured on prefixes of 16 to 512 blocks and 15 shapes of both dims: a step of a
+// wide tile 1.2 us alone on a CU and 1.8 with a second one (heads of 64: 0.8 and
+// 1.2), of a narrow one 2.1 and 3.3 (0.75 and 1.2).  64 tokens of 32 query and 8
+// key/value heads over 16,384 positions: 45 us with 12 or 16 pieces of wide tiles,
+// 58 with 32, 60 with narrow ones; 21 rows of 16 and 2 heads of 64 over 4032: 9.5
+// with 16 pieces of narrow tiles, 12.5 with 15 of wide ones.  More workgroups than
+// fit at once lose the keys that tiles share in L2 (500 rows of 32 heads over
+// 32,768 positions: 349 in 3 pieces, 379 in 7).  Where the sequences' own keys fill
+// the chip for a fourth of the prefix's time or more, it takes fewer places (100
+// tokens with 1500 own keys each behind 12,800: 107 us in 4 pieces, 134 in 16).
+// Over 21 shapes the rule is 3% slower on average than the best of 15 numbers of
+// pieces and both tiles, and 17% at most.
+static AttentionPlan prefix_plan(int64_t M, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t n, bool wide_only,
+                                 int64_t own_groups, int64_t own_blocks) {
+    AttentionPlan best = {wide_only, 0, 0};
+    const int64_t rows = M * (q_heads / kv_heads);
+    const double piece = (double)(M * q_heads) * (dim + 2) * 8 / 2.4e6;
+    const double narrow[2] = {dim == 128 ? 2.1 : 0.75, dim == 128 ? 3.3 : 1.2}, wide[2] = {dim == 128 ? 1.2 : 0.8, dim == 128 ? 1.8 : 1.2};
+    // half the bound: the sequences are of many lengths
+    const double own = own_groups < kSlots / 2 ? 0.0 : (double)own_groups * (double)own_blocks * narrow[0] / 8;
+    double least = 0.0;
+    for (int w = wide_only; w <= (rows > kRows ? 1 : 0); ++w) {
+        const int64_t T = w ? kWideRows : kRows, at_once = w ? 1 : kNarrowWaves;
+        const double* step = w ? wide : narrow;
+        const int64_t tiles = (rows + T - 1) / T * kv_heads, pieces = w ? (n + 1) / 2 : (n + 3) / 4;
+        const int64_t places = own >= (double)tiles * (double)n * step[0] / (4 * at_once) ? 192 : kSlots;
+        const int64_t fit = clamp64(places / tiles, 1, kMaxParts / 2 - 1);
+        for (int64_t p = 1; p <= (pieces < fit ? pieces : fit); ++p) {
+            const int64_t blocks = (n + p - 1) / p, steps = 1 + (blocks + at_once - 1) / at_once;
+            const int64_t rounds = (tiles * p + kSlots - 1) / kSlots;
+            const double cost = (double)(steps * rounds) * step[tiles * p > kSlots / 2] + (double)p * piece;
+            if (best.parts == 0 || cost < least) {
+                least = cost;
+                best.wide = w != 0;
+                best.parts = (int32_t)p;
+            }
+        }
+    }
+    return best;
 }
 
 SharedPlan shared_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len, int64_t shared) {
     SharedPlan p;
     const int64_t common = shared * kKvBlock;
-    p.own = attention_plan(M, B, q_heads, kv_heads, dim, max_len > common ? max_len - common : 0);
+    p.own = few_parts_plan(M, B, q_heads, kv_heads, dim, max_len > common ? max_len - common : 0);
     p.own.parts = p.own.parts < kOwnParts ? p.own.parts : kOwnParts;
-    const int64_t rows = M * (q_heads / kv_heads);
-    p.prefix.wide = rows > kRows;
-    const int64_t T = p.prefix.wide ? kWideRows : kRows, tiles = (rows + T - 1) / T;
-    const int64_t want = 512 / (tiles * kv_heads), most = p.prefix.wide ? shared / 4 : shared / 8;
-    p.prefix.parts = (int32_t)clamp64(want < most ? want : most, 1, kMaxParts - kOwnParts);
+    const int64_t group = q_heads / kv_heads, T = p.own.wide ? kWideRows : kRows;
+    const int64_t own_groups = tile_first(M, B, group, T, tiles_per_row(M, B, group, T)) * kv_heads * p.own.parts;
+    const int64_t own_blocks = max_len > common ? (clamp64(max_len, 0, (int64_t)1 << 31) - common) / kKvBlock + 1 : 0;
+    p.prefix = prefix_plan(M, q_heads, kv_heads, dim, shared, p.own.wide, own_groups, own_blocks);
     p.workspace_bytes = (size_t)(p.prefix.parts + p.own.parts) * (size_t)(M * q_heads) * (size_t)(dim + 2) * sizeof(float);
     return p;
 }
@@ -1156,6 +1219,21 @@ static void attention_join(const AttentionArgs& a, hipStream_t s) {
         attention_join_kernel<D, 1, 2><<<four, threads, 0, s>>>(a);
 }
 
+// The join of a batch: where the rows alone fill the chip, a wave takes a row and all
+// its parts.
+template <int D>
+static void attention_join_batch(const AttentionArgs& a, hipStream_t s) {
+    const int64_t rows = a.seqs.M * a.q_heads;
+    if (rows < 1024 || a.all_parts <= 8) return attention_join<D>(a, s);
+    const dim3 four((unsigned)((rows + 3) / 4)), threads(256);
+    if (a.all_parts > 32)
+        attention_join_kernel<D, 1, 64><<<four, threads, 0, s>>>(a);
+    else if (a.all_parts > 16)
+        attention_join_kernel<D, 1, 32><<<four, threads, 0, s>>>(a);
+    else
+        attention_join_kernel<D, 1, 16><<<four, threads, 0, s>>>(a);
+}
+
 template <int D>
 static void attention_of(const AttentionArgs& a, hipStream_t s) {
     if (a.window > 0)
@@ -1191,7 +1269,7 @@ static void attention_shared_of(const AttentionArgs& a, const SharedPlan& p, con
         attention_shared_kernel<D, true, false><<<grid, block, 0, s>>>(prefix, own, g);
     else
         attention_shared_kernel<D, false, false><<<grid, block, 0, s>>>(prefix, own, g);
-    attention_join<D>(a, s);
+    attention_join_batch<D>(a, s);
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s) {

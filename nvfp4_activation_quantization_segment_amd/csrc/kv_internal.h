@@ -147,8 +147,9 @@ struct AttentionPlan {
 AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t s);
 
-// A bound on the keys that a tile sees through a window, for attention_plan.
-int64_t window_bound(int64_t max_len, int32_t causal, int32_t window, int32_t sinks);
+// The same through a window.
+AttentionPlan window_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len,
+                          int32_t causal, int32_t window, int32_t sinks);
 
 // The workgroups of a call over a shared prefix: tiles of a head and all of them.
 struct SharedGrid {
