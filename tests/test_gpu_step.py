@@ -119,6 +119,21 @@ def test_norms_of_what_is_not_finite(nv):
         assert torch.equal(q.cpu().isnan(), bad[:, by_axis][:, None, :].expand(-1, 2, -1))
 
 
+def test_norm_of_rows_further_apart_than_2_gib(nv):
+    """Offsets past 32 bits, in elements and in bytes."""
+    far = (1 << 31) + 64
+    flat = torch.zeros(2 * far + 512, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(flat, (3, 2, 128), (far, 128, 1))
+    host = normal(gen(8), 3, 2, 128)
+    x.copy_(host)
+    out = torch.as_strided(flat, (3, 2, 128), (far, 128, 1), 256)
+    tables = tables_for([64], [9])
+    positions = torch.tensor([[8], [0], [5]], dtype=torch.int32)
+    nv.norm_rope(x, tables=[t.cuda() for t in tables], positions=positions.cuda(), q_out=out)
+    check_norm(out, host, None, 1e-6, tables, positions, False)
+    assert same(x, host)
+
+
 def test_norm_rope_of_no_rows(nv):
     x = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     q, k = nv.norm_rope(x, x)
@@ -213,6 +228,37 @@ def test_extend_with_many_requests_without_rows_between(nv, rows):
     past, table, stack = [10] * count, [[b, -1] for b in range(count)], list(range(count, count + 9))
     step, t = run_extend(nv, past, more, table, stack, rows)
     check_extend(step, t, step_ref.extend(past, more, table, list(stack), rows), table)
+
+
+@pytest.mark.parametrize("rows", [50, 4500])
+def test_extend_into_unaligned_outputs(nv, rows):
+    """Positions and slots at any multiple of their elements; what lies beside them is left alone."""
+    past, more, table, stack = make_requests(rows, 30, 300, rows // 20, 30, 400)
+    want = step_ref.extend(past, more, [list(t) for t in table], list(stack), rows)
+    for shift in (1, 2, 3):
+        positions = torch.full((rows + 4, 1), -8, dtype=torch.int32, device="cuda")
+        slots = torch.full((rows + 4,), -8, dtype=torch.int64, device="cuda")
+        other = nv.KvStep.empty(30, rows)
+        step = nv.KvStep(other.row_start, other.lens, other.free_count, other.missing, positions[shift:shift + rows],
+                         slots[shift:shift + rows], other.workspace)
+        nv.kv_extend(i32(past), i32(more), i32(table), i32(stack), i32([len(stack)]), step)
+        assert positions.flatten().tolist() == [-8] * shift + want["positions"] + [-8] * (4 - shift)
+        assert slots.tolist() == [-8] * shift + want["slots"] + [-8] * (4 - shift)
+
+
+def test_extend_without_positions_or_slots(nv):
+    """Either is left out by the C entry point's null pointer."""
+    past, more, table, stack = make_requests(3, 20, 300, 40, 8, 90)
+    want = step_ref.extend(past, more, [list(t) for t in table], list(stack), 500)
+    for which in ((True, False), (False, True), (False, False)):
+        t, free, s = i32(table), i32(stack), nv.KvStep.empty(20, 500)
+        s.positions.fill_(-8), s.slots.fill_(-8)
+        nv.nvfp4_kv_extend(nv.make_kv_tables(t, free), i32(past), i32(more), i32([len(stack)]), 500, s.row_start, s.lens,
+                           s.free_count, s.missing, s.positions if which[0] else None, s.slots if which[1] else None,
+                           s.workspace, s.workspace.numel())
+        assert s.row_start.tolist() == want["row_start"] and s.lens.tolist() == want["lens"]
+        assert s.positions.flatten().tolist() == (want["positions"] if which[0] else [-8] * 500)
+        assert s.slots.tolist() == (want["slots"] if which[1] else [-8] * 500)
 
 
 def test_extend_with_a_stack_that_makes_no_sense(nv):
@@ -560,6 +606,8 @@ class Serving:
         self.more, self.done = i32([0] * self.count), i32([0] * self.count)
         self.base = i32([shared_blocks * BLOCK] * self.count)
         self.x = torch.zeros(self.rows, 12, self.dim, dtype=torch.bfloat16, device="cuda")
+        # rows of no request are not written by the attention, and the quantizer's one scale is that of all rows
+        self.o = torch.zeros(self.rows, 4 * self.heads, self.dim, dtype=torch.bfloat16, device="cuda")
 
     def step(self):
         nv, h = self.nv, self.heads
@@ -571,11 +619,10 @@ class Serving:
                             split=True)
         nv.kv_write(self.cache, k, self.x[:, 5 * h:], s.row_start, s.lens, self.table)
         if self.shared is not None:
-            o = nv.kv_attention(q, self.cache, s.row_start, s.lens, self.table, causal_block=1, shared=self.shared)
+            nv.kv_attention(q, self.cache, s.row_start, s.lens, self.table, causal_block=1, shared=self.shared, out=self.o)
         else:
-            o = nv.kv_attention(q, self.cache, s.row_start, s.lens, self.table, causal_block=1, window=100, sinks=4)
-        self.o = o
-        return nv.quantize(o.reshape(self.rows, -1))
+            nv.kv_attention(q, self.cache, s.row_start, s.lens, self.table, causal_block=1, window=100, sinks=4, out=self.o)
+        return nv.quantize(self.o.reshape(self.rows, -1))
 
 
 @pytest.mark.parametrize("shared", [0, 3])
@@ -630,7 +677,7 @@ def test_a_serving_step_eager_and_captured(nv, shared):
         o, tol = step_ref.attention(made.double().numpy(), ref, rs, lens, np.array(table), np.float64(np.float32(128 ** -0.5)), 1,
                                     *((0, 0) if shared else (100, 4)), shared=np.arange(shared) if shared else None)
         check(eager.o[:used], o[:used], tol[:used])
-        assert all(a.shape == b.shape for a, b in zip(out, graph_out))
+        assert all(torch.equal(a, b) for a, b in zip(out, graph_out)) and bool(out[2].isfinite().all()), f"replay {turn}"
         assert same(eager.o[:used], captured.o[:used]), f"replay {turn}"
         for name in ("lens", "table", "n_free", "free"):
             assert torch.equal(getattr(eager, name), getattr(captured, name)), name
