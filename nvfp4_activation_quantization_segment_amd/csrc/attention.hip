@@ -41,9 +41,9 @@ __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000
 // What the rows of a launch see of the past.
 //   PLAIN   every key below their limit
 //   WINDOW  of these, the last `window` positions and the first `sinks`
-//   PREFIX  rows of all sequences against the blocks that they share
-//   OWN     rows against their own sequence's keys behind the shared blocks
-enum Mode { PLAIN, WINDOW, PREFIX, OWN };
+//   SHARED  rows of all sequences the blocks that they share (a.prefix), or rows
+//           their own sequence's keys behind these
+enum Mode { PLAIN, WINDOW, SHARED };
 
 struct Tile {
     bool any;
@@ -61,7 +61,7 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int64_t unit, 
     Tile t;
     t.any = false;
     const SeqArgs& q = a.seqs;
-    if constexpr (MODE == PREFIX) {
+    if (MODE == SHARED && a.prefix) {
         // one run of rows, from the first sequence's to the last's
         const RowRange r = row_range(q.row_start[0], q.row_start[q.B], q.M);
         const int64_t rows = (r.last - r.first) * a.group;
@@ -88,7 +88,7 @@ __device__ __forceinline__ Tile find_tile(const AttentionArgs& a, int64_t unit, 
     t.rows = (int32_t)(n * a.group);
     t.len = at.len;
     t.bad = kv_length_bad(t.len, q.table_blocks);
-    if constexpr (MODE == OWN) t.bad = t.bad || t.len - t.n < a.shared * kKvBlock;
+    if constexpr (MODE == SHARED) t.bad = t.bad || t.len - t.n < a.shared * kKvBlock;
     return t;
 }
 
@@ -135,9 +135,9 @@ __device__ __forceinline__ Blocks blocks_of(const AttentionArgs& a, int32_t seen
         const KvWindowBlocks w = kv_window_blocks(n, low, a.sinks);
         return Blocks{w.count, w.first, w.skipped};
     }
-    if constexpr (MODE == OWN) {
-        const int32_t shared = (int32_t)a.shared;
-        return Blocks{n > shared ? n - shared : 0, 0, shared};
+    if constexpr (MODE == SHARED) {
+        const int32_t skipped = a.prefix ? 0 : (int32_t)a.shared;
+        return Blocks{n > skipped ? n - skipped : 0, 0, skipped};
     }
     return Blocks{n, n, 0};
 }
@@ -506,6 +506,7 @@ __device__ __forceinline__ void narrow_tile(const AttentionArgs& a, NarrowShared
 #pragma unroll
                 for (int d = 0; d < kDT; ++d) {
                     f32x16 hit = f32x16{};
+                    asm volatile("" : "+v"(s[0]), "+v"(s[1]));  // taken anew for each, not held in registers
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         u32x4 nans;
@@ -980,32 +981,28 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
 // other.
 // ---------------------------------------------------------------------------
 template <int D, bool PREFIX_WIDE, bool OWN_WIDE>
-__global__ __launch_bounds__(64 * kWideWaves, 2) void attention_shared_kernel(AttentionArgs prefix, AttentionArgs own,
-                                                                              SharedGrid g) {
+__global__ __launch_bounds__(64 * kWideWaves, 2) void attention_shared_kernel(AttentionArgs a, SharedGrid g) {
     static_assert(kNarrowWaves == kWideWaves, "one size of workgroup");
     __shared__ union {
         NarrowShared<D> narrow;
-        WideShared<D, PREFIX> prefix_wide;
-        WideShared<D, OWN> own_wide;
+        WideShared<D, SHARED> wide;
     } share;
     uint32_t at = blockIdx.y * gridDim.x + blockIdx.x;
-    const uint32_t heads = own.cache.heads;
-    if (at < g.prefix_groups) {
-        const uint32_t each = g.prefix_units * heads, z = at / each, x = at - z * each;
-        if constexpr (PREFIX_WIDE)
-            wide_tile<D, PREFIX>(prefix, share.prefix_wide, wide_place(x, z, g.prefix_units, heads));
-        else
-            narrow_tile<D, PREFIX>(prefix, share.narrow,
-                                   narrow_place(x % g.prefix_units, x / g.prefix_units, z, g.prefix_units));
-        return;
-    }
-    at -= g.prefix_groups;
-    if (at >= g.own_groups) return;
-    const uint32_t each = g.own_units * heads, z = at / each, x = at - z * each;
-    if constexpr (OWN_WIDE)
-        wide_tile<D, OWN>(own, share.own_wide, wide_place(x, z, g.own_units, heads));
+    const bool of_prefix = at < g.prefix_groups;
+    // one way for both, with these taken by selects
+    a.seqs.table = of_prefix ? g.shared : a.seqs.table;
+    a.causal = of_prefix ? 0 : a.causal;
+    a.parts = of_prefix ? a.first_part : a.parts;
+    a.first_part = of_prefix ? 0 : a.first_part;
+    a.prefix = of_prefix;
+    const uint32_t units = of_prefix ? g.prefix_units : g.own_units, heads = a.cache.heads, each = units * heads;
+    at -= of_prefix ? 0 : g.prefix_groups;
+    if (!of_prefix && at >= g.own_groups) return;
+    const uint32_t z = at / each, x = at - z * each;
+    if (of_prefix ? PREFIX_WIDE : OWN_WIDE)
+        wide_tile<D, SHARED>(a, share.wide, wide_place(x, z, units, heads));
     else
-        narrow_tile<D, OWN>(own, share.narrow, narrow_place(x % g.own_units, x / g.own_units, z, g.own_units));
+        narrow_tile<D, SHARED>(a, share.narrow, narrow_place(x % units, x / units, z, units));
 }
 
 // Joins the parts of each row; rows that no sequence has are left alone.  WAVES
@@ -1246,10 +1243,7 @@ static void attention_of(const AttentionArgs& a, hipStream_t s) {
 template <int D>
 static void attention_shared_of(const AttentionArgs& a, const SharedPlan& p, const int32_t* shared, hipStream_t s) {
     const int64_t heads = a.cache.heads, rows = a.seqs.M * a.group;
-    AttentionArgs prefix = a, own = a;
-    prefix.seqs.table = shared;
-    prefix.causal = 0;
-    prefix.parts = p.prefix.parts;
+    AttentionArgs own = a;
     own.parts = p.own.parts;
     own.first_part = p.prefix.parts;
     const int64_t T = p.own.wide ? kWideRows : kRows, PT = p.prefix.wide ? kWideRows : kRows;
@@ -1257,6 +1251,7 @@ static void attention_shared_of(const AttentionArgs& a, const SharedPlan& p, con
     // both below 2^30: M q_heads is at most 2^28, tiles are at most 2 a row and
     // head, and the keys are cut only where there are few of them
     SharedGrid g;
+    g.shared = shared;
     g.prefix_units = (uint32_t)((rows + PT - 1) / PT);
     g.own_units = (uint32_t)tile_first(a.seqs.M, a.seqs.B, a.group, T, own.seqs.per_row);
     g.prefix_groups = (uint32_t)(g.prefix_units * heads * p.prefix.parts);
@@ -1264,11 +1259,11 @@ static void attention_shared_of(const AttentionArgs& a, const SharedPlan& p, con
     const uint32_t groups = g.prefix_groups + g.own_groups, row = groups < (1u << 20) ? groups : 1u << 20;
     const dim3 grid(row, (groups + row - 1) / row), block(64 * kWideWaves);
     if (p.prefix.wide && p.own.wide)
-        attention_shared_kernel<D, true, true><<<grid, block, 0, s>>>(prefix, own, g);
+        attention_shared_kernel<D, true, true><<<grid, block, 0, s>>>(own, g);
     else if (p.prefix.wide)
-        attention_shared_kernel<D, true, false><<<grid, block, 0, s>>>(prefix, own, g);
+        attention_shared_kernel<D, true, false><<<grid, block, 0, s>>>(own, g);
     else
-        attention_shared_kernel<D, false, false><<<grid, block, 0, s>>>(prefix, own, g);
+        attention_shared_kernel<D, false, false><<<grid, block, 0, s>>>(own, g);
     attention_join_batch<D>(a, s);
 }
 

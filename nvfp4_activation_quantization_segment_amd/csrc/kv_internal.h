@@ -123,6 +123,7 @@ struct AttentionArgs {
     int32_t window;    // last positions that a row sees, 0: all
     int32_t sinks;     // and first ones
     int64_t shared;    // blocks of the shared prefix
+    int32_t prefix;    // the rows are taken against it (else against what is behind it)
 };
 
 hipError_t launch_rope_table(float2* table, int64_t rows, int32_t pairs, double theta, hipStream_t s);
@@ -151,8 +152,10 @@ hipError_t launch_attention(const AttentionArgs& a, hipStream_t s);
 AttentionPlan window_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len,
                           int32_t causal, int32_t window, int32_t sinks);
 
-// The workgroups of a call over a shared prefix: tiles of a head and all of them.
+// A call over a shared prefix: its workgroups, tiles of a head and all of them.  (The
+// pieces of the prefix are those before the sequences' first one.)
 struct SharedGrid {
+    const int32_t* shared;  // the prefix's blocks
     uint32_t prefix_units, prefix_groups, own_units, own_groups;
 };
 
