@@ -692,6 +692,17 @@ def _empty(dev: torch.device, stream, shape, dtype=torch.bfloat16) -> torch.Tens
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _output_like(name: str, t, x: torch.Tensor, stream, shape):
+    """The caller's output once checked, or a new one of x's type on x's device, and its description."""
+    if t is not None:
+        return t, make_heads(name, t, shape)
+    if stream is None:  # of the stream that is current there, which the call runs on
+        t = x.new_empty(shape)
+    else:
+        t = _empty(x.device, stream, shape, x.dtype)
+    return t, Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
+
+
 def _output(name: str, t, dev: torch.device, stream, shape):
     """The caller's output once checked, or a new one, and its description."""
     if t is not None:
@@ -787,9 +798,9 @@ def norm_rope(q: torch.Tensor, k: torch.Tensor | None = None, q_weight: torch.Te
             raise ValueError(f"k: expected [{rows}, heads, {dim}], got {list(k.shape)}")
     wq, wk = _norm_weight("q_weight", q_weight, dim, dev), _norm_weight("k_weight", k_weight, dim, dev)
     r = None if positions is None else make_rope_params(tables, positions, rows, split, dev)
-    q_out, ho = _output("q_out", q_out, dev, stream, shape)
+    q_out, ho = _output_like("q_out", q_out, q, stream, shape)
     if k is not None:
-        k_out, ko = _output("k_out", k_out, dev, stream, k.shape)
+        k_out, ko = _output_like("k_out", k_out, k, stream, k.shape)
     if rows:
         _call("nvfp4_norm_rope", lib.nvfp4_norm_rope, dev, stream, hq, heads, wq, hk, k_heads, wk, rows, dim, float(eps), r,
               ho, ko)
@@ -953,11 +964,11 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
     else:
         name, fn, size_of = "nvfp4_kv_attention", lib.nvfp4_kv_attention, lib.nvfp4_kv_attention_workspace_bytes
         sizes, args = (max_len,), (scale, causal_block, max_len)
-    out, ho = _output("out", out, dev, stream, shape)
+    out, ho = _output_like("out", out, q, stream, shape)
     if workspace is None and rows:
         need = size_of(rows, s.count, q_heads, c.heads, dim, *sizes)
         if need:
-            workspace = _empty(dev, stream, (need,), torch.uint8)
+            workspace = q.new_empty((need,), dtype=torch.uint8) if stream is None else _empty(dev, stream, (need,), torch.uint8)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -1103,9 +1114,9 @@ def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free
     lens_at, done_at = _int32("lens", lens, n, dev), _int32("done", done, n, dev)
     count_at = _int32("free_count", free_count, 1, dev)
     if lens_out is None:
-        lens_out = _empty(dev, stream, (n,), torch.int32)
+        lens_out = lens.new_empty((n,)) if stream is None else _empty(dev, stream, (n,), torch.int32)
     if free_count_out is None:
-        free_count_out = _empty(dev, stream, (1,), torch.int32)
+        free_count_out = lens.new_empty((1,)) if stream is None else _empty(dev, stream, (1,), torch.int32)
     if workspace is None:
         need = lib.nvfp4_kv_release_workspace_bytes(n)
         if need:
