@@ -1,5 +1,7 @@
 // Attention over the paged 8-bit key/value cache:
-//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - max),  j < limit(row).
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - max),  j < limit(row),
+// of all these j, of those in a window and the first ones, or of a prefix that
+// many sequences share and of their own keys, joined.
 //
 // The rows of a tile are the queries of one sequence and one key/value head,
 // (token, query head of the group) in that order, 32 to a wave.  Scores are
@@ -19,8 +21,9 @@
 // sum is taken before that rounding).  Two bf16 halves of each p would double
 // these products; as it is the outputs' error against 64 bits is 0.0021 to 0.0023
 // of their size, where binary32 probabilities and the output's own rounding give
-// 0.0016 to 0.0017.  Scores, maxima, sums and outputs are held in
-// binary32.
+// 0.0016 to 0.0017.  (Through a window and over a prefix the rounded ones are
+// summed: where a few keys have the weight the error was 0.0025, and is 0.0024.)
+// Scores, maxima, sums and outputs are held in binary32.
 #include "kv_device.h"
 
 namespace nvfp4 {
@@ -121,6 +124,15 @@ __device__ __forceinline__ int32_t low_of_row(const AttentionArgs& a, const Tile
     return low_of(a, t, __builtin_amdgcn_readfirstlane(at / a.group));
 }
 
+// A window's tile goes over the blocks that some of its rows see, no others: 32
+// tokens of 32 query and 8 key/value heads through 4096 of up to 16,384 keys, 240 MB,
+// take 49 us (all keys: 118), 4.9 TB/s; prompts of 12,000 rows through 1000 keys
+// 207 to 220 us on different cards (all keys: 361), of 18 blocks a tile 15.7 full
+// ones' worth of keys.  A path of its own for the blocks at a window's ends, which
+// passes over 32 keys that a wave does not see, made these 256 (accumulators copied
+// between the paths); tiles that begin at a common block and go round, so as to
+// read the same ones at a time, changed nothing.
+//
 // The blocks that a tile goes over, in order: what it sees of the first ones, and
 // then those from the one where `jump` leads.
 struct Blocks {
@@ -978,7 +990,13 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
 // A batch over a shared prefix: the first workgroups take tiles of all sequences'
 // rows against pieces of the prefix, the others each sequence's rows against its
 // own keys, in one launch, so that the loads of the one fill the waits of the
-// other.
+// other.  64 tokens of 32 query and 8 key/value heads, up to 1024 own keys each
+// behind 16,384, 103 MB: 40 us and 5 for the join (two launches after one another
+// 48 and 11; the prefix alone takes 32, the own keys alone 26); what is left is the
+// pieces' sums (13 of them, 14 MB written and read) and the chains of loads at both
+// ends.  500 rows of 32 heads over 32,768: 304 to 335 us, 950 TFLOP/s, the matrix
+// pipes busy 39% of the cycles: 432 workgroups for 512 places, and 18 tiles of 128
+// rows that hold 17.5.
 // ---------------------------------------------------------------------------
 template <int D, bool PREFIX_WIDE, bool OWN_WIDE>
 __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_shared_kernel(AttentionArgs a, SharedGrid g) {

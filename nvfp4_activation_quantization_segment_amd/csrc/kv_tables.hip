@@ -49,9 +49,11 @@ __device__ __forceinline__ int32_t blocks_of(int64_t len, int64_t table_blocks) 
 // block need not wait for one another.
 //
 // Up to 1024 requests, every workgroup takes the sums of all of them by itself,
-// into LDS, and then its 4096 rows: one launch.  What that costs is the chain of
-// loads (past; a request's last block; free blocks), about 3 us whatever the
-// number of rows.  A step in place whose rows need several workgroups, of which
+// into LDS, and then its 4096 rows: one launch.  A request marks its first row,
+// and a running maximum over the rows finds each row's request (a search for each
+// took 12 us where this takes 8).  What it costs is the chain of loads (past; a
+// request's last block; free blocks): 32 tokens 4.2 us in a graph, a million rows
+// of 1001 requests 8.2, 12 MB written.  A step in place whose rows need several workgroups, of which
 // one writes what the others read, and more requests than that take a launch for
 // the sums and one for the rows.
 // ---------------------------------------------------------------------------
@@ -323,7 +325,8 @@ __global__ __launch_bounds__(256) void extend_rows_kernel(ExtendArgs a) {
 // the first ones of all of them in flight together and kept in registers.  Their
 // places on the stack follow from how many blocks the requests before give back:
 // one workgroup finds that out in LDS, several of them by a launch that counts
-// before the one that moves.
+// before the one that moves.  32 requests 4.3 us in a graph, 4099 requests 9.7 (one
+// after the other by a wave, tables read twice: 11.4 and 17.5).
 // ---------------------------------------------------------------------------
 constexpr int kEach = 2;                 // requests of a wave
 constexpr int kKept = 4;                 // times 64 entries of each that it keeps
