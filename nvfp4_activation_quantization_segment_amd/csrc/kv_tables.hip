@@ -37,86 +37,6 @@ __device__ __forceinline__ int64_t group_scan(int64_t x, int64_t* slot, int64_t&
     return x + before;
 }
 
-// Blocks that `len` positions take of a table.
-__device__ __forceinline__ int32_t blocks_of(int64_t len, int64_t table_blocks) {
-    return (int32_t)clamp64(len <= 0 ? 0 : (len + kKvBlock - 1) / kKvBlock, 0, table_blocks);
-}
-
-// ---------------------------------------------------------------------------
-// Extending.  The requests come first: rows and blocks of each, as running sums.
-// Then the rows: each finds its request, and the row that starts a block writes
-// the table's entry.  A block's number comes from the sums alone, so rows of one
-// block need not wait for one another.
-//
-// Up to 1024 requests, every workgroup takes the sums of all of them by itself,
-// into LDS, and then its 4096 rows: one launch.  A request marks its first row,
-// and a running maximum over the rows finds each row's request (a search for each
-// took 12 us where this takes 8).  What it costs is the chain of loads (past; a
-// request's last block; free blocks): 32 tokens 4.2 us in a graph, a million rows
-// of 1001 requests 8.2, 12 MB written.  A step in place whose rows need several workgroups, of which
-// one writes what the others read, and more requests than that take a launch for
-// the sums and one for the rows.
-// ---------------------------------------------------------------------------
-// One request's part of a round of sums.
-struct Asked {
-    int64_t past, rows, blocks;  // held; rows given, blocks taken
-    int64_t first, taken;        // its first row, blocks of the requests before
-};
-struct Sums {
-    int64_t rows, blocks;
-};
-
-__device__ __forceinline__ Asked ask(const ExtendArgs& a, int64_t b, Sums& sums, int64_t* slot) {
-    Asked q;
-    q.past = b < a.B ? a.past[b] : 0;
-    const int64_t want = b < a.B ? clamp64(a.more[b], 0, INT32_MAX - clamp64(q.past, 0, INT32_MAX)) : 0;
-    int64_t rows, blocks;
-    const int64_t end = sums.rows + group_scan(want, slot, rows);
-    q.first = clamp64(end - want, 0, a.M);
-    q.rows = clamp64(end, 0, a.M) - q.first;
-    q.blocks = blocks_of(q.past + q.rows, a.table_blocks) - blocks_of(q.past, a.table_blocks);
-    q.taken = sums.blocks + group_scan(q.blocks, slot, blocks) - q.blocks;
-    sums.rows += rows;
-    sums.blocks += blocks;
-    return q;
-}
-
-__device__ __forceinline__ void write_asked(const ExtendArgs& a, int64_t b, const Asked& q) {
-    if (b < a.B) {
-        a.row_start[b + 1] = (int32_t)(q.first + q.rows);
-        a.lens[b] = (int32_t)(q.past + q.rows);
-    }
-}
-__device__ __forceinline__ void write_stack(const ExtendArgs& a, int64_t had, int64_t blocks) {
-    a.row_start[0] = 0;
-    *a.free_left = (int32_t)(had > blocks ? had - blocks : 0);
-    *a.missing = (int32_t)(blocks > had ? blocks - had : 0);
-}
-
-// Position, and slot, of a row of a request; the table's entry where it starts a
-// block.  last: the entry of the request's last block, where that has room left.
-__device__ __forceinline__ void write_row(const ExtendArgs& a, int64_t row, int64_t b, int64_t past, int64_t first,
-                                          int64_t taken, int64_t had, int32_t last) {
-    const int64_t pos = past + row - first, at = floor_div(pos, kKvBlock);
-    int64_t slot = -1;
-    if (pos >= 0 && at < a.table_blocks) {
-        const int64_t fresh = at - blocks_of(past, a.table_blocks), place = had - 1 - taken - fresh;
-        const int32_t page = fresh < 0 ? last : place >= 0 ? a.free_blocks[place] : -1;
-        if (fresh >= 0 && pos % kKvBlock == 0) a.table[b * a.ld_table + at] = page;
-        slot = page < 0 ? -1 : (int64_t)page * kKvBlock + pos % kKvBlock;
-    }
-    if (a.positions) a.positions[row] = (int32_t)pos;
-    if (a.slots) a.slots[row] = slot;
-}
-__device__ __forceinline__ void write_no_row(const ExtendArgs& a, int64_t row) {
-    if (a.positions) a.positions[row] = -1;
-    if (a.slots) a.slots[row] = -1;
-}
-// Column of the block that a request's next position falls into, where it has begun.
-__device__ __forceinline__ int64_t last_column(const ExtendArgs& a, int64_t past) {
-    return past > 0 && past % kKvBlock != 0 && past / kKvBlock < a.table_blocks ? past / kKvBlock : -1;
-}
-
 // Inclusive sum, or maximum, over a wave's lanes of what `combine` joins.
 template <class Combine>
 __device__ __forceinline__ uint32_t wave_scan(uint32_t x, Combine combine) {
@@ -153,6 +73,110 @@ __device__ __forceinline__ uint32_t group_scan32(uint32_t x, uint32_t* slot, uin
 __device__ __forceinline__ uint32_t add_up(uint32_t x, uint32_t y) { return __builtin_elementwise_add_sat(x, y); }
 __device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) { return x > y ? x : y; }
 
+// Blocks that `len` positions take of a table.
+__device__ __forceinline__ int32_t blocks_of(int64_t len, int64_t table_blocks) {
+    return (int32_t)clamp64(len <= 0 ? 0 : (len + kKvBlock - 1) / kKvBlock, 0, table_blocks);
+}
+
+// ---------------------------------------------------------------------------
+// Extending.  The requests come first: rows and blocks of each, as running sums.
+// Then the rows: each finds its request, and the row that starts a block writes
+// the table's entry.  A block's number comes from the sums alone, so rows of one
+// block need not wait for one another.
+//
+// Up to 4096 requests, every workgroup takes the sums of all of them by itself,
+// into LDS, and then its 4096 rows: one launch.  A request marks its first row,
+// and a running maximum over the rows finds each row's request (a search for each
+// took 12 us where this takes 8).  What it costs is the chain of loads (past; a
+// request's last block; free blocks): 32 tokens 4.2 us in a graph, a million rows
+// of 1001 requests 8.2, 12 MB written.  A step in place whose rows need several workgroups, of which
+// one writes what the others read, and more requests than that take a launch for
+// the sums and one for the rows.
+// ---------------------------------------------------------------------------
+// Requests b .. b + R - 1 of a thread: what they get, and the sums before them.
+template <int R>
+struct Asked {
+    int32_t past[R];
+    int32_t first[R], rows[R];    // rows given
+    int32_t taken[R], blocks[R];  // blocks that the requests before take, and they
+};
+// The requests before a round, and after it all of them.
+struct Sums {
+    uint32_t rows, blocks;  // rows stop at 2^32 - 1, far above M
+};
+
+template <int R>
+__device__ __forceinline__ Asked<R> ask(const ExtendArgs& a, int64_t b, Sums& sums, uint32_t (&slot)[2][kWaves]) {
+    Asked<R> q;
+    const int32_t M = (int32_t)a.M;
+    uint32_t want[R], rows = 0, blocks = 0, all;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        q.past[i] = b + i < a.B ? a.past[b + i] : 0;
+        const int32_t asked = b + i < a.B ? a.more[b + i] : 0, room = INT32_MAX - (q.past[i] > 0 ? q.past[i] : 0);
+        want[i] = asked < 0 ? 0 : asked < room ? asked : room;
+        rows = add_up(rows, want[i]);
+    }
+    uint32_t start = add_up(sums.rows, group_scan32(rows, slot[0], all, add_up));
+    sums.rows = add_up(sums.rows, all);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        q.first[i] = start < (uint32_t)M ? (int32_t)start : M;
+        q.rows[i] = want[i] < (uint32_t)(M - q.first[i]) ? (int32_t)want[i] : M - q.first[i];
+        q.blocks[i] = blocks_of((int64_t)q.past[i] + q.rows[i], a.table_blocks) - blocks_of(q.past[i], a.table_blocks);
+        start = add_up(start, want[i]);
+        blocks += (uint32_t)q.blocks[i];
+    }
+    uint32_t taken = sums.blocks + group_scan32(blocks, slot[1], all, add_up);
+    sums.blocks += all;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        q.taken[i] = (int32_t)taken;
+        taken += (uint32_t)q.blocks[i];
+    }
+    return q;
+}
+
+template <int R>
+__device__ __forceinline__ void write_asked(const ExtendArgs& a, int64_t b, const Asked<R>& q) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (b + i < a.B) {
+            a.row_start[b + i + 1] = q.first[i] + q.rows[i];
+            a.lens[b + i] = q.past[i] + q.rows[i];
+        }
+}
+__device__ __forceinline__ void write_stack(const ExtendArgs& a, int64_t had, int64_t blocks) {
+    a.row_start[0] = 0;
+    *a.free_left = (int32_t)(had > blocks ? had - blocks : 0);
+    *a.missing = (int32_t)(blocks > had ? blocks - had : 0);
+}
+
+// Position, and slot, of a row of a request; the table's entry where it starts a
+// block.  last: the entry of the request's last block, where that has room left.
+__device__ __forceinline__ void write_row(const ExtendArgs& a, int64_t row, int64_t b, int64_t past, int64_t first,
+                                          int64_t taken, int64_t had, int32_t last) {
+    const int64_t pos = past + row - first, at = floor_div(pos, kKvBlock);
+    int64_t slot = -1;
+    if (pos >= 0 && at < a.table_blocks) {
+        const int64_t fresh = at - blocks_of(past, a.table_blocks), place = had - 1 - taken - fresh;
+        const int32_t page = fresh < 0 ? last : place >= 0 ? a.free_blocks[place] : -1;
+        if (fresh >= 0 && pos % kKvBlock == 0) a.table[b * a.ld_table + at] = page;
+        slot = page < 0 ? -1 : (int64_t)page * kKvBlock + pos % kKvBlock;
+    }
+    if (a.positions) a.positions[row] = (int32_t)pos;
+    if (a.slots) a.slots[row] = slot;
+}
+__device__ __forceinline__ void write_no_row(const ExtendArgs& a, int64_t row) {
+    if (a.positions) a.positions[row] = -1;
+    if (a.slots) a.slots[row] = -1;
+}
+// Column of the block that a request's next position falls into, where it has begun.
+__device__ __forceinline__ int64_t last_column(const ExtendArgs& a, int64_t past) {
+    return past > 0 && past % kKvBlock != 0 && past / kKvBlock < a.table_blocks ? past / kKvBlock : -1;
+}
+
+constexpr int kMostEach = 4;  // requests of a thread
 constexpr int kRowsEach = 4;
 constexpr int kGroupRows = kThreads * kRowsEach;
 
@@ -164,36 +188,35 @@ struct __align__(16) Request {
     int32_t last;     // the entry of the block that has room left
 };
 
+template <int R>
 __global__ __launch_bounds__(kThreads) void extend_kernel(ExtendArgs a) {
-    __shared__ uint32_t slot[3][kWaves];
-    __shared__ Request request[kThreads];
+    __shared__ uint32_t slot[2][kWaves], rows_slot[kWaves];
+    __shared__ Request request[kThreads * R];
     __shared__ __align__(16) uint32_t mark[kGroupRows];  // request + 1 at its first row here
     const int32_t had = (int32_t)clamp64(*a.free_count, 0, a.capacity);
-    const int t = threadIdx.x;
+    const int t = threadIdx.x, b0 = R * t;
     const int32_t row0 = (int32_t)(blockIdx.x * kGroupRows), M = (int32_t)a.M;
     *reinterpret_cast<uint4*>(&mark[kRowsEach * t]) = make_uint4(0, 0, 0, 0);
-    const int32_t past = t < a.B ? a.past[t] : 0, asked = t < a.B ? a.more[t] : 0;
-    // a request's last entry is on its way while the sums are taken
-    const int64_t column = last_column(a, past);
-    const int32_t entry = column >= 0 ? a.table[t * a.ld_table + column] : -1;
-    const int32_t room = INT32_MAX - (past > 0 ? past : 0);
-    const uint32_t want = asked < 0 ? 0 : asked < room ? asked : room;
-    uint32_t total, taken_all;
-    const uint32_t start = group_scan32(want, slot[0], total, add_up);  // saturates: far above M
-    const int32_t first = start < (uint32_t)M ? (int32_t)start : M;
-    const int32_t rows = want < (uint32_t)(M - first) ? (int32_t)want : M - first;
-    const int32_t have = blocks_of(past, a.table_blocks);
-    const int32_t take = blocks_of((int64_t)past + rows, a.table_blocks) - have;
-    const int32_t taken = (int32_t)group_scan32((uint32_t)take, slot[1], taken_all, add_up);
-    // a position's shift wraps where past - first leaves 32 bits, and back where the row is added
-    request[t] = Request{(int32_t)((uint32_t)past - (uint32_t)first), have, had - 1 - taken + have, entry};
-    if (rows > 0 && first + rows > row0 && first < row0 + kGroupRows) mark[first > row0 ? first - row0 : 0] = t + 1;
+    // the requests' last entries are on their way while the sums are taken
+    int32_t entry[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t column = b0 + i < a.B ? last_column(a, a.past[b0 + i]) : -1;
+        entry[i] = column >= 0 ? a.table[(b0 + i) * a.ld_table + column] : -1;
+    }
+    Sums sums = {0, 0};
+    const Asked<R> q = ask<R>(a, b0, sums, slot);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        // a position's shift wraps where past - first leaves 32 bits, and back where the row is added
+        const int32_t have = blocks_of(q.past[i], a.table_blocks), first = q.first[i];
+        request[b0 + i] = Request{(int32_t)((uint32_t)q.past[i] - (uint32_t)first), have, had - 1 - q.taken[i] + have, entry[i]};
+        if (q.rows[i] > 0 && first + q.rows[i] > row0 && first < row0 + kGroupRows)
+            mark[first > row0 ? first - row0 : 0] = b0 + i + 1;
+    }
     if (blockIdx.x == 0) {
-        if (t < a.B) {
-            a.row_start[t + 1] = first + rows;
-            a.lens[t] = past + rows;
-        }
-        if (t == 0) write_stack(a, had, taken_all);
+        write_asked<R>(a, b0, q);
+        if (t == 0) write_stack(a, had, sums.blocks);
     }
     __syncthreads();
     const uint4 marks = *reinterpret_cast<const uint4*>(&mark[kRowsEach * t]);
@@ -201,8 +224,8 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(ExtendArgs a) {
 #pragma unroll
     for (int i = 1; i < kRowsEach; ++i) of[i] = larger(of[i], of[i - 1]);
     uint32_t none;
-    const uint32_t before = group_scan32(of[kRowsEach - 1], slot[2], none, larger);
-    const int32_t used = total < (uint32_t)M ? (int32_t)total : M;
+    const uint32_t before = group_scan32(of[kRowsEach - 1], rows_slot, none, larger);
+    const int32_t used = sums.rows < (uint32_t)M ? (int32_t)sums.rows : M;
     int32_t position[kRowsEach];
     int64_t where[kRowsEach];
 #pragma unroll
@@ -212,13 +235,13 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(ExtendArgs a) {
         position[i] = -1;
         where[i] = -1;
         if (row >= used || b == 0) continue;
-        const Request q = request[b - 1];
-        const int32_t pos = (int32_t)((uint32_t)q.shift + (uint32_t)row), at = pos >> 6;
+        const Request of_row = request[b - 1];
+        const int32_t pos = (int32_t)((uint32_t)of_row.shift + (uint32_t)row), at = pos >> 6;
         position[i] = pos;
         if (pos < 0 || at >= a.table_blocks) continue;
-        int32_t page = q.last;
-        if (at >= q.first) {
-            page = q.top - at >= 0 ? a.free_blocks[q.top - at] : -1;
+        int32_t page = of_row.last;
+        if (at >= of_row.first) {
+            page = of_row.top - at >= 0 ? a.free_blocks[of_row.top - at] : -1;
             if (pos % kKvBlock == 0) a.table[(b - 1) * a.ld_table + at] = page;
         }
         where[i] = page < 0 ? -1 : (int64_t)page * kKvBlock + pos % kKvBlock;
@@ -249,14 +272,15 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(ExtendArgs a) {
 }
 
 __global__ __launch_bounds__(kThreads) void extend_requests_kernel(ExtendArgs a) {
-    __shared__ int64_t slot[kWaves];
+    __shared__ uint32_t slot[2][kWaves];
     const int64_t had = clamp64(*a.free_count, 0, a.capacity);
     Sums sums = {0, 0};
-    for (int64_t b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int64_t b = b0 + threadIdx.x;
-        const Asked q = ask(a, b, sums, slot);
-        write_asked(a, b, q);
-        if (b < a.B) a.taken[b] = (int32_t)q.taken;
+    for (int64_t b0 = kMostEach * (int64_t)threadIdx.x; b0 - kMostEach * (int64_t)threadIdx.x < a.B; b0 += kThreads * kMostEach) {
+        const Asked<kMostEach> q = ask<kMostEach>(a, b0, sums, slot);
+        write_asked<kMostEach>(a, b0, q);
+#pragma unroll
+        for (int i = 0; i < kMostEach; ++i)
+            if (b0 + i < a.B) a.taken[b0 + i] = q.taken[i];
     }
     if (threadIdx.x == 0) {
         a.state[0] = (int32_t)had;
@@ -451,8 +475,11 @@ __global__ __launch_bounds__(kThreads) void release_move_kernel(ReleaseArgs a, c
 hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t s) {
     const unsigned groups = (unsigned)((a.M + kGroupRows - 1) / kGroupRows);
     const bool in_place = a.lens == a.past || a.free_left == a.free_count;
-    if (a.B <= kThreads && (groups == 1 || !in_place)) {
-        extend_kernel<<<dim3(groups), dim3(kThreads), 0, s>>>(a);
+    if (a.B <= kThreads * kMostEach && (groups == 1 || !in_place)) {
+        if (a.B <= kThreads)
+            extend_kernel<1><<<dim3(groups), dim3(kThreads), 0, s>>>(a);
+        else
+            extend_kernel<kMostEach><<<dim3(groups), dim3(kThreads), 0, s>>>(a);
     } else {
         extend_requests_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(a);
         extend_rows_kernel<<<dim3((unsigned)((a.M + 255) / 256)), dim3(256), 0, s>>>(a);

@@ -191,7 +191,8 @@ EXTENDS = [  # requests, past at most, new at most, columns, free blocks, rows
     (63, 300, 3, 6, 70, 100), (64, 300, 3, 6, 70, 150), (65, 300, 1, 6, 70, 65), (200, 900, 40, 16, 300, 4096),
     (200, 900, 40, 16, 300, 4097), (1023, 100, 2, 3, 2000, 2046), (1024, 100, 2, 3, 2000, 2049), (1025, 100, 9, 3, 2000, 9000),
     (3000, 1000, 1, 17, 3000, 3000), (5, 100, 5000, 90, 500, 30000), (4100, 70, 13, 3, 5000, 60000),
-    (3, 0, 100000, 1700, 5000, 300000),
+    (3, 0, 100000, 1700, 5000, 300000), (1026, 100, 9, 3, 2000, 4096), (4093, 100, 9, 3, 9000, 20000),
+    (4096, 100, 2, 3, 9000, 4096), (4097, 100, 2, 3, 9000, 4000), (9000, 200, 3, 5, 20000, 30000),
 ]
 
 
