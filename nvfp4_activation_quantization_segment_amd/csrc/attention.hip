@@ -648,7 +648,7 @@ __device__ __forceinline__ Place narrow_place(uint32_t x, uint32_t y, uint32_t z
 }
 
 template <int D, int MODE>
-__global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * kNarrowWaves, D == 64 && MODE != PLAIN ? 3 : 2) void attention_narrow_kernel(AttentionArgs a) {
     __shared__ NarrowShared<D> share;
     narrow_tile<D, MODE>(a, share, narrow_place(blockIdx.x, blockIdx.y, blockIdx.z, gridDim.x));
 }
@@ -999,7 +999,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
 // rows that hold 17.5.
 // ---------------------------------------------------------------------------
 template <int D, bool PREFIX_WIDE, bool OWN_WIDE>
-__global__ __launch_bounds__(64 * kWideWaves, 2) void attention_shared_kernel(AttentionArgs a, SharedGrid g) {
+__global__ __launch_bounds__(64 * kWideWaves, D == 64 ? 3 : 2) void attention_shared_kernel(AttentionArgs a, SharedGrid g) {
     static_assert(kNarrowWaves == kWideWaves, "one size of workgroup");
     __shared__ union {
         NarrowShared<D> narrow;
