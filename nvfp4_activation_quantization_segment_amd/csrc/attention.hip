@@ -648,7 +648,7 @@ __device__ __forceinline__ Place narrow_place(uint32_t x, uint32_t y, uint32_t z
 }
 
 template <int D, int MODE>
-__global__ __launch_bounds__(64 * kNarrowWaves, D == 64 && MODE != PLAIN ? 3 : 2) void attention_narrow_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * kNarrowWaves, 2) void attention_narrow_kernel(AttentionArgs a) {
     __shared__ NarrowShared<D> share;
     narrow_tile<D, MODE>(a, share, narrow_place(blockIdx.x, blockIdx.y, blockIdx.z, gridDim.x));
 }
@@ -997,6 +997,9 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
 // ends.  500 rows of 32 heads over 32,768: 304 to 335 us, 950 TFLOP/s, the matrix
 // pipes busy 39% of the cycles: 432 workgroups for 512 places, and 18 tiles of 128
 // rows that hold 17.5.
+// Heads of 64 leave room for three workgroups on a CU, which many tiles of few keys
+// use: 40 x 2 tokens of 36 and 12 heads behind 12,800 positions 30 us (33.5 with
+// two), 30 x 4 of 16 and 16 heads behind 3840 13.7 (17.3).
 // ---------------------------------------------------------------------------
 template <int D, bool PREFIX_WIDE, bool OWN_WIDE>
 __global__ __launch_bounds__(64 * kWideWaves, D == 64 ? 3 : 2) void attention_shared_kernel(AttentionArgs a, SharedGrid g) {
