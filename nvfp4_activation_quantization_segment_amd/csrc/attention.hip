@@ -1042,8 +1042,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
     __shared__ Dims share[4][64];
     const int64_t all_rows = a.seqs.M * a.q_heads;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-    const int64_t at = (int64_t)blockIdx.x * (4 / WAVES) + wave / WAVES;
-    if (at >= all_rows) return;  // with one wave a row only: no barrier below
+    const int64_t at = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (4 / WAVES) + wave / WAVES;
+    if (at >= all_rows) return;  // whole workgroups, or with one wave a row: no barrier below
     const int64_t token = at / a.q_heads;
     const int32_t head = (int32_t)(at - token * a.q_heads);
     const int32_t first = a.seqs.row_start[0], last = a.seqs.row_start[a.seqs.B];
@@ -1219,10 +1219,16 @@ static void attention_tiles(AttentionArgs a, hipStream_t s) {
     }
 }
 
+// n workgroups of 256, in two dimensions where their threads would pass 2^32 in one.
+static dim3 join_grid(int64_t n) {
+    const int64_t row = n < ((int64_t)1 << 20) ? n : (int64_t)1 << 20;
+    return dim3((unsigned)row, (unsigned)((n + row - 1) / row));
+}
+
 template <int D>
 static void attention_join(const AttentionArgs& a, hipStream_t s) {
     const int64_t rows = a.seqs.M * a.q_heads;
-    const dim3 four((unsigned)((rows + 3) / 4)), one((unsigned)rows), threads(256);
+    const dim3 four = join_grid((rows + 3) / 4), one = join_grid(rows), threads(256);
     if (a.all_parts > 32)
         attention_join_kernel<D, 4, 16><<<one, threads, 0, s>>>(a);
     else if (a.all_parts > 16)
@@ -1243,7 +1249,7 @@ template <int D>
 static void attention_join_batch(const AttentionArgs& a, hipStream_t s) {
     const int64_t rows = a.seqs.M * a.q_heads;
     if (rows < 1024 || a.all_parts <= 8) return attention_join<D>(a, s);
-    const dim3 four((unsigned)((rows + 3) / 4)), threads(256);
+    const dim3 four = join_grid((rows + 3) / 4), threads(256);
     if (a.all_parts > 32)
         attention_join_kernel<D, 1, 64><<<four, threads, 0, s>>>(a);
     else if (a.all_parts > 16)

@@ -569,6 +569,33 @@ def test_shared_prefix_errors_of_single_sequences(nv, bound):
     assert torch.equal(got.isnan(), nan) and same(got[~nan], clean[~nan])
 
 
+def test_a_shared_prefix_of_as_many_rows_as_there_may_be(nv):
+    """2^20 sequences of a token and 64 heads, whose joins pass 2^32 threads: 65 keys each, checked where it samples."""
+    count, heads, dim = 1 << 20, 64, 64
+    pool = Pool(nv, 345, 1, dim, [128])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(346)
+    q = torch.randn(count, heads, dim, generator=g, device="cuda", dtype=torch.bfloat16)
+    rs = torch.arange(count + 1, dtype=torch.int32, device="cuda")
+    lens = torch.full((count,), BLOCK + 1, dtype=torch.int32, device="cuda")
+    table = pool.tab[0, :2].expand(count, 2).contiguous()
+    out = nv.kv_attention(q, pool.gpu, rs, lens, table, causal_block=1, shared=pool.tab[0, :1].contiguous())
+    sample = torch.tensor([0, 1, 2, 65535, 65536, 262143, 262144, 524288, 999999, count - 2, count - 1], device="cuda")
+    n = len(sample)
+    want, tol = step_ref.attention(q[sample].cpu().double().numpy(), pool.ref, list(range(n + 1)), [BLOCK + 1] * n,
+                                   np.repeat(pool.table, n, 0), np.float64(np.float32(dim ** -0.5)), 1, shared=pool.table[0, :1])
+    check(out[sample], want, tol)
+    # every row against the same keys in binary32: off by no more than the roundings to bf16 of p, of the sum's p and of o
+    k, v = (torch.from_numpy(pool.ref.sequence(kind, 0, pool.table[0], BLOCK + 1)).float().cuda() for kind in range(2))
+    most = 0.0
+    for i in range(0, count, 1 << 16):
+        x = q[i:i + (1 << 16)].reshape(-1, dim).float()
+        p = torch.softmax(x @ k.t().contiguous() * dim ** -0.5, 1)
+        far = (out[i:i + (1 << 16)].reshape(-1, dim).float() - p @ v).abs() - 3.1 * 2.0 ** -8 * (p @ v.abs())
+        most = max(most, float(far.max()))
+    assert most <= 0, most
+
+
 def test_shared_prefix_with_rows_that_make_no_sense_stays_in_bounds(nv):
     pool, common = shared_pool(nv, 342, 1, 64, 2, [(10, 2), (70, 3)])
     q = normal(gen(343), 60, 2, 64).cuda()
@@ -684,6 +711,35 @@ def test_a_serving_step_eager_and_captured(nv, shared):
             assert torch.equal(getattr(eager, name), getattr(captured, name)), name
         for a, b in ((eager.cache.k, captured.cache.k), (eager.cache.v, captured.cache.v)):
             assert torch.equal(a, b)
+
+
+def test_norms_and_tables_on_other_streams(nv):
+    """On a side stream that is given or current, behind work that is still running there: what they give on the main one."""
+    x = normal(gen(360), 300, 6, 128).cuda()
+    past, more, table, stack = make_requests(361, 30, 300, 40, 9, 90)
+    want = step_ref.extend(past, more, [list(t) for t in table], list(stack), 900)
+    norm = nv.norm_rope(x)
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for given in (True, False):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                y = big @ big
+            late = x + 0 * y[:300, :1, None].bfloat16().nan_to_num(0)
+            p, t, free, n = i32(past), i32(table), i32(stack), i32([len(stack)])
+        kw = dict(stream=side) if given else {}
+        with torch.cuda.stream(torch.cuda.current_stream() if given else side):
+            got = nv.norm_rope(late, **kw)
+            step = nv.kv_extend(p, i32(more) if not given else more_on(side, more), t, free, n, nv.KvStep.empty(30, 900, **kw), **kw)
+        side.synchronize()
+        assert same(got, norm)
+        assert step.slots.tolist() == want["slots"] and step.lens.tolist() == want["lens"]
+
+
+def more_on(side, more):
+    with torch.cuda.stream(side):
+        return i32(more)
 
 
 @pytest.mark.parametrize("kw", [dict(window=200, sinks=5), "shared"])
