@@ -262,6 +262,15 @@ def test_extend_without_positions_or_slots(nv):
         assert s.slots.tolist() == (want["slots"] if which[1] else [-8] * 500)
 
 
+def test_slots_past_32_bits(nv):
+    """Slots of blocks up to the largest number, held and taken."""
+    table, stack = [[2**31 - 1, -1, -1], [2**30, 2**25, -1]], [3, 2**25 - 1, 2**25, 2**31 - 1]
+    past, more = [10, 100], [100, 60]
+    step, t = run_extend(nv, past, more, table, stack, 200)
+    check_extend(step, t, step_ref.extend(past, more, table, list(stack), 200), table)
+    assert int(step.slots.max()) == (2**31 - 1) * BLOCK + 63
+
+
 def test_extend_with_a_stack_that_makes_no_sense(nv):
     """A count below 0 or past the capacity stays in bounds: none, or all of the stack."""
     for count, usable in ((-4, 0), (100, 6)):
@@ -604,6 +613,40 @@ def test_shared_prefix_with_rows_that_make_no_sense_stays_in_bounds(nv):
             nv.kv_attention(q, pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1, max_len=bound, shared=i32(common.tolist()))
             nv.kv_attention(q, pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1, max_len=bound, window=9, sinks=2)
     torch.cuda.synchronize()
+
+
+def test_a_pool_past_4_gib_through_windows_and_behind_prefixes(nv):
+    """Blocks whose offsets pass 32 bits: the same rows through the pool's first and last blocks."""
+    heads, dim, n = 8, 128, 200
+    blocks = 2**32 // (heads * 64 * dim) + 100  # 4 GiB of keys and as much of values
+    pool = nv.KvCache.empty(blocks, heads, dim)
+    g = gen(7)
+    k, v, q = (normal(g, n, h, dim).cuda() for h in (heads, heads, 2 * heads))
+    rs, lens = i32([0, n]), i32([n])
+    got = []
+    for table in ([0, 1, 2, 3], [blocks - 1, blocks - 90, blocks - 2, blocks - 50]):
+        tab, few = i32([table]), i32([0, 5])
+        nv.kv_write(pool, k, v, rs, lens, tab)
+        got.append([nv.kv_attention(x, pool, r, lens, tab, causal_block=1, **kw) for x, r in ((q, rs), (q[-5:], few))
+                    for kw in (dict(window=70, sinks=3), dict(shared=tab[0, :1].contiguous()), dict(shared=tab[0, :3].contiguous()))
+                    if not (r is rs and "shared" in kw)])
+    for a, b in zip(*got):
+        assert same(a, b) and bool(a.isfinite().all())
+
+
+@pytest.mark.parametrize("rows", [1, 40, 130])
+def test_a_window_at_the_end_of_the_longest_sequence(nv, rows):
+    """Positions up to 2^31 - 65 in a table that names one block throughout: the bytes of a short sequence of it."""
+    pool = Pool(nv, 290, 2, 64, [BLOCK])
+    q = normal(gen(291), rows, 4, 64).cuda()
+    got = []
+    for blocks in ((1 << 25) - 1, 101):
+        table = torch.full((1, blocks), int(pool.table[0, 0]), dtype=torch.int32, device="cuda")
+        for window, sinks, c in ((1000, 5, 1), (1, 0, 1), (500, 100, 64), (77, 0, 0)):
+            got.append(nv.kv_attention(q, pool.gpu, i32([0, rows]), i32([blocks * BLOCK]), table, causal_block=c, window=window,
+                                       sinks=sinks, max_len=6464))
+    for a, b in zip(got[:4], got[4:]):
+        assert same(a, b) and bool(a.isfinite().all())
 
 
 # ---------------------------------------------------------------------------
