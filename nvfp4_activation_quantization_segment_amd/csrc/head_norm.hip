@@ -2,8 +2,8 @@
 //   n_i = x_i w_i / sqrt(mean_j x_j^2 + eps),  y1 = n1 c - n2 s,  y2 = n2 c + n1 s,
 // over each head of the queries and of the keys, in binary32 from the elements
 // to the one rounding to bf16.  Every element is read once and written once:
-// bound by memory.  37,810 rows of 56 and 56 heads of 128, three axes: 421 us,
-// 5.15 TB/s read and written (a copy of 2 GiB reaches 4.9); 32 rows of 32 and 8
+// bound by memory.  37,810 rows of 56 and 56 heads of 128, three axes: 412 us,
+// 5.26 TB/s read and written (a copy of 2 GiB reaches 4.9); 32 rows of 32 and 8
 // heads 3.4 us in a graph, a chain of positions, angles and sums.
 #include "kv_device.h"
 #include "rope_device.h"
@@ -29,13 +29,40 @@ __device__ __forceinline__ float head_sum(float x, int lanes) {
     return x;
 }
 
+__device__ __forceinline__ void rotate(float& n1, float& n2, float2 turn) {
+    const float y1 = n1 * turn.x - n2 * turn.y, y2 = n2 * turn.x + n1 * turn.y;
+    n1 = y1;
+    n2 = y2;
+}
+template <int N>
+__device__ __forceinline__ void angles(float2 (&c)[N], const float2* t) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float4 v = reinterpret_cast<const float4*>(t)[i];
+        c[2 * i] = make_float2(v.x, v.y);
+        c[2 * i + 1] = make_float2(v.z, v.w);
+    }
+}
+
+template <bool STREAM>
+__device__ __forceinline__ void store(uint16_t* p, const float* f) {
+    const u32x4 v = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+    if constexpr (STREAM)
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+    else
+        *reinterpret_cast<u32x4*>(p) = v;
+}
+
 // A workgroup takes a few rows of the queries or of the keys; a unit of 16 dims
-// of a head is a lane's, and a head's units are neighbouring lanes (as many as
-// the next power of two), so that its sum stays in the wave.  The angles of the
-// rows are looked up once, into LDS, and the next unit's loads are ahead of this
-// one's sum and stores.  A lane's dims are the same in every head it takes: its
-// weights stay in registers.
-template <bool SPLIT>
+// of a head, two times 8 of them, is a lane's, and a head's units are
+// neighbouring lanes (as many as the next power of two), so that its sum stays in
+// the wave.  The first 8 dims of neighbouring lanes lie side by side, and the
+// second 8 half a head (or half of what is rotated, or of what is not) further on:
+// every load and store of theirs is whole lines.  The angles of the rows are
+// looked up once, into LDS, and the next unit's loads are ahead of this one's sum
+// and stores.  A lane's dims are the same in every head it takes: its weights stay
+// in registers.
+template <bool SPLIT, bool STREAM>
 __global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormArgs a) {
     __shared__ __align__(16) float2 turn[kTurns];
     const bool keys = blockIdx.x >= a.part[0].groups;
@@ -45,9 +72,11 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormArgs a) {
     const int lanes = 1 << a.log_lanes;
     const int u = threadIdx.x & (lanes - 1);
     const bool mine = u < a.units;
-    const int turning = a.rope.total / 8;
-    // the unit's two times 8 dims
-    const int low = SPLIT && u < turning ? 8 * u : 16 * u, high = SPLIT && u < turning ? a.rope.total + 8 * u : 16 * u + 8;
+    const int total = a.rope.total, turning = total / 8;
+    // SPLIT: the first and second elements of 8 pairs, or what is not rotated
+    const int after = 2 * total + 8 * (u - turning), rest = 8 * (a.units - turning);
+    const int low = SPLIT && u >= turning ? after : 8 * u;
+    const int high = !SPLIT ? 8 * (a.units + u) : u < turning ? total + 8 * u : after + rest;
     int at = threadIdx.x >> a.log_lanes;
     int h = at % p.heads, in = at / p.heads;
     const auto load = [&](u32x4& x, u32x4& y) {
@@ -69,16 +98,16 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = 1.0f;
     }
-    if (a.rope.total > 0) {
+    if (total > 0) {
         const Axes axes = axes_of(a.rope);
-        for (int i = threadIdx.x; i < rows * a.rope.total; i += kThreads) {
-            const int j = i / a.rope.total;
-            turn[i] = rope_turn(axes, positions_of(a.rope, row0 + j), i - j * a.rope.total);
+        for (int i = threadIdx.x; i < rows * total; i += kThreads) {
+            const int j = i / total;
+            turn[i] = rope_turn(axes, positions_of(a.rope, row0 + j), i - j * total);
         }
         __syncthreads();
     }
     while (in < rows) {
-        const float2* t = turn + in * a.rope.total + 8 * u;
+        const float2* t = turn + in * total;
         uint16_t* out = p.out.data + (row0 + in) * p.out.row + h * p.out.head;
         float f[16];
 #pragma unroll
@@ -113,28 +142,28 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(NormArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[i] = f[i] * r * w[i];
-        if (u < turning) {
-            float2 c[8];
+        if constexpr (SPLIT) {
+            if (u < turning) {
+                float2 c[8];
+                angles<8>(c, t + 8 * u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 v = reinterpret_cast<const float4*>(t)[i];
-                c[2 * i] = make_float2(v.x, v.y);
-                c[2 * i + 1] = make_float2(v.z, v.w);
+                for (int i = 0; i < 8; ++i) rotate(f[i], f[8 + i], c[i]);
             }
+        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float& n1 = f[SPLIT ? i : 2 * i];
-                float& n2 = f[SPLIT ? 8 + i : 2 * i + 1];
-                const float y1 = n1 * c[i].x - n2 * c[i].y, y2 = n2 * c[i].x + n1 * c[i].y;
-                n1 = y1;
-                n2 = y2;
+            for (int half = 0; half < 2; ++half) {
+                const int pair = 4 * (half * a.units + u);
+                if (pair < total) {
+                    float2 c[4];
+                    angles<4>(c, t + pair);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rotate(f[8 * half + 2 * i], f[8 * half + 2 * i + 1], c[i]);
+                }
             }
         }
         if (mine) {
-            *reinterpret_cast<u32x4*>(out + low) =
-                u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
-            *reinterpret_cast<u32x4*>(out + high) = u32x4{pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]),
-                                                           pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15])};
+            store<STREAM>(out + low, f);
+            store<STREAM>(out + high, f + 8);
         }
     }
 }
@@ -158,11 +187,21 @@ hipError_t launch_norm_rope(const NormArgs& args, hipStream_t s) {
         p.step_rows = together / p.heads;
         p.groups = (uint32_t)((a.M + p.rows - 1) / p.rows);
     }
+    // Outputs that the 256 MB memory-side cache does not hold are streamed past it,
+    // others left there for the calls that read them.  (37,810 rows of 112 heads 412
+    // us, 422 without; 30,000 of 40, split, 110 and 128; with 16 dims of a lane side
+    // by side, so that stores covered halves of lines, streaming them took 446.)
+    const int64_t heads = (int64_t)a.part[0].heads + a.part[1].heads;
+    const bool stream = a.M * heads * a.units > ((int64_t)256 << 20) / 32;
     const dim3 grid(a.part[0].groups + a.part[1].groups), block(kThreads);
-    if (a.rope.split)
-        norm_rope_kernel<true><<<grid, block, 0, s>>>(a);
+    if (a.rope.split && stream)
+        norm_rope_kernel<true, true><<<grid, block, 0, s>>>(a);
+    else if (a.rope.split)
+        norm_rope_kernel<true, false><<<grid, block, 0, s>>>(a);
+    else if (stream)
+        norm_rope_kernel<false, true><<<grid, block, 0, s>>>(a);
     else
-        norm_rope_kernel<false><<<grid, block, 0, s>>>(a);
+        norm_rope_kernel<false, false><<<grid, block, 0, s>>>(a);
     return hipGetLastError();
 }
 

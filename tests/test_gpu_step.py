@@ -134,6 +134,30 @@ def test_norm_of_rows_further_apart_than_2_gib(nv):
     assert same(x, host)
 
 
+@pytest.mark.parametrize("dim,pairs,split", [(128, [16, 24, 24], False), (128, [24], True), (80, [40], True), (96, [], False)])
+def test_norms_of_more_than_the_caches_hold(nv, dim, pairs, split):
+    """Outputs past 256 MB, which are stored another way: the bytes of calls on a few rows each."""
+    rows, heads, kv_heads = 21001, 50, 9
+    g = torch.Generator(device="cuda")
+    g.manual_seed(dim)
+    x = torch.randn(rows, heads + kv_heads, dim, generator=g, device="cuda", dtype=torch.bfloat16)
+    x = torch.cat([x, x.flip(0)])  # 42,002 rows
+    rows = len(x)
+    assert x.numel() * 2 > 256 << 20
+    size = [31 + 3 * a for a in range(len(pairs))]
+    tables = [t.cuda() for t in tables_for(pairs, size)]
+    positions = torch.stack([torch.randint(0, n, (rows,), generator=g, device="cuda") for n in size], 1).int() if pairs else None
+    w = [torch.randn(dim, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    call = lambda a, b: nv.norm_rope(x[a:b, :heads], x[a:b, heads:], *w, tables=tables, split=split,  # noqa: E731
+                                     positions=None if positions is None else positions[a:b])
+    got = call(0, rows)
+    for a in range(0, rows, 7000):
+        b = min(rows, a + 7000)
+        assert all(torch.equal(y[a:b].view(torch.int16), z.view(torch.int16)) for y, z in zip(got, call(a, b)))
+    few = [t.cpu() for t in tables]
+    check_norm(got[1][-3:], x[-3:, heads:].cpu(), w[1].cpu(), 1e-6, few, None if positions is None else positions[-3:].cpu(), split)
+
+
 def test_norm_rope_of_no_rows(nv):
     x = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     q, k = nv.norm_rope(x, x)
