@@ -1127,9 +1127,10 @@ AttentionPlan attention_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_h
 
 // Where no sequence sees many more keys than the others (through a window, or
 // behind a prefix), fewer pieces: until one workgroup for each CU.  The last 4096
-// of 16,384 keys, 32 and 8 heads: 32 tokens 63 us in one piece, 70 in four and
-// their join; 8 tokens 29 in four, 30 in eight.  Behind a prefix they take the
-// CUs' other places (64 tokens, up to 1024 own keys: 45 us in one piece, 57 in four).
+// of 16,384 keys, 32 and 8 heads, calls from Python after one another: 32 tokens 69
+// us in one piece, 84 in four with their join; 8 tokens 35 in four, 36 in eight, 48
+// in one.  Behind a prefix they take the CUs' other places (64 tokens, up to 1024
+// own keys, in a graph: 45 us in one piece, 57 in four).
 static AttentionPlan few_parts_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t max_len) {
     const bool wide = plan_for(M, B, q_heads, kv_heads, dim, max_len, kSlots).wide;
     return plan_for(M, B, q_heads, kv_heads, dim, max_len, wide ? kSlots : kSlots / 2);
@@ -1153,14 +1154,14 @@ AttentionPlan window_plan(int64_t M, int64_t B, int32_t q_heads, int32_t kv_head
 // wide tile 1.2 us alone on a CU and 1.8 with a second one (heads of 64: 0.8 and
 // 1.2), of a narrow one 2.1 and 3.3 (0.75 and 1.2).  64 tokens of 32 query and 8
 // key/value heads over 16,384 positions: 45 us with 12 or 16 pieces of wide tiles,
-// 58 with 32, 60 with narrow ones; 21 rows of 16 and 2 heads of 64 over 4032: 9.5
+// 58 with 32, 75 and more with narrow ones; 21 rows of 16 and 2 heads of 64 over 4032: 9.5
 // with 16 pieces of narrow tiles, 12.5 with 15 of wide ones.  More workgroups than
 // fit at once lose the keys that tiles share in L2 (500 rows of 32 heads over
 // 32,768 positions: 349 in 3 pieces, 379 in 7).  Where the sequences' own keys fill
 // the chip for a fourth of the prefix's time or more, it takes fewer places (100
-// tokens with 1500 own keys each behind 12,800: 107 us in 4 pieces, 134 in 16).
-// Over 21 shapes the rule is 3% slower on average than the best of 15 numbers of
-// pieces and both tiles, and 17% at most.
+// tokens with 1500 own keys each behind 12,800: 126 us a call in 4 pieces, 153 in
+// 16).  Over 21 shapes calls take 5% longer on average than with the best of 15
+// numbers of pieces and both tiles, and 16% at most.
 static AttentionPlan prefix_plan(int64_t M, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t n, bool wide_only,
                                  int64_t own_groups, int64_t own_blocks) {
     AttentionPlan best = {wide_only, 0, 0};
