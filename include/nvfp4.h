@@ -618,6 +618,16 @@ nvfp4_status nvfp4_kv_attention_shared(const nvfp4_heads* q, int64_t M, int32_t 
                                        float scale, int32_t causal_block, int64_t max_len, const nvfp4_heads* out,
                                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* Rows of no sequence become 0.  The attention calls leave them as they were, so that a
+ * call whose rows are not all in use (a captured step that is made for its largest)
+ * leaves there what the output held before, and nvfp4_norm_rope gives NaN in rows at
+ * position -1; nvfp4_quantize takes one scale from all M rows, these among them.  out
+ * [M, heads, dim]: rows before row_start[0] and from row_start[count] on (DEVICE int32
+ * [count + 1]) are written, no others.  dim a multiple of 16, at most 512; 1 <= M <=
+ * 2^23; M * heads <= 2^28; 1 <= count <= 2^20. */
+nvfp4_status nvfp4_kv_clear_rest(const nvfp4_heads* out, int64_t M, int32_t heads, int32_t dim, const int32_t* row_start,
+                                 int64_t count, void* stream);
+
 /* ---- Single-step entry points ------------------------------------------
  * Elementwise versions of single producer steps, running the very device
  * functions the producer kernels use, so that each step can be checked over

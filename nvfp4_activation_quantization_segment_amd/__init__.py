@@ -128,6 +128,7 @@ def _load():
         "nvfp4_kv_extend": (I32, [TABLES, P, P, P, I64, P, P, P, P, P, P, P, ctypes.c_size_t, V]),
         "nvfp4_kv_release_workspace_bytes": (ctypes.c_size_t, [I64]),
         "nvfp4_kv_release": (I32, [TABLES, P, P, I64, P, P, P, P, ctypes.c_size_t, V]),
+        "nvfp4_kv_clear_rest": (I32, [HEADS, I64, I32, I32, P, I64, V]),
         "nvfp4_step_modulate": (I32, [P, P, P, P, I64, V]),
         "nvfp4_step_swiglu": (I32, [P, P, P, I64, V]),
         "nvfp4_step_block_scale": (I32, [P, P, P, I64, V]),
@@ -434,6 +435,10 @@ def nvfp4_kv_release(tables, lens, done, keep, free_count, lens_out, free_left, 
     _check("nvfp4_kv_release",
            lib.nvfp4_kv_release(tables, _ptr(lens), _ptr(done), keep, _ptr(free_count), _ptr(lens_out), _ptr(free_left),
                                 _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def nvfp4_kv_clear_rest(out, M, heads, dim, row_start, count, stream=None):
+    _check("nvfp4_kv_clear_rest", lib.nvfp4_kv_clear_rest(out, M, heads, dim, _ptr(row_start), count, _stream(stream)))
 
 
 def nvfp4_step_modulate(x, scale, shift, y, n, stream=None):
@@ -920,7 +925,7 @@ def kv_read(cache: KvCache, rows: int, row_start: torch.Tensor, lens: torch.Tens
 def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
                  scale: float | None = None, causal_block: int = 0, max_len: int | None = None,
                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None, window: int = 0,
-                 sinks: int = 0, shared: torch.Tensor | None = None) -> torch.Tensor:
+                 sinks: int = 0, shared: torch.Tensor | None = None, clear_rest: bool = False) -> torch.Tensor:
     """Attention of the queries q [rows, q_heads, dim] (bf16) over their sequences' cached keys and values.
 
     Rows and positions as in kv_write.  causal_block: 0 for no mask, 1 for causal, c for runs of c positions that
@@ -933,7 +938,12 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
     window).  shared: int32 [blocks] on the GPU, the cache blocks of a prefix that all sequences begin with; they stand
     for the first entries of every table, and the rows of all sequences are taken against them together.  The new rows
     lie behind it (NaN where they do not).  Not both at once.  Their workspaces are those of
-    nvfp4_kv_attention_window_workspace_bytes and nvfp4_kv_attention_shared_workspace_bytes."""
+    nvfp4_kv_attention_window_workspace_bytes and nvfp4_kv_attention_shared_workspace_bytes.
+
+    clear_rest: rows of no sequence become 0, by a launch of its own (nvfp4_kv_clear_rest).  Without it they stay as they
+    were: in a new output what its memory held, in q itself norm_rope's NaN of rows at position -1.  Give it wherever
+    not all rows are in use (a captured step that is made for its largest) and the output goes to `quantize`, which
+    takes one scale from all rows."""
     dev, c = cache.device, cache.struct
     _same_device(dev, q, out, workspace)
     hq = make_heads("q", q)
@@ -975,6 +985,8 @@ def kv_attention(q: torch.Tensor, cache: KvCache, row_start: torch.Tensor, lens:
     if rows:
         _call(name, fn, dev, stream, hq, rows, q_heads, c, s, *args, ho, None if workspace is None else workspace.data_ptr(),
               size)
+        if clear_rest:
+            _call("nvfp4_kv_clear_rest", lib.nvfp4_kv_clear_rest, dev, stream, ho, rows, q_heads, dim, s.row_start, s.count)
     return out
 
 

@@ -292,6 +292,16 @@ nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens
     return report_hip(launch_kv_release(a, (hipStream_t)stream));
 }
 
+nvfp4_status nvfp4_kv_clear_rest(const nvfp4_heads* out, int64_t M, int32_t heads, int32_t dim, const int32_t* row_start,
+                                 int64_t count, void* stream) {
+    if (M < 1 || heads < 1 || dim < 1 || count < 1 || !row_start) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (dim % 16 != 0 || dim > 512 || M > kMaxRows || M * heads > ((int64_t)1 << 28) || count > kMaxSeqs) return NVFP4_ERR_SHAPE;
+    const nvfp4_status st = check_heads(out, M, heads, dim, true);
+    if (st != NVFP4_OK) return st;
+    if (!aligned(row_start, 4)) return NVFP4_ERR_ALIGNMENT;
+    return report_hip(launch_kv_clear_rest(out_of(out), M, heads, dim, row_start, count, (hipStream_t)stream));
+}
+
 size_t nvfp4_kv_attention_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
                                           int64_t max_len) {
     if (!attention_sizes_ok(M, count, q_heads, heads, dim, max_len)) return 0;

@@ -138,6 +138,8 @@ hipError_t launch_kv_read(const CacheArgs& c, const SeqArgs& q, const HeadsOut& 
 hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t s);
 int64_t kv_release_groups(int64_t B);  // workgroups of a release
 hipError_t launch_kv_release(const ReleaseArgs& a, hipStream_t s);
+hipError_t launch_kv_clear_rest(const HeadsOut& out, int64_t M, int32_t heads, int32_t dim, const int32_t* row_start, int64_t B,
+                                hipStream_t s);
 
 // How an attention call is cut: from sizes the host knows.
 struct AttentionPlan {

@@ -1,5 +1,6 @@
 // Block tables, row starts, positions and slots of a batch, built on the GPU
-// from the requests' lengths; and the blocks of finished requests given back.
+// from the requests' lengths; the blocks of finished requests given back; and the
+// rows that no request has cleared.
 // All of it is integers, a few bytes for each row and request: what takes the
 // time is the chain of loads that depend on one another, and the launches.
 #include "kv_device.h"
@@ -470,6 +471,24 @@ __global__ __launch_bounds__(kThreads) void release_move_kernel(ReleaseArgs a, c
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.free_left = (int32_t)clamp64(had + others + all, 0, a.capacity);
 }
 
+// ---------------------------------------------------------------------------
+// Clearing.  A workgroup takes a row of no sequence at a time, 16 bytes a thread,
+// as many whole heads at once as its threads hold.  Nothing to clear: two loads
+// and the launch.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void clear_rest_kernel(HeadsOut out, int64_t M, int32_t pieces, int32_t heads,
+                                                         const int32_t* row_start, int64_t B) {
+    const RowRange used = row_range(row_start[0], row_start[B], M);
+    const int64_t rest = M - (used.last - used.first);
+    const int32_t together = 256 / pieces, first = (int32_t)threadIdx.x / pieces, piece = (int32_t)threadIdx.x % pieces;
+    if (first >= together) return;
+    for (int64_t i = blockIdx.x; i < rest; i += gridDim.x) {
+        const int64_t row = i < used.first ? i : i + (used.last - used.first);
+        uint16_t* p = out.data + row * out.row + 8 * piece;
+        for (int32_t h = first; h < heads; h += together) *reinterpret_cast<u32x4*>(p + h * out.head) = u32x4{0, 0, 0, 0};
+    }
+}
+
 }  // namespace
 
 hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t s) {
@@ -493,6 +512,13 @@ hipError_t launch_kv_release(const ReleaseArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)kv_release_groups(a.B)), block(kThreads);
     if (grid.x > 1) release_count_kernel<<<grid, block, 0, s>>>(a);
     release_move_kernel<<<grid, block, 0, s>>>(a, grid.x > 1 ? a.state : a.free_count);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_clear_rest(const HeadsOut& out, int64_t M, int32_t heads, int32_t dim, const int32_t* row_start, int64_t B,
+                                hipStream_t s) {
+    // 8 workgroups for each of 256 CUs, which take several rows where there are more
+    clear_rest_kernel<<<dim3((unsigned)clamp64(M, 1, 2048)), dim3(256), 0, s>>>(out, M, dim / 8, heads, row_start, B);
     return hipGetLastError();
 }
 

@@ -830,3 +830,104 @@ def test_other_streams_and_the_same_bytes(nv, kw):
         s.synchronize()
     for o in got:
         assert same(o, want)
+
+
+# ---------------------------------------------------------------------------
+# rows of no request
+# ---------------------------------------------------------------------------
+KINDS = ["plain", "window", "shared"]
+
+
+def kind_args(kind, common):
+    return {"plain": {}, "window": dict(window=50, sinks=3), "shared": dict(shared=common)}[kind]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim,heads,group,rows,layout", [(64, 1, 1, 1, "plain"), (128, 2, 4, 67, "qkv"), (64, 3, 5, 300, "heads"),
+                                                         (128, 1, 70, 9, "plain")])
+def test_rows_of_no_sequence_are_cleared(nv, kind, dim, heads, group, rows, layout):
+    """And no others: the sequences' rows have the bytes of a call without it, what lies beside the output is untouched.
+    Row starts that make no sense stay in bounds."""
+    pool = Pool(nv, 370, heads, dim, [200 + rows, 200 + rows])
+    pool.tab[1, 0] = pool.tab[0, 0]
+    common = pool.tab[0, :1].contiguous()
+    q = normal(gen(371), rows, heads * group, dim).cuda()
+    for rs in ([0, 0, 0], [0, rows // 2, rows], [rows // 3, rows // 2, rows - rows // 4], [rows, rows, rows], [0, 0, 1],
+               [rows - 1, rows, rows], [-5, 1, rows + 9], [2**31 - 1, 0, -2**31], [5, 2, 1]):
+        call = lambda x, **kw: nv.kv_attention(x, pool.gpu, i32(rs), pool.lens, pool.tab, causal_block=1,  # noqa: E731
+                                               **kind_args(kind, common), **kw)
+        first = min(max(rs[0], 0), rows)
+        last = min(max(rs[2], first), rows)
+        made = strided(torch.full_like(q, 5.0), layout)
+        call(q, out=made)
+        out = strided(torch.full_like(q, float("nan")), layout)
+        assert call(q, out=out, clear_rest=True) is out
+        rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+        rest[first:last] = False
+        assert bool((made[rest] == 5).all()) and bool((out.view(torch.int16)[rest] == 0).all())
+        if sorted(rs) == rs:
+            assert same(out[~rest], made[~rest])
+        if layout == "qkv":
+            wide = torch.as_strided(out, (rows, 3 * heads * group, dim), (3 * heads * group * dim, dim, 1), 0)
+            assert bool((wide[:, :heads * group] == 7).all()) and bool((wide[:, 2 * heads * group:] == 7).all())
+
+
+def test_clearing_rows_further_apart_than_2_gib(nv):
+    """Offsets past 32 bits, and more rows than workgroups."""
+    far = (1 << 31) + 64
+    flat = torch.ones(2 * far + 512, dtype=torch.bfloat16, device="cuda")
+    out = torch.as_strided(flat, (3, 2, 128), (far, 128, 1))
+    nv.nvfp4_kv_clear_rest(nv.make_heads("out", out), 3, 2, 128, i32([1, 2]), 1)
+    assert bool((out[[0, 2]] == 0).all()) and bool((out[1] == 1).all())
+    assert int((flat == 0).sum()) == 2 * 2 * 128
+    many = torch.ones(5000, 1, 16, dtype=torch.bfloat16, device="cuda")
+    nv.nvfp4_kv_clear_rest(nv.make_heads("out", many), 5000, 1, 16, i32([2001, 2001, 2004]), 2)
+    assert (many[:, 0, :] == 1).all(1).nonzero().flatten().tolist() == [2001, 2002, 2003] and int((many == 0).sum()) == 4997 * 16
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("where", ["kept", "new", "queries"])
+def test_rows_of_no_request_do_not_reach_the_quantizer(nv, kind, where):
+    """Steps of few rows after one of many and large ones, eager and replayed: the quantizer's scale and codes are those of
+    the rows in use, whichever output the attention writes."""
+    rows, heads, dim = 130, 2, 128
+    cache, common = nv.KvCache.empty(30, heads, dim), i32([0])
+    table = i32([[0] + list(range(1, 8)), [0] + list(range(8, 15))])
+    prefix = normal(gen(380), BLOCK, heads, dim, sigma=0.1).cuda()
+    nv.kv_write(cache, prefix, prefix, i32([0, BLOCK]), i32([BLOCK]), common[None])
+    x = torch.zeros(rows, 12, dim, dtype=torch.bfloat16, device="cuda")
+    base, more, free, n_free = i32([BLOCK, BLOCK]), i32([0, 0]), i32(list(range(15, 30))), i32([15])
+    step = nv.KvStep.empty(2, rows)
+    o, tables = torch.zeros(rows, 8, dim, dtype=torch.bfloat16, device="cuda"), [nv.rope_table(1024, 64)]
+
+    def run():
+        s = nv.kv_extend(base, more, table, free, n_free, step)
+        q, k = nv.norm_rope(x[:, :8], x[:, 8:10], tables=tables, positions=s.positions, split=True)
+        nv.kv_write(cache, k, x[:, 10:], s.row_start, s.lens, table)
+        out = nv.kv_attention(q, cache, s.row_start, s.lens, table, causal_block=1, clear_rest=True, **kind_args(kind, common),
+                              **{"kept": dict(out=o), "new": {}, "queries": dict(out=q)}[where])
+        return (out, *nv.quantize(out.reshape(rows, -1)))
+
+    run()  # what a first call sets up stays out of the capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = run()
+    for turn, (counts, size) in enumerate([((100, 30), 50.0), ((1, 1), 1.0), ((0, 3), 0.5), ((70, 60), 20.0), ((0, 0), 1.0),
+                                           ((5, 0), 2.0)]):
+        dirt = torch.full((200, 8, dim), float("nan"), dtype=torch.bfloat16, device="cuda")  # what a new output may hold
+        del dirt
+        x.copy_(normal(gen(381 + turn), rows, 12, dim))
+        x[:, 10:] *= size
+        more.copy_(i32(list(counts)))
+        used = sum(counts)
+        for got in (run(), None):
+            if got is None:
+                graph.replay()
+                torch.cuda.synchronize()
+                got = replayed
+            out, codes, scales, tensor_scale, amax = got
+            assert bool((out[used:] == 0).all()) and bool(out.isfinite().all())
+            assert float(amax) == float(out[:used].abs().max() if used else 0), (turn, used)
+            if used:
+                alone = nv.quantize(out[:used].reshape(used, -1).contiguous())
+                assert torch.equal(alone[0][:used], codes[:used]) and torch.equal(alone[2], tensor_scale)

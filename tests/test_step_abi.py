@@ -97,6 +97,22 @@ def test_release_refusals(nv):
     assert f(None, *[good[n] for n in names], None) == INVALID
 
 
+def test_clear_rest_refusals(nv):
+    f = nv.lib.nvfp4_kv_clear_rest
+    call = lambda out=None, M=10, h=8, d=128, rs=FAKE, n=2: f(out or heads(nv), M, h, d, rs, n, None)  # noqa: E731
+    for bad, want in HEADS_ERRORS:
+        assert call(heads(nv, **bad)) == want, bad
+    for bad in OVERLAPS:
+        assert call(heads(nv, **bad)) == INVALID, bad
+    for M, want in ROWS_ERRORS:
+        assert call(M=M) == want, M
+    assert call(h=0) == INVALID and call(M=1 << 23, h=33) == SHAPE and call(M=1, h=(1 << 28) + 1) == SHAPE
+    assert call(d=0) == INVALID and call(d=120) == SHAPE and call(d=528) == SHAPE
+    assert call(rs=None) == INVALID and call(rs=FAKE + 2) == ALIGNMENT
+    assert call(n=0) == INVALID and call(n=(1 << 20) + 1) == SHAPE
+    assert f(None, 10, 8, 128, FAKE, 2, None) == INVALID
+
+
 @pytest.mark.parametrize("kind", ["window", "shared"])
 def test_attention_refusals(nv, kind):
     def call(q=None, M=10, q_heads=8, c=None, s=None, scale=0.1, causal=1, max_len=64, out=None, ws=FAKE, size=1 << 40,
