@@ -579,11 +579,19 @@ nvfp4_status nvfp4_kv_extend(const nvfp4_kv_tables* tables, const int32_t* past,
  * stays as it is.  keep: the first entries of every table that are not the request's
  * own (a shared prefix).  lens_out may be lens and free_left may be free_count.  The
  * workspace needs nvfp4_kv_release_workspace_bytes(count) bytes (16-byte aligned; may
- * be NULL when that is 0). */
+ * be NULL when that is 0).
+ * A length of 0 says that a request holds no block.  Where its table still names the
+ * kept ones, the next request in its place has to begin behind them: extended from 0 it
+ * would put blocks of its own over the prefix's entries, which no release with that
+ * `keep` gives back.  nvfp4_kv_release_to_prefix is for that: lens_out[b] of finished
+ * requests becomes 64 * keep (at most 64 * table_blocks). */
 size_t nvfp4_kv_release_workspace_bytes(int64_t count);
 nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens, const int32_t* done, int64_t keep,
                               const int32_t* free_count, int32_t* lens_out, int32_t* free_left, void* workspace,
                               size_t workspace_bytes, void* stream);
+nvfp4_status nvfp4_kv_release_to_prefix(const nvfp4_kv_tables* tables, const int32_t* lens, const int32_t* done, int64_t keep,
+                                        const int32_t* free_count, int32_t* lens_out, int32_t* free_left, void* workspace,
+                                        size_t workspace_bytes, void* stream);
 
 /* nvfp4_kv_attention through a window: of the positions below its limit, the row at
  * position p sees those above p - window and the first `sinks`; the others' blocks

@@ -128,6 +128,7 @@ def _load():
         "nvfp4_kv_extend": (I32, [TABLES, P, P, P, I64, P, P, P, P, P, P, P, ctypes.c_size_t, V]),
         "nvfp4_kv_release_workspace_bytes": (ctypes.c_size_t, [I64]),
         "nvfp4_kv_release": (I32, [TABLES, P, P, I64, P, P, P, P, ctypes.c_size_t, V]),
+        "nvfp4_kv_release_to_prefix": (I32, [TABLES, P, P, I64, P, P, P, P, ctypes.c_size_t, V]),
         "nvfp4_kv_clear_rest": (I32, [HEADS, I64, I32, I32, P, I64, V]),
         "nvfp4_step_modulate": (I32, [P, P, P, P, I64, V]),
         "nvfp4_step_swiglu": (I32, [P, P, P, I64, V]),
@@ -435,6 +436,13 @@ def nvfp4_kv_release(tables, lens, done, keep, free_count, lens_out, free_left, 
     _check("nvfp4_kv_release",
            lib.nvfp4_kv_release(tables, _ptr(lens), _ptr(done), keep, _ptr(free_count), _ptr(lens_out), _ptr(free_left),
                                 _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def nvfp4_kv_release_to_prefix(tables, lens, done, keep, free_count, lens_out, free_left, workspace, workspace_bytes,
+                               stream=None):
+    _check("nvfp4_kv_release_to_prefix",
+           lib.nvfp4_kv_release_to_prefix(tables, _ptr(lens), _ptr(done), keep, _ptr(free_count), _ptr(lens_out),
+                                          _ptr(free_left), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def nvfp4_kv_clear_rest(out, M, heads, dim, row_start, count, stream=None):
@@ -1109,11 +1117,14 @@ def kv_extend(past: torch.Tensor, more: torch.Tensor, table: torch.Tensor, free:
 
 def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free: torch.Tensor, free_count: torch.Tensor,
                keep: int = 0, lens_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
-               workspace: torch.Tensor | None = None, stream=None):
+               workspace: torch.Tensor | None = None, stream=None, to_prefix: bool = False):
     """Takes the blocks of finished requests (done[b] != 0) back onto the stack free[:free_count], on the GPU: returns the
     lengths, 0 for those, and the stack's size after it.
 
-    keep: the first entries of every table that are not the request's own (a shared prefix).  The stack grows in place;
+    keep: the first entries of every table that are not the request's own (a shared prefix).  to_prefix: the lengths of
+    finished requests become 64 * keep instead of 0, so that the next request in their place begins behind the prefix
+    that its table still names; from a length of 0 kv_extend would put new blocks over those entries, which no release
+    with this `keep` gives back.  The stack grows in place;
     lens_out may be `lens` and free_count_out `free_count`.  A workspace of nvfp4_kv_release_workspace_bytes(requests)
     bytes is allocated with torch when none is given, on the stream that the call runs on."""
     dev = table.device
@@ -1135,7 +1146,9 @@ def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free
             workspace = _empty(dev, stream, (need,), torch.uint8)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be contiguous and on {dev}")
-    _call("nvfp4_kv_release", lib.nvfp4_kv_release, dev, stream, t, lens_at, done_at, keep, count_at,
+    name, fn = ("nvfp4_kv_release_to_prefix", lib.nvfp4_kv_release_to_prefix) if to_prefix else \
+        ("nvfp4_kv_release", lib.nvfp4_kv_release)
+    _call(name, fn, dev, stream, t, lens_at, done_at, keep, count_at,
           _int32("lens_out", lens_out, n, dev), _int32("free_count_out", free_count_out, 1, dev),
           None if workspace is None else workspace.data_ptr(),
           0 if workspace is None else workspace.numel() * workspace.element_size())

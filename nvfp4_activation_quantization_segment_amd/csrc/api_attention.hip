@@ -136,6 +136,37 @@ nvfp4_status run_attention(AttentionArgs& a, const AttentionPlan& p, void* works
     return report_hip(launch_attention(a, (hipStream_t)stream));
 }
 
+// to_prefix: a finished request's length becomes that of the kept blocks, else 0.
+nvfp4_status run_release(const nvfp4_kv_tables* tables, const int32_t* lens, const int32_t* done, int64_t keep, bool to_prefix,
+                         const int32_t* free_count, int32_t* lens_out, int32_t* free_left, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    nvfp4_status st;
+    if ((st = check_tables(tables)) != NVFP4_OK) return st;
+    if (!lens || !done || !free_count || !lens_out || !free_left || keep < 0) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (!aligned(lens, 4) || !aligned(done, 4) || !aligned(free_count, 4) || !aligned(lens_out, 4) || !aligned(free_left, 4))
+        return NVFP4_ERR_ALIGNMENT;
+    const size_t need = nvfp4_kv_release_workspace_bytes(tables->count);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return NVFP4_ERR_INVALID_ARGUMENT;
+    if (need > 0 && !aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
+    ReleaseArgs a;
+    a.B = tables->count;
+    a.lens = lens;
+    a.done = done;
+    a.table = tables->table;
+    a.ld_table = tables->ld_table;
+    a.table_blocks = tables->table_blocks;
+    a.keep = keep < tables->table_blocks ? keep : tables->table_blocks;
+    a.done_len = to_prefix ? (int32_t)(a.keep * kKvBlock) : 0;
+    a.free_blocks = tables->free_blocks;
+    a.capacity = tables->capacity;
+    a.free_count = free_count;
+    a.lens_out = lens_out;
+    a.free_left = free_left;
+    a.state = (int32_t*)workspace;
+    a.totals = (int64_t*)((char*)workspace + kStateBytes);
+    return report_hip(launch_kv_release(a, (hipStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -266,30 +297,13 @@ size_t nvfp4_kv_release_workspace_bytes(int64_t count) {
 nvfp4_status nvfp4_kv_release(const nvfp4_kv_tables* tables, const int32_t* lens, const int32_t* done, int64_t keep,
                               const int32_t* free_count, int32_t* lens_out, int32_t* free_left, void* workspace,
                               size_t workspace_bytes, void* stream) {
-    nvfp4_status st;
-    if ((st = check_tables(tables)) != NVFP4_OK) return st;
-    if (!lens || !done || !free_count || !lens_out || !free_left || keep < 0) return NVFP4_ERR_INVALID_ARGUMENT;
-    if (!aligned(lens, 4) || !aligned(done, 4) || !aligned(free_count, 4) || !aligned(lens_out, 4) || !aligned(free_left, 4))
-        return NVFP4_ERR_ALIGNMENT;
-    const size_t need = nvfp4_kv_release_workspace_bytes(tables->count);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return NVFP4_ERR_INVALID_ARGUMENT;
-    if (need > 0 && !aligned(workspace, 16)) return NVFP4_ERR_ALIGNMENT;
-    ReleaseArgs a;
-    a.B = tables->count;
-    a.lens = lens;
-    a.done = done;
-    a.table = tables->table;
-    a.ld_table = tables->ld_table;
-    a.table_blocks = tables->table_blocks;
-    a.keep = keep < tables->table_blocks ? keep : tables->table_blocks;
-    a.free_blocks = tables->free_blocks;
-    a.capacity = tables->capacity;
-    a.free_count = free_count;
-    a.lens_out = lens_out;
-    a.free_left = free_left;
-    a.state = (int32_t*)workspace;
-    a.totals = (int64_t*)((char*)workspace + kStateBytes);
-    return report_hip(launch_kv_release(a, (hipStream_t)stream));
+    return run_release(tables, lens, done, keep, false, free_count, lens_out, free_left, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status nvfp4_kv_release_to_prefix(const nvfp4_kv_tables* tables, const int32_t* lens, const int32_t* done, int64_t keep,
+                                        const int32_t* free_count, int32_t* lens_out, int32_t* free_left, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+    return run_release(tables, lens, done, keep, true, free_count, lens_out, free_left, workspace, workspace_bytes, stream);
 }
 
 nvfp4_status nvfp4_kv_clear_rest(const nvfp4_heads* out, int64_t M, int32_t heads, int32_t dim, const int32_t* row_start,

@@ -98,6 +98,7 @@ struct ReleaseArgs {
     const int32_t* done;
     const int32_t* table;
     int64_t ld_table, table_blocks, keep;
+    int32_t done_len;     // what a finished request's length becomes
     int32_t* free_blocks;
     int64_t capacity;
     const int32_t* free_count;

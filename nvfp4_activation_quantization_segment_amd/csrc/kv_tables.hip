@@ -381,7 +381,7 @@ __device__ __forceinline__ Released take(const ReleaseArgs& a, int64_t b0) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         r.blocks[i] = done[i] != 0 ? blocks_of(r.lens[i], a.table_blocks) : 0;
-        r.lens[i] = done[i] != 0 ? 0 : r.lens[i];
+        r.lens[i] = done[i] != 0 ? a.done_len : r.lens[i];
 #pragma unroll
         for (int k = 0; k < kKept; ++k) r.page[i][k] = entry_of(a, b0 + i, a.keep + 64 * k + lane, r.blocks[i]);
     }

@@ -833,6 +833,50 @@ def test_other_streams_and_the_same_bytes(nv, kw):
 
 
 # ---------------------------------------------------------------------------
+# requests behind a prefix that stays
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("count,keep", [(1, 1), (5, 3), (40, 2), (700, 1)])
+def test_a_pool_behind_a_prefix_through_many_steps_in_place(nv, count, keep):
+    """Requests come, grow and finish behind kept blocks: no block is held twice or lost, the tables go on naming the
+    prefix, and new rows begin behind it."""
+    r = random.Random(count)
+    columns, own = keep + 6, 4 * count
+    prefix, stack = list(range(keep)), list(range(keep, keep + own))
+    table = [prefix + [-1] * 6 for _ in range(count)]
+    past = [keep * BLOCK] * count
+    lens, free, n_free, t = i32(past), i32(stack), i32([own]), i32(table)
+    rows = 130 * count
+    step = nv.KvStep.empty(count, rows, lens=lens, free_count=n_free)
+    for turn in range(12):
+        done = [int(r.random() < 0.4) for _ in range(count)]
+        now = [keep * BLOCK if d else p for d, p in zip(done, past)]
+        more = [min(r.choice([0, 1, 1, 30, 130]), columns * BLOCK - p) for p in now]
+        nv.kv_release(lens, i32(done), t, free, n_free, keep=keep, lens_out=lens, free_count_out=n_free, to_prefix=True)
+        step_ref.release(past, done, table, stack, keep, own)
+        assert lens.tolist() == now and n_free.tolist() == [len(stack)]
+        nv.kv_extend(lens, i32(more), t, free, n_free, step)
+        want = step_ref.extend(now, more, table, stack, rows)
+        check_extend(step, t, want, table)
+        past = want["lens"]
+        held = [p for b in range(count) for p in table[b][keep:-(-past[b] // BLOCK)] if p >= 0]
+        assert sorted(held + stack) == list(range(keep, keep + own))
+        assert all(row[:keep] == prefix for row in table)
+
+
+@pytest.mark.parametrize("count,columns", [(3, 4), (99, 7)])
+def test_lengths_of_what_is_released_to_a_prefix(nv, count, columns):
+    """64 * keep, at most what the table holds; the others' as they were; blocks as without it."""
+    lens, _, table, stack = make_requests(count, count, columns * BLOCK, 1, columns, 3)
+    done = [b % 3 == 0 for b in range(count)]
+    for keep in (0, 1, columns, columns + 1, 2**31 - 1):
+        free = [i32(stack + [-5] * (count * columns)) for _ in range(2)]
+        out = [nv.kv_release(i32(lens), i32(done), i32(table), f, i32([len(stack)]), keep=keep, to_prefix=to)
+               for f, to in zip(free, (False, True))]
+        assert torch.equal(*free) and torch.equal(out[0][1], out[1][1])
+        assert out[1][0].tolist() == [min(keep, columns) * BLOCK if d else n for d, n in zip(done, lens)]
+
+
+# ---------------------------------------------------------------------------
 # rows of no request
 # ---------------------------------------------------------------------------
 KINDS = ["plain", "window", "shared"]

@@ -97,6 +97,20 @@ def test_release_refusals(nv):
     assert f(None, *[good[n] for n in names], None) == INVALID
 
 
+def test_release_to_prefix_refuses_what_release_does(nv):
+    f = nv.lib.nvfp4_kv_release_to_prefix
+    names = ("lens", "done", "keep", "free_count", "lens_out", "free_left", "ws", "size")
+    good = dict(zip(names, [FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, 1 << 20]))
+    call = lambda t=None, **kw: f(t or tables(nv), *[{**good, **kw}[n] for n in names], None)  # noqa: E731
+    for bad, want in TABLE_ERRORS:
+        assert call(tables(nv, **bad)) == want, bad
+    for name in ("lens", "done", "free_count", "lens_out", "free_left"):
+        assert call(**{name: None}) == INVALID and call(**{name: FAKE + 2}) == ALIGNMENT, name
+    assert call(keep=-1) == INVALID and f(None, *[good[n] for n in names], None) == INVALID
+    need, many = nv.nvfp4_kv_release_workspace_bytes(1000), tables(nv, count=1000)
+    assert call(many, ws=None) == INVALID and call(many, size=need - 1) == INVALID and call(many, ws=FAKE + 8) == ALIGNMENT
+
+
 def test_clear_rest_refusals(nv):
     f = nv.lib.nvfp4_kv_clear_rest
     call = lambda out=None, M=10, h=8, d=128, rs=FAKE, n=2: f(out or heads(nv), M, h, d, rs, n, None)  # noqa: E731
