@@ -1099,7 +1099,8 @@ def kv_extend(past: torch.Tensor, more: torch.Tensor, table: torch.Tensor, free:
     the step; the blocks they need come from the top of the stack free[:free_count], into the table [requests, blocks]
     (in place; an entry is -1 where the stack is empty, and `missing` counts those).  step.row_start, step.lens, the
     table and step.positions are what kv_write, rope and kv_attention take; step.slots is each row's block * 64 +
-    position % 64.  Rows of no request get -1 in both.  step.lens may be `past` and step.free_count `free_count`."""
+    position % 64.  Rows of no request get -1 in both.  step.lens may be `past` and step.free_count `free_count`.  With
+    no requests or no rows nothing is given."""
     dev = step.device
     if dev.type != "cuda":
         raise ValueError(f"expected tensors on a GPU, got {dev}")
@@ -1109,9 +1110,20 @@ def kv_extend(past: torch.Tensor, more: torch.Tensor, table: torch.Tensor, free:
     if t.count != n:
         raise ValueError(f"a table of {t.count} requests, a step of {n}")
     row_start, lens, left, missing, positions, slots, workspace = step.memory
-    _call("nvfp4_kv_extend", lib.nvfp4_kv_extend, dev, stream, t, _int32("past", past, n, dev), _int32("more", more, n, dev),
-          _int32("free_count", free_count, 1, dev), step.rows, row_start, lens, left, missing, positions, slots, workspace,
-          step._size)
+    past_at, more_at, count_at = _int32("past", past, n, dev), _int32("more", more, n, dev), _int32("free_count", free_count, 1, dev)
+    if n and step.rows:
+        _call("nvfp4_kv_extend", lib.nvfp4_kv_extend, dev, stream, t, past_at, more_at, count_at, step.rows, row_start, lens,
+              left, missing, positions, slots, workspace, step._size)
+        return step
+    # no request or no row: nothing is given
+    with torch.cuda.stream(_torch_stream(stream, dev)):
+        step.row_start.zero_()
+        step.missing.zero_()
+        if lens != past_at:
+            step.lens.copy_(past)
+        torch.clamp(free_count, 0, t.capacity, out=step.free_count)
+        step.positions.fill_(-1)
+        step.slots.fill_(-1)
     return step
 
 
@@ -1136,20 +1148,24 @@ def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free
         raise ValueError(f"keep: expected 0 to 2^31 - 1, got {keep}")
     lens_at, done_at = _int32("lens", lens, n, dev), _int32("done", done, n, dev)
     count_at = _int32("free_count", free_count, 1, dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"the workspace must be contiguous and on {dev}")
     if lens_out is None:
         lens_out = lens.new_empty((n,)) if stream is None else _empty(dev, stream, (n,), torch.int32)
     if free_count_out is None:
         free_count_out = lens.new_empty((1,)) if stream is None else _empty(dev, stream, (1,), torch.int32)
+    lens_out_at, left_at = _int32("lens_out", lens_out, n, dev), _int32("free_count_out", free_count_out, 1, dev)
+    if not n:  # nothing to take back
+        with torch.cuda.stream(_torch_stream(stream, dev)):
+            torch.clamp(free_count, 0, t.capacity, out=free_count_out)
+        return lens_out, free_count_out
     if workspace is None:
         need = lib.nvfp4_kv_release_workspace_bytes(n)
         if need:
             workspace = _empty(dev, stream, (need,), torch.uint8)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be contiguous and on {dev}")
     name, fn = ("nvfp4_kv_release_to_prefix", lib.nvfp4_kv_release_to_prefix) if to_prefix else \
         ("nvfp4_kv_release", lib.nvfp4_kv_release)
-    _call(name, fn, dev, stream, t, lens_at, done_at, keep, count_at,
-          _int32("lens_out", lens_out, n, dev), _int32("free_count_out", free_count_out, 1, dev),
+    _call(name, fn, dev, stream, t, lens_at, done_at, keep, count_at, lens_out_at, left_at,
           None if workspace is None else workspace.data_ptr(),
           0 if workspace is None else workspace.numel() * workspace.element_size())
     return lens_out, free_count_out

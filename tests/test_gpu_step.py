@@ -833,6 +833,53 @@ def test_other_streams_and_the_same_bytes(nv, kw):
 
 
 # ---------------------------------------------------------------------------
+# no rows, no requests
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("requests,rows", [(3, 0), (0, 5), (0, 0)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_extend_of_no_rows_or_no_requests(nv, requests, rows, in_place):
+    """What the definition gives: nothing.  Also captured, and on a stream that is given."""
+    past, more, stack = [7, 64, -3][:requests], [4, 90, 0][:requests], [4, 5, 6]
+    table = torch.full((requests, 4), -1, dtype=torch.int32, device="cuda")
+    for count, free_after in ((3, 3), (-2, 0), (9, 5)):
+        n, c, free = i32(past), i32([count]), i32(stack + [-5, -5])
+        step = nv.KvStep.empty(requests, rows, **(dict(lens=n, free_count=c) if in_place else {}))
+        asked, side = i32(more), torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            nv.kv_extend(n, asked, table, free, c, step)
+        for how in range(3):
+            step.row_start.fill_(9), step.missing.fill_(9), step.positions.fill_(9), step.slots.fill_(9)
+            if how == 0:
+                assert nv.kv_extend(n, asked, table, free, c, step) is step
+            elif how == 1:
+                side.wait_stream(torch.cuda.current_stream())
+                nv.kv_extend(n, asked, table, free, c, step, stream=side)
+                side.synchronize()
+            else:
+                graph.replay()
+                torch.cuda.synchronize()
+            want = step_ref.extend(past, more, table.tolist() or [[]], list(range(free_after)), rows)
+            check_extend(step, table, want, table.tolist())
+            assert n.tolist() == past and free.tolist() == stack + [-5, -5] and int(table.max()) == -1 if requests else True
+
+
+def test_release_of_no_requests(nv):
+    none, table = i32([]), torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+    for count, after in ((2, 2), (-4, 0), (8, 3)):
+        free = i32([1, 2, -5])
+        lens, left = nv.kv_release(none, none, table, free, i32([count]))
+        assert lens.shape == (0,) and left.tolist() == [after] and free.tolist() == [1, 2, -5]
+        c = i32([count])
+        assert nv.kv_release(none, none, table, free, c, free_count_out=c, to_prefix=True)[1] is c and c.tolist() == [after]
+    with pytest.raises(TypeError, match="done: expected int32"):
+        nv.kv_release(none, none.long(), table, i32([1]), i32([1]))
+    with pytest.raises(ValueError, match="a table of 0 requests, a step of 2"):
+        nv.kv_extend(none, none, table, i32([1]), i32([1]), nv.KvStep.empty(2, 3))
+
+
+# ---------------------------------------------------------------------------
 # requests behind a prefix that stays
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("count,keep", [(1, 1), (5, 3), (40, 2), (700, 1)])
