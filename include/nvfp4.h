@@ -562,7 +562,7 @@ typedef struct {
  * position % 64, to slots[m] (int64; -1 where there is no block); rows of no request
  * get -1 in both.  Either may be NULL.  row_start, lens, table and positions are what
  * nvfp4_kv_write, nvfp4_rope and nvfp4_kv_attention take: nothing of a step's tables
- * passes the host.  lens may be past and free_left may be free_count (a step in
+ * passes the host.  (slots are for a program's own kernels: no call here takes them.)  lens may be past and free_left may be free_count (a step in
  * place); otherwise outputs must not overlap one another or the inputs.  *free_count
  * is taken as at least 0 and at most capacity.  1 <= M <= 2^23.  The workspace needs
  * nvfp4_kv_extend_workspace_bytes(count) bytes (16-byte aligned). */
@@ -597,7 +597,9 @@ nvfp4_status nvfp4_kv_release_to_prefix(const nvfp4_kv_tables* tables, const int
  * position p sees those above p - window and the first `sinks`; the others' blocks
  * are not read.  causal_block bounds what a row sees ahead of it, as there (with 0 all
  * of its sequence).  window >= 1, sinks >= 0.  What hidden positions hold has no
- * effect; everything else as nvfp4_kv_attention has it.  The workspace needs
+ * effect.  The sum that divides is of the probabilities as they were rounded to bf16,
+ * where nvfp4_kv_attention adds them before: a key that has all the weight gives its
+ * value as it is.  Everything else as nvfp4_kv_attention has it.  The workspace needs
  * nvfp4_kv_attention_window_workspace_bytes(...) bytes for the same sizes (16-byte
  * aligned; may be NULL when that is 0). */
 size_t nvfp4_kv_attention_window_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,
@@ -616,7 +618,8 @@ nvfp4_status nvfp4_kv_attention_window(const nvfp4_heads* q, int64_t M, int32_t 
  * softmax.  The new rows of every sequence lie behind the prefix: rows of one with
  * lens[b] - n < 64 * shared_blocks give NaN.  max_len bounds the lengths, prefix
  * included.  1 <= shared_blocks <= (2^31 - 1) / 64; the tables hold the prefix too
- * (lens[b] <= 64 * table_blocks).  Everything else as nvfp4_kv_attention has it.  The
+ * (lens[b] <= 64 * table_blocks).  The rounded probabilities are what is summed, as
+ * through a window.  Everything else as nvfp4_kv_attention has it.  The
  * workspace needs nvfp4_kv_attention_shared_workspace_bytes(...) bytes for the same
  * sizes (16-byte aligned). */
 size_t nvfp4_kv_attention_shared_workspace_bytes(int64_t M, int64_t count, int32_t q_heads, int32_t heads, int32_t dim,

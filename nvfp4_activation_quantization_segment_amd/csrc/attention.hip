@@ -22,7 +22,7 @@
 // these products; as it is the outputs' error against 64 bits is 0.0021 to 0.0023
 // of their size, where binary32 probabilities and the output's own rounding give
 // 0.0016 to 0.0017.  (Through a window and over a prefix the rounded ones are
-// summed: where a few keys have the weight the error was 0.0025, and is 0.0024.)
+// summed: where a few keys have the weight the error was 0.0025, and is 0.0023.)
 // Scores, maxima, sums and outputs are held in binary32.
 #include "kv_device.h"
 
@@ -127,8 +127,8 @@ __device__ __forceinline__ int32_t low_of_row(const AttentionArgs& a, const Tile
 // A window's tile goes over the blocks that some of its rows see, no others: 32
 // tokens of 32 query and 8 key/value heads through 4096 of up to 16,384 keys, 240 MB,
 // take 49 us (all keys: 118), 4.9 TB/s; prompts of 12,000 rows through 1000 keys
-// 207 to 220 us on different cards (all keys: 361), of 18 blocks a tile 15.7 full
-// ones' worth of keys.  A path of its own for the blocks at a window's ends, which
+// 207 to 224 us on different cards (all keys: 361); their 3032 tiles go over 15.2
+// blocks each on average, for 13.3 full ones' worth of keys.  A path of its own for the blocks at a window's ends, which
 // passes over 32 keys that a wave does not see, made these 256 (accumulators copied
 // between the paths); tiles that begin at a common block and go round, so as to
 // read the same ones at a time, changed nothing.
@@ -381,9 +381,8 @@ __device__ __forceinline__ bf16x8 seen_ones(const f32x16& s, int k) {
 // formed.  Bound by memory: 32 single tokens of 32 query and 8 key/value heads
 // over 1 to 16,384 keys each, 539 MB, take 114 us and 5 for the join, 4.6 TB/s
 // of cache read; four over 65,536 keys 102 us, 5.3 TB/s.  With D = 128 all 256
-// vector registers are in use and 2 spill (12 bytes of scratch a lane), with
-// 41 scalar ones that go to lanes of a vector register; D = 64 spills 46 scalar
-// ones only.
+// vector registers are in use and 3 spill (16 bytes of scratch a lane; through a
+// window 1, 8 bytes); D = 64 takes up to 186 and spills none.
 // ---------------------------------------------------------------------------
 constexpr int kNarrowWaves = 4;
 
@@ -993,8 +992,9 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void attention_wide_kernel(Atte
 // other.  64 tokens of 32 query and 8 key/value heads, up to 1024 own keys each
 // behind 16,384, 103 MB: 40 us and 5 for the join (two launches after one another
 // 48 and 11; the prefix alone takes 32, the own keys alone 26); what is left is the
-// pieces' sums (13 of them, 14 MB written and read) and the chains of loads at both
-// ends.  500 rows of 32 heads over 32,768: 304 to 335 us, 950 TFLOP/s, the matrix
+// prefix's blocks, one in flight at a time (1.2 us each with a CU to themselves, of
+// which the matrix instructions are 0.41), the pieces' sums (13 of them, 14 MB written
+// and read) and the chains of loads at both ends.  500 rows of 32 heads over 32,768: 304 to 335 us, 950 TFLOP/s, the matrix
 // pipes busy 39% of the cycles: 432 workgroups for 512 places, and 18 tiles of 128
 // rows that hold 17.5.
 // Heads of 64 leave room for three workgroups on a CU, which many tiles of few keys
@@ -1245,7 +1245,8 @@ static void attention_join(const AttentionArgs& a, hipStream_t s) {
 }
 
 // The join of a batch: where the rows alone fill the chip, a wave takes a row and all
-// its parts.
+// its parts.  (There are at most 31 of the prefix and 16 own ones; the loads past a
+// row's parts take part 0 again.)
 template <int D>
 static void attention_join_batch(const AttentionArgs& a, hipStream_t s) {
     const int64_t rows = a.seqs.M * a.q_heads;
